@@ -306,6 +306,68 @@ MOE_API int moe_backward(const moe_config* cfg, const void* x, const void* W_r, 
                  void* dW_gate, void* dW_down, const moe_shared_ffn* shared, void* ws,
                  moe_stream_t stream);
 
+/* ---- the residual stream around a block ----
+ * A block F (this layer, or any other) reads a normalised copy of the residual
+ * stream x and adds its output u to it:
+ *   leave:  n  = post_norm ? w_post * u / rms(u) : u
+ *           x' = res_scale * x + out_scale * g * n
+ *   enter:  z  = w_pre * x' / rms(x')       (x' = x where leave = 0)
+ * with rms(v) = sqrt(mean_i v_i^2 + eps) per token.  leave and enter in one
+ * call fuse the end of one block with the start of the next: the stream is
+ * read and written once.  z is formed from x' before x' is rounded to the
+ * storage type.  The gate g is absent (1), a learned fp32 vector over the
+ * channels, an fp32 scalar per token, or a full [T,d] tensor in the act dtype. */
+#define MOE_GATE_NONE 0
+#define MOE_GATE_CHANNEL 1 /* gate[d] fp32    */
+#define MOE_GATE_TOKEN 2   /* gate[T] fp32    */
+#define MOE_GATE_FULL 3    /* gate[T,d] act   */
+#define MOE_NORM_MAX_D 16384
+
+typedef struct {
+    int32_t T;         /* tokens                                                */
+    int32_t d;         /* width, 1..MOE_NORM_MAX_D (any; a row that is a multiple
+                          of 16 bytes takes the wide-load path)                 */
+    int32_t dtype;     /* MOE_DTYPE_F32 or MOE_DTYPE_BF16: x, u, x', z, full gate */
+    int32_t leave;     /* 1: x' = res_scale x + out_scale g n; 0: x' = x        */
+    int32_t post_norm; /* 1: n = w_post u / rms(u); 0: n = u   (0 if leave = 0) */
+    int32_t enter;     /* 1: emit z   (1 if leave = 0)                          */
+    int32_t gate;      /* MOE_GATE_*  (NONE if leave = 0)                       */
+    float eps;         /* > 0                                                   */
+    float res_scale;   /* finite                                                */
+    float out_scale;   /* finite                                                */
+} moe_norm_config;
+
+/* MOE_OK, MOE_ERR_INVALID_ARG, or MOE_ERR_UNSUPPORTED (d > MOE_NORM_MAX_D). */
+MOE_API int moe_check_norm_config(const moe_norm_config* cfg);
+
+/* Bytes of workspace of moe_block_norm_backward. */
+MOE_API int moe_norm_workspace_size(const moe_norm_config* cfg, size_t* bytes);
+
+/* Forward.  x, u [T,d]; w_post, w_pre [d] fp32; gate by cfg->gate; out: x_out,
+ * z [T,d].  Pointers of absent parts (u, w_post, gate, x_out where leave = 0 or
+ * the part is off; w_pre, z where enter = 0) are NULL.  x_out may be x and z
+ * may be u (each row is read before it is written); no other overlap.        */
+MOE_API int moe_block_norm(const moe_norm_config* cfg, const void* x, const void* u,
+                           const float* w_post, const void* gate, const float* w_pre, void* x_out,
+                           void* z, moe_stream_t stream);
+
+/* Backward at the stored stream x_out (the x given where leave = 0).  With
+ *   G = dx_out + r w_pre dz - x_out r^3/d <w_pre dz, x_out>,  r = 1/rms(x_out):
+ *   dx = res_scale G (G where leave = 0);  dn = out_scale g G;
+ *   du = dn, or dn through the post norm as above;
+ *   dw_pre = sum_t dz x_out r;  dw_post = sum_t dn u / rms(u);
+ *   dgate = out_scale G n, summed over tokens (channel) or channels (token).
+ * dx_out (the gradient that reaches x_out along the stream) may be NULL where
+ * enter = 1: zero.  u is read where post_norm = 1 or a gate is given (else it
+ * may be NULL).  dw_post, dw_pre [d] fp32; dgate in the gate's shape and type.
+ * Gradients of absent parts are NULL.  The statistics are formed again from
+ * x_out and u, so nothing but these tensors is kept from the forward.        */
+MOE_API int moe_block_norm_backward(const moe_norm_config* cfg, const void* x_out, const void* u,
+                                    const float* w_post, const void* gate, const float* w_pre,
+                                    const void* dx_out, const void* dz, void* dx, void* du,
+                                    float* dw_post, void* dgate, float* dw_pre, void* ws,
+                                    moe_stream_t stream);
+
 /* ---- status and bookkeeping ---- */
 
 /* Text of a status code (static storage). */

@@ -137,6 +137,10 @@ _SIGS = {
     "moe_grouped_ffn_backward": [ctypes.c_void_p] * 17,
     "moe_router_backward": [ctypes.c_void_p] * 17,
     "moe_backward": [ctypes.c_void_p] * 27,
+    "moe_check_norm_config": [ctypes.c_void_p],
+    "moe_norm_workspace_size": [ctypes.c_void_p, ctypes.c_void_p],
+    "moe_block_norm": [ctypes.c_void_p] * 9,
+    "moe_block_norm_backward": [ctypes.c_void_p] * 15,
     "moe_last_device_status": [ctypes.c_void_p, ctypes.c_void_p],
     "moe_selftest_bounded_wait": [ctypes.c_ulonglong, ctypes.c_void_p],
 }
@@ -414,3 +418,7 @@ class MoELayer:
                      g["dbias"] if bias is not None else None, g["dW_up"], g["dW_gate"],
                      g["dW_down"], self.ws, stream, shared=self.shared_block())
         return g
+
+
+# the operators around the layer (imported last: they use the helpers above)
+from .block import *  # noqa: E402,F401,F403

@@ -1,0 +1,142 @@
+"""The operators around the layer: binding of their C entry points.
+
+Residual-stream norms (``moe_block_norm`` and its backward).  As in the
+package's root, every function mirrors the C entry point of the same name and
+the classes own the output buffers and workspaces of one configuration.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+import top_routing_expert_moe_gb300 as _moe
+
+__all__ = ["GATE_NONE", "GATE_CHANNEL", "GATE_TOKEN", "GATE_FULL", "NormConfig",
+           "check_norm_config", "norm_workspace_size", "moe_block_norm",
+           "moe_block_norm_backward", "BlockNorm"]
+
+GATE_NONE, GATE_CHANNEL, GATE_TOKEN, GATE_FULL = 0, 1, 2, 3
+
+_p, _s, _call = _moe._p, _moe._s, _moe._call
+
+
+def _checked(t, shape, dtype, name):
+    """The tensor, after a check of its shape and type (None passes)."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch tensor")
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+        raise ValueError(f"{name}: expected {tuple(shape)} {dtype}, got {tuple(t.shape)} {t.dtype}")
+    return t
+
+
+# ----------------------------------------------------------------- residual stream
+class NormConfig(ctypes.Structure):
+    """Mirror of ``moe_norm_config`` (include/moe.h)."""
+    _fields_ = [("T", ctypes.c_int32), ("d", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("leave", ctypes.c_int32), ("post_norm", ctypes.c_int32),
+                ("enter", ctypes.c_int32), ("gate", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("res_scale", ctypes.c_float), ("out_scale", ctypes.c_float)]
+
+    def __init__(self, T, d, dtype=_moe.BF16, leave=1, post_norm=0, enter=1, gate=GATE_NONE,
+                 eps=1e-6, res_scale=1.0, out_scale=1.0):
+        super().__init__(T, d, dtype, int(leave), int(post_norm), int(enter), gate, eps, res_scale,
+                         out_scale)
+
+    @property
+    def torch_dtype(self):
+        return torch.bfloat16 if self.dtype == _moe.BF16 else torch.float32
+
+    @property
+    def gate_shape(self):
+        """(shape, dtype) of the gate, or None."""
+        return {GATE_NONE: None, GATE_CHANNEL: ((self.d,), torch.float32),
+                GATE_TOKEN: ((self.T,), torch.float32),
+                GATE_FULL: ((self.T, self.d), self.torch_dtype)}[self.gate]
+
+
+def check_norm_config(cfg: NormConfig) -> int:
+    return _moe.load_library().moe_check_norm_config(ctypes.byref(cfg))
+
+
+def norm_workspace_size(cfg: NormConfig) -> int:
+    v = ctypes.c_size_t()
+    _call("moe_norm_workspace_size", ctypes.byref(cfg), ctypes.byref(v))
+    return v.value
+
+
+def moe_block_norm(cfg, x, u, w_post, gate, w_pre, x_out, z, stream=None):
+    _call("moe_block_norm", ctypes.byref(cfg), _p(x), _p(u), _p(w_post), _p(gate), _p(w_pre),
+          _p(x_out), _p(z), _s(stream))
+
+
+def moe_block_norm_backward(cfg, x_out, u, w_post, gate, w_pre, dx_out, dz, dx, du, dw_post, dgate,
+                            dw_pre, ws, stream=None):
+    _call("moe_block_norm_backward", ctypes.byref(cfg), _p(x_out), _p(u), _p(w_post), _p(gate),
+          _p(w_pre), _p(dx_out), _p(dz), _p(dx), _p(du), _p(dw_post), _p(dgate), _p(dw_pre),
+          _p(ws), _s(stream))
+
+
+class BlockNorm:
+    """One place on the residual stream: leaving a block (normalise its output
+    u, gate it, scale it, add it to the stream x), entering the next (the
+    normalised copy z), or both in one pass.  Owns its outputs and workspace."""
+
+    def __init__(self, cfg: NormConfig, device="cuda"):
+        rc = check_norm_config(cfg)
+        if rc != 0:
+            raise _moe.MoEError(rc, "moe_check_norm_config")
+        self.cfg = c = cfg
+        self.device = torch.device(device)
+        e = lambda on, *s, dtype=c.torch_dtype: (  # noqa: E731
+            torch.empty(*s, dtype=dtype, device=self.device) if on else None)
+        self.x_out = e(c.leave, c.T, c.d)
+        self.z = e(c.enter, c.T, c.d)
+        self._grads = self._ws = None
+
+    def _check(self, **tensors):
+        c = self.cfg
+        rows, vec = ((c.T, c.d), c.torch_dtype), ((c.d,), torch.float32)
+        spec = dict(x=rows, x_out=rows, u=rows, dx_out=rows, dz=rows, w_post=vec, w_pre=vec)
+        for n, t in tensors.items():
+            want = c.gate_shape if n == "gate" else spec[n]
+            if want is None:
+                if t is not None:
+                    raise ValueError(f"{n} given, but the configuration has none")
+                continue
+            _checked(t, *want, n)
+
+    def forward(self, x, u=None, w_pre=None, w_post=None, gate=None, stream=None):
+        """(x_out, z): the stream after the block (x itself without ``leave``)
+        and its normalised copy (None without ``enter``)."""
+        self._check(x=x, u=u, w_pre=w_pre, w_post=w_post, gate=gate)
+        moe_block_norm(self.cfg, x, u, w_post, gate, w_pre, self.x_out, self.z, stream)
+        return (self.x_out if self.cfg.leave else x), self.z
+
+    def grads(self):
+        if self._grads is None:
+            c = self.cfg
+            e = lambda on, *s, dtype=c.torch_dtype: (  # noqa: E731
+                torch.empty(*s, dtype=dtype, device=self.device) if on else None)
+            f32 = torch.float32
+            self._grads = dict(dx=e(1, c.T, c.d), du=e(c.leave, c.T, c.d),
+                               dw_pre=e(c.enter, c.d, dtype=f32),
+                               dw_post=e(c.post_norm, c.d, dtype=f32),
+                               dgate=(e(1, *c.gate_shape[0], dtype=c.gate_shape[1])
+                                      if c.gate != GATE_NONE else None))
+            self._ws = torch.empty(max(norm_workspace_size(c), 256), dtype=torch.uint8,
+                                   device=self.device)
+        return self._grads
+
+    def backward(self, x_out, dx_out=None, dz=None, u=None, w_pre=None, w_post=None, gate=None,
+                 stream=None):
+        """Gradients dx, du, dw_pre, dw_post, dgate (None where absent) at the
+        stored stream x_out (x where the configuration does not leave a block),
+        given those of x_out along the stream (None: zero) and of z."""
+        self._check(x_out=x_out, dx_out=dx_out, dz=dz, u=u, w_pre=w_pre, w_post=w_post, gate=gate)
+        g = self.grads()
+        moe_block_norm_backward(self.cfg, x_out, u, w_post, gate, w_pre, dx_out, dz, g["dx"],
+                                g["du"], g["dw_post"], g["dgate"], g["dw_pre"], self._ws, stream)
+        return g

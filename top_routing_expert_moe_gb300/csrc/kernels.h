@@ -51,4 +51,13 @@ int launch_ffn_backward(const moe_config& c, const void* x_perm, const int32_t* 
                         void* dx_perm, void* dW_up, void* dW_gate, void* dW_down,
                         const moe_shared_ffn* shared, void* ws, cudaStream_t st);
 
+// norm.cu (the residual stream's norms around a block)
+size_t norm_ws_bytes(const moe_norm_config& c);
+int launch_block_norm(const moe_norm_config& c, const void* x, const void* u, const float* w_post,
+                      const void* gate, const float* w_pre, void* x_out, void* z, cudaStream_t st);
+int launch_block_norm_backward(const moe_norm_config& c, const void* x_out, const void* u,
+                               const float* w_post, const void* gate, const float* w_pre,
+                               const void* dx_out, const void* dz, void* dx, void* du,
+                               float* dw_post, void* dgate, float* dw_pre, void* ws, cudaStream_t st);
+
 }  // namespace moe
