@@ -368,6 +368,64 @@ MOE_API int moe_block_norm_backward(const moe_norm_config* cfg, const void* x_ou
                                     float* dw_post, void* dgate, float* dw_pre, void* ws,
                                     moe_stream_t stream);
 
+/* ---- balance loss over sequences ----
+ * Beside moe_route's whole-batch statistics: the f.P balance loss per sequence
+ * and the z loss, with gradients.  For sequence s with n_s routed tokens
+ * (topk_idx[t,0] >= 0), p_t = softmax(logits_t / tau), lse_t = log sum exp:
+ *   c_se = those tokens' entries of topk_idx equal to e,  P_se = (1/n_s) sum_t p_te
+ *   balance = balance_coef * mean over sequences with n_s > 0 of
+ *             sum_e (E c_se / (k n_s)) P_se
+ *   z       = z_coef * (1/n) sum_t lse_t^2 over all n routed tokens
+ * Counts carry no gradient.  A logit of -inf is an expert masked for that token
+ * (p = 0); a routed token whose logits are all -inf adds nothing but its counts
+ * and n.  NaN or +inf in a routed token's logits is recorded as
+ * MOE_ERR_NONFINITE; masked tokens' logits are not looked at.                 */
+typedef struct {
+    int32_t T;            /* tokens                                           */
+    int32_t E;            /* experts, 1..256                                  */
+    int32_t k;            /* experts per token, 1..min(E, 16)                 */
+    int32_t S;            /* sequences, 1..65536                              */
+    float balance_coef;   /* finite                                           */
+    float z_coef;         /* finite                                           */
+    float temperature;    /* tau > 0, or 0 for 1                              */
+} moe_balance_config;
+
+MOE_API int moe_check_balance_config(const moe_balance_config* cfg);
+
+/* Bytes of workspace of moe_balance_loss. */
+MOE_API int moe_balance_workspace_size(const moe_balance_config* cfg, size_t* bytes);
+
+/* Forward.  logits [T,E] fp32; topk_idx [T,k] int32, -1 = no expert;
+ * seq_offsets [S+1] int32 (device), ascending from 0 to T, or NULL for one
+ * sequence (S = 1).  Out: loss[3] fp32 = {balance + z, balance, z};
+ * counts [S,E] int32; pbar [S,E] fp32 (0 for a sequence without tokens);
+ * grad_w [S,E+2] fp32 = what the backward needs of each sequence.
+ * Offsets out of order or outside 0..T, and expert indices outside -1..E-1,
+ * are recorded as MOE_ERR_DEVICE_BOUNDS and clamped or left out.             */
+MOE_API int moe_balance_loss(const moe_balance_config* cfg, const float* logits,
+                             const int32_t* topk_idx, const int32_t* seq_offsets, float* loss,
+                             int32_t* counts, float* pbar, float* grad_w, void* ws,
+                             moe_stream_t stream);
+
+/* Backward: dlogits [T,E] fp32 = dloss * d(balance + z)/dlogits, with grad_w
+ * from the forward; dloss: one fp32 on the device, or NULL for 1.            */
+MOE_API int moe_balance_loss_backward(const moe_balance_config* cfg, const float* logits,
+                                      const int32_t* topk_idx, const int32_t* seq_offsets,
+                                      const float* grad_w, const float* dloss, float* dlogits,
+                                      moe_stream_t stream);
+
+/* moe_backward with a further gradient on the router logits (dlogits_aux [T,E]
+ * fp32 or NULL), such as moe_balance_loss_backward's: it is added to the
+ * router's own before dx, dW_r and dbias are formed.                         */
+MOE_API int moe_backward_aux(const moe_config* cfg, const void* x, const void* W_r, const void* W_up,
+                 const void* W_gate, const void* W_down, const float* logits,
+                 const int32_t* topk_idx, const float* gate, const int32_t* slot_of,
+                 const int32_t* perm_token, const int32_t* offsets, const void* x_perm,
+                 const void* h_saved, const void* act, const void* y_perm, const float* stats,
+                 const float* dlogits_aux, const void* dout, void* dx, void* dW_r, float* dbias,
+                 void* dW_up, void* dW_gate, void* dW_down, const moe_shared_ffn* shared, void* ws,
+                 moe_stream_t stream);
+
 /* ---- status and bookkeeping ---- */
 
 /* Text of a status code (static storage). */

@@ -141,6 +141,11 @@ _SIGS = {
     "moe_norm_workspace_size": [ctypes.c_void_p, ctypes.c_void_p],
     "moe_block_norm": [ctypes.c_void_p] * 9,
     "moe_block_norm_backward": [ctypes.c_void_p] * 15,
+    "moe_check_balance_config": [ctypes.c_void_p],
+    "moe_balance_workspace_size": [ctypes.c_void_p, ctypes.c_void_p],
+    "moe_balance_loss": [ctypes.c_void_p] * 10,
+    "moe_balance_loss_backward": [ctypes.c_void_p] * 8,
+    "moe_backward_aux": [ctypes.c_void_p] * 28,
     "moe_last_device_status": [ctypes.c_void_p, ctypes.c_void_p],
     "moe_selftest_bounded_wait": [ctypes.c_ulonglong, ctypes.c_void_p],
 }
@@ -304,6 +309,17 @@ def moe_backward(cfg, x, W_r, W_up, W_gate, W_down, logits, topk_idx, gate, slot
           _p(dbias), _p(dW_up), _p(dW_gate), _p(dW_down), _sh(shared), _p(ws), _s(stream))
 
 
+def moe_backward_aux(cfg, x, W_r, W_up, W_gate, W_down, logits, topk_idx, gate, slot_of,
+                     perm_token, offsets, x_perm, h_saved, act, y_perm, stats, dlogits_aux, dout,
+                     dx, dW_r, dbias, dW_up, dW_gate, dW_down, ws, stream=None, shared=None):
+    """moe_backward with a further gradient on the router logits (or None)."""
+    _call("moe_backward_aux", ctypes.byref(cfg), _p(x), _p(W_r), _p(W_up), _p(W_gate), _p(W_down),
+          _p(logits), _p(topk_idx), _p(gate), _p(slot_of), _p(perm_token), _p(offsets),
+          _p(x_perm), _p(h_saved), _p(act), _p(y_perm), _p(stats), _p(dlogits_aux), _p(dout),
+          _p(dx), _p(dW_r), _p(dbias), _p(dW_up), _p(dW_gate), _p(dW_down), _sh(shared), _p(ws),
+          _s(stream))
+
+
 # ----------------------------------------------------------------- convenience layer
 class MoELayer:
     """Owns the routing cache, permuted buffers and workspace of one layer
@@ -407,16 +423,21 @@ class MoELayer:
                             act=self.act_shared, y=self.y_shared, dout=dout, dh=dh, dx=dx,
                             dW_up=g["dW_up_s"], dW_gate=g["dW_gate_s"], dW_down=g["dW_down_s"])
 
-    def backward(self, dout, stream=None):
+    def backward(self, dout, stream=None, dlogits_aux=None):
+        """Gradients of the last forward.  ``dlogits_aux`` [T, E] fp32: a further
+        gradient on the router logits (a balance loss's), added to the router's own."""
         if self._inputs is None:
             raise RuntimeError("backward() needs a forward() first")
         x, W_r, W_up, W_gate, W_down, bias = self._inputs
         g = self.grads()
-        moe_backward(self.cfg, x, W_r, W_up, W_gate, W_down, self.logits, self.topk_idx, self.gate,
-                     self.slot_of, self.perm_token, self.offsets, self.x_perm, self.h_saved,
-                     self.act, self.y_perm, self.stats, dout, g["dx"], g["dW_r"],
-                     g["dbias"] if bias is not None else None, g["dW_up"], g["dW_gate"],
-                     g["dW_down"], self.ws, stream, shared=self.shared_block())
+        if dlogits_aux is not None and (tuple(dlogits_aux.shape) != (self.cfg.T, self.cfg.E) or
+                                        dlogits_aux.dtype != torch.float32):
+            raise ValueError("dlogits_aux must be a [T, E] fp32 tensor")
+        moe_backward_aux(self.cfg, x, W_r, W_up, W_gate, W_down, self.logits, self.topk_idx,
+                         self.gate, self.slot_of, self.perm_token, self.offsets, self.x_perm,
+                         self.h_saved, self.act, self.y_perm, self.stats, dlogits_aux, dout,
+                         g["dx"], g["dW_r"], g["dbias"] if bias is not None else None, g["dW_up"],
+                         g["dW_gate"], g["dW_down"], self.ws, stream, shared=self.shared_block())
         return g
 
 

@@ -1,6 +1,7 @@
 """The operators around the layer: binding of their C entry points.
 
-Residual-stream norms (``moe_block_norm`` and its backward).  As in the
+Residual-stream norms (``moe_block_norm``) and the router's per-sequence balance
+loss (``moe_balance_loss``), each with its backward.  As in the
 package's root, every function mirrors the C entry point of the same name and
 the classes own the output buffers and workspaces of one configuration.
 """
@@ -14,7 +15,9 @@ import top_routing_expert_moe_gb300 as _moe
 
 __all__ = ["GATE_NONE", "GATE_CHANNEL", "GATE_TOKEN", "GATE_FULL", "NormConfig",
            "check_norm_config", "norm_workspace_size", "moe_block_norm",
-           "moe_block_norm_backward", "BlockNorm"]
+           "moe_block_norm_backward", "BlockNorm", "BalanceConfig", "check_balance_config",
+           "balance_workspace_size", "moe_balance_loss", "moe_balance_loss_backward",
+           "BalanceLoss"]
 
 GATE_NONE, GATE_CHANNEL, GATE_TOKEN, GATE_FULL = 0, 1, 2, 3
 
@@ -140,3 +143,77 @@ class BlockNorm:
         moe_block_norm_backward(self.cfg, x_out, u, w_post, gate, w_pre, dx_out, dz, g["dx"],
                                 g["du"], g["dw_post"], g["dgate"], g["dw_pre"], self._ws, stream)
         return g
+
+
+# ----------------------------------------------------------------- balance loss
+class BalanceConfig(ctypes.Structure):
+    """Mirror of ``moe_balance_config`` (include/moe.h)."""
+    _fields_ = [("T", ctypes.c_int32), ("E", ctypes.c_int32), ("k", ctypes.c_int32),
+                ("S", ctypes.c_int32), ("balance_coef", ctypes.c_float),
+                ("z_coef", ctypes.c_float), ("temperature", ctypes.c_float)]
+
+    def __init__(self, T, E, k, S=1, balance_coef=0.01, z_coef=0.0, temperature=1.0):
+        super().__init__(T, E, k, S, balance_coef, z_coef, temperature)
+
+
+def check_balance_config(cfg: BalanceConfig) -> int:
+    return _moe.load_library().moe_check_balance_config(ctypes.byref(cfg))
+
+
+def balance_workspace_size(cfg: BalanceConfig) -> int:
+    v = ctypes.c_size_t()
+    _call("moe_balance_workspace_size", ctypes.byref(cfg), ctypes.byref(v))
+    return v.value
+
+
+def moe_balance_loss(cfg, logits, topk_idx, seq_offsets, loss, counts, pbar, grad_w, ws, stream=None):
+    _call("moe_balance_loss", ctypes.byref(cfg), _p(logits), _p(topk_idx), _p(seq_offsets),
+          _p(loss), _p(counts), _p(pbar), _p(grad_w), _p(ws), _s(stream))
+
+
+def moe_balance_loss_backward(cfg, logits, topk_idx, seq_offsets, grad_w, dloss, dlogits, stream=None):
+    _call("moe_balance_loss_backward", ctypes.byref(cfg), _p(logits), _p(topk_idx),
+          _p(seq_offsets), _p(grad_w), _p(dloss), _p(dlogits), _s(stream))
+
+
+class BalanceLoss:
+    """The router's balance and z losses over sequences.  ``forward`` returns
+    loss [3] (their sum, balance, z) and fills ``counts`` and ``pbar`` [S, E];
+    ``backward`` returns the gradient on the logits, for
+    ``MoELayer.backward(dout, dlogits_aux=...)``."""
+
+    def __init__(self, cfg: BalanceConfig, device="cuda"):
+        rc = check_balance_config(cfg)
+        if rc != 0:
+            raise _moe.MoEError(rc, "moe_check_balance_config")
+        self.cfg, dev = cfg, torch.device(device)
+        e = lambda *s, dtype=torch.float32: torch.empty(*s, dtype=dtype, device=dev)  # noqa: E731
+        self.loss = e(3)
+        self.counts = e(cfg.S, cfg.E, dtype=torch.int32)
+        self.pbar = e(cfg.S, cfg.E)
+        self.grad_w = e(cfg.S, cfg.E + 2)
+        self.dlogits = e(cfg.T, cfg.E)
+        self.ws = e(max(balance_workspace_size(cfg), 256), dtype=torch.uint8)
+        self._inputs = None
+
+    def forward(self, logits, topk_idx, seq_offsets=None, stream=None):
+        c = self.cfg
+        _checked(logits, (c.T, c.E), torch.float32, "logits")
+        _checked(topk_idx, (c.T, c.k), torch.int32, "topk_idx")
+        _checked(seq_offsets, (c.S + 1,), torch.int32, "seq_offsets")
+        moe_balance_loss(c, logits, topk_idx, seq_offsets, self.loss, self.counts, self.pbar,
+                         self.grad_w, self.ws, stream)
+        self._inputs = (logits, topk_idx, seq_offsets)
+        return self.loss
+
+    def backward(self, dloss=None, stream=None):
+        """dlogits [T, E] of the last forward, times ``dloss`` (one fp32 on the
+        device; None: 1)."""
+        if self._inputs is None:
+            raise RuntimeError("backward() needs a forward() first")
+        if dloss is not None and (dloss.numel() != 1 or dloss.dtype != torch.float32):
+            raise ValueError("dloss must be one fp32")
+        logits, topk_idx, seq_offsets = self._inputs
+        moe_balance_loss_backward(self.cfg, logits, topk_idx, seq_offsets, self.grad_w, dloss,
+                                  self.dlogits, stream)
+        return self.dlogits

@@ -69,4 +69,47 @@ int moe_block_norm_backward(const moe_norm_config* c, const void* x_out, const v
                                       dgate, dw_pre, ws, (cudaStream_t)stream);
 }
 
+int moe_check_balance_config(const moe_balance_config* c) {
+    if (!c || c->T < 1 || c->E < 1 || c->k < 1 || c->k > c->E || c->S < 1) return MOE_ERR_INVALID_ARG;
+    if (!std::isfinite(c->balance_coef) || !std::isfinite(c->z_coef)) return MOE_ERR_INVALID_ARG;
+    if (!std::isfinite(c->temperature) || c->temperature < 0.f) return MOE_ERR_INVALID_ARG;
+    if (c->E > 256 || c->k > 16 || c->S > 65536 || c->T > (1 << 30)) return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+
+int moe_balance_workspace_size(const moe_balance_config* c, size_t* bytes) {
+    const int r = moe_check_balance_config(c);
+    if (r) return r;
+    if (!bytes) return MOE_ERR_INVALID_ARG;
+    *bytes = balance_ws_bytes(*c);
+    return MOE_OK;
+}
+
+int moe_balance_loss(const moe_balance_config* c, const float* logits, const int32_t* topk_idx,
+                     const int32_t* seq_offsets, float* loss, int32_t* counts, float* pbar,
+                     float* grad_w, void* ws, moe_stream_t stream) {
+    const int r = moe_check_balance_config(c);
+    if (r) return r;
+    if (!ok_ptr(logits) || !ok_ptr(topk_idx) || !aligned16(seq_offsets) || !ok_ptr(loss) ||
+        !ok_ptr(counts) || !ok_ptr(pbar) || !ok_ptr(grad_w) || !ok_ptr(ws))
+        return MOE_ERR_INVALID_ARG;
+    if (!seq_offsets && c->S != 1) return MOE_ERR_INVALID_ARG;
+    return launch_balance_loss(*c, logits, topk_idx, seq_offsets, loss, counts, pbar, grad_w, ws,
+                               (cudaStream_t)stream);
+}
+
+int moe_balance_loss_backward(const moe_balance_config* c, const float* logits,
+                              const int32_t* topk_idx, const int32_t* seq_offsets,
+                              const float* grad_w, const float* dloss, float* dlogits,
+                              moe_stream_t stream) {
+    const int r = moe_check_balance_config(c);
+    if (r) return r;
+    if (!ok_ptr(logits) || !ok_ptr(topk_idx) || !aligned16(seq_offsets) || !ok_ptr(grad_w) ||
+        !aligned16(dloss) || !ok_ptr(dlogits))
+        return MOE_ERR_INVALID_ARG;
+    if (!seq_offsets && c->S != 1) return MOE_ERR_INVALID_ARG;
+    return launch_balance_loss_backward(*c, logits, topk_idx, seq_offsets, grad_w, dloss, dlogits,
+                                        (cudaStream_t)stream);
+}
+
 }  // extern "C"

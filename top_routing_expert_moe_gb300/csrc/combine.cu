@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(256) router_bwd_token_kernel(
     const float* __restrict__ dgate, const float* __restrict__ stats,
     const T* __restrict__ dx_perm, const T* __restrict__ dx_shared, const float* __restrict__ WrT,
     int Tn, int d, int E, int k, int normalize, int st, float inv_tau, float aux_coef,
-    float* __restrict__ dlogits, T* __restrict__ dx)
+    const float* __restrict__ dl_aux, float* __restrict__ dlogits, T* __restrict__ dx)
 {
     pdl_wait();      // the preceding kernel's writes are visible from here on
     pdl_trigger();
@@ -230,6 +230,10 @@ __global__ void __launch_bounds__(256) router_bwd_token_kernel(
         }
         dl0 *= inv_tau;
         dl1 *= inv_tau;
+        if (dl_aux) {                              // a further loss's gradient on the logits
+            if (lane < E) dl0 += dl_aux[(size_t)t * E + lane];
+            if (lane + 32 < E) dl1 += dl_aux[(size_t)t * E + lane + 32];
+        }
         if (lane < E) { dlogits[(size_t)t * E + lane] = dl0; s_dl[wib][lane] = dl0; }
         if (lane + 32 < E) { dlogits[(size_t)t * E + lane + 32] = dl1; s_dl[wib][lane + 32] = dl1; }
         if (!WITH_DX) continue;
@@ -279,7 +283,8 @@ __global__ void __launch_bounds__(256) router_dlogits_kernel(
     const float* __restrict__ logits, const int32_t* __restrict__ topk,
     const float* __restrict__ gate, const int32_t* __restrict__ slot_of,
     const float* __restrict__ dgate, const float* __restrict__ stats, int Tn, int E, int k,
-    int normalize, int st, float inv_tau, float aux_coef, float* __restrict__ dlogits)
+    int normalize, int st, float inv_tau, float aux_coef, const float* __restrict__ dl_aux,
+    float* __restrict__ dlogits)
 {
     pdl_wait();      // the preceding kernel's writes are visible from here on
     pdl_trigger();
@@ -371,8 +376,14 @@ __global__ void __launch_bounds__(256) router_dlogits_kernel(
             dl1 += p1 * (c1 - s2);
         }
         if (!routed) dl0 = dl1 = 0.f;
-        if (valid && e0 < E) dlogits[tb * E + e0] = dl0 * inv_tau;
-        if (valid && e1 < E) dlogits[tb * E + e1] = dl1 * inv_tau;
+        dl0 *= inv_tau;
+        dl1 *= inv_tau;
+        if (dl_aux) {                              // a further loss's gradient on the logits
+            if (valid && e0 < E) dl0 += dl_aux[tb * E + e0];
+            if (valid && e1 < E) dl1 += dl_aux[tb * E + e1];
+        }
+        if (valid && e0 < E) dlogits[tb * E + e0] = dl0;
+        if (valid && e1 < E) dlogits[tb * E + e1] = dl1;
     }
 }
 
@@ -941,8 +952,9 @@ size_t router_bwd_ws_bytes(const moe_config& c) {
 int launch_router_backward(const moe_config& c, const void* x, const void* Wr,
                            const float* logits, const int32_t* topk, const float* gate,
                            const int32_t* slot_of, const float* dgate, const void* dx_perm,
-                           const void* dx_shared, const float* stats, void* dx, void* dWr,
-                           float* dbias, float* dlogits, void* ws, cudaStream_t st)
+                           const void* dx_shared, const float* stats, const float* dl_aux,
+                           void* dx, void* dWr, float* dbias, float* dlogits, void* ws,
+                           cudaStream_t st)
 {
     const int ns = dwr_nsplit(c);
     uint8_t* w = static_cast<uint8_t*>(ws);
@@ -973,7 +985,7 @@ int launch_router_backward(const moe_config& c, const void* x, const void* Wr,
 #define MOE_DL(GG)                                                                                   \
     MOE_LAUNCH(router_dlogits_kernel<GG>, grid_dl, 256, 0, st, logits, topk, gate, slot_of, dgate,   \
                stats, c.T, c.E, c.k, c.normalize_gates, c.straight_through, inv_tau, c.aux_coef, \
-               dlogits)
+               dl_aux, dlogits)
             if (g == 2) MOE_DL(2);
             else if (g == 4) MOE_DL(4);
             else if (g == 8) MOE_DL(8);
@@ -998,7 +1010,7 @@ int launch_router_backward(const moe_config& c, const void* x, const void* Wr,
         MOE_LAUNCH(transpose_wr_f32_kernel<T>, 64, 256, 0, st, static_cast<const T*>(Wr), WrT, c.d, c.E);
         MOE_LAUNCH(router_bwd_token_kernel<T, true>, grid, 256, 0, st, logits, topk, gate, slot_of, dgate, stats, static_cast<const T*>(dx_perm),
             static_cast<const T*>(dx_shared), WrT, c.T, c.d, c.E, c.k, c.normalize_gates,
-            c.straight_through, inv_tau, c.aux_coef, dlogits, static_cast<T*>(dx));
+            c.straight_through, inv_tau, c.aux_coef, dl_aux, dlogits, static_cast<T*>(dx));
         MOE_LAUNCH(dwr_partial_kernel<T, DWR_EB>, pgrid, 256, dwr_smem, st, static_cast<const T*>(x), dlogits,
                                                                    c.T, c.d, c.E, chunk, part, part_db);
         MOE_LAUNCH(dwr_reduce_kernel<T>, (c.d * c.E / 4 + DWR_RED_COLS - 1) / DWR_RED_COLS, DWR_RED_COLS * DWR_RED_GROUPS, 0, st, part, part_db, ns, c.d, c.E, static_cast<T*>(dWr), dbias);

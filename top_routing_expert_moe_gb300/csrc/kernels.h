@@ -36,8 +36,9 @@ size_t router_bwd_ws_bytes(const moe_config& c);
 int launch_router_backward(const moe_config& c, const void* x, const void* Wr,
                            const float* logits, const int32_t* topk, const float* gate,
                            const int32_t* slot_of, const float* dgate, const void* dx_perm,
-                           const void* dx_shared, const float* stats, void* dx, void* dWr,
-                           float* dbias, float* dlogits, void* ws, cudaStream_t st);
+                           const void* dx_shared, const float* stats, const float* dl_aux,
+                           void* dx, void* dWr, float* dbias, float* dlogits, void* ws,
+                           cudaStream_t st);
 
 // ffn.cu (grouped GEMMs: tcgen05 path for bf16, SIMT path for fp32)
 size_t ffn_ws_bytes(const moe_config& c);
@@ -59,5 +60,14 @@ int launch_block_norm_backward(const moe_norm_config& c, const void* x_out, cons
                                const float* w_post, const void* gate, const float* w_pre,
                                const void* dx_out, const void* dz, void* dx, void* du,
                                float* dw_post, void* dgate, float* dw_pre, void* ws, cudaStream_t st);
+
+// balance.cu (per-sequence balance loss and z loss)
+size_t balance_ws_bytes(const moe_balance_config& c);
+int launch_balance_loss(const moe_balance_config& c, const float* logits, const int32_t* topk,
+                        const int32_t* seq, float* loss, int32_t* counts, float* pbar,
+                        float* grad_w, void* ws, cudaStream_t st);
+int launch_balance_loss_backward(const moe_balance_config& c, const float* logits, const int32_t* topk,
+                                 const int32_t* seq, const float* grad_w, const float* dloss,
+                                 float* dlogits, cudaStream_t st);
 
 }  // namespace moe

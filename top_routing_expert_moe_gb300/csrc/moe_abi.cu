@@ -126,6 +126,25 @@ BwdLayout bwd_layout(const moe_config& c) {
     return L;
 }
 
+// moe_router_backward with a further gradient on the logits (dl_aux, may be NULL)
+int router_backward(const moe_config* c, const void* x, const void* W_r, const float* logits,
+                        const int32_t* topk_idx, const float* gate, const int32_t* slot_of,
+                        const float* dgate, const void* dx_perm, const moe_shared_ffn* shared,
+                        const float* stats, const float* dl_aux, void* dx, void* dW_r,
+                        float* dbias, float* dlogits, void* ws, moe_stream_t stream) {
+    int r = moe_check_config(c);
+    if (r) return r;
+    if (!ok_ptr(x) || !ok_ptr(W_r) || !ok_ptr(logits) || !ok_ptr(topk_idx) || !ok_ptr(gate) ||
+        !ok_ptr(slot_of) || !ok_ptr(dgate) || !ok_ptr(dx_perm) || !ok_opt(stats) || !ok_opt(dl_aux) || !ok_ptr(dx) ||
+        !ok_ptr(dW_r) || !ok_opt(dbias) || !ok_opt(dlogits) || !ok_ptr(ws) ||
+        !shared_ok(*c, shared, SH_ROUTER_BWD))
+        return MOE_ERR_INVALID_ARG;
+    if (c->aux_coef != 0.0f && !stats) return MOE_ERR_INVALID_ARG;
+    return launch_router_backward(*c, x, W_r, logits, topk_idx, gate, slot_of, dgate, dx_perm,
+                                  shared ? shared->dx : nullptr, stats, dl_aux, dx, dW_r, dbias,
+                                  dlogits, ws, (cudaStream_t)stream);
+}
+
 }  // namespace
 
 extern "C" {
@@ -280,26 +299,18 @@ int moe_router_backward(const moe_config* c, const void* x, const void* W_r, con
                         const float* dgate, const void* dx_perm, const moe_shared_ffn* shared,
                         const float* stats, void* dx, void* dW_r, float* dbias, float* dlogits,
                         void* ws, moe_stream_t stream) {
-    int r = moe_check_config(c);
-    if (r) return r;
-    if (!ok_ptr(x) || !ok_ptr(W_r) || !ok_ptr(logits) || !ok_ptr(topk_idx) || !ok_ptr(gate) ||
-        !ok_ptr(slot_of) || !ok_ptr(dgate) || !ok_ptr(dx_perm) || !ok_opt(stats) || !ok_ptr(dx) ||
-        !ok_ptr(dW_r) || !ok_opt(dbias) || !ok_opt(dlogits) || !ok_ptr(ws) ||
-        !shared_ok(*c, shared, SH_ROUTER_BWD))
-        return MOE_ERR_INVALID_ARG;
-    if (c->aux_coef != 0.0f && !stats) return MOE_ERR_INVALID_ARG;
-    return launch_router_backward(*c, x, W_r, logits, topk_idx, gate, slot_of, dgate, dx_perm,
-                                  shared ? shared->dx : nullptr, stats, dx, dW_r, dbias, dlogits,
-                                  ws, (cudaStream_t)stream);
+    return router_backward(c, x, W_r, logits, topk_idx, gate, slot_of, dgate, dx_perm, shared, stats,
+                           nullptr, dx, dW_r, dbias, dlogits, ws, stream);
 }
 
-int moe_backward(const moe_config* c, const void* x, const void* W_r, const void* W_up,
+int moe_backward_aux(const moe_config* c, const void* x, const void* W_r, const void* W_up,
                  const void* W_gate, const void* W_down, const float* logits,
                  const int32_t* topk_idx, const float* gate, const int32_t* slot_of,
                  const int32_t* perm_token, const int32_t* offsets, const void* x_perm,
                  const void* h_saved, const void* act, const void* y_perm, const float* stats,
-                 const void* dout, void* dx, void* dW_r, float* dbias, void* dW_up, void* dW_gate,
-                 void* dW_down, const moe_shared_ffn* shared, void* ws, moe_stream_t stream) {
+                 const float* dlogits_aux, const void* dout, void* dx, void* dW_r, float* dbias,
+                 void* dW_up, void* dW_gate, void* dW_down, const moe_shared_ffn* shared, void* ws,
+                 moe_stream_t stream) {
     int r = moe_check_config(c);
     if (r) return r;
     if (!ok_ptr(ws)) return MOE_ERR_INVALID_ARG;
@@ -325,8 +336,20 @@ int moe_backward(const moe_config* c, const void* x, const void* W_r, const void
     if ((r = moe_grouped_ffn_backward(c, x_perm, offsets, W_up, W_gate, W_down, h_saved, act, dy, dh,
                                       dxp, dW_up, dW_gate, dW_down, shp, rest, stream)))
         return r;
-    return moe_router_backward(c, x, W_r, logits, topk_idx, gate, slot_of, dgate, dxp, shp, stats,
-                               dx, dW_r, dbias, dlogits, rest, stream);
+    return router_backward(c, x, W_r, logits, topk_idx, gate, slot_of, dgate, dxp, shp, stats,
+                           dlogits_aux, dx, dW_r, dbias, dlogits, rest, stream);
+}
+
+int moe_backward(const moe_config* c, const void* x, const void* W_r, const void* W_up,
+                 const void* W_gate, const void* W_down, const float* logits,
+                 const int32_t* topk_idx, const float* gate, const int32_t* slot_of,
+                 const int32_t* perm_token, const int32_t* offsets, const void* x_perm,
+                 const void* h_saved, const void* act, const void* y_perm, const float* stats,
+                 const void* dout, void* dx, void* dW_r, float* dbias, void* dW_up, void* dW_gate,
+                 void* dW_down, const moe_shared_ffn* shared, void* ws, moe_stream_t stream) {
+    return moe_backward_aux(c, x, W_r, W_up, W_gate, W_down, logits, topk_idx, gate, slot_of,
+                            perm_token, offsets, x_perm, h_saved, act, y_perm, stats, nullptr, dout,
+                            dx, dW_r, dbias, dW_up, dW_gate, dW_down, shared, ws, stream);
 }
 
 const char* moe_error_string(int code) {
