@@ -426,6 +426,71 @@ MOE_API int moe_backward_aux(const moe_config* cfg, const void* x, const void* W
                  void* dW_up, void* dW_gate, void* dW_down, const moe_shared_ffn* shared, void* ws,
                  moe_stream_t stream);
 
+/* ---- microscaled 4-bit numbers ----
+ * A block of 32 consecutive elements along the reduction axis shares one
+ * power-of-two scale.  With amax the block's largest magnitude:
+ *   scale byte s = max(exponent(amax) - 2, 0), biased by 127 (value 2^(s-127));
+ *                  255 where the block holds an infinity or NaN (value NaN)
+ *   code  = x 2^(127-s) to the nearest of +-{0, .5, 1, 1.5, 2, 3, 4, 6}, ties to
+ *           the even code, magnitudes above 6 to 6; 0 in a block of byte 255
+ * Codes: two to a byte, the lower index in the low 4 bits, rows of K/2 bytes.
+ * Scales: tiles of 128 rows x 128 elements, 512 bytes each, row tiles outermost:
+ *   byte of (row r, element i) = ((r/128) * ceil(K/128) + i/128) * 512
+ *                                + (r%32) * 16 + (r%128)/32 * 4 + (i%128)/32
+ * (the order in which the tensor cores take them, so that a tile is one copy).
+ * Bytes of rows or elements past the tensor's end are 0.                     */
+/* Bytes of the scale tiles of a [rows,K] tensor. */
+MOE_API int moe_mx4_scale_bytes(int64_t rows, int32_t K, size_t* bytes);
+
+/* Rows: x [rows,K] (dtype MOE_DTYPE_*), K a multiple of 32 -> codes [rows,K/2],
+ * scales.  rows_used: one int32 on the device (moe_permute's offsets + E), or
+ * NULL for all: rows from it on are not read, their codes are not written, and
+ * their scale bytes are 0 within its tile of 128 and not written beyond.     */
+MOE_API int moe_mx4_quantize(int32_t dtype, int64_t rows, int32_t K, const void* x,
+                             const int32_t* rows_used, void* codes, void* scales,
+                             moe_stream_t stream);
+
+/* Weights: W [E,K,N] with blocks along K -> codes [E,N,K/2] (each expert's
+ * matrix transposed) and E scale sets of moe_mx4_scale_bytes(N, K) bytes.
+ * K a multiple of 32, N of 8.                                                */
+MOE_API int moe_mx4_quantize_weight(int32_t dtype, int32_t E, int32_t K, int32_t N, const void* W,
+                                    void* codes, void* scales, moe_stream_t stream);
+
+/* The values that codes and scales stand for: out [sets,rows,K] in dtype
+ * (exact in both types; sets = 1 for rows, E for weights: out is [E,N,K]).   */
+MOE_API int moe_mx4_dequantize(int32_t dtype, int32_t sets, int64_t rows, int32_t K,
+                               const void* codes, const void* scales, void* out,
+                               moe_stream_t stream);
+
+#define MOE_MX4_ACT_NONE 0
+#define MOE_MX4_ACT_SILU 1
+#define MOE_MX4_ACT_SWIGLU 2
+
+typedef struct {
+    int64_t rows;      /* rows of x and out (the segments' upper bound)        */
+    int32_t K;         /* reduction width, a multiple of 32                    */
+    int32_t N;         /* output width, a multiple of 8                        */
+    int32_t E;         /* experts, 1..64                                       */
+    int32_t act;       /* MOE_MX4_ACT_*                                        */
+    int32_t out_dtype; /* MOE_DTYPE_F32 or MOE_DTYPE_BF16                      */
+} moe_mx4_product_config;
+
+MOE_API int moe_check_mx4_product_config(const moe_mx4_product_config* cfg);
+
+/* Grouped product over the segments of moe_permute (offsets [E+1], device,
+ * multiples of 128):  u = Q(x) Q(W_e)  for the rows of segment e, fp32
+ * accumulation, then out = u, silu(u), or silu(g) u with g = Q(x) Q(Wg_e).
+ *   x_codes/x_scales: moe_mx4_quantize of x [rows,K]; w_*, wg_*:
+ *   moe_mx4_quantize_weight of W, Wg [E,K,N] (wg_* NULL but for SWIGLU);
+ *   out [rows,N]: rows from offsets[E] on are not written.
+ * Offsets that descend, are no multiples of 128 or leave 0..rows are recorded as
+ * MOE_ERR_DEVICE_BOUNDS, and nothing is written.                             */
+MOE_API int moe_mx4_grouped_product(const moe_mx4_product_config* cfg, const void* x_codes,
+                                    const void* x_scales, const int32_t* offsets,
+                                    const void* w_codes, const void* w_scales,
+                                    const void* wg_codes, const void* wg_scales, void* out,
+                                    moe_stream_t stream);
+
 /* ---- status and bookkeeping ---- */
 
 /* Text of a status code (static storage). */

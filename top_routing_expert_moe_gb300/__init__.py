@@ -146,6 +146,13 @@ _SIGS = {
     "moe_balance_loss": [ctypes.c_void_p] * 10,
     "moe_balance_loss_backward": [ctypes.c_void_p] * 8,
     "moe_backward_aux": [ctypes.c_void_p] * 28,
+    "moe_mx4_scale_bytes": [ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p],
+    "moe_mx4_quantize": [ctypes.c_int32, ctypes.c_int64, ctypes.c_int32] + [ctypes.c_void_p] * 5,
+    "moe_mx4_quantize_weight": [ctypes.c_int32] * 4 + [ctypes.c_void_p] * 4,
+    "moe_mx4_dequantize": [ctypes.c_int32, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32]
+                          + [ctypes.c_void_p] * 4,
+    "moe_check_mx4_product_config": [ctypes.c_void_p],
+    "moe_mx4_grouped_product": [ctypes.c_void_p] * 10,
     "moe_last_device_status": [ctypes.c_void_p, ctypes.c_void_p],
     "moe_selftest_bounded_wait": [ctypes.c_ulonglong, ctypes.c_void_p],
 }

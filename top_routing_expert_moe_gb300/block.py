@@ -1,7 +1,8 @@
 """The operators around the layer: binding of their C entry points.
 
 Residual-stream norms (``moe_block_norm``) and the router's per-sequence balance
-loss (``moe_balance_loss``), each with its backward.  As in the
+loss (``moe_balance_loss``), each with its backward, and microscaled 4-bit
+numbers with the experts' grouped product (``moe_mx4_*``).  As in the
 package's root, every function mirrors the C entry point of the same name and
 the classes own the output buffers and workspaces of one configuration.
 """
@@ -17,7 +18,10 @@ __all__ = ["GATE_NONE", "GATE_CHANNEL", "GATE_TOKEN", "GATE_FULL", "NormConfig",
            "check_norm_config", "norm_workspace_size", "moe_block_norm",
            "moe_block_norm_backward", "BlockNorm", "BalanceConfig", "check_balance_config",
            "balance_workspace_size", "moe_balance_loss", "moe_balance_loss_backward",
-           "BalanceLoss"]
+           "BalanceLoss", "MX4_ACT_NONE", "MX4_ACT_SILU", "MX4_ACT_SWIGLU", "MX4Tensor",
+           "mx4_scale_bytes", "moe_mx4_quantize", "moe_mx4_quantize_weight", "moe_mx4_dequantize",
+           "mx4_quantize", "mx4_quantize_weight", "MX4ProductConfig", "check_mx4_product_config",
+           "moe_mx4_grouped_product", "MX4Product"]
 
 GATE_NONE, GATE_CHANNEL, GATE_TOKEN, GATE_FULL = 0, 1, 2, 3
 
@@ -217,3 +221,133 @@ class BalanceLoss:
         moe_balance_loss_backward(self.cfg, logits, topk_idx, seq_offsets, self.grad_w, dloss,
                                   self.dlogits, stream)
         return self.dlogits
+
+
+# ----------------------------------------------------------------- microscaled 4-bit numbers
+MX4_ACT_NONE, MX4_ACT_SILU, MX4_ACT_SWIGLU = 0, 1, 2
+
+
+def mx4_scale_bytes(rows: int, K: int) -> int:
+    v = ctypes.c_size_t()
+    _call("moe_mx4_scale_bytes", rows, K, ctypes.byref(v))
+    return v.value
+
+
+def moe_mx4_quantize(dtype, rows, K, x, rows_used, codes, scales, stream=None):
+    _call("moe_mx4_quantize", dtype, rows, K, _p(x), _p(rows_used), _p(codes), _p(scales), _s(stream))
+
+
+def moe_mx4_quantize_weight(dtype, E, K, N, W, codes, scales, stream=None):
+    _call("moe_mx4_quantize_weight", dtype, E, K, N, _p(W), _p(codes), _p(scales), _s(stream))
+
+
+def moe_mx4_dequantize(dtype, sets, rows, K, codes, scales, out, stream=None):
+    _call("moe_mx4_dequantize", dtype, sets, rows, K, _p(codes), _p(scales), _p(out), _s(stream))
+
+
+def _mx4_dtype(t: torch.Tensor) -> int:
+    try:
+        return {torch.bfloat16: _moe.BF16, torch.float32: _moe.F32}[t.dtype]
+    except KeyError:
+        raise ValueError(f"expected bfloat16 or float32, got {t.dtype}") from None
+
+
+class MX4Tensor:
+    """4-bit numbers [rows, K] or, for expert weights, [E, rows, K]: ``codes``
+    (two to a byte) and ``scales`` (tiles, see include/moe.h)."""
+
+    def __init__(self, shape, device="cuda"):
+        *sets, rows, K = shape
+        if len(sets) > 1:
+            raise ValueError("expected [rows, K] or [E, rows, K]")
+        self.shape = tuple(shape)
+        n = sets[0] if sets else 1
+        self.codes = torch.empty(*shape[:-1], K // 2, dtype=torch.uint8, device=device)
+        self.scales = torch.empty(n * mx4_scale_bytes(rows, K), dtype=torch.uint8, device=device)
+
+    def dequantize(self, dtype=torch.bfloat16, stream=None):
+        out = torch.empty(self.shape, dtype=dtype, device=self.codes.device)
+        sets = self.shape[0] if len(self.shape) == 3 else 1
+        moe_mx4_dequantize(_mx4_dtype(out), sets, self.shape[-2], self.shape[-1], self.codes,
+                           self.scales, out, stream)
+        return out
+
+
+def mx4_quantize(x, rows_used=None, out=None, stream=None) -> MX4Tensor:
+    """Quantise rows x [rows, K] along K (K a multiple of 32) into ``out`` or a new
+    tensor.  ``rows_used``: one int32 on the device, rows from it on are left out."""
+    if x.dim() != 2:
+        raise ValueError("x: expected [rows, K]")
+    if out is None:
+        out = MX4Tensor(x.shape, x.device)
+    elif out.shape != tuple(x.shape):
+        raise ValueError(f"out: expected {tuple(x.shape)}, got {out.shape}")
+    if rows_used is not None and (rows_used.numel() != 1 or rows_used.dtype != torch.int32):
+        raise ValueError("rows_used must be one int32")
+    moe_mx4_quantize(_mx4_dtype(x), x.shape[0], x.shape[1], x, rows_used, out.codes, out.scales, stream)
+    return out
+
+
+def mx4_quantize_weight(W, stream=None) -> MX4Tensor:
+    """Quantise expert weights W [E, K, N] along K: an MX4Tensor [E, N, K]."""
+    if W.dim() != 3:
+        raise ValueError("W: expected [E, K, N]")
+    E, K, N = W.shape
+    out = MX4Tensor((E, N, K), W.device)
+    moe_mx4_quantize_weight(_mx4_dtype(W), E, K, N, W, out.codes, out.scales, stream)
+    return out
+
+
+class MX4ProductConfig(ctypes.Structure):
+    """Mirror of ``moe_mx4_product_config`` (include/moe.h)."""
+    _fields_ = [("rows", ctypes.c_int64), ("K", ctypes.c_int32), ("N", ctypes.c_int32),
+                ("E", ctypes.c_int32), ("act", ctypes.c_int32), ("out_dtype", ctypes.c_int32)]
+
+    def __init__(self, rows, K, N, E, act=MX4_ACT_NONE, out_dtype=_moe.BF16):
+        super().__init__(rows, K, N, E, act, out_dtype)
+
+    @property
+    def torch_dtype(self):
+        return torch.bfloat16 if self.out_dtype == _moe.BF16 else torch.float32
+
+
+def check_mx4_product_config(cfg: MX4ProductConfig) -> int:
+    return _moe.load_library().moe_check_mx4_product_config(ctypes.byref(cfg))
+
+
+def moe_mx4_grouped_product(cfg, x_codes, x_scales, offsets, w_codes, w_scales, wg_codes, wg_scales,
+                            out, stream=None):
+    _call("moe_mx4_grouped_product", ctypes.byref(cfg), _p(x_codes), _p(x_scales), _p(offsets),
+          _p(w_codes), _p(w_scales), _p(wg_codes), _p(wg_scales), _p(out), _s(stream))
+
+
+class MX4Product:
+    """out = act(Q(x) Q(W_e)) over expert segments: quantises the rows of x and
+    multiplies them with weights from ``mx4_quantize_weight``.  Owns the 4-bit
+    rows and the output."""
+
+    def __init__(self, cfg: MX4ProductConfig, device="cuda"):
+        rc = check_mx4_product_config(cfg)
+        if rc != 0:
+            raise _moe.MoEError(rc, "moe_check_mx4_product_config")
+        self.cfg = cfg
+        self.xq = MX4Tensor((cfg.rows, cfg.K), device)
+        self.out = torch.empty(cfg.rows, cfg.N, dtype=cfg.torch_dtype, device=device)
+
+    def forward(self, x, offsets, w: MX4Tensor, wg: MX4Tensor | None = None, stream=None):
+        """out [rows, N] (rows from offsets[E] on are not written); x [rows, K] bf16
+        or fp32, offsets [E + 1] int32 as from moe_permute, w (and the gate wg for
+        SwiGLU) [E, N, K]."""
+        c = self.cfg
+        if tuple(x.shape) != (c.rows, c.K):
+            raise ValueError(f"x: expected {(c.rows, c.K)}, got {tuple(x.shape)}")
+        _checked(offsets, (c.E + 1,), torch.int32, "offsets")
+        if (wg is not None) != (c.act == MX4_ACT_SWIGLU):
+            raise ValueError("wg is required iff act is MX4_ACT_SWIGLU")
+        for t, n in ((w, "w"), (wg, "wg")):
+            if t is not None and t.shape != (c.E, c.N, c.K):
+                raise ValueError(f"{n}: expected {(c.E, c.N, c.K)}, got {t.shape}")
+        mx4_quantize(x, offsets[c.E:], self.xq, stream)
+        moe_mx4_grouped_product(c, self.xq.codes, self.xq.scales, offsets, w.codes, w.scales,
+                                wg.codes if wg else None, wg.scales if wg else None, self.out, stream)
+        return self.out

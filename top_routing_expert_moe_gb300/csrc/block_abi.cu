@@ -14,6 +14,12 @@ bool ok_ptr(const void* p) { return p != nullptr && aligned16(p); }
 // a pointer that is there exactly when `on`
 bool ok_if(bool on, const void* p) { return on ? ok_ptr(p) : p == nullptr; }
 bool is_flag(int v) { return v == 0 || v == 1; }
+bool is_dtype(int v) { return v == MOE_DTYPE_F32 || v == MOE_DTYPE_BF16; }
+// a tensor of 4-bit numbers: rows, and a width that is whole blocks
+int mx4_shape(int64_t rows, int K) {
+    if (rows < 1 || K < 1) return MOE_ERR_INVALID_ARG;
+    return K % 32 || K > (1 << 24) || rows > (1LL << 31) - 256 ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
 
 }  // namespace
 
@@ -110,6 +116,67 @@ int moe_balance_loss_backward(const moe_balance_config* c, const float* logits,
     if (!seq_offsets && c->S != 1) return MOE_ERR_INVALID_ARG;
     return launch_balance_loss_backward(*c, logits, topk_idx, seq_offsets, grad_w, dloss, dlogits,
                                         (cudaStream_t)stream);
+}
+
+int moe_mx4_scale_bytes(int64_t rows, int32_t K, size_t* bytes) {
+    const int r = mx4_shape(rows, K);
+    if (r) return r;
+    if (!bytes) return MOE_ERR_INVALID_ARG;
+    *bytes = (size_t)((rows + 127) / 128) * ((K + 127) / 128) * 512;
+    return MOE_OK;
+}
+
+int moe_mx4_quantize(int32_t dtype, int64_t rows, int32_t K, const void* x, const int32_t* rows_used,
+                     void* codes, void* scales, moe_stream_t stream) {
+    if (!is_dtype(dtype)) return MOE_ERR_INVALID_ARG;
+    const int r = mx4_shape(rows, K);
+    if (r) return r;
+    // rows_used points into an offsets array, so 4-byte alignment is enough
+    if (!ok_ptr(x) || (reinterpret_cast<uintptr_t>(rows_used) & 3u) || !ok_ptr(codes) || !ok_ptr(scales))
+        return MOE_ERR_INVALID_ARG;
+    return launch_mx4_quantize(dtype, rows, K, x, rows_used, codes, scales, (cudaStream_t)stream);
+}
+
+int moe_mx4_quantize_weight(int32_t dtype, int32_t E, int32_t K, int32_t N, const void* W,
+                            void* codes, void* scales, moe_stream_t stream) {
+    if (!is_dtype(dtype) || E < 1) return MOE_ERR_INVALID_ARG;
+    const int r = mx4_shape(N, K);
+    if (r) return r;
+    if (N % 8 || N > (1 << 22) || E > 65535) return MOE_ERR_UNSUPPORTED;
+    if (!ok_ptr(W) || !ok_ptr(codes) || !ok_ptr(scales)) return MOE_ERR_INVALID_ARG;
+    return launch_mx4_quantize_weight(dtype, E, K, N, W, codes, scales, (cudaStream_t)stream);
+}
+
+int moe_mx4_dequantize(int32_t dtype, int32_t sets, int64_t rows, int32_t K, const void* codes,
+                       const void* scales, void* out, moe_stream_t stream) {
+    if (!is_dtype(dtype) || sets < 1) return MOE_ERR_INVALID_ARG;
+    const int r = mx4_shape(rows, K);
+    if (r) return r;
+    if (!ok_ptr(codes) || !ok_ptr(scales) || !ok_ptr(out)) return MOE_ERR_INVALID_ARG;
+    return launch_mx4_dequantize(dtype, sets, rows, K, codes, scales, out, (cudaStream_t)stream);
+}
+
+int moe_check_mx4_product_config(const moe_mx4_product_config* c) {
+    if (!c || c->N < 1 || c->E < 1 || !is_dtype(c->out_dtype)) return MOE_ERR_INVALID_ARG;
+    if (c->act < MOE_MX4_ACT_NONE || c->act > MOE_MX4_ACT_SWIGLU) return MOE_ERR_INVALID_ARG;
+    const int r = mx4_shape(c->rows, c->K);
+    if (r) return r;
+    if (c->N % 8 || c->N > (1 << 22) || c->E > 64 || c->rows > (1 << 30)) return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+
+int moe_mx4_grouped_product(const moe_mx4_product_config* c, const void* x_codes, const void* x_scales,
+                            const int32_t* offsets, const void* w_codes, const void* w_scales,
+                            const void* wg_codes, const void* wg_scales, void* out,
+                            moe_stream_t stream) {
+    const int r = moe_check_mx4_product_config(c);
+    if (r) return r;
+    const bool dual = c->act == MOE_MX4_ACT_SWIGLU;
+    if (!ok_ptr(x_codes) || !ok_ptr(x_scales) || !ok_ptr(offsets) || !ok_ptr(w_codes) ||
+        !ok_ptr(w_scales) || !ok_if(dual, wg_codes) || !ok_if(dual, wg_scales) || !ok_ptr(out))
+        return MOE_ERR_INVALID_ARG;
+    return launch_mx4_product(*c, x_codes, x_scales, offsets, w_codes, w_scales, wg_codes, wg_scales,
+                              out, (cudaStream_t)stream);
 }
 
 }  // extern "C"

@@ -70,4 +70,15 @@ int launch_balance_loss_backward(const moe_balance_config& c, const float* logit
                                  const int32_t* seq, const float* grad_w, const float* dloss,
                                  float* dlogits, cudaStream_t st);
 
+// mx4.cu, mx4_gemm.cu (microscaled 4-bit numbers)
+int launch_mx4_quantize(int dtype, int64_t rows, int K, const void* x, const int32_t* rows_used,
+                        void* codes, void* scales, cudaStream_t st);
+int launch_mx4_quantize_weight(int dtype, int E, int K, int N, const void* W, void* codes, void* scales,
+                               cudaStream_t st);
+int launch_mx4_dequantize(int dtype, int sets, int64_t rows, int K, const void* codes, const void* scales,
+                          void* out, cudaStream_t st);
+int launch_mx4_product(const moe_mx4_product_config& c, const void* xq, const void* xs, const int32_t* offsets,
+                       const void* wq, const void* ws, const void* gq, const void* gs, void* out,
+                       cudaStream_t st);
+
 }  // namespace moe
