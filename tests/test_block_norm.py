@@ -262,6 +262,23 @@ def test_lengths(T, d):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+def test_long_batches_of_every_form(form, dt):
+    """Batches that go through the shared-memory ring (several rows a CTA)."""
+    check(1303, 520, dt, form, seed=11)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,d", [(304, 8), (3000, 16), (5000, 264), (303, 1024), (305, 2816),
+                                 (700, 4096), (640, 4104), (700, 8192), (320, 16384)])
+def test_long_batches_of_every_width(T, d, dt):
+    check(T, d, dt, (1, 1, 1, "channel"), seed=d)
+    check(T, d, dt, (1, 1, 1, "full"), seed=d)
+
+
+@pytest.mark.gpu
 def test_stream_gradient_absent_is_zero():
     form = (1, 1, 1, "none")
     v = make(9, 128, torch.float32, *form)

@@ -106,7 +106,7 @@ def shared_block(**tensors) -> MoESharedFFN:
         raise ValueError(f"unknown shared-expert fields {sorted(unknown)}")
     b = MoESharedFFN()
     for n, t in tensors.items():
-        setattr(b, n, None if t is None else _p(t).value)
+        setattr(b, n, _p(t))
     b._tensors = dict(tensors)
     return b
 
@@ -187,6 +187,7 @@ def error_string(code: int) -> str:
 
 
 def _p(t):
+    """Device address of a tensor (None stays None); ctypes takes the plain int."""
     if t is None:
         return None
     if not isinstance(t, torch.Tensor):
@@ -195,16 +196,18 @@ def _p(t):
         raise ValueError("tensors passed to the MoE library must live on the GPU")
     if not t.is_contiguous():
         raise ValueError("tensors passed to the MoE library must be contiguous")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _s(stream):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    """Handle of the stream, or of the current device's current stream."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _call(name, *args):
-    rc = getattr(load_library(), name)(*args)
+    rc = getattr(_lib or load_library(), name)(*args)
     if rc != 0:
         raise MoEError(rc, name)
 

@@ -34,7 +34,7 @@ def _checked(t, shape, dtype, name):
         return None
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch tensor")
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+    if t.shape != shape or t.dtype != dtype:
         raise ValueError(f"{name}: expected {tuple(shape)} {dtype}, got {tuple(t.shape)} {t.dtype}")
     return t
 
@@ -97,30 +97,30 @@ class BlockNorm:
             raise _moe.MoEError(rc, "moe_check_norm_config")
         self.cfg = c = cfg
         self.device = torch.device(device)
+        self._rows, self._vec, self._dt = (c.T, c.d), (c.d,), c.torch_dtype
+        self._gate, self._leave = c.gate_shape, bool(c.leave)
         e = lambda on, *s, dtype=c.torch_dtype: (  # noqa: E731
             torch.empty(*s, dtype=dtype, device=self.device) if on else None)
         self.x_out = e(c.leave, c.T, c.d)
         self.z = e(c.enter, c.T, c.d)
         self._grads = self._ws = None
 
-    def _check(self, **tensors):
-        c = self.cfg
-        rows, vec = ((c.T, c.d), c.torch_dtype), ((c.d,), torch.float32)
-        spec = dict(x=rows, x_out=rows, u=rows, dx_out=rows, dz=rows, w_post=vec, w_pre=vec)
-        for n, t in tensors.items():
-            want = c.gate_shape if n == "gate" else spec[n]
-            if want is None:
-                if t is not None:
-                    raise ValueError(f"{n} given, but the configuration has none")
-                continue
-            _checked(t, *want, n)
+    def _check(self, rows, w_pre, w_post, gate):
+        for n, t in rows:
+            _checked(t, self._rows, self._dt, n)
+        _checked(w_pre, self._vec, torch.float32, "w_pre")
+        _checked(w_post, self._vec, torch.float32, "w_post")
+        if self._gate is not None:
+            _checked(gate, *self._gate, "gate")
+        elif gate is not None:
+            raise ValueError("gate given, but the configuration has none")
 
     def forward(self, x, u=None, w_pre=None, w_post=None, gate=None, stream=None):
         """(x_out, z): the stream after the block (x itself without ``leave``)
         and its normalised copy (None without ``enter``)."""
-        self._check(x=x, u=u, w_pre=w_pre, w_post=w_post, gate=gate)
+        self._check((("x", x), ("u", u)), w_pre, w_post, gate)
         moe_block_norm(self.cfg, x, u, w_post, gate, w_pre, self.x_out, self.z, stream)
-        return (self.x_out if self.cfg.leave else x), self.z
+        return (self.x_out if self._leave else x), self.z
 
     def grads(self):
         if self._grads is None:
@@ -142,7 +142,7 @@ class BlockNorm:
         """Gradients dx, du, dw_pre, dw_post, dgate (None where absent) at the
         stored stream x_out (x where the configuration does not leave a block),
         given those of x_out along the stream (None: zero) and of z."""
-        self._check(x_out=x_out, dx_out=dx_out, dz=dz, u=u, w_pre=w_pre, w_post=w_post, gate=gate)
+        self._check((("x_out", x_out), ("dx_out", dx_out), ("dz", dz), ("u", u)), w_pre, w_post, gate)
         g = self.grads()
         moe_block_norm_backward(self.cfg, x_out, u, w_post, gate, w_pre, dx_out, dz, g["dx"],
                                 g["du"], g["dw_post"], g["dgate"], g["dw_pre"], self._ws, stream)

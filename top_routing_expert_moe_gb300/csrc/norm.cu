@@ -2,8 +2,8 @@
 //
 //   leave:  n = w_post u r_u (or u),  x' = a x + b g n     r_v = 1/sqrt(mean v^2 + eps)
 //   enter:  z = w_pre x' r
-// A row is held in registers by one group of threads (16 elements a thread), so
-// each tensor passes through HBM once.  All sums are fp32.
+// A row belongs to one group of threads, so each tensor passes through HBM once.
+// All sums are fp32.
 //
 // Backward, for one row, with G the gradient of x':
 //   a_i = w_pre dz,  G = dx' + r a - x' (r^3/d) A,            A   = sum a x'
@@ -16,84 +16,80 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "tma.cuh"
 
 namespace moe {
 
 namespace {
 
-constexpr int EPT = 16;          // elements of a row per thread
 constexpr int SMALL_ROWS = 4;    // rows per CTA when a warp holds a row
 
-template <int N>
-__device__ __forceinline__ void warp_sums(float (&v)[N]) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-}
-
 // Sums over the threads of a row: a warp, or the whole CTA through shared memory
-// (buf: 32 x N floats; the caller alternates two buffers, so one barrier a call
-// is enough), warps added in order.
-template <int N>
-__device__ __forceinline__ void row_sums(float (&v)[N], float* buf) {
-    warp_sums(v);
-    if (blockDim.x <= 32) return;
-    const int w = threadIdx.x >> 5, nw = blockDim.x >> 5;
-    if ((threadIdx.x & 31) == 0)
+// (buf: 32 x 8 floats; the caller alternates two buffers, so one barrier a call
+// is enough).  Fixed order.
+__device__ __forceinline__ float row_sum(float v, float* buf) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) buf[w * N + i] = v[i];
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (blockDim.x <= 32) return v;
+    const int lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+    if (lane == 0) buf[threadIdx.x >> 5] = v;
     __syncthreads();
+    v = lane < nw ? buf[lane] : 0.f;
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = buf[i];
-    for (int j = 1; j < nw; ++j)
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+// Six sums at once.  The first three steps of the butterfly halve the values a lane
+// carries as they double the lanes it stands for, so that four lanes end with one
+// value's sum: 9 shuffles instead of 30.
+__device__ __forceinline__ void row_sums6(float (&s)[6], float* buf) {
+    const int lane = threadIdx.x & 31;
+    const bool b4 = lane & 16, b3 = lane & 8, b2 = lane & 4;
+    float a[4], b[2], v;
+    const float s8[8] = {s[0], s[1], s[2], s[3], s[4], s[5], 0.f, 0.f};
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] += buf[j * N + i];
+    for (int i = 0; i < 4; ++i)
+        a[i] = (b4 ? s8[i + 4] : s8[i]) + __shfl_xor_sync(0xffffffffu, b4 ? s8[i] : s8[i + 4], 16);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        b[i] = (b3 ? a[i + 2] : a[i]) + __shfl_xor_sync(0xffffffffu, b3 ? a[i] : a[i + 2], 8);
+    v = (b2 ? b[1] : b[0]) + __shfl_xor_sync(0xffffffffu, b2 ? b[0] : b[1], 4);
+    v += __shfl_xor_sync(0xffffffffu, v, 2);
+    v += __shfl_xor_sync(0xffffffffu, v, 1);                 // the sum of value lane / 4
+    int step = 4;
+    if (blockDim.x > 32) {
+        if ((lane & 3) == 0) buf[(threadIdx.x >> 5) * 8 + (lane >> 2)] = v;
+        __syncthreads();
+        const int nw = blockDim.x >> 5;
+        v = 0.f;
+        for (int w = lane >> 3; w < nw; w += 4) v += buf[w * 8 + (lane & 7)];
+        v += __shfl_xor_sync(0xffffffffu, v, 8);
+        v += __shfl_xor_sync(0xffffffffu, v, 16);            // value lane % 8
+        step = 1;
+    }
+#pragma unroll
+    for (int i = 0; i < 6; ++i) s[i] = __shfl_sync(0xffffffffu, v, i * step);
 }
 
-// A thread's share of a row: vectors tid, tid + TPR, ... of VEC elements.
+// ---------------------------------------------------------------- rows read directly
+// For rows of no whole 16 bytes (VEC = 1), short batches and very wide rows.  A
+// thread's share: vectors tid, tid + threads, ... of VEC elements, EPT in all.
 template <typename T, int VEC>
-__device__ __forceinline__ void load_row(const T* p, int nvec, float (&v)[EPT]) {
+__device__ __forceinline__ void load_vec(const T* p, int c, int nvec, float (&v)[VEC]) {
 #pragma unroll
-    for (int i = 0; i < EPT / VEC; ++i) {
-        const int c = threadIdx.x + i * blockDim.x;
-        if constexpr (VEC == 1) {
-            v[i] = c < nvec ? to_f<T>(p[c]) : 0.f;
-        } else {
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) v[i * VEC + j] = 0.f;
-            if (c < nvec) load16_f<T>(p + c * VEC, v + i * VEC);
-        }
-    }
+    for (int j = 0; j < VEC; ++j) v[j] = 0.f;
+    if (c >= nvec) return;
+    if constexpr (VEC == 1) v[0] = to_f<T>(p[c]);
+    else if constexpr (VEC * sizeof(T) == 32) {                  // 8 fp32 of a channel vector
+        load16_f<T>(p + c * VEC, v);
+        load16_f<T>(p + c * VEC + 4, v + 4);
+    } else load16_f<T>(p + c * VEC, v);
 }
 template <typename T, int VEC>
-__device__ __forceinline__ void store_row(T* p, int nvec, const float (&v)[EPT]) {
-#pragma unroll
-    for (int i = 0; i < EPT / VEC; ++i) {
-        const int c = threadIdx.x + i * blockDim.x;
-        if (c >= nvec) continue;
-        if constexpr (VEC == 1) p[c] = from_f<T>(v[i]);
-        else store16_f<T>(p + c * VEC, v + i * VEC);
-    }
-}
-// fp32 vector over the channels, in the thread's share
-template <int VEC>
-__device__ __forceinline__ void load_vec(const float* p, int nvec, float (&v)[EPT]) {
-#pragma unroll
-    for (int i = 0; i < EPT / VEC; ++i) {
-        const int c = threadIdx.x + i * blockDim.x;
-        if constexpr (VEC == 1) {
-            v[i] = c < nvec ? __ldg(p + c) : 0.f;
-        } else {
-#pragma unroll
-            for (int j = 0; j < VEC; j += 4) {
-                const float4 f = c < nvec ? __ldg(reinterpret_cast<const float4*>(p + c * VEC + j))
-                                          : make_float4(0.f, 0.f, 0.f, 0.f);
-                v[i * VEC + j] = f.x; v[i * VEC + j + 1] = f.y;
-                v[i * VEC + j + 2] = f.z; v[i * VEC + j + 3] = f.w;
-            }
-        }
-    }
+__device__ __forceinline__ void store_vec(T* p, int c, int nvec, const float (&v)[VEC]) {
+    if (c >= nvec) return;
+    if constexpr (VEC == 1) p[c] = from_f<T>(v[0]);
+    else store16_f<T>(p + c * VEC, v);
 }
 
 struct NormArgs {
@@ -105,182 +101,181 @@ struct NormArgs {
     float eps, ra, ob;
 };
 
-template <typename T, int VEC, int MAXT>
+template <typename T, int VEC, int EPT, int MAXT>
 __global__ void __launch_bounds__(MAXT) block_norm_kernel(const NormArgs a) {
     pdl_wait();
     pdl_trigger();
+    constexpr int NC = EPT / VEC;
     __shared__ float buf[2][32];
     const int nvec = a.d / VEC;
     const float invd = 1.f / (float)a.d;
     for (int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y; t < a.T;
          t += (int64_t)gridDim.x * blockDim.y) {
         const size_t o = (size_t)t * a.d;
-        float y[EPT], u[EPT], w[EPT];
-        load_row<T, VEC>(static_cast<const T*>(a.x) + o, nvec, y);
+        float y[NC][VEC], u[NC][VEC], w[VEC];
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            const int c = threadIdx.x + i * blockDim.x;
+            load_vec<T, VEC>(static_cast<const T*>(a.x) + o, c, nvec, y[i]);
+            if (a.leave) load_vec<T, VEC>(static_cast<const T*>(a.u) + o, c, nvec, u[i]);
+        }
         if (a.leave) {
-            load_row<T, VEC>(static_cast<const T*>(a.u) + o, nvec, u);
-            float c = a.ob;
-            if (a.gmode == MOE_GATE_TOKEN) c *= static_cast<const float*>(a.gate)[t];
+            float f = a.ob;
+            if (a.gmode == MOE_GATE_TOKEN) f *= static_cast<const float*>(a.gate)[t];
             if (a.post) {
-                float s[1] = {0.f};
+                float s = 0.f;
 #pragma unroll
-                for (int i = 0; i < EPT; ++i) s[0] = fmaf(u[i], u[i], s[0]);
-                row_sums<1>(s, buf[0]);
-                c *= 1.f / sqrtf(s[0] * invd + a.eps);
-                load_vec<VEC>(a.w_post, nvec, w);
+                for (int i = 0; i < NC; ++i)
 #pragma unroll
-                for (int i = 0; i < EPT; ++i) u[i] *= w[i];
-            }
-            if (a.gmode == MOE_GATE_CHANNEL || a.gmode == MOE_GATE_FULL) {
-                if (a.gmode == MOE_GATE_CHANNEL) load_vec<VEC>(static_cast<const float*>(a.gate), nvec, w);
-                else load_row<T, VEC>(static_cast<const T*>(a.gate) + o, nvec, w);
-#pragma unroll
-                for (int i = 0; i < EPT; ++i) u[i] *= w[i];
+                    for (int j = 0; j < VEC; ++j) s = fmaf(u[i][j], u[i][j], s);
+                f *= rsqrtf(row_sum(s, buf[0]) * invd + a.eps);
             }
 #pragma unroll
-            for (int i = 0; i < EPT; ++i) y[i] = fmaf(a.ra, y[i], c * u[i]);
-            store_row<T, VEC>(static_cast<T*>(a.x_out) + o, nvec, y);
+            for (int i = 0; i < NC; ++i) {
+                const int c = threadIdx.x + i * blockDim.x;
+                if (a.post) {
+                    load_vec<float, VEC>(a.w_post, c, nvec, w);
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) u[i][j] *= w[j];
+                }
+                if (a.gmode == MOE_GATE_CHANNEL || a.gmode == MOE_GATE_FULL) {
+                    if (a.gmode == MOE_GATE_CHANNEL)
+                        load_vec<float, VEC>(static_cast<const float*>(a.gate), c, nvec, w);
+                    else load_vec<T, VEC>(static_cast<const T*>(a.gate) + o, c, nvec, w);
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) u[i][j] *= w[j];
+                }
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) y[i][j] = fmaf(a.ra, y[i][j], f * u[i][j]);
+                store_vec<T, VEC>(static_cast<T*>(a.x_out) + o, c, nvec, y[i]);
+            }
         }
         if (a.enter) {
-            float s[1] = {0.f};
+            float s = 0.f;
 #pragma unroll
-            for (int i = 0; i < EPT; ++i) s[0] = fmaf(y[i], y[i], s[0]);
-            row_sums<1>(s, buf[1]);
-            const float r = 1.f / sqrtf(s[0] * invd + a.eps);
-            load_vec<VEC>(a.w_pre, nvec, w);
+            for (int i = 0; i < NC; ++i)
 #pragma unroll
-            for (int i = 0; i < EPT; ++i) y[i] *= r * w[i];
-            store_row<T, VEC>(static_cast<T*>(a.z) + o, nvec, y);
+                for (int j = 0; j < VEC; ++j) s = fmaf(y[i][j], y[i][j], s);
+            const float r = rsqrtf(row_sum(s, buf[1]) * invd + a.eps);
+#pragma unroll
+            for (int i = 0; i < NC; ++i) {
+                const int c = threadIdx.x + i * blockDim.x;
+                load_vec<float, VEC>(a.w_pre, c, nvec, w);
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) y[i][j] *= r * w[j];
+                store_vec<T, VEC>(static_cast<T*>(a.z) + o, c, nvec, y[i]);
+            }
         }
         // buf[0] and buf[1] alternate unless only one of the norms is on
         if (a.post != a.enter && blockDim.x > 32) __syncthreads();
     }
 }
 
-template <typename T, int VEC, int MAXT>
+// The row is read twice, for the sums and for the outputs (the second time from the
+// caches): the channel sums leave no registers to hold it.
+template <typename T, int VEC, int EPT, int MAXT>
 __global__ void __launch_bounds__(MAXT) block_norm_bwd_kernel(const NormArgs a) {
     pdl_wait();
     pdl_trigger();
-    __shared__ float buf[2][32 * 6];
+    constexpr int NC = EPT / VEC;
+    __shared__ float buf[2][32 * 8];
     extern __shared__ float comb[];            // [SMALL_ROWS][d] when a CTA holds several rows
     const int nvec = a.d / VEC;
     const float invd = 1.f / (float)a.d;
-    float acc_pre[EPT], acc_post[EPT], acc_g[EPT];
+    float acc_pre[NC][VEC], acc_post[NC][VEC], acc_g[NC][VEC];
 #pragma unroll
-    for (int i = 0; i < EPT; ++i) acc_pre[i] = acc_post[i] = acc_g[i] = 0.f;
+    for (int i = 0; i < NC; ++i)
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) acc_pre[i][j] = acc_post[i][j] = acc_g[i][j] = 0.f;
     const bool need_u = a.leave && (a.post || a.gmode != MOE_GATE_NONE);
     int par = 0;
     for (int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y; t < a.T;
          t += (int64_t)gridDim.x * blockDim.y, par ^= 1) {
         const size_t o = (size_t)t * a.d;
-        float y[EPT], u[EPT], dz[EPT], G[EPT], w[EPT], q[EPT];
-        if (a.enter) {
-            load_row<T, VEC>(static_cast<const T*>(a.x) + o, nvec, y);
-            load_row<T, VEC>(static_cast<const T*>(a.dz) + o, nvec, dz);
-        }
-        if (a.dx_out) load_row<T, VEC>(static_cast<const T*>(a.dx_out) + o, nvec, G);
-        else
-#pragma unroll
-            for (int i = 0; i < EPT; ++i) G[i] = 0.f;
-        if (need_u) load_row<T, VEC>(static_cast<const T*>(a.u) + o, nvec, u);
-        else
-#pragma unroll
-            for (int i = 0; i < EPT; ++i) u[i] = 0.f;
-        // q = b g w_post
         float tok = a.ob;
         if (a.gmode == MOE_GATE_TOKEN) tok *= static_cast<const float*>(a.gate)[t];
-        if (a.post) load_vec<VEC>(a.w_post, nvec, q);
-        else
+        // one chunk: x', dz, dx', u, w_pre, w_post, gate (a token's gate is in tok)
+        auto load = [&](int i, float (&y)[VEC], float (&dz)[VEC], float (&G)[VEC], float (&u)[VEC],
+                        float (&wz)[VEC], float (&wq)[VEC], float (&g)[VEC]) {
+            const int c = threadIdx.x + i * blockDim.x;
 #pragma unroll
-            for (int i = 0; i < EPT; ++i) q[i] = 1.f;
-        if (a.gmode == MOE_GATE_CHANNEL) load_vec<VEC>(static_cast<const float*>(a.gate), nvec, w);
-        else if (a.gmode == MOE_GATE_FULL) load_row<T, VEC>(static_cast<const T*>(a.gate) + o, nvec, w);
-        else
-#pragma unroll
-            for (int i = 0; i < EPT; ++i) w[i] = 1.f;       // (the token gate is in tok)
-        // s: y^2, a y, u^2, q u dx', q u a, q u y  (q without the factor tok)
+            for (int j = 0; j < VEC; ++j) { y[j] = dz[j] = G[j] = u[j] = wz[j] = 0.f; wq[j] = g[j] = 1.f; }
+            if (a.enter) {
+                load_vec<T, VEC>(static_cast<const T*>(a.x) + o, c, nvec, y);
+                load_vec<T, VEC>(static_cast<const T*>(a.dz) + o, c, nvec, dz);
+                load_vec<float, VEC>(a.w_pre, c, nvec, wz);
+            }
+            if (a.dx_out) load_vec<T, VEC>(static_cast<const T*>(a.dx_out) + o, c, nvec, G);
+            if (need_u) load_vec<T, VEC>(static_cast<const T*>(a.u) + o, c, nvec, u);
+            if (a.post) load_vec<float, VEC>(a.w_post, c, nvec, wq);
+            if (a.gmode == MOE_GATE_CHANNEL) load_vec<float, VEC>(static_cast<const float*>(a.gate), c, nvec, g);
+            else if (a.gmode == MOE_GATE_FULL) load_vec<T, VEC>(static_cast<const T*>(a.gate) + o, c, nvec, g);
+        };
+        // s: y^2, a y, u^2, q u dx', q u a, q u y  with a = w_pre dz, q = g w_post
         float s[6] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        float wp[EPT];
-        if (a.enter) {
-            load_vec<VEC>(a.w_pre, nvec, wp);
 #pragma unroll
-            for (int i = 0; i < EPT; ++i) {
-                s[0] = fmaf(y[i], y[i], s[0]);
-                s[1] = fmaf(wp[i] * dz[i], y[i], s[1]);
+        for (int i = 0; i < NC; ++i) {
+            float y[VEC], dz[VEC], G[VEC], u[VEC], wz[VEC], wq[VEC], g[VEC];
+            load(i, y, dz, G, u, wz, wq, g);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                const float az = wz[j] * dz[j], qu = wq[j] * g[j] * u[j];
+                s[0] = fmaf(y[j], y[j], s[0]);
+                s[1] = fmaf(az, y[j], s[1]);
+                s[2] = fmaf(u[j], u[j], s[2]);
+                s[3] = fmaf(qu, G[j], s[3]);
+                s[4] = fmaf(qu, az, s[4]);
+                s[5] = fmaf(qu, y[j], s[5]);
             }
         }
-        if (need_u) {
-#pragma unroll
-            for (int i = 0; i < EPT; ++i) {
-                const float qu = q[i] * w[i] * u[i];
-                s[2] = fmaf(u[i], u[i], s[2]);
-                s[3] = fmaf(qu, G[i], s[3]);
-                if (a.enter) {
-                    s[4] = fmaf(qu, wp[i] * dz[i], s[4]);
-                    s[5] = fmaf(qu, y[i], s[5]);
-                }
-            }
-        }
-        row_sums<6>(s, buf[par]);
-        float r = 0.f, ca = 0.f;
-        if (a.enter) {
-            r = 1.f / sqrtf(s[0] * invd + a.eps);
-            ca = r * r * r * invd * s[1];
-#pragma unroll
-            for (int i = 0; i < EPT; ++i) {
-                G[i] += r * (wp[i] * dz[i]) - ca * y[i];
-                acc_pre[i] = fmaf(dz[i], r * y[i], acc_pre[i]);
-            }
-        }
-        if (!a.leave) {
-            store_row<T, VEC>(static_cast<T*>(a.dx) + o, nvec, G);
-            continue;
-        }
-        const float S = s[3] + r * s[4] - ca * s[5];     // sum q u G, without tok
-        float out[EPT];
-#pragma unroll
-        for (int i = 0; i < EPT; ++i) out[i] = a.ra * G[i];
-        store_row<T, VEC>(static_cast<T*>(a.dx) + o, nvec, out);
-        const float ru = a.post ? 1.f / sqrtf(s[2] * invd + a.eps) : 1.f;
+        row_sums6(s, buf[par]);
+        const float r = a.enter ? rsqrtf(s[0] * invd + a.eps) : 0.f;
+        const float ca = r * r * r * invd * s[1];
+        const float S = s[3] + r * s[4] - ca * s[5];         // sum q u G, without tok
+        const float ru = a.post ? rsqrtf(s[2] * invd + a.eps) : 1.f;
+        const float cu = a.post ? tok * ru * ru * ru * invd * S : 0.f;
         if (a.gmode == MOE_GATE_TOKEN && threadIdx.x == 0)
             static_cast<float*>(a.dgate)[t] = a.ob * ru * S;
-        if (a.gmode == MOE_GATE_CHANNEL) {
 #pragma unroll
-            for (int i = 0; i < EPT; ++i) acc_g[i] = fmaf(a.ob * G[i], q[i] * u[i] * ru, acc_g[i]);
-        } else if (a.gmode == MOE_GATE_FULL) {
+        for (int i = 0; i < NC; ++i) {
+            const int c = threadIdx.x + i * blockDim.x;
+            float y[VEC], dz[VEC], G[VEC], u[VEC], wz[VEC], wq[VEC], g[VEC], out[VEC];
+            load(i, y, dz, G, u, wz, wq, g);
 #pragma unroll
-            for (int i = 0; i < EPT; ++i) out[i] = a.ob * G[i] * (q[i] * u[i] * ru);
-            store_row<T, VEC>(static_cast<T*>(a.dgate) + o, nvec, out);
+            for (int j = 0; j < VEC; ++j) {
+                G[j] += r * (wz[j] * dz[j]) - ca * y[j];
+                acc_pre[i][j] = fmaf(dz[j], r * y[j], acc_pre[i][j]);
+                out[j] = a.leave ? a.ra * G[j] : G[j];
+            }
+            store_vec<T, VEC>(static_cast<T*>(a.dx) + o, c, nvec, out);
+            if (!a.leave) continue;
+            if (a.gmode == MOE_GATE_FULL) {
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) out[j] = a.ob * G[j] * (wq[j] * u[j] * ru);
+                store_vec<T, VEC>(static_cast<T*>(a.dgate) + o, c, nvec, out);
+            }
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                const float h = tok * ru * G[j];
+                acc_post[i][j] = fmaf(g[j] * h, u[j], acc_post[i][j]);
+                acc_g[i][j] = fmaf(wq[j] * h, u[j], acc_g[i][j]);
+                out[j] = wq[j] * g[j] * h - cu * u[j];
+            }
+            store_vec<T, VEC>(static_cast<T*>(a.du) + o, c, nvec, out);
         }
-        const float cu = a.post ? tok * ru * ru * ru * invd * S : 0.f;
-#pragma unroll
-        for (int i = 0; i < EPT; ++i) {
-            const float dn = tok * w[i] * G[i];
-            acc_post[i] = fmaf(dn, u[i] * ru, acc_post[i]);
-            out[i] = a.post ? ru * q[i] * dn - cu * u[i] : dn;
-        }
-        store_row<T, VEC>(static_cast<T*>(a.du) + o, nvec, out);
     }
     // this CTA's partial sums of the channel gradients
-    auto flush = [&](int which, const float (&acc)[EPT]) {
+    auto flush = [&](int which, const float (&acc)[NC][VEC]) {
         float* dst = a.part + ((size_t)which * gridDim.x + blockIdx.x) * a.d;
-        if (blockDim.y == 1) {
+        float* to = blockDim.y == 1 ? dst : comb + threadIdx.y * a.d;
 #pragma unroll
-            for (int i = 0; i < EPT / VEC; ++i) {
-                const int c = threadIdx.x + i * blockDim.x;
-                if (c < nvec)
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j) dst[c * VEC + j] = acc[i * VEC + j];
-            }
-            return;
-        }
-#pragma unroll
-        for (int i = 0; i < EPT / VEC; ++i) {
+        for (int i = 0; i < NC; ++i) {
             const int c = threadIdx.x + i * blockDim.x;
             if (c < nvec)
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) comb[threadIdx.y * a.d + c * VEC + j] = acc[i * VEC + j];
+                for (int j = 0; j < VEC; ++j) to[c * VEC + j] = acc[i][j];
         }
+        if (blockDim.y == 1) return;
         __syncthreads();
         for (int c = threadIdx.y * blockDim.x + threadIdx.x; c < a.d; c += blockDim.x * blockDim.y) {
             float v = comb[c];
@@ -292,6 +287,348 @@ __global__ void __launch_bounds__(MAXT) block_norm_bwd_kernel(const NormArgs a) 
     if (a.enter) flush(0, acc_pre);
     if (a.post) flush(1, acc_post);
     if (a.gmode == MOE_GATE_CHANNEL) flush(2, acc_g);
+}
+
+// ---------------------------------------------------------------- rows through a ring
+// Long batches of 16-byte rows.  A CTA is one row wide (8 elements a thread) and
+// persistent; its rows' tensors arrive by bulk copies in a ring of shared-memory
+// stages, so loads run ahead of the two dependent phases of a row (sums, then
+// outputs) that kept registers and memory waiting on each other; the vectors
+// over the channels stay in registers.  A stage is free once the CTA's first
+// reduction of its row has passed (every thread has taken its share), so that
+// barrier doubles as the ring's release.  A copy that never arrives is given up
+// after the bounded wait (recorded; the outputs are then undefined).
+constexpr int RE = 8;                      // elements of a row per thread
+constexpr int MAX_STAGES = 8;
+
+struct RingArgs {
+    NormArgs n;
+    const void* in[5];                     // the rows' tensors, in the stage's order
+    int nin, stages;
+    int* status;
+};
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
+// Elements in pairs: one packed instruction does two fp32 operations, and these
+// kernels are bound by the instructions they issue before they are by HBM.
+struct f2 { uint64_t v; };
+__device__ __forceinline__ f2 pk(float lo, float hi) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpk(f2 a, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(a.v)); }
+__device__ __forceinline__ f2 operator*(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ f2 both(float x) { return pk(x, x); }
+__device__ __forceinline__ float sum2(f2 a) {
+    float lo, hi;
+    unpk(a, lo, hi);
+    return lo + hi;
+}
+constexpr int RP = RE / 2;                 // pairs a thread
+
+// A thread's 8 elements of a staged row; fp32 rows as two halves, so that the
+// 16-byte accesses of neighbouring threads stay neighbours.
+template <typename T>
+__device__ __forceinline__ int part_of(int half) { return (threadIdx.x + half * blockDim.x) * (16 / (int)sizeof(T)); }
+template <typename T>
+__device__ __forceinline__ void take(const T* p, int d, f2 (&v)[RP]) {
+    constexpr int V = 16 / sizeof(T);
+#pragma unroll
+    for (int h = 0; h < RE / V; ++h) {
+        const int c = part_of<T>(h);
+        float f[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) f[j] = 0.f;
+        if (c < d) load16_f<T>(p + c, f);
+#pragma unroll
+        for (int j = 0; j < V / 2; ++j) v[h * V / 2 + j] = pk(f[2 * j], f[2 * j + 1]);
+    }
+}
+template <typename T>
+__device__ __forceinline__ void give(T* p, int d, const f2 (&v)[RP]) {
+    constexpr int V = 16 / sizeof(T);
+#pragma unroll
+    for (int h = 0; h < RE / V; ++h) {
+        const int c = part_of<T>(h);
+        float f[V];
+#pragma unroll
+        for (int j = 0; j < V / 2; ++j) unpk(v[h * V / 2 + j], f[2 * j], f[2 * j + 1]);
+        if (c < d) store16_f<T>(p + c, f);
+    }
+}
+// the fp32 channel vector's share that goes with it
+template <typename T>
+__device__ __forceinline__ void channel(const float* p, int d, f2 (&v)[RP]) {
+    constexpr int V = 16 / sizeof(T);
+#pragma unroll
+    for (int h = 0; h < RE / V; ++h) {
+        const int c = part_of<T>(h);
+#pragma unroll
+        for (int j = 0; j < V; j += 2)
+            v[(h * V + j) / 2] = c < d ? pk(__ldg(p + c + j), __ldg(p + c + j + 1)) : both(0.f);
+    }
+}
+__device__ __forceinline__ void fill(f2 (&v)[RP], float x) {
+#pragma unroll
+    for (int i = 0; i < RP; ++i) v[i] = both(x);
+}
+__device__ __forceinline__ float dot2(const f2 (&a)[RP], const f2 (&b)[RP]) {
+    f2 s = a[0] * b[0];
+#pragma unroll
+    for (int i = 1; i < RP; ++i) s = fma2(a[i], b[i], s);
+    return sum2(s);
+}
+
+struct RowRing {
+    uint32_t base, bar0;
+    uint32_t row_bytes;
+    int it = 0;
+    volatile int* abort_flag;
+
+    __device__ __forceinline__ void issue(const RingArgs& a, int64_t row, int i) {
+        const int s = i % a.stages;
+        mbar_expect_tx(bar0 + s * 8, row_bytes * a.nin);
+        for (int j = 0; j < a.nin; ++j)
+            bulk_load(base + (uint32_t)(s * a.nin + j) * row_bytes,
+                      static_cast<const uint8_t*>(a.in[j]) + (size_t)row * row_bytes, row_bytes, bar0 + s * 8);
+    }
+    __device__ __forceinline__ void start(const RingArgs& a) {
+        for (int i = 0; i < a.stages; ++i) {
+            const int64_t row = blockIdx.x + (int64_t)i * gridDim.x;
+            if (row < a.n.T) issue(a, row, i);
+        }
+    }
+    __device__ __forceinline__ void wait(const RingArgs& a) {
+        mbar_wait(bar0 + (it % a.stages) * 8, (uint32_t)(it / a.stages) & 1u, abort_flag, a.status);
+    }
+    __device__ __forceinline__ void refill(const RingArgs& a) {
+        const int64_t row = blockIdx.x + (int64_t)(it + a.stages) * gridDim.x;
+        if (row < a.n.T && !*abort_flag) issue(a, row, it + a.stages);
+    }
+    // after an aborted wait: no copy is in flight when the CTA ends
+    __device__ __forceinline__ void drain(const RingArgs& a, int n) {
+        for (int i = n > a.stages ? n - a.stages : 0; i < n; ++i)
+            mbar_drain(bar0 + (i % a.stages) * 8, (uint32_t)(i / a.stages) & 1u);
+    }
+};
+
+#define NORM_RING_SETUP()                                                                       \
+    extern __shared__ __align__(128) uint8_t ring_smem[];                                       \
+    __shared__ __align__(8) uint64_t bars[MAX_STAGES];                                          \
+    __shared__ int abort_s;                                                                     \
+    const NormArgs& n = a.n;                                                                    \
+    const int d = n.d;                                                                          \
+    const float invd = 1.f / (float)d;                                                          \
+    RowRing ring;                                                                               \
+    ring.base = smem_u32(ring_smem);                                                            \
+    ring.bar0 = smem_u32(bars);                                                                 \
+    ring.row_bytes = (uint32_t)(d * sizeof(T));                                                 \
+    ring.abort_flag = &abort_s;                                                                 \
+    if (threadIdx.x == 0) {                                                                     \
+        for (int i = 0; i < a.stages; ++i) mbar_init(ring.bar0 + i * 8, 1);                     \
+        abort_s = 0;                                                                            \
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");                      \
+    }                                                                                           \
+    __syncthreads();                                                                            \
+    pdl_wait();                                                                                 \
+    pdl_trigger();                                                                              \
+    if (threadIdx.x == 0) ring.start(a)
+
+// in: x, u (leave), gate (full)
+template <typename T, int MAXT>
+__global__ void __launch_bounds__(MAXT) block_norm_ring_kernel(const __grid_constant__ RingArgs a) {
+    __shared__ float buf[2][32];
+    NORM_RING_SETUP();
+    f2 wq[RP], wz[RP];                     // g w_post, w_pre
+    fill(wq, 1.f);
+    if (n.post) channel<T>(n.w_post, d, wq);
+    if (n.gmode == MOE_GATE_CHANNEL) {
+        channel<T>(static_cast<const float*>(n.gate), d, wz);
+#pragma unroll
+        for (int i = 0; i < RP; ++i) wq[i] = wq[i] * wz[i];
+    }
+    if (n.enter) channel<T>(n.w_pre, d, wz);
+    for (int64_t t = blockIdx.x; t < n.T; t += gridDim.x, ++ring.it) {
+        const T* st = reinterpret_cast<const T*>(ring_smem) + (size_t)(ring.it % a.stages) * a.nin * d;
+        const size_t o = (size_t)t * d;
+        float tok = n.ob;
+        if (n.gmode == MOE_GATE_TOKEN) tok *= __ldg(static_cast<const float*>(n.gate) + t);
+        ring.wait(a);
+        f2 y[RP], u[RP];
+        take<T>(st, d, y);
+        if (n.leave) {
+            take<T>(st + d, d, u);
+            const float s = n.post ? dot2(u, u) : 0.f;
+            if (n.gmode == MOE_GATE_FULL) {
+                f2 g[RP];
+                take<T>(st + 2 * d, d, g);
+#pragma unroll
+                for (int i = 0; i < RP; ++i) u[i] = u[i] * g[i];
+            }
+            if (n.post) tok *= rsqrtf(row_sum(s, buf[0]) * invd + n.eps);
+            const f2 c = both(tok), ra = both(n.ra);
+#pragma unroll
+            for (int i = 0; i < RP; ++i) y[i] = fma2(c * wq[i], u[i], ra * y[i]);
+            give<T>(static_cast<T*>(n.x_out) + o, d, y);
+        }
+        if (n.enter) {
+            const f2 r = both(rsqrtf(row_sum(dot2(y, y), buf[1]) * invd + n.eps));
+#pragma unroll
+            for (int i = 0; i < RP; ++i) y[i] = y[i] * (r * wz[i]);
+            give<T>(static_cast<T*>(n.z) + o, d, y);
+        }
+        // both buffers alternate with two norms; otherwise a barrier keeps a row's sums
+        // (and with no norm at all its stage) from the next row
+        if (!(n.post && n.enter) || blockDim.x <= 32) __syncthreads();
+        if (threadIdx.x == 0) ring.refill(a);
+    }
+    if (threadIdx.x == 0 && *ring.abort_flag) ring.drain(a, ring.it + a.stages);
+}
+
+// in: x_out, dz (enter), dx_out (if given), u (post or gate), gate (full)
+template <typename T, int MAXT>
+__global__ void __launch_bounds__(MAXT) block_norm_bwd_ring_kernel(const __grid_constant__ RingArgs a) {
+    __shared__ float buf[2][32 * 8];
+    NORM_RING_SETUP();
+    f2 wq[RP], wz[RP], wg[RP];             // w_post, w_pre, the channel gate
+    f2 acc_pre[RP], acc_post[RP], acc_g[RP];
+    fill(acc_pre, 0.f);
+    fill(acc_post, 0.f);
+    fill(acc_g, 0.f);
+    fill(wq, 1.f);
+    fill(wg, 1.f);
+    fill(wz, 1.f);
+    if (n.post) channel<T>(n.w_post, d, wq);
+    if (n.enter) channel<T>(n.w_pre, d, wz);
+    if (n.gmode == MOE_GATE_CHANNEL) channel<T>(static_cast<const float*>(n.gate), d, wg);
+    const bool need_u = n.leave && (n.post || n.gmode != MOE_GATE_NONE);
+    // the tensors' places in a stage
+    const int p_dz = 1, p_dx = n.enter ? 2 : 0, p_u = p_dx + (n.dx_out ? 1 : 0), p_g = p_u + 1;
+    for (int64_t t = blockIdx.x; t < n.T; t += gridDim.x, ++ring.it) {
+        const T* st = reinterpret_cast<const T*>(ring_smem) + (size_t)(ring.it % a.stages) * a.nin * d;
+        const size_t o = (size_t)t * d;
+        float tok = n.ob;
+        if (n.gmode == MOE_GATE_TOKEN) tok *= __ldg(static_cast<const float*>(n.gate) + t);
+        ring.wait(a);
+        f2 y[RP], G[RP], u[RP], dz[RP], g[RP];       // (b and a token gate are in tok)
+        // s: y^2, a y, u^2, q u dx', q u a, q u y  with a = w_pre dz, q = g w_post
+        float s[6] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        fill(G, 0.f);
+        if (n.dx_out) take<T>(st + (size_t)p_dx * d, d, G);
+        if (n.enter) {
+            take<T>(st, d, y);
+            take<T>(st + (size_t)p_dz * d, d, dz);
+            s[0] = dot2(y, y);
+        } else {
+            fill(y, 0.f);
+            fill(dz, 0.f);
+        }
+        if (need_u) {
+            take<T>(st + (size_t)p_u * d, d, u);
+            if (n.gmode == MOE_GATE_FULL) take<T>(st + (size_t)p_g * d, d, g);
+            else
+#pragma unroll
+                for (int i = 0; i < RP; ++i) g[i] = wg[i];
+            f2 s3 = both(0.f), s4 = s3, s5 = s3, s1 = s3;
+#pragma unroll
+            for (int i = 0; i < RP; ++i) {
+                const f2 qu = (g[i] * wq[i]) * u[i], az = wz[i] * dz[i];
+                s1 = fma2(az, y[i], s1);
+                s3 = fma2(qu, G[i], s3);
+                s4 = fma2(qu, az, s4);
+                s5 = fma2(qu, y[i], s5);
+            }
+            s[1] = sum2(s1);
+            s[2] = dot2(u, u);
+            s[3] = sum2(s3);
+            s[4] = sum2(s4);
+            s[5] = sum2(s5);
+        } else {
+            fill(u, 0.f);
+            fill(g, 1.f);
+            f2 s1 = both(0.f);
+#pragma unroll
+            for (int i = 0; i < RP; ++i) s1 = fma2(wz[i] * dz[i], y[i], s1);
+            s[1] = sum2(s1);
+        }
+        row_sums6(s, buf[ring.it & 1]);
+        if (blockDim.x <= 32) __syncwarp();
+        if (threadIdx.x == 0) ring.refill(a);
+        float r = 0.f, ca = 0.f;
+        f2 out[RP];
+        if (n.enter) {
+            r = rsqrtf(s[0] * invd + n.eps);
+            ca = r * r * r * invd * s[1];
+            const f2 r2 = both(r), c2 = both(-ca);
+#pragma unroll
+            for (int i = 0; i < RP; ++i) {
+                const f2 rz = r2 * dz[i];
+                acc_pre[i] = fma2(rz, y[i], acc_pre[i]);
+                G[i] = fma2(rz, wz[i], fma2(c2, y[i], G[i]));
+            }
+        }
+        if (!n.leave) {
+            give<T>(static_cast<T*>(n.dx) + o, d, G);
+            continue;
+        }
+        const f2 ra = both(n.ra);
+#pragma unroll
+        for (int i = 0; i < RP; ++i) out[i] = ra * G[i];
+        give<T>(static_cast<T*>(n.dx) + o, d, out);
+        const float S = s[3] + r * s[4] - ca * s[5];
+        const float ru = n.post ? rsqrtf(s[2] * invd + n.eps) : 1.f;
+        if (n.gmode == MOE_GATE_TOKEN && threadIdx.x == 0) static_cast<float*>(n.dgate)[t] = n.ob * ru * S;
+        // with h = b u r_u G (a token gate's factor apart): dw_post += g h, dgate = w_post h
+        const f2 tr = both(tok * ru), br = both(n.ob * ru);
+        const f2 cu = both(n.post ? -tok * ru * ru * ru * invd * S : 0.f);
+        if (n.gmode == MOE_GATE_FULL) {
+#pragma unroll
+            for (int i = 0; i < RP; ++i) out[i] = wq[i] * ((br * u[i]) * G[i]);
+            give<T>(static_cast<T*>(n.dgate) + o, d, out);
+        }
+#pragma unroll
+        for (int i = 0; i < RP; ++i) {
+            const f2 tG = tr * G[i], h = tG * u[i];
+            acc_post[i] = fma2(g[i], h, acc_post[i]);
+            acc_g[i] = fma2(wq[i], h, acc_g[i]);
+            out[i] = fma2(cu, u[i], (g[i] * wq[i]) * tG);
+        }
+        give<T>(static_cast<T*>(n.du) + o, d, out);
+    }
+    auto flush = [&](int which, const f2 (&acc)[RP]) {
+        constexpr int V = 16 / sizeof(T);
+        float* dst = n.part + ((size_t)which * gridDim.x + blockIdx.x) * d;
+#pragma unroll
+        for (int h = 0; h < RE / V; ++h) {
+            const int c = part_of<T>(h);
+            if (c < d)
+#pragma unroll
+                for (int j = 0; j < V; j += 2) {
+                    float lo, hi;
+                    unpk(acc[(h * V + j) / 2], lo, hi);
+                    *reinterpret_cast<float2*>(dst + c + j) = make_float2(lo, hi);
+                }
+        }
+    };
+    if (n.enter) flush(0, acc_pre);
+    if (n.post) flush(1, acc_post);
+    if (n.gmode == MOE_GATE_CHANNEL) flush(2, acc_g);
+    if (threadIdx.x == 0 && *ring.abort_flag) ring.drain(a, ring.it + a.stages);
 }
 
 // Column sums of the CTAs' partials: 32 columns x 32 row lanes a CTA, each lane
@@ -321,36 +658,120 @@ __global__ void __launch_bounds__(1024) norm_reduce_kernel(const NormReduceArgs 
     }
 }
 
-// threads of a row, rows per CTA
+// the direct kernels: elements a thread, threads of a row, rows per CTA
+int direct_ept(const moe_norm_config& c) { return c.d <= 8 * 1024 ? 8 : 16; }
 dim3 norm_block(const moe_norm_config& c) {
-    const int tpr = ((c.d + EPT - 1) / EPT + 31) / 32 * 32;
+    const int ept = direct_ept(c), tpr = ((c.d + ept - 1) / ept + 31) / 32 * 32;
     return dim3(tpr, tpr == 32 ? SMALL_ROWS : 1);
 }
 bool wide_rows(const moe_norm_config& c) { return (c.d * (c.dtype == MOE_DTYPE_BF16 ? 2 : 4)) % 16 == 0; }
 
+// The ring's launch: threads, stages and CTAs, or none (0 stages) where the direct
+// kernels serve: rows of no whole 16 bytes, rows too wide for two stages, and
+// batches of fewer than RING_ROWS rows an SM, where filling a ring is all there is.
+constexpr int RING_ROWS = 2;
+struct RingPlan { int threads, stages, grid; size_t smem; };
+RingPlan ring_plan(const moe_norm_config& c, int nin, int regs) {
+    RingPlan p = {0, 0, 0, 0};
+    const int es = c.dtype == MOE_DTYPE_BF16 ? 2 : 4;
+    p.threads = ((c.d + RE - 1) / RE + 31) / 32 * 32;
+    if (!wide_rows(c) || p.threads > 1024 || c.T < (int64_t)RING_ROWS * num_sms()) return p;
+    const int stage = nin * c.d * es;
+    // CTAs an SM by registers and threads, fewer where they would not have three stages
+    // each (228 KB an SM, 3 KB of it a CTA's fixed part)
+    int per_sm = std::max(1, std::min(std::min(32, 65536 / (regs * p.threads)), 2048 / p.threads));
+    auto room = [&](int n) { return std::min(200 * 1024, 224 * 1024 / n - 3072); };
+    while (per_sm > 1 && room(per_sm) < 3 * stage) --per_sm;
+    p.stages = std::min(MAX_STAGES, room(per_sm) / stage);
+    if (p.stages < 2) { p.stages = 0; return p; }
+    p.smem = (size_t)p.stages * stage;
+    p.grid = (int)std::min<int64_t>(c.T, (int64_t)per_sm * num_sms());
+    return p;
+}
+int fwd_inputs(const moe_norm_config& c) { return 1 + c.leave + (c.gate == MOE_GATE_FULL); }
+bool bwd_needs_u(const moe_norm_config& c) { return c.leave && (c.post_norm || c.gate != MOE_GATE_NONE); }
+int bwd_inputs(const moe_norm_config& c) {   // with dx_out
+    return 1 + 2 * c.enter + bwd_needs_u(c) + (c.gate == MOE_GATE_FULL);
+}
+RingPlan bwd_ring(const moe_norm_config& c) { return ring_plan(c, bwd_inputs(c), 128); }
+
 // CTAs of the backward: as many as the GPU holds, none with less than a row
 int bwd_grid(const moe_norm_config& c) {
+    const RingPlan p = bwd_ring(c);
+    if (p.stages) return p.grid;
+    // up to four rows a CTA before there are more CTAs than SMs: each adds a row to the
+    // partial sums that the last kernel reads
     const dim3 b = norm_block(c);
-    const int per_sm = std::max(1, 512 / (int)(b.x * b.y));
-    return (int)std::max<int64_t>(1, std::min<int64_t>(((int64_t)c.T + b.y - 1) / b.y, (int64_t)num_sms() * per_sm));
+    const int64_t rows = std::max<int64_t>(1, std::min<int64_t>(4, c.T / num_sms())) * b.y;
+    const int per_sm = std::max(1, 1024 / (int)(b.x * b.y));
+    return (int)std::min<int64_t>((c.T + rows - 1) / rows, (int64_t)num_sms() * per_sm);
+}
+
+template <typename T>
+int launch_fwd_ring(const RingPlan& p, const RingArgs& r, cudaStream_t st) {
+    static bool done[2][64] = {};
+    const bool big = p.threads > 512;
+    if (const int e = big ? smem_attr_once(block_norm_ring_kernel<T, 1024>, 200 * 1024, done[0])
+                          : smem_attr_once(block_norm_ring_kernel<T, 512>, 200 * 1024, done[1])) return e;
+    if (big) MOE_LAUNCH((block_norm_ring_kernel<T, 1024>), p.grid, p.threads, p.smem, st, r);
+    else MOE_LAUNCH((block_norm_ring_kernel<T, 512>), p.grid, p.threads, p.smem, st, r);
+    return MOE_OK;
+}
+template <typename T>
+int launch_bwd_ring(const RingPlan& p, const RingArgs& r, cudaStream_t st) {
+    static bool done[2][64] = {};
+    const bool big = p.threads > 512;
+    if (const int e = big ? smem_attr_once(block_norm_bwd_ring_kernel<T, 1024>, 200 * 1024, done[0])
+                          : smem_attr_once(block_norm_bwd_ring_kernel<T, 512>, 200 * 1024, done[1])) return e;
+    if (big) MOE_LAUNCH((block_norm_bwd_ring_kernel<T, 1024>), p.grid, p.threads, p.smem, st, r);
+    else MOE_LAUNCH((block_norm_bwd_ring_kernel<T, 512>), p.grid, p.threads, p.smem, st, r);
+    return MOE_OK;
 }
 
 template <typename T, int VEC>
 int launch_fwd(const moe_norm_config& c, const NormArgs& a, cudaStream_t st) {
+    const RingPlan p = ring_plan(c, fwd_inputs(c), 64);
+    if (p.stages) {
+        RingArgs r = {};
+        r.n = a;
+        r.in[r.nin++] = a.x;
+        if (c.leave) r.in[r.nin++] = a.u;
+        if (c.gate == MOE_GATE_FULL) r.in[r.nin++] = a.gate;
+        r.stages = p.stages;
+        r.status = device_status_ptr();
+        return launch_fwd_ring<T>(p, r, st);
+    }
     const dim3 b = norm_block(c);
     const int grid = (int)std::min<int64_t>(((int64_t)c.T + b.y - 1) / b.y, (int64_t)num_sms() * 64);
-    if (b.x <= 256) MOE_LAUNCH((block_norm_kernel<T, VEC, 256>), grid, b, 0, st, a);
-    else MOE_LAUNCH((block_norm_kernel<T, VEC, 1024>), grid, b, 0, st, a);
+    if (direct_ept(c) == 16) MOE_LAUNCH((block_norm_kernel<T, VEC, 16, 1024>), grid, b, 0, st, a);
+    else if (b.x <= 256) MOE_LAUNCH((block_norm_kernel<T, VEC, 8, 256>), grid, b, 0, st, a);
+    else MOE_LAUNCH((block_norm_kernel<T, VEC, 8, 1024>), grid, b, 0, st, a);
     return MOE_OK;
 }
 template <typename T, int VEC>
 int launch_bwd(const moe_norm_config& c, const NormArgs& a, float* dwpre, float* dwpost, cudaStream_t st) {
     const dim3 b = norm_block(c);
     const int grid = bwd_grid(c);
+    const RingPlan p = bwd_ring(c);
     const size_t smem = b.y > 1 ? (size_t)b.y * c.d * 4 : 0;
-    if (b.x <= 256) MOE_LAUNCH((block_norm_bwd_kernel<T, VEC, 256>), grid, b, smem, st, a);
-    else if (b.x <= 512) MOE_LAUNCH((block_norm_bwd_kernel<T, VEC, 512>), grid, b, smem, st, a);
-    else MOE_LAUNCH((block_norm_bwd_kernel<T, VEC, 1024>), grid, b, smem, st, a);
+    if (p.stages) {
+        RingArgs q = {};
+        q.n = a;
+        if (c.enter) q.in[q.nin++] = a.x;
+        if (c.enter) q.in[q.nin++] = a.dz;
+        if (a.dx_out) q.in[q.nin++] = a.dx_out;
+        if (bwd_needs_u(c)) q.in[q.nin++] = a.u;
+        if (c.gate == MOE_GATE_FULL) q.in[q.nin++] = a.gate;
+        q.stages = p.stages;
+        q.status = device_status_ptr();
+        if (const int e = launch_bwd_ring<T>(p, q, st)) return e;
+    } else if (direct_ept(c) == 16) {
+        MOE_LAUNCH((block_norm_bwd_kernel<T, VEC, 16, 1024>), grid, b, smem, st, a);
+    } else if (b.x <= 256) {
+        MOE_LAUNCH((block_norm_bwd_kernel<T, VEC, 8, 256>), grid, b, smem, st, a);
+    } else {
+        MOE_LAUNCH((block_norm_bwd_kernel<T, VEC, 8, 1024>), grid, b, smem, st, a);
+    }
     NormReduceArgs r;
     r.part = a.part;
     r.rows = grid;
