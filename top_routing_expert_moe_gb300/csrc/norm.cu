@@ -394,36 +394,49 @@ __device__ __forceinline__ float dot2(const f2 (&a)[RP], const f2 (&b)[RP]) {
     return sum2(s);
 }
 
+// Rows blockIdx.x + i gridDim.x pass through the stages in turn.  `slot` and
+// `phase` follow the row being worked on.  One warp watches the barriers: it waits
+// for the next row's stage before it joins the current row's last reduction, whose
+// CTA barrier then tells the others.
 struct RowRing {
-    uint32_t base, bar0;
-    uint32_t row_bytes;
-    int it = 0;
+    uint32_t base, bar0, row_bytes, stage_bytes;
+    int stages, slot = 0;
+    uint32_t phase = 0;
     volatile int* abort_flag;
 
-    __device__ __forceinline__ void issue(const RingArgs& a, int64_t row, int i) {
-        const int s = i % a.stages;
-        mbar_expect_tx(bar0 + s * 8, row_bytes * a.nin);
+    __device__ __forceinline__ void issue(const RingArgs& a, int64_t row, int s) const {
+        mbar_expect_tx(bar0 + s * 8, stage_bytes);
         for (int j = 0; j < a.nin; ++j)
-            bulk_load(base + (uint32_t)(s * a.nin + j) * row_bytes,
+            bulk_load(base + s * stage_bytes + j * row_bytes,
                       static_cast<const uint8_t*>(a.in[j]) + (size_t)row * row_bytes, row_bytes, bar0 + s * 8);
     }
-    __device__ __forceinline__ void start(const RingArgs& a) {
-        for (int i = 0; i < a.stages; ++i) {
-            const int64_t row = blockIdx.x + (int64_t)i * gridDim.x;
-            if (row < a.n.T) issue(a, row, i);
+    __device__ __forceinline__ void start(const RingArgs& a) const {
+        int64_t row = blockIdx.x;
+        for (int i = 0; i < stages && row < a.n.T; ++i, row += gridDim.x) issue(a, row, i);
+    }
+    __device__ __forceinline__ void wait(const RingArgs& a, int s, uint32_t ph) const {
+        mbar_wait(bar0 + s * 8, ph, abort_flag, a.status);
+    }
+    // before the row's last reduction: the next row's stage
+    __device__ __forceinline__ void wait_next(const RingArgs& a, int64_t t) const {
+        if (threadIdx.x < 32 && t + gridDim.x < a.n.T)
+            wait(a, slot + 1 == stages ? 0 : slot + 1, slot + 1 == stages ? phase ^ 1u : phase);
+    }
+    // after it, by one thread: the stage of the current row t takes a later row
+    __device__ __forceinline__ void refill(const RingArgs& a, int64_t t) const {
+        const int64_t row = t + (int64_t)stages * gridDim.x;
+        if (row < a.n.T && !*abort_flag) issue(a, row, slot);
+    }
+    __device__ __forceinline__ void next() {
+        if (++slot == stages) {
+            slot = 0;
+            phase ^= 1u;
         }
     }
-    __device__ __forceinline__ void wait(const RingArgs& a) {
-        mbar_wait(bar0 + (it % a.stages) * 8, (uint32_t)(it / a.stages) & 1u, abort_flag, a.status);
-    }
-    __device__ __forceinline__ void refill(const RingArgs& a) {
-        const int64_t row = blockIdx.x + (int64_t)(it + a.stages) * gridDim.x;
-        if (row < a.n.T && !*abort_flag) issue(a, row, it + a.stages);
-    }
-    // after an aborted wait: no copy is in flight when the CTA ends
-    __device__ __forceinline__ void drain(const RingArgs& a, int n) {
-        for (int i = n > a.stages ? n - a.stages : 0; i < n; ++i)
-            mbar_drain(bar0 + (i % a.stages) * 8, (uint32_t)(i / a.stages) & 1u);
+    // after an aborted wait: no copy is in flight when the CTA ends (a stage's last
+    // phase is the current one or the one before)
+    __device__ __forceinline__ void drain() const {
+        for (int s = 0; s < stages; ++s) mbar_drain(bar0 + s * 8, s < slot ? phase ^ 1u : phase);
     }
 };
 
@@ -438,6 +451,8 @@ struct RowRing {
     ring.base = smem_u32(ring_smem);                                                            \
     ring.bar0 = smem_u32(bars);                                                                 \
     ring.row_bytes = (uint32_t)(d * sizeof(T));                                                 \
+    ring.stage_bytes = ring.row_bytes * a.nin;                                                  \
+    ring.stages = a.stages;                                                                     \
     ring.abort_flag = &abort_s;                                                                 \
     if (threadIdx.x == 0) {                                                                     \
         for (int i = 0; i < a.stages; ++i) mbar_init(ring.bar0 + i * 8, 1);                     \
@@ -447,7 +462,8 @@ struct RowRing {
     __syncthreads();                                                                            \
     pdl_wait();                                                                                 \
     pdl_trigger();                                                                              \
-    if (threadIdx.x == 0) ring.start(a)
+    if (threadIdx.x == 0) ring.start(a);                                                        \
+    ring.wait(a, 0, 0)
 
 // in: x, u (leave), gate (full)
 template <typename T, int MAXT>
@@ -463,12 +479,11 @@ __global__ void __launch_bounds__(MAXT) block_norm_ring_kernel(const __grid_cons
         for (int i = 0; i < RP; ++i) wq[i] = wq[i] * wz[i];
     }
     if (n.enter) channel<T>(n.w_pre, d, wz);
-    for (int64_t t = blockIdx.x; t < n.T; t += gridDim.x, ++ring.it) {
-        const T* st = reinterpret_cast<const T*>(ring_smem) + (size_t)(ring.it % a.stages) * a.nin * d;
+    for (int64_t t = blockIdx.x; t < n.T; t += gridDim.x, ring.next()) {
+        const T* st = reinterpret_cast<const T*>(ring_smem + ring.slot * ring.stage_bytes);
         const size_t o = (size_t)t * d;
         float tok = n.ob;
         if (n.gmode == MOE_GATE_TOKEN) tok *= __ldg(static_cast<const float*>(n.gate) + t);
-        ring.wait(a);
         f2 y[RP], u[RP];
         take<T>(st, d, y);
         if (n.leave) {
@@ -487,17 +502,22 @@ __global__ void __launch_bounds__(MAXT) block_norm_ring_kernel(const __grid_cons
             give<T>(static_cast<T*>(n.x_out) + o, d, y);
         }
         if (n.enter) {
-            const f2 r = both(rsqrtf(row_sum(dot2(y, y), buf[1]) * invd + n.eps));
+            const float s = dot2(y, y);
+            ring.wait_next(a, t);
+            const f2 r = both(rsqrtf(row_sum(s, buf[1]) * invd + n.eps));
 #pragma unroll
             for (int i = 0; i < RP; ++i) y[i] = y[i] * (r * wz[i]);
             give<T>(static_cast<T*>(n.z) + o, d, y);
         }
         // both buffers alternate with two norms; otherwise a barrier keeps a row's sums
         // (and with no norm at all its stage) from the next row
-        if (!(n.post && n.enter) || blockDim.x <= 32) __syncthreads();
-        if (threadIdx.x == 0) ring.refill(a);
+        if (!(n.post && n.enter) || blockDim.x <= 32) {
+            if (!n.enter) ring.wait_next(a, t);
+            __syncthreads();
+        }
+        if (threadIdx.x == 0) ring.refill(a, t);
     }
-    if (threadIdx.x == 0 && *ring.abort_flag) ring.drain(a, ring.it + a.stages);
+    if (threadIdx.x == 0 && *ring.abort_flag) ring.drain();
 }
 
 // in: x_out, dz (enter), dx_out (if given), u (post or gate), gate (full)
@@ -517,14 +537,14 @@ __global__ void __launch_bounds__(MAXT) block_norm_bwd_ring_kernel(const __grid_
     if (n.enter) channel<T>(n.w_pre, d, wz);
     if (n.gmode == MOE_GATE_CHANNEL) channel<T>(static_cast<const float*>(n.gate), d, wg);
     const bool need_u = n.leave && (n.post || n.gmode != MOE_GATE_NONE);
+    int par = 0;
     // the tensors' places in a stage
     const int p_dz = 1, p_dx = n.enter ? 2 : 0, p_u = p_dx + (n.dx_out ? 1 : 0), p_g = p_u + 1;
-    for (int64_t t = blockIdx.x; t < n.T; t += gridDim.x, ++ring.it) {
-        const T* st = reinterpret_cast<const T*>(ring_smem) + (size_t)(ring.it % a.stages) * a.nin * d;
+    for (int64_t t = blockIdx.x; t < n.T; t += gridDim.x, ring.next(), par ^= 1) {
+        const T* st = reinterpret_cast<const T*>(ring_smem + ring.slot * ring.stage_bytes);
         const size_t o = (size_t)t * d;
         float tok = n.ob;
         if (n.gmode == MOE_GATE_TOKEN) tok *= __ldg(static_cast<const float*>(n.gate) + t);
-        ring.wait(a);
         f2 y[RP], G[RP], u[RP], dz[RP], g[RP];       // (b and a token gate are in tok)
         // s: y^2, a y, u^2, q u dx', q u a, q u y  with a = w_pre dz, q = g w_post
         float s[6] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
@@ -566,9 +586,10 @@ __global__ void __launch_bounds__(MAXT) block_norm_bwd_ring_kernel(const __grid_
             for (int i = 0; i < RP; ++i) s1 = fma2(wz[i] * dz[i], y[i], s1);
             s[1] = sum2(s1);
         }
-        row_sums6(s, buf[ring.it & 1]);
+        ring.wait_next(a, t);
+        row_sums6(s, buf[par]);
         if (blockDim.x <= 32) __syncwarp();
-        if (threadIdx.x == 0) ring.refill(a);
+        if (threadIdx.x == 0) ring.refill(a, t);
         float r = 0.f, ca = 0.f;
         f2 out[RP];
         if (n.enter) {
@@ -628,7 +649,7 @@ __global__ void __launch_bounds__(MAXT) block_norm_bwd_ring_kernel(const __grid_
     if (n.enter) flush(0, acc_pre);
     if (n.post) flush(1, acc_post);
     if (n.gmode == MOE_GATE_CHANNEL) flush(2, acc_g);
-    if (threadIdx.x == 0 && *ring.abort_flag) ring.drain(a, ring.it + a.stages);
+    if (threadIdx.x == 0 && *ring.abort_flag) ring.drain();
 }
 
 // Column sums of the CTAs' partials: 32 columns x 32 row lanes a CTA, each lane
