@@ -6,11 +6,12 @@
 //   dl_t = (1/tau) [ p (w_s - <w_s, p>) + (2 coef_z / n) lse_t p ],
 //          w_se = (coef / S') E c_se / (k n_s^2),   S' sequences with tokens
 //
-// Three kernels: partial sums over chunks of tokens, their sum per sequence, and
-// the total; the backward streams the logits once more.  G lanes hold a token's
-// experts (E / G each), so a warp's loads of 32 / G tokens are contiguous.
-// Floating sums run in a fixed order (no float atomics); counts use integer
-// atomics in shared memory, whose order does not matter.
+// Forward: partial sums over chunks of tokens, then one CTA a sequence adds them
+// and the last of those forms the losses.  The backward streams the logits once
+// more.  G lanes hold a token's experts, 4 or 8 each, so that the softmax needs
+// log2(G) shuffles and a warp's loads of 32 / G tokens stay contiguous.  Floating
+// sums run in a fixed order (no float atomics); counts use integer atomics in
+// shared memory, whose order does not matter.
 #include <algorithm>
 
 #include "common.cuh"
@@ -21,9 +22,10 @@ namespace moe {
 namespace {
 
 constexpr int THREADS = 256;
-constexpr int CHUNK = 256;       // tokens per CTA of the forward's first kernel
+constexpr int SEQ_THREADS = 512;
+constexpr float LOG2E = 1.44269504f;
 
-// A record holds one (chunk, sequence) pair's sums: E probability sums, n, the sum
+// A record holds one (chunk of tokens, sequence) pair's sums: E probability sums, n, the sum
 // of lse^2, then E counts (int32).  Chunks and sequences both ascend, so pair
 // (b, s) has the record b + s of its own: every step to the next pair raises one.
 __host__ __device__ inline size_t rec_floats(int E) { return 2 * (size_t)E + 2; }
@@ -34,8 +36,9 @@ struct BalArgs {
     const float *grad_w, *dloss;
     float *rec, *seqsum, *loss, *pbar, *gw, *dlogits;
     int32_t* counts;
+    unsigned* ticket;
     int* status;
-    int T, E, k, S, nchunk;
+    int T, E, k, S, chunk;                           // tokens of a CTA
     float bcoef, zcoef, inv_tau;
 };
 
@@ -69,18 +72,44 @@ __device__ __forceinline__ float group_sum(float v) {
     return v;
 }
 
-// Softmax of one token over its G lanes; lane holds experts lane, lane + G, ...
-// (R of them).  lse = -inf and p = 0 where every logit is -inf.
+// A lane's experts: R in groups of W (4 where E is a multiple of 4: one 16-byte
+// access each, else 1), group i at (lane + i G) W.
+template <int G, int R, int W> struct Row {
+    static constexpr int N = R / W;
+    __device__ __forceinline__ static int expert(int gl, int i) { return (gl + (i / W) * G) * W + i % W; }
+    __device__ __forceinline__ static void load(const float* row, int E, int gl, bool in, float (&v)[R]) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int e = (gl + i * G) * W;
+            if constexpr (W == 4) {
+                const float4 f = in && e < E ? __ldg(reinterpret_cast<const float4*>(row + e))
+                                             : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+                v[4 * i] = f.x; v[4 * i + 1] = f.y; v[4 * i + 2] = f.z; v[4 * i + 3] = f.w;
+            } else {
+                v[i] = in && e < E ? __ldg(row + e) : -INFINITY;
+            }
+        }
+    }
+    __device__ __forceinline__ static void store(float* row, int E, int gl, const float (&v)[R]) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int e = (gl + i * G) * W;
+            if (e >= E) continue;
+            if constexpr (W == 4) *reinterpret_cast<float4*>(row + e) = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+            else row[e] = v[i];
+        }
+    }
+};
+
+// Softmax of one token's logits over its G lanes, in place, in powers of two
+// (k2 = log2(e) / tau); returns lse (-inf, with p = 0, where every logit is -inf or
+// the token is masked; NaN where one is NaN or +inf).
 template <int G, int R>
-__device__ __forceinline__ float softmax_row(const float* row, int E, int gl, bool on, float inv_tau,
-                                             float (&p)[R], bool& bad) {
+__device__ __forceinline__ float softmax_row(float (&p)[R], bool on, float k2) {
     float m = -INFINITY;
-    bad = false;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-        const int e = gl + i * G;
-        p[i] = on && e < E ? __ldg(row + e) * inv_tau : -INFINITY;
-        bad |= isnan(p[i]) || p[i] == INFINITY;
+        p[i] = on ? p[i] * k2 : -INFINITY;
         m = fmaxf(m, p[i]);
     }
     m = group_max<G>(m);
@@ -88,20 +117,21 @@ __device__ __forceinline__ float softmax_row(const float* row, int E, int gl, bo
     const float mm = m == -INFINITY ? 0.f : m;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-        p[i] = expf(p[i] - mm);
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p[i]) : "f"(p[i] - mm));   // 2 ulp
         z += p[i];
     }
     z = group_sum<G>(z);
-    const float iz = z == 0.f ? 0.f : 1.f / z;       // (NaN stays NaN)
+    const float iz = z == 0.f ? 0.f : __fdividef(1.f, z);   // (1 <= z <= E, or NaN)
 #pragma unroll
     for (int i = 0; i < R; ++i) p[i] *= iz;
-    return z == 0.f ? -INFINITY : m + logf(z);
+    return z == 0.f ? -INFINITY : (m + __log2f(z)) * 0.69314718f;
 }
 
-template <int G, int R>
+template <int G, int R, int W>
 __global__ void __launch_bounds__(THREADS) balance_partial_kernel(const BalArgs a) {
     pdl_wait();
     pdl_trigger();
+    using L = Row<G, R, W>;
     constexpr int TOK = THREADS / G;                 // tokens at a time
     extern __shared__ float sm[];                    // [8 warps][E + 2] sums, [E] counts
     float* wsum = sm;
@@ -109,14 +139,16 @@ __global__ void __launch_bounds__(THREADS) balance_partial_kernel(const BalArgs 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int gl = tid % G, grp = tid / G;
     const int b = blockIdx.x;
-    const int t0 = b * CHUNK, t1 = min(a.T, t0 + CHUNK);
-    if (b == 0)                                      // offsets: ascending from 0 to T
-        for (int s = tid; s <= a.S; s += THREADS)
-            if (a.seq) {
+    const int t0 = b * a.chunk, t1 = min(a.T, t0 + a.chunk);
+    if (b == 0) {
+        if (tid == 0) *a.ticket = 0;
+        if (a.seq)                                   // offsets: ascending from 0 to T
+            for (int s = tid; s <= a.S; s += THREADS) {
                 const int v = a.seq[s], nx = s < a.S ? a.seq[s + 1] : a.T;
                 if (v > nx || v < 0 || (s == 0 && v != 0) || (s == a.S && v != a.T))
                     set_status(a.status, MOE_ERR_DEVICE_BOUNDS);
             }
+    }
     int t = t0;
     for (int s = a.seq ? seq_of(a, t0) : 0; t < t1; ++s) {
         const int end = min(t1, a.seq ? seq_at(a, s + 1) : a.T);
@@ -130,12 +162,13 @@ __global__ void __launch_bounds__(THREADS) balance_partial_kernel(const BalArgs 
         for (int base = t; base < stop; base += TOK) {
             const int tt = base + grp;
             const bool in = tt < stop;
-            const bool on = in && a.topk[(size_t)tt * a.k] >= 0;
             float p[R];
-            bool bad;
-            const float lse = softmax_row<G, R>(a.logits + (size_t)tt * a.E, a.E, gl, on, a.inv_tau, p, bad);
+            L::load(a.logits + (size_t)tt * a.E, a.E, gl, in, p);
+            const int32_t* pick = a.topk + (size_t)tt * a.k;
+            const bool on = in && __ldg(pick) >= 0;
+            const float lse = softmax_row<G, R>(p, on, a.inv_tau * LOG2E);
             if (on) {
-                if (bad) set_status(a.status, MOE_ERR_NONFINITE);
+                if (isnan(lse)) set_status(a.status, MOE_ERR_NONFINITE);
 #pragma unroll
                 for (int i = 0; i < R; ++i) sum[i] += p[i];
                 if (gl == 0) {
@@ -145,7 +178,7 @@ __global__ void __launch_bounds__(THREADS) balance_partial_kernel(const BalArgs 
             }
             if (in)
                 for (int j = gl; j < a.k; j += G) {
-                    const int e = a.topk[(size_t)tt * a.k + j];
+                    const int e = __ldg(pick + j);
                     if (e >= a.E || e < -1) set_status(a.status, MOE_ERR_DEVICE_BOUNDS);
                     else if (e >= 0 && on) atomicAdd(cnt + e, 1);
                 }
@@ -161,7 +194,7 @@ __global__ void __launch_bounds__(THREADS) balance_partial_kernel(const BalArgs 
         if (lane < G) {
 #pragma unroll
             for (int i = 0; i < R; ++i)
-                if (gl + i * G < a.E) wsum[warp * (a.E + 2) + gl + i * G] = sum[i];
+                if (L::expert(gl, i) < a.E) wsum[warp * (a.E + 2) + L::expert(gl, i)] = sum[i];
             if (lane == 0) {
                 wsum[warp * (a.E + 2) + a.E] = n;
                 wsum[warp * (a.E + 2) + a.E + 1] = zz;
@@ -171,6 +204,7 @@ __global__ void __launch_bounds__(THREADS) balance_partial_kernel(const BalArgs 
         float* rec = a.rec + (size_t)(b + s) * rec_floats(a.E);
         for (int i = tid; i < a.E + 2; i += THREADS) {
             float v = 0.f;
+#pragma unroll
             for (int w = 0; w < 8; ++w) v += wsum[w * (a.E + 2) + i];
             rec[i] = v;
         }
@@ -180,151 +214,195 @@ __global__ void __launch_bounds__(THREADS) balance_partial_kernel(const BalArgs 
     }
 }
 
-// One CTA per sequence: its records in order, in double (up to T / CHUNK of them).
-__global__ void __launch_bounds__(THREADS) balance_sequence_kernel(const BalArgs a) {
+// One CTA per sequence adds its records: P groups of threads take every P-th one
+// (P a power of two), then the groups' sums are added pairwise.  The last CTA to
+// finish adds the sequences and writes the losses and the backward's two factors,
+// coef / S' and 2 coef_z / n.
+__host__ __device__ inline int seq_groups(int E) {
+    int P = 1;
+    while (2 * P * (E + 2) <= SEQ_THREADS) P *= 2;
+    return P;
+}
+__global__ void __launch_bounds__(SEQ_THREADS) balance_sequence_kernel(const BalArgs a) {
     pdl_wait();
     pdl_trigger();
-    const int s = blockIdx.x, E = a.E;
+    const int s = blockIdx.x, E = a.E, W = E + 2, tid = threadIdx.x;
     const int beg = a.seq ? seq_at(a, s) : 0;
     const int end = s + 1 >= a.S ? a.T : seq_at(a, s + 1);
-    const int b0 = beg / CHUNK, b1 = end > beg ? (end - 1) / CHUNK : b0 - 1;
-    __shared__ double tot[2];                        // n, sum lse^2
-    __shared__ double part[THREADS / 32];
-    for (int i = threadIdx.x; i < 2; i += THREADS) {
-        double v = 0.0;
-        for (int b = b0; b <= b1; ++b) v += a.rec[(size_t)(b + s) * rec_floats(E) + E + i];
-        tot[i] = v;
+    const int b0 = beg / a.chunk, b1 = end > beg ? (end - 1) / a.chunk : b0 - 1;
+    extern __shared__ float sd[];                    // [P][W] sums, then [P][E] counts
+    const int P = seq_groups(E);
+    int* sc = reinterpret_cast<int*>(sd + P * W);
+    __shared__ float part[SEQ_THREADS / 32];
+    const int col = tid % W, g = tid / W;
+    if (g < P) {
+        float v = 0.f;
+        int c = 0;
+#pragma unroll 4
+        for (int b = b0 + g; b <= b1; b += P) {
+            const float* r = a.rec + (size_t)(b + s) * rec_floats(E);
+            v += r[col];
+            if (col < E) c += __float_as_int(r[W + col]);
+        }
+        sd[g * W + col] = v;
+        if (col < E) sc[g * E + col] = c;
     }
     __syncthreads();
-    const double n = tot[0], in = n > 0.0 ? 1.0 / n : 0.0;
-    double fp = 0.0;
-    for (int e = threadIdx.x; e < E; e += THREADS) {
-        double v = 0.0;
-        int c = 0;
-        for (int b = b0; b <= b1; ++b) {
-            const float* r = a.rec + (size_t)(b + s) * rec_floats(E);
-            v += r[e];
-            c += __float_as_int(r[E + 2 + e]);
+    for (int h = P / 2; h > 0; h >>= 1) {
+        if (g < h) {
+            sd[g * W + col] += sd[(g + h) * W + col];
+            if (col < E) sc[g * E + col] += sc[(g + h) * E + col];
         }
-        const double P = v * in, f = (double)E * c * in / a.k;
-        a.counts[(size_t)s * E + e] = c;
-        a.pbar[(size_t)s * E + e] = (float)P;
-        a.gw[(size_t)s * (E + 2) + e] = (float)(f * in);   // times coef / S' in the backward
-        fp += f * P;
+        __syncthreads();
+    }
+    const float n = sd[E], zz = sd[E + 1], in = n > 0.f ? 1.f / n : 0.f;
+    float fp = 0.f;
+    if (tid < E) {
+        const float p = sd[tid] * in, f = (float)E * (float)sc[tid] * in / (float)a.k;
+        a.counts[(size_t)s * E + tid] = sc[tid];
+        a.pbar[(size_t)s * E + tid] = p;
+        a.gw[(size_t)s * W + tid] = f * in;          // times coef / S' in the backward
+        fp = f * p;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) fp += __shfl_xor_sync(0xffffffffu, fp, o);
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = fp;
+    if ((tid & 31) == 0) part[tid >> 5] = fp;
     __syncthreads();
-    if (threadIdx.x == 0) {
-        double v = 0.0;
-        for (int w = 0; w < THREADS / 32; ++w) v += part[w];
-        a.seqsum[s * 3] = (float)v;
-        a.seqsum[s * 3 + 1] = (float)n;
-        a.seqsum[s * 3 + 2] = (float)tot[1];
+    __shared__ unsigned order;
+    if (tid == 0) {
+        float v = 0.f;
+        for (int w = 0; w < SEQ_THREADS / 32; ++w) v += part[w];
+        a.seqsum[s * 3] = v;
+        a.seqsum[s * 3 + 1] = n;
+        a.seqsum[s * 3 + 2] = zz;
+        __threadfence();
+        order = atomicAdd(a.ticket, 1u);
+    }
+    __syncthreads();
+    if (order != (unsigned)a.S - 1) return;
+    __threadfence();
+    float v[4] = {0.f, 0.f, 0.f, 0.f};               // sum f P, sequences, tokens, sum lse^2
+    for (int i = tid; i < a.S; i += SEQ_THREADS) {
+        v[0] += __ldcg(a.seqsum + i * 3);
+        const float ni = __ldcg(a.seqsum + i * 3 + 1);
+        v[1] += ni > 0.f;
+        v[2] += ni;
+        v[3] += __ldcg(a.seqsum + i * 3 + 2);
+    }
+    __shared__ float tot[4][SEQ_THREADS / 32];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+        if ((tid & 31) == 0) tot[i][tid >> 5] = v[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[i] = 0.f;
+        for (int w = 0; w < SEQ_THREADS / 32; ++w) v[i] += tot[i][w];
+    }
+    const float ns = fmaxf(v[1], 1.f), nt = fmaxf(v[2], 1.f);
+    if (tid == 0) {
+        const float b = a.bcoef * v[0] / ns, z = a.zcoef * v[3] / nt;
+        a.loss[0] = b + z;
+        a.loss[1] = b;
+        a.loss[2] = z;
+    }
+    for (int i = tid; i < a.S; i += SEQ_THREADS) {
+        a.gw[(size_t)i * W + E] = a.bcoef / ns;
+        a.gw[(size_t)i * W + E + 1] = 2.f * a.zcoef / nt;
     }
 }
 
-// The losses, and the two factors of the backward: coef / S' and 2 coef_z / n,
-// written beside every sequence's weights.
-__global__ void __launch_bounds__(THREADS) balance_total_kernel(const BalArgs a) {
-    pdl_wait();
-    pdl_trigger();
-    __shared__ double sm[4][THREADS];
-    double v[4] = {0, 0, 0, 0};                      // sum f P, sequences, tokens, sum lse^2
-    for (int s = threadIdx.x; s < a.S; s += THREADS) {
-        v[0] += a.seqsum[s * 3];
-        v[1] += a.seqsum[s * 3 + 1] > 0.f;
-        v[2] += a.seqsum[s * 3 + 1];
-        v[3] += a.seqsum[s * 3 + 2];
-    }
-    for (int i = 0; i < 4; ++i) sm[i][threadIdx.x] = v[i];
-    __syncthreads();
-    for (int h = THREADS / 2; h > 0; h >>= 1) {
-        if (threadIdx.x < h)
-            for (int i = 0; i < 4; ++i) sm[i][threadIdx.x] += sm[i][threadIdx.x + h];
-        __syncthreads();
-    }
-    const double ns = fmax(sm[1][0], 1.0), n = fmax(sm[2][0], 1.0);
-    if (threadIdx.x == 0) {
-        const double b = a.bcoef * sm[0][0] / ns, z = a.zcoef * sm[3][0] / n;
-        a.loss[0] = (float)(b + z);
-        a.loss[1] = (float)b;
-        a.loss[2] = (float)z;
-    }
-    for (int s = threadIdx.x; s < a.S; s += THREADS) {
-        a.gw[(size_t)s * (a.E + 2) + a.E] = (float)(a.bcoef / ns);
-        a.gw[(size_t)s * (a.E + 2) + a.E + 1] = (float)(2.0 * a.zcoef / n);
-    }
-}
-
-template <int G, int R>
+template <int G, int R, int W>
 __global__ void __launch_bounds__(THREADS) balance_bwd_kernel(const BalArgs a) {
     pdl_wait();
     pdl_trigger();
+    using L = Row<G, R, W>;
     constexpr int TOK = THREADS / G;
     const int gl = threadIdx.x % G, grp = threadIdx.x / G;
     const float up = (a.dloss ? __ldg(a.dloss) : 1.f) * a.inv_tau;
-    for (int base = blockIdx.x * TOK; base < a.T; base += gridDim.x * TOK) {
+    const int t0 = blockIdx.x * a.chunk, t1 = min(a.T, t0 + a.chunk);
+    // the sequence of this group's token, its end and its weights; they ascend with t
+    int s = a.seq ? seq_of(a, min(t0 + grp, a.T - 1)) : 0, end = -1;
+    float w[R], cz = 0.f;
+    for (int base = t0; base < t1; base += TOK) {
         const int t = base + grp;
-        const bool in = t < a.T;
-        const bool on = in && a.topk[(size_t)t * a.k] >= 0;
-        float p[R], w[R];
-        bool bad;
-        const float lse = softmax_row<G, R>(a.logits + (size_t)t * a.E, a.E, gl, on, a.inv_tau, p, bad);
-        const float* gw = a.grad_w + (size_t)(on && a.seq ? seq_of(a, t) : 0) * (a.E + 2);
-        const float cb = __ldg(gw + a.E), cz = __ldg(gw + a.E + 1);
+        const bool in = t < t1;
+        float p[R];
+        L::load(a.logits + (size_t)t * a.E, a.E, gl, in, p);
+        const bool on = in && __ldg(a.topk + (size_t)t * a.k) >= 0;
+        if (in && t >= end) {
+            while (s + 1 < a.S && seq_at(a, s + 1) <= t) ++s;
+            end = s + 1 < a.S ? seq_at(a, s + 1) : a.T;
+            const float* gw = a.grad_w + (size_t)s * (a.E + 2);
+            const float cb = __ldg(gw + a.E);
+            cz = __ldg(gw + a.E + 1);
+#pragma unroll
+            for (int i = 0; i < R; ++i) w[i] = L::expert(gl, i) < a.E ? cb * __ldg(gw + L::expert(gl, i)) : 0.f;
+        }
+        const float lse = softmax_row<G, R>(p, on, a.inv_tau * LOG2E);
         float dot = 0.f;
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-            const int e = gl + i * G;
-            w[i] = e < a.E ? cb * __ldg(gw + e) : 0.f;
-            dot = fmaf(w[i], p[i], dot);
-        }
+        for (int i = 0; i < R; ++i) dot = fmaf(on ? w[i] : 0.f, p[i], dot);
         dot = group_sum<G>(dot);
         const float zl = lse == -INFINITY ? 0.f : cz * lse;
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-            const int e = gl + i * G;
-            if (in && e < a.E) a.dlogits[(size_t)t * a.E + e] = on ? up * (p[i] * (w[i] - dot + zl)) : 0.f;
-        }
+        for (int i = 0; i < R; ++i) p[i] = on ? up * (p[i] * (w[i] - dot + zl)) : 0.f;
+        if (in) L::store(a.dlogits + (size_t)t * a.E, a.E, gl, p);
     }
 }
 
-// lanes per token and experts per lane: the fewest lanes that leave a lane at most
-// eight experts, at least 4 so that a row's loads stay together
-template <template <int, int> class F, class... A>
+// Lanes per token: the fewest that leave each at most eight experts.
+template <template <int, int, int> class F, class... A>
 int by_experts(int E, A&&... args) {
-    if (E <= 4) return F<4, 1>::go(args...);
-    if (E <= 8) return F<8, 1>::go(args...);
-    if (E <= 16) return F<16, 1>::go(args...);
-    if (E <= 32) return F<32, 1>::go(args...);
-    if (E <= 64) return F<32, 2>::go(args...);
-    if (E <= 128) return F<32, 4>::go(args...);
-    return F<32, 8>::go(args...);
+    if (E % 4 == 0) {
+        if (E <= 4) return F<1, 4, 4>::go(args...);
+        if (E <= 8) return F<2, 4, 4>::go(args...);
+        if (E <= 16) return F<4, 4, 4>::go(args...);
+        if (E <= 32) return F<4, 8, 4>::go(args...);
+        if (E <= 64) return F<8, 8, 4>::go(args...);
+        if (E <= 128) return F<16, 8, 4>::go(args...);
+        return F<32, 8, 4>::go(args...);
+    }
+    if (E <= 8) return F<2, 4, 1>::go(args...);
+    if (E <= 16) return F<4, 4, 1>::go(args...);
+    if (E <= 32) return F<4, 8, 1>::go(args...);
+    if (E <= 64) return F<8, 8, 1>::go(args...);
+    if (E <= 128) return F<16, 8, 1>::go(args...);
+    return F<32, 8, 1>::go(args...);
 }
 
-template <int G, int R> struct Partial {
+// Tokens of a CTA: about four CTAs an SM, but whole passes (THREADS / G tokens), at
+// most 512 tokens, and no fewer than 32 (a chunk's record is 2 E + 2 words).
+int chunk_of(const moe_balance_config& c) {
+    const int g = c.E <= 4 && c.E % 4 == 0 ? 1 : c.E <= 8 ? 2 : c.E <= 32 ? 4 : c.E <= 64 ? 8 : c.E <= 128 ? 16 : 32;
+    const int pass = std::max(32, THREADS / g);
+    const int want = (c.T + 4 * num_sms() - 1) / (4 * num_sms());
+    return std::min(512, std::max(1, (want + pass - 1) / pass) * pass);
+}
+int n_chunks(const moe_balance_config& c) { return (c.T + chunk_of(c) - 1) / chunk_of(c); }
+
+template <int G, int R, int W> struct Partial {
     static int go(const BalArgs& a, cudaStream_t st) {
         const size_t smem = (size_t)(8 * (a.E + 2) + a.E) * 4;
-        MOE_LAUNCH((balance_partial_kernel<G, R>), a.nchunk, THREADS, smem, st, a);
+        MOE_LAUNCH((balance_partial_kernel<G, R, W>), (a.T + a.chunk - 1) / a.chunk, THREADS, smem, st, a);
         return MOE_OK;
     }
 };
-template <int G, int R> struct Backward {
+template <int G, int R, int W> struct Backward {
     static int go(const BalArgs& a, cudaStream_t st) {
-        const int tok = THREADS / G;
-        const int grid = std::max(1, std::min((a.T + tok - 1) / tok, 8 * num_sms()));
-        MOE_LAUNCH((balance_bwd_kernel<G, R>), grid, THREADS, 0, st, a);
+        MOE_LAUNCH((balance_bwd_kernel<G, R, W>), (a.T + a.chunk - 1) / a.chunk, THREADS, 0, st, a);
         return MOE_OK;
     }
 };
 
-int n_chunks(const moe_balance_config& c) { return (c.T + CHUNK - 1) / CHUNK; }
+size_t rec_bytes(const moe_balance_config& c) { return align_up((size_t)(n_chunks(c) + c.S) * rec_floats(c.E) * 4); }
 
 BalArgs bal_args(const moe_balance_config& c) {
     BalArgs a = {};
-    a.T = c.T; a.E = c.E; a.k = c.k; a.S = c.S; a.nchunk = n_chunks(c);
+    a.T = c.T; a.E = c.E; a.k = c.k; a.S = c.S; a.chunk = chunk_of(c);
     a.bcoef = c.balance_coef; a.zcoef = c.z_coef;
     a.inv_tau = c.temperature > 0.f ? 1.f / c.temperature : 1.f;
     a.status = device_status_ptr();
@@ -334,7 +412,7 @@ BalArgs bal_args(const moe_balance_config& c) {
 }  // namespace
 
 size_t balance_ws_bytes(const moe_balance_config& c) {
-    return align_up((size_t)(n_chunks(c) + c.S) * rec_floats(c.E) * 4) + align_up((size_t)c.S * 12);
+    return rec_bytes(c) + align_up((size_t)c.S * 12) + 256;
 }
 
 int launch_balance_loss(const moe_balance_config& c, const float* logits, const int32_t* topk,
@@ -344,11 +422,10 @@ int launch_balance_loss(const moe_balance_config& c, const float* logits, const 
     a.logits = logits; a.topk = topk; a.seq = seq; a.loss = loss; a.counts = counts; a.pbar = pbar;
     a.gw = grad_w;
     a.rec = static_cast<float*>(ws);
-    a.seqsum = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) +
-                                        align_up((size_t)(n_chunks(c) + c.S) * rec_floats(c.E) * 4));
+    a.seqsum = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + rec_bytes(c));
+    a.ticket = reinterpret_cast<unsigned*>(static_cast<uint8_t*>(ws) + rec_bytes(c) + align_up((size_t)c.S * 12));
     if (const int r = by_experts<Partial>(c.E, a, st)) return r;
-    MOE_LAUNCH(balance_sequence_kernel, c.S, THREADS, 0, st, a);
-    MOE_LAUNCH(balance_total_kernel, 1, THREADS, 0, st, a);
+    MOE_LAUNCH(balance_sequence_kernel, c.S, SEQ_THREADS, (size_t)seq_groups(c.E) * (2 * c.E + 2) * 4, st, a);
     return MOE_OK;
 }
 
