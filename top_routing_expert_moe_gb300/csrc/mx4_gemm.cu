@@ -4,25 +4,32 @@
 //   u[r, n] = sum_i x[r, i] W_e[n, i],  x and W e2m1 codes times 2^(s - 127) per
 //   32 elements along i;  out = u, silu(u), or silu(g) u with g from a second W.
 //
-// A persistent kernel like the bf16 grouped GEMM (gemm_tc.cu): a CTA pair takes
-// 256 rows x 256 accumulator columns, warp-specialised:
-//   warp 0      TMA producer: per stage of 256 elements, 128 bytes a row, this
-//               CTA's 128 rows of x, its 128 rows of W (for SwiGLU the even CTA's
-//               are the gate's, the odd CTA's the up matrix's) and the scale tiles:
-//               its rows' and all 256 columns'.
-//   warp 1      the even CTA's thread copies the stage's scale tiles to tensor
-//               memory (tcgen05.cp, 32 lanes x 16 bytes, to all four lane
-//               quarters) and issues the block-scaled MMAs, 64 elements each.
-//   warps 2-9   epilogue: activation, rounding, TMA stores of 32 x 64-byte boxes.
+// A persistent kernel like the bf16 grouped GEMM (gemm_tc.cu).  A CTA pair takes
+// 256 rows x 256 accumulator columns (a single CTA 128 x 256 where segments are
+// short), warp-specialised:
+//   warp 0       TMA producer: per stage of 256 elements, 128 bytes a row, this CTA's
+//                128 rows of x and its 128 rows of W (for SwiGLU the even CTA's are
+//                the gate's, the odd CTA's the up matrix's).
+//   warp 1       the even CTA's issues the block-scaled MMAs, 64 elements each.
+//   warps 2-9    epilogue: activation, rounding, TMA stores of 32-row x 128-byte boxes.
+//   warps 10-13  scale tiles: to shared memory by cp.async, then to tensor memory.
 //
-// Tensor memory: 512 columns = two accumulators of 256 that overlap in 32, and
-// 24 columns of scales.  A tile's epilogue drains the overlapping columns first;
-// the next tile's MMAs start as soon as it has.
+// What it costs (8192 x 4096 x 8192, us): MMAs alone 74; with the epilogue's stores,
+// the loads and the scales 95.  Before the issuing warp stayed together (one thread
+// of a divergent branch moved every operand to a uniform register first) the same
+// stages took 131: at 4 bits a stage's MMAs last 512 cycles, so the issuing thread's
+// instructions and every wait on its way count.  Scales by tcgen05.cp from the stage
+// (six of 512 bytes) cost 1 % more, but the three TMA loads that bring them cost 12 %:
+// two loads a stage is what the producer can issue in the time of its MMAs.
+//
+// Tensor memory: two accumulators of 256 columns that overlap in 128, and buffers of
+// 24 columns of scales.  A tile's epilogue takes the overlapping columns to registers
+// first; the next tile's MMAs start as soon as it has.
 //
 // Codes are K-major with 128-byte swizzle, so a step of 64 elements (32 bytes)
 // advances the descriptor as a bf16 step of 16 does.  A scale tile (128 rows x 4
-// blocks, 512 bytes) is stored as tcgen05.cp takes it: row r's four bytes are
-// word r / 32 of the 16 bytes of lane r % 32.
+// blocks, 512 bytes) holds row r's four bytes as word r / 32 of the 16 bytes of lane
+// r % 32, which is how tensor memory holds them, once in each lane quarter.
 #include <cuda.h>
 
 #include <algorithm>
@@ -41,32 +48,35 @@ constexpr int BN = 256;                    // accumulator columns per tile (SwiG
 constexpr int BKB = 128;                   // bytes of a row per stage: 256 elements
 constexpr int A_BYTES = BM * BKB;
 constexpr int SF_TILE = 512;               // scale bytes of 128 rows x 128 elements
+constexpr int SF_SLOT = 6 * SF_TILE;       // a stage's: two tiles of x, four of W
+constexpr int SF_AHEAD = 4, SF_SLOTS = SF_AHEAD + 1;
 constexpr int NUM_EPI_WARPS = 8;
-constexpr int NTHREADS = 64 + 32 * NUM_EPI_WARPS;
+constexpr int NUM_SF_WARPS = 4;           // one per lane quarter of tensor memory
+constexpr int NTHREADS = 64 + 32 * (NUM_EPI_WARPS + NUM_SF_WARPS);
 constexpr int STAGING_BYTES = NUM_EPI_WARPS * 4096;
 constexpr int CTRL_BYTES = 1024;
 constexpr int TMEM_COLS = 512;
-constexpr int ACC1 = 224;                  // second accumulator's first column (columns 224-255 overlap)
-constexpr int SFA_COL = 480, SFB_COL = 488;
+constexpr int ACC1 = 128;                  // second accumulator's first column (columns 128-255 overlap)
+constexpr int SF_COL = 384, SF_COLS = 24;  // buffers of 24 columns: 8 of x's scales, 16 of W's
 constexpr int RASTER_ROWS = 4096;          // rows of x that pass over an expert's weights together
 
 template <int CG> struct Ring {            // CG CTAs a tile: stages and their bytes per CTA
     static constexpr int B_ROWS = BN / CG;
-    static constexpr int SFA_OFF = A_BYTES + B_ROWS * BKB;
-    static constexpr int SFB_OFF = SFA_OFF + 2 * SF_TILE;
-    static constexpr int BYTES = SFB_OFF + 4 * SF_TILE;            // a multiple of 1024
+    static constexpr int BYTES = A_BYTES + B_ROWS * BKB;
     static constexpr int STAGES = CG == 1 ? 3 : 5;
-    static constexpr int SMEM = 1024 + STAGES * BYTES + STAGING_BYTES + CTRL_BYTES;
+    static constexpr int SF_BUFS = STAGES;               // see the scale warps
+    static constexpr int SMEM = 1024 + STAGES * BYTES + STAGING_BYTES + SF_SLOTS * SF_SLOT + CTRL_BYTES;
 };
 static_assert(Ring<1>::BYTES % 1024 == 0 && Ring<2>::BYTES % 1024 == 0, "128B swizzle atoms");
 static_assert(Ring<1>::SMEM <= 232448 && Ring<2>::SMEM <= 232448, "227 KB of dynamic shared memory");
 
 struct Mx4Params {
-    CUtensorMap tmA, tmB0, tmB1, tmSA, tmSB0, tmSB1, tmO;
+    CUtensorMap tmA, tmB0, tmB1, tmO;
+    const uint4 *sa, *sb0, *sb1;           // scale tiles of x, and of the accumulator's two halves' W
     const int32_t* offsets;
     int* status;
     int64_t rows;
-    int E, K, N, n_blocks, act, f32;
+    int E, K, N, n_blocks, act;
 };
 
 __device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr) {
@@ -75,12 +85,6 @@ __device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr) {
     d |= (uint64_t)(1024 >> 4) << 32;      // 8-row groups
     d |= (uint64_t)1 << 46;                // descriptor version
     d |= (uint64_t)2 << 61;                // 128-byte swizzle
-    return d;
-}
-__device__ __forceinline__ uint64_t desc_scales(uint32_t saddr) {   // 32 x 16 bytes, no swizzle
-    uint64_t d = (uint64_t)((saddr & 0x3FFFFu) >> 4);
-    d |= (uint64_t)(128 >> 4) << 32;       // 8 rows of 16 bytes
-    d |= (uint64_t)1 << 46;
     return d;
 }
 // kind::mxf4: e2m1 x e2m1, scales of 8 exponent bits for 32 elements; `half` picks the
@@ -93,6 +97,18 @@ __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* v) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
     uint32_t r[32];
     asm volatile(
@@ -110,25 +126,36 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
 }
 
 template <int CG>
-__device__ __forceinline__ void mma_mx4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
-                                        uint32_t sfb, uint32_t accumulate) {
+__device__ __forceinline__ void mma_mx4(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc,
+                                        uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
     if constexpr (CG == 1)
         asm volatile(
-            "{\n.reg .pred p;\nsetp.ne.b32 p, %6, 0;\n"
-            "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(d),
-            "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate));
+            "{\n.reg .pred p;\n.reg .b64 da, db;\nsetp.ne.b32 p, %7, 0;\nmov.b64 da, {%1, %3};\nmov.b64 db, {%2, %3};\n"
+            "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], da, db, %4, [%5], [%6], p;\n}" ::"r"(d),
+            "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate));
     else
         asm volatile(
-            "{\n.reg .pred p;\nsetp.ne.b32 p, %6, 0;\n"
-            "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(d),
-            "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate));
+            "{\n.reg .pred p;\n.reg .b64 da, db;\nsetp.ne.b32 p, %7, 0;\nmov.b64 da, {%1, %3};\nmov.b64 db, {%2, %3};\n"
+            "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], da, db, %4, [%5], [%6], p;\n}" ::"r"(d),
+            "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate));
 }
-template <int CG>
-__device__ __forceinline__ void copy_scales(uint32_t taddr, uint64_t sdesc) {
-    if constexpr (CG == 1)
-        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
-    else
-        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t p;
+    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+    return p;
+}
+// words of this warp's 32 lanes, from column taddr on
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint4 (&v)[2]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0].x),
+                 "r"(v[0].y), "r"(v[0].z), "r"(v[0].w), "r"(v[1].x), "r"(v[1].y), "r"(v[1].z), "r"(v[1].w)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint4 (&v)[4]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(v[0].x), "r"(v[0].y), "r"(v[0].z), "r"(v[0].w), "r"(v[1].x), "r"(v[1].y), "r"(v[1].z), "r"(v[1].w),
+        "r"(v[2].x), "r"(v[2].y), "r"(v[2].z), "r"(v[2].w), "r"(v[3].x), "r"(v[3].y), "r"(v[3].z), "r"(v[3].w)
+        : "memory");
 }
 template <int CG>
 __device__ __forceinline__ void commit_all(uint32_t bar) {
@@ -150,9 +177,39 @@ __device__ __forceinline__ void commit_local(uint32_t bar) {
         asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
                      : "memory");
 }
+// Bounded wait (CG = 2: acquire at cluster scope), as mbar_wait, but the clock and the
+// flags are looked at every 1024 tries only: a stage of these kernels lasts no longer
+// than one look at them.
 template <int CG>
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {
-    return CG == 1 ? mbar_wait(bar, parity, abort_flag, status) : mbar_wait_cl(bar, parity, abort_flag, status);
+    unsigned long long t0 = 0;
+    for (uint32_t it = 1;; ++it) {
+        if (CG == 1 ? mbar_try(bar, parity) : mbar_try_cl(bar, parity)) return true;
+        if ((it & 1023) == 0) {
+            if (*abort_flag) return false;
+            const unsigned long long now = gtimer();
+            if (t0 == 0) t0 = now;
+            const bool late = now - t0 > WAIT_NS;
+            if (late) set_status(status, MOE_ERR_TIMEOUT);
+            if (late || timeout_pending(status)) {
+                *abort_flag = 1;
+                return false;
+            }
+        }
+    }
+}
+// a whole warp waits: one lane looks
+template <int CG>
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {
+    int got = 0;
+    if ((threadIdx.x & 31) == 0) got = wait_bar<CG>(bar, parity, abort_flag, status);
+    return __shfl_sync(0xffffffffu, got, 0) != 0;
+}
+// Arrival on the pair's even CTA.  What it announces (tensor memory written or read)
+// is ordered by the tcgen05 waits and fences around it, so it carries no release of
+// ordinary memory to the cluster, which costs more than a stage's MMAs.
+__device__ __forceinline__ void arrive_pair(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 template <int CG>
 __device__ __forceinline__ void drain_bar(uint32_t bar, uint32_t parity) {
@@ -181,28 +238,30 @@ __device__ __forceinline__ Mx4Tile decode(const int* offs, const int* prefix, in
     return {lo, offs[lo] + m * CG * BM, r / gm, mb - m * CG};
 }
 
-template <int CG>
+template <int CG, bool F32, bool DUAL>
 __global__ void __launch_bounds__(NTHREADS, 1) mx4_grouped_kernel(const __grid_constant__ Mx4Params P) {
     using R = Ring<CG>;
-    constexpr int S = R::STAGES;
+    constexpr int S = R::STAGES, SB = R::SF_BUFS;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t* ctrl = base + S * R::BYTES + STAGING_BYTES;
+    uint8_t* sf_smem = base + S * R::BYTES + STAGING_BYTES;
+    uint8_t* ctrl = sf_smem + SF_SLOTS * SF_SLOT;
     uint64_t* full = reinterpret_cast<uint64_t*>(ctrl);
     uint64_t* empty = full + 8;
     uint64_t* tfull = empty + 8;
     uint64_t* tempty = tfull + 1;
-    uint64_t* drain = tempty + 1;
+    uint64_t* sfull = tempty + 1;          // [SF_BUFS]
+    uint64_t* drain = sfull + 8;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     int* offs = reinterpret_cast<int*>(tmem_slot + 2);   // [E + 1]
     int* prefix = offs + 66;                             // [E + 1]
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const uint32_t rank = CG == 1 ? 0u : cluster_rank();
     const bool leader = rank == 0;
     const int unit = (int)blockIdx.x / CG, nunits = (int)gridDim.x / CG;
-    const bool dual = P.act == MOE_MX4_ACT_SWIGLU;
+    constexpr bool dual = DUAL;            // SwiGLU: gate and up
 
     if (tid == 0) {
         for (int s = 0; s < S; ++s) {
@@ -211,6 +270,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) mx4_grouped_kernel(const __grid_c
         }
         mbar_init(smem_u32(tfull), 1);
         mbar_init(smem_u32(tempty), CG * NUM_EPI_WARPS);
+        for (int b = 0; b < R::SF_BUFS; ++b) mbar_init(smem_u32(&sfull[b]), CG * NUM_SF_WARPS);
         mbar_init(smem_u32(drain), 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -256,8 +316,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) mx4_grouped_kernel(const __grid_c
 
     if (warp == 0 && lane == 0) {
         // ------------------------------------------------ TMA producer (each CTA)
-        const CUtensorMap* maps[7] = {&P.tmA, &P.tmB0, &P.tmSA, &P.tmSB0, &P.tmO, &P.tmB1, &P.tmSB1};
-        for (int i = 0; i < (dual ? 7 : 5); ++i)
+        const CUtensorMap* maps[4] = {&P.tmA, &P.tmB0, &P.tmO, &P.tmB1};
+        for (int i = 0; i < (dual ? 4 : 3); ++i)
             asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(maps[i])) : "memory");
         int it = 0;
         bool ok = live;
@@ -278,92 +338,215 @@ __global__ void __launch_bounds__(NTHREADS, 1) mx4_grouped_kernel(const __grid_c
                     else tma_load3_pair(m, dst, bar, c0, c1, c2);
                 };
                 ld(&P.tmA, st, kb * BKB, am, 0);
-                ld(&P.tmSA, st + R::SFA_OFF, 0, kb * 2, am / BM);
                 // 128 rows of W at a time: box rows of the weight maps
                 if (dual) {
                     if (CG == 1 || rank == 0) ld(&P.tmB0, st + A_BYTES, kb * BKB, t.nb * 128, t.e);
                     if (CG == 1 || rank == 1)
                         ld(&P.tmB1, st + A_BYTES + (CG == 1 ? 128 * BKB : 0), kb * BKB, t.nb * 128, t.e);
-                    const int nt = (P.N + 127) / 128;
-                    ld(&P.tmSB0, st + R::SFB_OFF, 0, kb * 2, t.e * nt + t.nb);
-                    ld(&P.tmSB1, st + R::SFB_OFF + 2 * SF_TILE, 0, kb * 2, t.e * nt + t.nb);
                 } else {
                     for (int h = 0; h < 2 / CG; ++h)
                         ld(&P.tmB0, st + A_BYTES + h * 128 * BKB, kb * BKB,
                            t.nb * BN + (CG == 1 ? h : (int)rank) * 128, t.e);
-                    const int nt = (P.N + 127) / 128;
-                    for (int h = 0; h < 2; ++h)
-                        ld(&P.tmSB0, st + R::SFB_OFF + h * 2 * SF_TILE, 0, kb * 2, t.e * nt + t.nb * 2 + h);
                 }
             }
         }
         if (leader)
             for (int i = max(0, it - S); i < it; ++i) drain_bar<CG>(smem_u32(&full[i % S]), (uint32_t)(i / S) & 1u);
-    } else if (warp == 1 && lane == 0 && leader) {
+    } else if (warp == 1 && leader) {
         // ------------------------------------------------ MMA issuer
-        int it = 0, tcount = 0;
+        // The warp stays together and elects a thread for the tcgen05 instructions: their
+        // operands then live in uniform registers, and a stage's four MMAs issue in less
+        // time than they take.  Descriptors differ in their low words only.
+        const uint32_t elected = elect_one();
+        const uint32_t a_lo = (uint32_t)desc_sw128(smem0), b_lo = (uint32_t)desc_sw128(smem0 + A_BYTES);
+        const uint32_t hi = (uint32_t)(desc_sw128(0) >> 32);
+        const uint32_t id0 = idesc_mx4(BM * CG, BN, 0), id1 = idesc_mx4(BM * CG, BN, 1);
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        const int tail = (P.K - (nk - 1) * 256 + 63) / 64;   // MMAs of a tile's last stage
+        int s = 0, tcount = 0;
+        uint32_t ph = 0;
         bool ok = live;
-        const uint32_t id[2] = {idesc_mx4(BM * CG, BN, 0), idesc_mx4(BM * CG, BN, 1)};
         for (int tix = unit; ok && tix < total; tix += nunits, ++tcount) {
             // the previous tile's epilogue is past the columns that both accumulators hold
             if (!wait_bar<CG>(smem_u32(tempty), ((uint32_t)tcount & 1u) ^ 1u, abort_flag, P.status)) break;
             tc_fence_after();
-            const uint32_t dt = tmem + (tcount & 1 ? ACC1 : 0);
-            uint32_t accum = 0;
-            for (int kb = 0; kb < nk; ++kb, ++it) {
-                const int s = it % S;
-                if (!wait_bar<CG>(smem_u32(&full[s]), (uint32_t)(it / S) & 1u, abort_flag, P.status)) {
+            const uint32_t dt = tm + (tcount & 1 ? ACC1 : 0);
+            for (int kb = 0; kb < nk; ++kb) {
+                if (!wait_bar<1>(smem_u32(&full[s]), ph, abort_flag, P.status) ||
+                    !wait_bar<1>(smem_u32(&sfull[s]), ph, abort_flag, P.status)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint32_t st = smem0 + s * R::BYTES;
+                __syncwarp();
+                if (elected) {
+                    const uint32_t al = a_lo + s * (R::BYTES >> 4), bl = b_lo + s * (R::BYTES >> 4);
+                    const uint32_t sf = tm + SF_COL + s * SF_COLS;
+                    const int steps = kb + 1 == nk ? tail : 4;
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    copy_scales<CG>(tmem + SFA_COL + k * 4, desc_scales(st + R::SFA_OFF + k * SF_TILE));
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        copy_scales<CG>(tmem + SFB_COL + k * 8 + h * 4,
-                                        desc_scales(st + R::SFB_OFF + (h * 2 + k) * SF_TILE));
+                    for (int ks = 0; ks < 4; ++ks)
+                        if (ks < steps)
+                            mma_mx4<CG>(dt, al + ks * 2, bl + ks * 2, hi, ks & 1 ? id1 : id0, sf + (ks >> 1) * 4,
+                                        sf + 8 + (ks >> 1) * 8, kb > 0 || ks > 0);
+                    commit_all<CG>(smem_u32(&empty[s]));
                 }
-                const int steps = min(4, (P.K - kb * 256 + 63) / 64);   // past K the codes are 0
-                for (int ks = 0; ks < steps; ++ks) {
-                    mma_mx4<CG>(dt, desc_sw128(st + ks * 32), desc_sw128(st + A_BYTES + ks * 32), id[ks & 1],
-                                tmem + SFA_COL + (ks >> 1) * 4, tmem + SFB_COL + (ks >> 1) * 8, accum);
-                    accum = 1;
+                __syncwarp();
+                if (++s == S) {
+                    s = 0;
+                    ph ^= 1u;
                 }
-                commit_all<CG>(smem_u32(&empty[s]));
             }
             if (!ok) break;
-            commit_all<CG>(smem_u32(tfull));
+            if (elected) commit_all<CG>(smem_u32(tfull));
+            __syncwarp();
         }
-        commit_local<CG>(smem_u32(drain));
-        drain_bar<CG>(smem_u32(drain), 0);
+        if (elected) {
+            commit_local<CG>(smem_u32(drain));
+            drain_bar<CG>(smem_u32(drain), 0);
+        }
+        __syncwarp();
+    } else if (warp >= 2 + NUM_EPI_WARPS) {
+        // ------------------------------------------------ scales (each CTA: its rows' and all columns')
+        // The four warps copy a stage's six tiles to shared memory, four stages ahead
+        // (cp.async; a tile is one warp's 32 x 16 bytes), and write them to tensor
+        // memory, each its lane quarter, as the MMA reads every quarter's copy.  A
+        // buffer there is free once the MMAs SF_BUFS = STAGES stages back have read
+        // it, which is when that stage's "empty" barrier completes.  (With more buffers
+        // than stages the barrier could pass that phase and the next unseen.)
+        const int w = warp - 2 - NUM_EPI_WARPS;
+        const uint32_t ta = tmem + ((uint32_t)((warp & 3) * 32) << 16) + SF_COL;
+        const uint32_t bar0 = CG == 1 ? smem_u32(&sfull[0]) : mapa_shared(smem_u32(&sfull[0]), 0);
+        const uint32_t sf0 = smem_u32(sf_smem) + lane * 16;
+        const int kt = (P.K + 127) / 128, nt = (P.N + 127) / 128, at = (int)((P.rows + BM - 1) / BM);
+        const int stages = unit < total ? ((total - 1 - unit) / nunits + 1) * nk : 0;
+        // this warp's tiles: w (0, 1: x's; 2, 3: the first k tile's W halves), and for the
+        // first two warps the second k tile's W halves
+        int f_tix = unit, f_kb = 0, f_slot = 0;         // the next stage to copy
+        const uint4 *pa = nullptr, *pb = nullptr;       // its tile's first words (k tile 0), null past the end
+        auto locate = [&]() {
+            if (f_tix >= total) return;
+            const Mx4Tile t = decode<CG>(offs, prefix, P.E, P.n_blocks, f_tix);
+            const int ra = t.m0 / BM + (int)rank;
+            auto wt = [&](int h) -> const uint4* {      // half h of the accumulator's columns
+                const int r = dual ? t.nb : t.nb * 2 + h;
+                return r < nt ? (dual && h ? P.sb1 : P.sb0) + ((int64_t)t.e * nt + r) * kt * 32 + lane : nullptr;
+            };
+            pa = w >= 2 ? wt(w - 2) : ra < at ? P.sa + (int64_t)ra * kt * 32 + lane : nullptr;
+            pb = w < 2 ? wt(w) : nullptr;
+        };
+        locate();
+        auto copy = [&]() {                             // one group a stage, empty ones past the last
+            if (f_tix < total) {
+                auto piece = [&](const uint4* p, int k, int tile) {
+                    const bool on = p && k < kt;
+                    const uint4* src = on ? p + k * 32 : P.sa;
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sf0 + f_slot * SF_SLOT + tile * SF_TILE),
+                                 "l"(src), "r"(on ? 16 : 0)
+                                 : "memory");
+                };
+                piece(pa, f_kb * 2 + (w == 1), w);
+                if (w < 2) piece(pb, f_kb * 2 + 1, 4 + w);
+                f_slot = f_slot + 1 == SF_SLOTS ? 0 : f_slot + 1;
+                if (++f_kb == nk) {
+                    f_kb = 0;
+                    f_tix += nunits;
+                    locate();
+                }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        for (int i = 0; i < SF_AHEAD; ++i) copy();
+        int slot = 0, buf = 0;
+        uint32_t ph = 1;                                // of the "empty" barrier looked at
+        bool ok = live;
+        for (int it = 0; it < stages; ++it) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(SF_AHEAD - 1) : "memory");
+            asm volatile("bar.sync 1, 128;" ::: "memory");   // every warp's tiles are there
+            uint4 a[2], b[4];
+            const uint8_t* t = sf_smem + slot * SF_SLOT + lane * 16;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) a[k] = *reinterpret_cast<const uint4*>(t + k * SF_TILE);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) b[k] = *reinterpret_cast<const uint4*>(t + (2 + k) * SF_TILE);
+            copy();      // into the slot that the previous stage's reads, before the barrier, left
+            ok = ok && warp_wait<1>(smem_u32(&empty[buf]), ph, abort_flag, P.status);
+            if (ok) {    // (a warp that gave up still joins the barriers above)
+                tc_fence_after();
+                tmem_st8(ta + buf * SF_COLS, a);
+                tmem_st16(ta + buf * SF_COLS + 8, b);
+                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if constexpr (CG == 1) mbar_arrive(bar0 + buf * 8);
+                    else arrive_pair(bar0 + buf * 8);
+                }
+            }
+            slot = slot + 1 == SF_SLOTS ? 0 : slot + 1;
+            if (++buf == SB) {
+                buf = 0;
+                ph ^= 1u;
+            }
+        }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
     } else if (warp >= 2) {
         // ------------------------------------------------ epilogue (each CTA, its 128 rows)
         const int qd = warp & 3, half = (warp - 2) / 4;
         const uint32_t bar_te = CG == 1 ? smem_u32(tempty) : mapa_shared(smem_u32(tempty), 0);
-        uint8_t* stg = base + S * R::BYTES + (warp - 2) * 4096;
-        int nst = 0;
-        // a 32-row x 64-byte box (64-byte swizzle): 32 bf16 or 16 fp32 columns
-        auto put = [&](const uint4 (&w)[4], int col, int row) {
-            uint8_t* buf = stg + (nst & 1) * 2048;
-            if (nst >= 2) {
-                if (lane == 0) bulk_wait_read<1>();
-                __syncwarp();
-            }
+        uint8_t* stg = base + S * R::BYTES + (warp - 2) * 4096 + lane * 128;
+        // 32 columns of this lane's row into piece `at` (16 bytes each, 128-byte swizzle)
+        // of the warp's 32-row x 128-byte staging box: bf16 half of it, fp32 all
+        auto stage_bf16 = [&](const float (&o)[32], int at) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                *reinterpret_cast<uint4*>(buf + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) = w[j];
+            for (int j = 0; j < 4; ++j) {
+                uint32_t p[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    __nv_bfloat162 b2 = __floats2bfloat162_rn(o[8 * j + 2 * k], o[8 * j + 2 * k + 1]);
+                    p[k] = *reinterpret_cast<uint32_t*>(&b2);
+                }
+                *reinterpret_cast<uint4*>(stg + (((at + j) ^ (lane & 7)) << 4)) = make_uint4(p[0], p[1], p[2], p[3]);
+            }
+        };
+        auto stage_f32 = [&](const float (&o)[32]) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                *reinterpret_cast<float4*>(stg + ((j ^ (lane & 7)) << 4)) =
+                    make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+        };
+        auto box_free = [&]() {                          // the last box has been read
+            if (lane == 0) bulk_wait_read<0>();
+            __syncwarp();
+        };
+        auto send = [&](int col, int row) {
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-                tma_store3(&P.tmO, smem_u32(buf), col, row, 0);
+                tma_store3(&P.tmO, smem_u32(stg), col, row, 0);
                 bulk_commit();
             }
-            ++nst;
         };
-        const int cpw = dual ? 2 : 4;                   // 32-column chunks of this warp
+        const bool silu = P.act == MOE_MX4_ACT_SILU;
+        // fp32 outputs take the exact form
+        auto act = [](float z) { return F32 ? silu_f(z) : silu_quick(z); };
+        // 64 neighbouring columns, in two halves of 32
+        auto store = [&](const float (&o)[2][32], int col, int row, bool valid) {
+            if (!valid || col >= P.N) return;
+            if constexpr (F32) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    if (col + 32 * i >= P.N) break;
+                    box_free();
+                    stage_f32(o[i]);
+                    send(col + 32 * i, row);
+                }
+            } else {
+                box_free();
+                stage_bf16(o[0], 0);
+                stage_bf16(o[1], 4);
+                send(col, row);
+            }
+        };
         int tcount = 0;
         for (int tix = unit; tix < total; tix += nunits, ++tcount) {
             const Mx4Tile t = decode<CG>(offs, prefix, P.E, P.n_blocks, tix);
@@ -371,66 +554,48 @@ __global__ void __launch_bounds__(NTHREADS, 1) mx4_grouped_kernel(const __grid_c
             const bool valid = (int)rank < t.valid;
             const int row = t.m0 + (int)rank * BM + qd * 32;
             const int col0 = t.nb * (dual ? 128 : BN);
-            const bool got = __all_sync(0xffffffffu, wait_bar<CG>(smem_u32(tfull), (uint32_t)tcount & 1u, abort_flag, P.status));
+            const bool got = warp_wait<CG>(smem_u32(tfull), (uint32_t)tcount & 1u, abort_flag, P.status);
             if (!got) break;
             tc_fence_after();
             const uint32_t ta = tmem + (buf ? ACC1 : 0) + ((uint32_t)(qd * 32) << 16);
-            // columns 224-255 of tensor memory are the first accumulator's last and the
-            // second's first: their warps drain them first
-            const bool owner = buf ? half == 0 : half == 1;
-            auto release = [&]() {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    if constexpr (CG == 1) mbar_arrive(bar_te);
-                    else mbar_arrive_remote(bar_te);
-                }
-            };
-            if (!owner) release();
-            for (int i = 0; i < cpw; ++i) {
-                const int c = half * cpw + (owner && !buf ? (i + cpw - 1) % cpw : i);
-                float v[32];
-                tmem_ld32(ta + c * 32, v);
-                if (dual) {
-                    float u[32];
-                    tmem_ld32(ta + 128 + c * 32, u);
+            // Columns 128-255 of tensor memory belong to both accumulators (the first's
+            // upper half, the second's lower): each warp takes its 64 of them to
+            // registers first, and releases them to the next tile's MMAs.
+            float v[2][32];
+            const int c = half * 64;
+            const uint32_t shared_cols = ta + (buf ? 0 : 128) + c, own_cols = ta + (buf ? 128 : 0) + c;
+            tmem_ld32(shared_cols, v[0]);
+            tmem_ld32(shared_cols + 32, v[1]);
+            tmem_wait_ld();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if constexpr (CG == 1) mbar_arrive(bar_te);
+                else arrive_pair(bar_te);
+            }
+            if constexpr (DUAL) {                       // gate: columns 0-127, up: 128-255
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {           // 16 columns: registers are short
+                    float o[16], (&w)[32] = v[i >> 1];
+                    const int k = (i & 1) * 16;
+                    tmem_ld16(own_cols + 16 * i, o);
                     tmem_wait_ld();
-                    if (owner && i == 0) release();
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = (P.f32 ? silu_f(v[j]) : silu_quick(v[j])) * u[j];
-                } else {
-                    tmem_wait_ld();
-                    if (owner && i == 0) release();
-                    if (P.act == MOE_MX4_ACT_SILU)
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) v[j] = P.f32 ? silu_f(v[j]) : silu_quick(v[j]);
+                    for (int j = 0; j < 16; ++j) w[k + j] = buf ? act(w[k + j]) * o[j] : act(o[j]) * w[k + j];
                 }
-                const int col = col0 + c * 32;
-                if (!valid || col >= P.N) continue;
-                if (P.f32) {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        if (col + h * 16 >= P.N) continue;
-                        uint4 w[4];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            w[j] = make_uint4(__float_as_uint(v[h * 16 + 4 * j]), __float_as_uint(v[h * 16 + 4 * j + 1]),
-                                              __float_as_uint(v[h * 16 + 4 * j + 2]), __float_as_uint(v[h * 16 + 4 * j + 3]));
-                        put(w, col + h * 16, row);
+                store(v, col0 + c, row, valid);
+            } else {
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {
+                    if (h) {
+                        tmem_ld32(own_cols, v[0]);
+                        tmem_ld32(own_cols + 32, v[1]);
+                        tmem_wait_ld();
                     }
-                } else {
-                    uint4 w[4];
+                    if (silu)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        uint32_t p[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            __nv_bfloat162 b2 = __floats2bfloat162_rn(v[8 * j + 2 * k], v[8 * j + 2 * k + 1]);
-                            p[k] = *reinterpret_cast<uint32_t*>(&b2);
-                        }
-                        w[j] = make_uint4(p[0], p[1], p[2], p[3]);
-                    }
-                    put(w, col, row);
+                        for (int i = 0; i < 64; ++i) v[i >> 5][i & 31] = act(v[i >> 5][i & 31]);
+                    store(v, col0 + ((buf == 0) == (h == 0) ? 128 : 0) + c, row, valid);
                 }
             }
         }
@@ -462,19 +627,10 @@ int codes_map(CUtensorMap* m, const void* p, int64_t rows, int sets, int K) {
     const uint32_t box[3] = {BKB, BM, 1};
     return encode_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, p, 3, dims, st, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
-// scale tiles [row tiles, K tiles, 128 words]: boxes of two K tiles
-int scales_map(CUtensorMap* m, const void* p, int64_t row_tiles, int K) {
-    const uint64_t kt = ((uint64_t)K + 127) / 128;
-    const uint64_t dims[3] = {SF_TILE / 4, kt, (uint64_t)row_tiles};
-    const uint64_t st[2] = {SF_TILE, SF_TILE * kt};
-    const uint32_t box[3] = {SF_TILE / 4, 2, 1};
-    return encode_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, p, 3, dims, st, box, CU_TENSOR_MAP_SWIZZLE_NONE);
-}
-
-template <int CG>
-int launch_mx4(const moe_mx4_product_config& c, const Mx4Params& P, cudaStream_t st) {
+template <int CG, bool F32, bool DUAL>
+int launch_mx4_t(const moe_mx4_product_config& c, const Mx4Params& P, cudaStream_t st) {
     static bool attr_done[64] = {};
-    if (const int r = smem_attr_once(mx4_grouped_kernel<CG>, Ring<CG>::SMEM, attr_done)) return r;
+    if (const int r = smem_attr_once(mx4_grouped_kernel<CG, F32, DUAL>, Ring<CG>::SMEM, attr_done)) return r;
     const int64_t mt = (c.rows / BM + CG - 1) / CG + (CG - 1) * c.E;   // a segment may round up
     const int64_t units = std::max<int64_t>(1, std::min<int64_t>(mt * P.n_blocks, num_sms() / CG));
     cudaLaunchConfig_t cfg = {};
@@ -492,13 +648,20 @@ int launch_mx4(const moe_mx4_product_config& c, const Mx4Params& P, cudaStream_t
     cfg.attrs = attr;
     cfg.numAttrs = CG == 2 ? 2 : 1;
     void* args[] = {const_cast<Mx4Params*>(&P)};
-    const cudaError_t e = cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(mx4_grouped_kernel<CG>), args);
+    const cudaError_t e = cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(mx4_grouped_kernel<CG, F32, DUAL>), args);
     note_launch();
     if (e != cudaSuccess) {
         (void)cudaGetLastError();
         return MOE_ERR_CUDA;
     }
     return MOE_OK;
+}
+
+template <int CG>
+int launch_mx4(const moe_mx4_product_config& c, const Mx4Params& P, cudaStream_t st) {
+    const bool f32 = c.out_dtype == MOE_DTYPE_F32, dual = c.act == MOE_MX4_ACT_SWIGLU;
+    if (dual) return f32 ? launch_mx4_t<CG, true, true>(c, P, st) : launch_mx4_t<CG, false, true>(c, P, st);
+    return f32 ? launch_mx4_t<CG, true, false>(c, P, st) : launch_mx4_t<CG, false, false>(c, P, st);
 }
 
 }  // namespace
@@ -509,29 +672,30 @@ int launch_mx4_product(const moe_mx4_product_config& c, const void* xq, const vo
     Mx4Params P;
     memset(&P, 0, sizeof(P));
     const bool dual = c.act == MOE_MX4_ACT_SWIGLU;
-    const int64_t nt = (c.N + 127) / 128;
     MX4_TRY(codes_map(&P.tmA, xq, c.rows, 1, c.K));
-    MX4_TRY(scales_map(&P.tmSA, xs, (c.rows + 127) / 128, c.K));
     // the accumulator's first half is the gate's for SwiGLU
     MX4_TRY(codes_map(&P.tmB0, dual ? gq : wq, c.N, c.E, c.K));
-    MX4_TRY(scales_map(&P.tmSB0, dual ? gs : ws, nt * c.E, c.K));
-    if (dual) {
-        MX4_TRY(codes_map(&P.tmB1, wq, c.N, c.E, c.K));
-        MX4_TRY(scales_map(&P.tmSB1, ws, nt * c.E, c.K));
-    }
+    if (dual) MX4_TRY(codes_map(&P.tmB1, wq, c.N, c.E, c.K));
+    P.sa = static_cast<const uint4*>(xs);
+    P.sb0 = static_cast<const uint4*>(dual ? gs : ws);
+    P.sb1 = static_cast<const uint4*>(ws);
     const bool f32 = c.out_dtype == MOE_DTYPE_F32;
     const uint64_t es = f32 ? 4 : 2;
     const uint64_t dims[3] = {(uint64_t)c.N, (uint64_t)c.rows, 1};
     const uint64_t strides[2] = {c.N * es, c.N * es * c.rows};
-    const uint32_t box[3] = {(uint32_t)(64 / es), 32, 1};
+    const uint32_t box[3] = {(uint32_t)(128 / es), 32, 1};
     MX4_TRY(encode_map(&P.tmO, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, out, 3,
-                       dims, strides, box, CU_TENSOR_MAP_SWIZZLE_64B));
+                       dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B));
     P.offsets = offsets;
     P.status = device_status_ptr();
     P.rows = c.rows;
-    P.E = c.E; P.K = c.K; P.N = c.N; P.act = c.act; P.f32 = f32;
+    P.E = c.E; P.K = c.K; P.N = c.N; P.act = c.act;
     P.n_blocks = dual ? (c.N + 127) / 128 : (c.N + BN - 1) / BN;
-    return launch_mx4<1>(c, P, st);
+    // A pair's tile is 256 rows: it pays where an expert has two 128-row blocks or more
+    // (each CTA then reads half of W's tile): 4096 rows of 8 experts, K = 4096, N = 14336
+    // SwiGLU 163 us against 200; with one block an expert half the pair idles: 1024 rows
+    // 94 against 87 us.  The host knows the rows' bound only, 127 of it an expert's padding.
+    return c.rows >= (int64_t)(256 + 127) * c.E ? launch_mx4<2>(c, P, st) : launch_mx4<1>(c, P, st);
 }
 
 }  // namespace moe
