@@ -372,6 +372,7 @@ class MoELayer:
         self._grads = None
         self._inputs = None
         self._shared_w = None
+        self._mx4 = None
 
     def _shared_fwd(self, x):
         if self.cfg.f_shared <= 0:
@@ -398,6 +399,40 @@ class MoELayer:
                         self.act, self.y_perm, self.ws, stream, shared=sh)
         moe_combine(c, self.y_perm, self.slot_of, self.gate, self.out, stream, shared=sh)
         self._inputs = (x, W_r, W_up, W_gate, W_down, bias)
+        return self.out
+
+    def forward_mx4(self, x, W_r, experts, bias=None, noise=None, token_mask=None, stream=None):
+        """The forward with both GEMMs' operands in microscaled 4-bit numbers:
+        ``experts`` (an MX4Experts) holds the weights, the rows are quantised on the
+        way.  bf16 layers without shared experts; there is no backward of it."""
+        c = self.cfg
+        if c.dtype != BF16 or c.f_shared > 0:
+            raise ValueError("forward_mx4 needs a bf16 layer without shared experts")
+        if (experts.gate is not None) != (c.ffn == SWIGLU):
+            raise ValueError("a gate matrix is required iff cfg.ffn is SWIGLU")
+        if experts.up.shape != (c.E, c.f, c.d) or experts.down.shape != (c.E, c.d, c.f):
+            raise ValueError("the experts' shapes are not this layer's")
+        if self._mx4 is None:
+            R, dev = self.rows_cap, self.out.device
+            self._mx4 = (MX4Tensor((R, c.d), dev), MX4Tensor((R, c.f), dev),
+                         MX4ProductConfig(R, c.d, c.f, c.E, MX4_ACT_SWIGLU if c.ffn == SWIGLU else MX4_ACT_SILU),
+                         MX4ProductConfig(R, c.f, c.d, c.E))
+        xq, aq, first, second = self._mx4
+        up, down, gate = experts.up, experts.down, experts.gate
+        self._inputs = None
+        moe_route(c, x, W_r, bias, noise, token_mask, self.logits, self.topk_idx, self.gate,
+                  self.counts, self.stats, self.ws, stream)
+        moe_permute(c, x, self.topk_idx, self.x_perm, self.perm_token, self.slot_of, self.kept,
+                    self.offsets, self.stats, self.ws, stream)
+        used = self.offsets[c.E:]
+        mx4_quantize(self.x_perm, used, xq, stream)
+        moe_mx4_grouped_product(first, xq.codes, xq.scales, self.offsets, up.codes, up.scales,
+                                gate.codes if gate else None, gate.scales if gate else None,
+                                self.act, stream)
+        mx4_quantize(self.act, used, aq, stream)
+        moe_mx4_grouped_product(second, aq.codes, aq.scales, self.offsets, down.codes, down.scales,
+                                None, None, self.y_perm, stream)
+        moe_combine(c, self.y_perm, self.slot_of, self.gate, self.out, stream)
         return self.out
 
     def grads(self):

@@ -21,7 +21,7 @@ __all__ = ["GATE_NONE", "GATE_CHANNEL", "GATE_TOKEN", "GATE_FULL", "NormConfig",
            "BalanceLoss", "MX4_ACT_NONE", "MX4_ACT_SILU", "MX4_ACT_SWIGLU", "MX4Tensor",
            "mx4_scale_bytes", "moe_mx4_quantize", "moe_mx4_quantize_weight", "moe_mx4_dequantize",
            "mx4_quantize", "mx4_quantize_weight", "MX4ProductConfig", "check_mx4_product_config",
-           "moe_mx4_grouped_product", "MX4Product"]
+           "moe_mx4_grouped_product", "MX4Product", "MX4Experts", "MoEBlock"]
 
 GATE_NONE, GATE_CHANNEL, GATE_TOKEN, GATE_FULL = 0, 1, 2, 3
 
@@ -351,3 +351,69 @@ class MX4Product:
         moe_mx4_grouped_product(c, self.xq.codes, self.xq.scales, offsets, w.codes, w.scales,
                                 wg.codes if wg else None, wg.scales if wg else None, self.out, stream)
         return self.out
+
+
+class MX4Experts:
+    """A layer's expert weights in 4 bits, for ``MoELayer.forward_mx4``: quantised
+    once from W_up, W_gate (SwiGLU) [E, d, f] and W_down [E, f, d]."""
+
+    def __init__(self, W_up, W_down, W_gate=None, stream=None):
+        self.up = mx4_quantize_weight(W_up, stream)
+        self.down = mx4_quantize_weight(W_down, stream)
+        self.gate = mx4_quantize_weight(W_gate, stream) if W_gate is not None else None
+
+
+# ----------------------------------------------------------------- the block
+class MoEBlock:
+    """The layer in its place on the residual stream:
+
+        z = w_in x / rms(x);  u = MoE(z);  n = w_out u / rms(u)  (or u)
+        x' = res_scale x + out_scale g n,   and the router's balance loss
+
+    ``weights`` of forward(): w_in [d] fp32, W_r, W_up, W_down and, where the
+    configuration has them, W_gate, bias, w_out [d] fp32, gate (see NormConfig),
+    shared (as MoELayer.forward takes it).  backward() returns the gradients by
+    the same names with a "d" before (dx too)."""
+
+    def __init__(self, cfg, post_norm=0, gate=GATE_NONE, eps=1e-6, res_scale=1.0, out_scale=1.0,
+                 sequences=1, balance_coef=0.01, z_coef=0.0, device="cuda"):
+        c = cfg
+        self.layer = _moe.MoELayer(cfg, device)
+        self.enter = BlockNorm(NormConfig(c.T, c.d, c.dtype, leave=0, eps=eps), device)
+        self.leave = BlockNorm(NormConfig(c.T, c.d, c.dtype, post_norm=post_norm, enter=0, gate=gate,
+                                          eps=eps, res_scale=res_scale, out_scale=out_scale), device)
+        self.balance = BalanceLoss(BalanceConfig(c.T, c.E, c.k, sequences, balance_coef, z_coef,
+                                                 c.temperature), device)
+        self._saved = None
+
+    def forward(self, x, weights, seq_offsets=None, noise=None, token_mask=None, stream=None):
+        """(x', loss [3]): the stream after the block and the router's losses."""
+        w = weights
+        z = self.enter.forward(x, w_pre=w["w_in"], stream=stream)[1]
+        u = self.layer.forward(z, w["W_r"], w["W_up"], w["W_down"], w.get("W_gate"), w.get("bias"),
+                               noise, token_mask, stream, shared=w.get("shared"))
+        x_out = self.leave.forward(x, u=u, w_post=w.get("w_out"), gate=w.get("gate"), stream=stream)[0]
+        loss = self.balance.forward(self.layer.logits, self.layer.topk_idx, seq_offsets, stream)
+        self._saved = (x, u, w)
+        return x_out, loss
+
+    def forward_mx4(self, x, weights, experts: MX4Experts, token_mask=None, stream=None):
+        """x' with the experts in 4 bits (serving: no loss, no backward)."""
+        w = weights
+        z = self.enter.forward(x, w_pre=w["w_in"], stream=stream)[1]
+        u = self.layer.forward_mx4(z, w["W_r"], experts, w.get("bias"), token_mask=token_mask, stream=stream)
+        self._saved = None
+        return self.leave.forward(x, u=u, w_post=w.get("w_out"), gate=w.get("gate"), stream=stream)[0]
+
+    def backward(self, dx_out, dloss=None, stream=None):
+        """Gradients of <dx_out, x'> + dloss (balance + z) (dloss None: 1)."""
+        if self._saved is None:
+            raise RuntimeError("backward() needs a forward() first")
+        x, u, w = self._saved
+        # the leave norm's gradients do not depend on x': it is not normalised there
+        gl = self.leave.backward(self.leave.x_out, dx_out=dx_out, u=u, w_post=w.get("w_out"),
+                                 gate=w.get("gate"), stream=stream)
+        g = dict(self.layer.backward(gl["du"], stream, dlogits_aux=self.balance.backward(dloss, stream)))
+        ge = self.enter.backward(x, dx_out=gl["dx"], dz=g["dx"], w_pre=w["w_in"], stream=stream)
+        g.update(dx=ge["dx"], dw_in=ge["dw_pre"], dw_out=gl["dw_post"], dgate=gl["dgate"])
+        return g
