@@ -39,10 +39,11 @@ __device__ __forceinline__ float row_sum(float v, float* buf) {
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
-// Six sums at once.  The first three steps of the butterfly halve the values a lane
-// carries as they double the lanes it stands for, so that four lanes end with one
-// value's sum: 9 shuffles instead of 30.
-__device__ __forceinline__ void row_sums6(float (&s)[6], float* buf) {
+// Six sums at once, in two steps around a CTA barrier.  Within a warp the first
+// three steps of the butterfly halve the values a lane carries as they double the
+// lanes it stands for, so that four lanes end with one value's sum: 9 shuffles
+// instead of 30.  Then every warp adds the warps' sums from shared memory.
+__device__ __forceinline__ float warp_sums6(const float (&s)[6]) {
     const int lane = threadIdx.x & 31;
     const bool b4 = lane & 16, b3 = lane & 8, b2 = lane & 4;
     float a[4], b[2], v;
@@ -55,20 +56,33 @@ __device__ __forceinline__ void row_sums6(float (&s)[6], float* buf) {
         b[i] = (b3 ? a[i + 2] : a[i]) + __shfl_xor_sync(0xffffffffu, b3 ? a[i] : a[i + 2], 8);
     v = (b2 ? b[1] : b[0]) + __shfl_xor_sync(0xffffffffu, b2 ? b[0] : b[1], 4);
     v += __shfl_xor_sync(0xffffffffu, v, 2);
-    v += __shfl_xor_sync(0xffffffffu, v, 1);                 // the sum of value lane / 4
-    int step = 4;
+    v += __shfl_xor_sync(0xffffffffu, v, 1);
+    return v;                                                // the sum of value lane / 4
+}
+__device__ __forceinline__ void put_sums6(float v, float* buf) {
+    const int lane = threadIdx.x & 31;
+    if ((lane & 3) == 0) buf[(threadIdx.x >> 5) * 8 + (lane >> 2)] = v;
+}
+__device__ __forceinline__ void get_sums6(float (&s)[6], const float* buf) {
+    const int lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+    float v = 0.f;
+    for (int w = lane >> 3; w < nw; w += 4) v += buf[w * 8 + (lane & 7)];
+    v += __shfl_xor_sync(0xffffffffu, v, 8);
+    v += __shfl_xor_sync(0xffffffffu, v, 16);                // value lane % 8
+#pragma unroll
+    for (int i = 0; i < 6; ++i) s[i] = __shfl_sync(0xffffffffu, v, i);
+}
+// in one call; rows of a warp need no barrier
+__device__ __forceinline__ void row_sums6(float (&s)[6], float* buf) {
+    const float v = warp_sums6(s);
     if (blockDim.x > 32) {
-        if ((lane & 3) == 0) buf[(threadIdx.x >> 5) * 8 + (lane >> 2)] = v;
+        put_sums6(v, buf);
         __syncthreads();
-        const int nw = blockDim.x >> 5;
-        v = 0.f;
-        for (int w = lane >> 3; w < nw; w += 4) v += buf[w * 8 + (lane & 7)];
-        v += __shfl_xor_sync(0xffffffffu, v, 8);
-        v += __shfl_xor_sync(0xffffffffu, v, 16);            // value lane % 8
-        step = 1;
+        get_sums6(s, buf);
+        return;
     }
 #pragma unroll
-    for (int i = 0; i < 6; ++i) s[i] = __shfl_sync(0xffffffffu, v, i * step);
+    for (int i = 0; i < 6; ++i) s[i] = __shfl_sync(0xffffffffu, v, i * 4);
 }
 
 // ---------------------------------------------------------------- rows read directly
@@ -347,18 +361,25 @@ template <typename T>
 __device__ __forceinline__ int part_of(int half) { return (threadIdx.x + half * blockDim.x) * (16 / (int)sizeof(T)); }
 template <typename T>
 __device__ __forceinline__ void take(const T* p, int d, f2 (&v)[RP]) {
-    constexpr int V = 16 / sizeof(T);
+    if constexpr (sizeof(T) == 2) {
+        // threads past the row's end read its last elements; sums and stores leave them out
+        const uint4 u = *reinterpret_cast<const uint4*>(p + min((int)threadIdx.x * RE, d - RE));
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-    for (int h = 0; h < RE / V; ++h) {
-        const int c = part_of<T>(h);
-        float f[V];
+        for (int i = 0; i < RP; ++i) v[i] = pk(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+    } else {
 #pragma unroll
-        for (int j = 0; j < V; ++j) f[j] = 0.f;
-        if (c < d) load16_f<T>(p + c, f);
-#pragma unroll
-        for (int j = 0; j < V / 2; ++j) v[h * V / 2 + j] = pk(f[2 * j], f[2 * j + 1]);
+        for (int h = 0; h < 2; ++h) {
+            const int c = part_of<T>(h);
+            const float4 f = c < d ? *reinterpret_cast<const float4*>(p + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+            v[2 * h] = pk(f.x, f.y);
+            v[2 * h + 1] = pk(f.z, f.w);
+        }
     }
 }
+// whether this thread's share counts in sums (fp32 shares past the end are zeros)
+template <typename T>
+__device__ __forceinline__ float live(int d) { return sizeof(T) == 4 || (int)threadIdx.x * RE < d ? 1.f : 0.f; }
 template <typename T>
 __device__ __forceinline__ void give(T* p, int d, const f2 (&v)[RP]) {
     constexpr int V = 16 / sizeof(T);
@@ -417,10 +438,11 @@ struct RowRing {
     __device__ __forceinline__ void wait(const RingArgs& a, int s, uint32_t ph) const {
         mbar_wait(bar0 + s * 8, ph, abort_flag, a.status);
     }
-    // before the row's last reduction: the next row's stage
-    __device__ __forceinline__ void wait_next(const RingArgs& a, int64_t t) const {
-        if (threadIdx.x < 32 && t + gridDim.x < a.n.T)
-            wait(a, slot + 1 == stages ? 0 : slot + 1, slot + 1 == stages ? phase ^ 1u : phase);
+    __device__ __forceinline__ int ahead(int k) const { return slot + k >= stages ? slot + k - stages : slot + k; }
+    // before the row's last barrier: the stage of the k-th row after it (k < stages)
+    __device__ __forceinline__ void wait_next(const RingArgs& a, int64_t t, int k = 1) const {
+        if (threadIdx.x < 32 && t + (int64_t)k * gridDim.x < a.n.T)
+            wait(a, ahead(k), slot + k >= stages ? phase ^ 1u : phase);
     }
     // after it, by one thread: the stage of the current row t takes a later row
     __device__ __forceinline__ void refill(const RingArgs& a, int64_t t) const {
@@ -470,6 +492,7 @@ template <typename T, int MAXT>
 __global__ void __launch_bounds__(MAXT) block_norm_ring_kernel(const __grid_constant__ RingArgs a) {
     __shared__ float buf[2][32];
     NORM_RING_SETUP();
+    const float on = live<T>(d);
     f2 wq[RP], wz[RP];                     // g w_post, w_pre
     fill(wq, 1.f);
     if (n.post) channel<T>(n.w_post, d, wq);
@@ -488,7 +511,7 @@ __global__ void __launch_bounds__(MAXT) block_norm_ring_kernel(const __grid_cons
         take<T>(st, d, y);
         if (n.leave) {
             take<T>(st + d, d, u);
-            const float s = n.post ? dot2(u, u) : 0.f;
+            const float s = n.post ? on * dot2(u, u) : 0.f;
             if (n.gmode == MOE_GATE_FULL) {
                 f2 g[RP];
                 take<T>(st + 2 * d, d, g);
@@ -502,7 +525,7 @@ __global__ void __launch_bounds__(MAXT) block_norm_ring_kernel(const __grid_cons
             give<T>(static_cast<T*>(n.x_out) + o, d, y);
         }
         if (n.enter) {
-            const float s = dot2(y, y);
+            const float s = on * dot2(y, y);
             ring.wait_next(a, t);
             const f2 r = both(rsqrtf(row_sum(s, buf[1]) * invd + n.eps));
 #pragma unroll
@@ -537,61 +560,62 @@ __global__ void __launch_bounds__(MAXT) block_norm_bwd_ring_kernel(const __grid_
     if (n.enter) channel<T>(n.w_pre, d, wz);
     if (n.gmode == MOE_GATE_CHANNEL) channel<T>(static_cast<const float*>(n.gate), d, wg);
     const bool need_u = n.leave && (n.post || n.gmode != MOE_GATE_NONE);
-    int par = 0;
-    // the tensors' places in a stage
-    const int p_dz = 1, p_dx = n.enter ? 2 : 0, p_u = p_dx + (n.dx_out ? 1 : 0), p_g = p_u + 1;
-    for (int64_t t = blockIdx.x; t < n.T; t += gridDim.x, ring.next(), par ^= 1) {
-        const T* st = reinterpret_cast<const T*>(ring_smem + ring.slot * ring.stage_bytes);
-        const size_t o = (size_t)t * d;
-        float tok = n.ob;
-        if (n.gmode == MOE_GATE_TOKEN) tok *= __ldg(static_cast<const float*>(n.gate) + t);
-        f2 y[RP], G[RP], u[RP], dz[RP], g[RP];       // (b and a token gate are in tok)
-        // s: y^2, a y, u^2, q u dx', q u a, q u y  with a = w_pre dz, q = g w_post
-        float s[6] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        fill(G, 0.f);
-        if (n.dx_out) take<T>(st + (size_t)p_dx * d, d, G);
+    // the tensors' places in a stage, in elements
+    const int p_dz = d, p_dx = n.enter ? 2 * d : 0, p_u = p_dx + (n.dx_out ? d : 0), p_g = p_u + d;
+    const float on = live<T>(d);
+    // A row's tensors, from its stage.  They are taken twice, for the sums and for the
+    // outputs: between the two lies a barrier, and the next row's sums come before it.
+    auto row = [&](int slot, f2 (&y)[RP], f2 (&dz)[RP], f2 (&G)[RP], f2 (&u)[RP], f2 (&g)[RP]) {
+        const T* st = reinterpret_cast<const T*>(ring_smem + slot * ring.stage_bytes);
+        if (n.dx_out) take<T>(st + p_dx, d, G);
+        else fill(G, 0.f);
         if (n.enter) {
             take<T>(st, d, y);
-            take<T>(st + (size_t)p_dz * d, d, dz);
-            s[0] = dot2(y, y);
+            take<T>(st + p_dz, d, dz);
         } else {
             fill(y, 0.f);
             fill(dz, 0.f);
         }
-        if (need_u) {
-            take<T>(st + (size_t)p_u * d, d, u);
-            if (n.gmode == MOE_GATE_FULL) take<T>(st + (size_t)p_g * d, d, g);
-            else
+        if (need_u) take<T>(st + p_u, d, u);
+        else fill(u, 0.f);
+        if (n.gmode == MOE_GATE_FULL) take<T>(st + p_g, d, g);
+        else
 #pragma unroll
-                for (int i = 0; i < RP; ++i) g[i] = wg[i];
-            f2 s3 = both(0.f), s4 = s3, s5 = s3, s1 = s3;
+            for (int i = 0; i < RP; ++i) g[i] = wg[i];
+    };
+    // this warp's part of y^2, a y, u^2, q u dx', q u a, q u y  (a = w_pre dz, q = g w_post)
+    auto sums = [&](int slot, float* to) {
+        f2 y[RP], dz[RP], G[RP], u[RP], g[RP];
+        row(slot, y, dz, G, u, g);
+        f2 s1 = both(0.f), s3 = s1, s4 = s1, s5 = s1;
 #pragma unroll
-            for (int i = 0; i < RP; ++i) {
-                const f2 qu = (g[i] * wq[i]) * u[i], az = wz[i] * dz[i];
-                s1 = fma2(az, y[i], s1);
+        for (int i = 0; i < RP; ++i) {
+            const f2 az = wz[i] * dz[i];
+            s1 = fma2(az, y[i], s1);
+            if (need_u) {
+                const f2 qu = (g[i] * wq[i]) * u[i];
                 s3 = fma2(qu, G[i], s3);
                 s4 = fma2(qu, az, s4);
                 s5 = fma2(qu, y[i], s5);
             }
-            s[1] = sum2(s1);
-            s[2] = dot2(u, u);
-            s[3] = sum2(s3);
-            s[4] = sum2(s4);
-            s[5] = sum2(s5);
-        } else {
-            fill(u, 0.f);
-            fill(g, 1.f);
-            f2 s1 = both(0.f);
-#pragma unroll
-            for (int i = 0; i < RP; ++i) s1 = fma2(wz[i] * dz[i], y[i], s1);
-            s[1] = sum2(s1);
         }
-        ring.wait_next(a, t);
-        row_sums6(s, buf[par]);
-        if (blockDim.x <= 32) __syncwarp();
-        if (threadIdx.x == 0) ring.refill(a, t);
+        const float s[6] = {on * dot2(y, y), on * sum2(s1), on * dot2(u, u), on * sum2(s3), on * sum2(s4), on * sum2(s5)};
+        put_sums6(warp_sums6(s), to);
+    };
+    int par = 0;
+    if (blockIdx.x < n.T) sums(0, buf[0]);
+    ring.wait_next(a, blockIdx.x);
+    __syncthreads();
+    for (int64_t t = blockIdx.x; t < n.T; t += gridDim.x, ring.next(), par ^= 1) {
+        if (t + gridDim.x < n.T) sums(ring.ahead(1), buf[par ^ 1]);
+        const size_t o = (size_t)t * d;
+        float tok = n.ob;
+        if (n.gmode == MOE_GATE_TOKEN) tok *= __ldg(static_cast<const float*>(n.gate) + t);
+        float s[6];
+        get_sums6(s, buf[par]);
+        f2 y[RP], G[RP], u[RP], dz[RP], g[RP], out[RP];   // (b and a token gate are in tok)
+        row(ring.slot, y, dz, G, u, g);
         float r = 0.f, ca = 0.f;
-        f2 out[RP];
         if (n.enter) {
             r = rsqrtf(s[0] * invd + n.eps);
             ca = r * r * r * invd * s[1];
@@ -603,33 +627,38 @@ __global__ void __launch_bounds__(MAXT) block_norm_bwd_ring_kernel(const __grid_
                 G[i] = fma2(rz, wz[i], fma2(c2, y[i], G[i]));
             }
         }
-        if (!n.leave) {
+        if (n.leave) {
+            const f2 ra = both(n.ra);
+#pragma unroll
+            for (int i = 0; i < RP; ++i) out[i] = ra * G[i];
+            give<T>(static_cast<T*>(n.dx) + o, d, out);
+            const float S = s[3] + r * s[4] - ca * s[5];
+            const float ru = n.post ? rsqrtf(s[2] * invd + n.eps) : 1.f;
+            if (n.gmode == MOE_GATE_TOKEN && threadIdx.x == 0) static_cast<float*>(n.dgate)[t] = n.ob * ru * S;
+            // with h = b u r_u G (a token gate's factor apart): dw_post += g h, dgate = w_post h
+            const f2 tr = both(tok * ru), br = both(n.ob * ru);
+            const f2 cu = both(n.post ? -tok * ru * ru * ru * invd * S : 0.f);
+            if (n.gmode == MOE_GATE_FULL) {
+#pragma unroll
+                for (int i = 0; i < RP; ++i) out[i] = wq[i] * ((br * u[i]) * G[i]);
+                give<T>(static_cast<T*>(n.dgate) + o, d, out);
+            }
+#pragma unroll
+            for (int i = 0; i < RP; ++i) {
+                const f2 tG = tr * G[i], h = tG * u[i];
+                acc_post[i] = fma2(g[i], h, acc_post[i]);
+                acc_g[i] = fma2(wq[i], h, acc_g[i]);
+                out[i] = fma2(cu, u[i], (g[i] * wq[i]) * tG);
+            }
+            give<T>(static_cast<T*>(n.du) + o, d, out);
+        } else {
             give<T>(static_cast<T*>(n.dx) + o, d, G);
-            continue;
         }
-        const f2 ra = both(n.ra);
-#pragma unroll
-        for (int i = 0; i < RP; ++i) out[i] = ra * G[i];
-        give<T>(static_cast<T*>(n.dx) + o, d, out);
-        const float S = s[3] + r * s[4] - ca * s[5];
-        const float ru = n.post ? rsqrtf(s[2] * invd + n.eps) : 1.f;
-        if (n.gmode == MOE_GATE_TOKEN && threadIdx.x == 0) static_cast<float*>(n.dgate)[t] = n.ob * ru * S;
-        // with h = b u r_u G (a token gate's factor apart): dw_post += g h, dgate = w_post h
-        const f2 tr = both(tok * ru), br = both(n.ob * ru);
-        const f2 cu = both(n.post ? -tok * ru * ru * ru * invd * S : 0.f);
-        if (n.gmode == MOE_GATE_FULL) {
-#pragma unroll
-            for (int i = 0; i < RP; ++i) out[i] = wq[i] * ((br * u[i]) * G[i]);
-            give<T>(static_cast<T*>(n.dgate) + o, d, out);
-        }
-#pragma unroll
-        for (int i = 0; i < RP; ++i) {
-            const f2 tG = tr * G[i], h = tG * u[i];
-            acc_post[i] = fma2(g[i], h, acc_post[i]);
-            acc_g[i] = fma2(wq[i], h, acc_g[i]);
-            out[i] = fma2(cu, u[i], (g[i] * wq[i]) * tG);
-        }
-        give<T>(static_cast<T*>(n.du) + o, d, out);
+        // the next row's sums are there, its successor's stage has arrived, and this row's
+        // stage is free
+        ring.wait_next(a, t, 2);
+        __syncthreads();
+        if (threadIdx.x == 0) ring.refill(a, t);
     }
     auto flush = [&](int which, const f2 (&acc)[RP]) {
         constexpr int V = 16 / sizeof(T);
@@ -704,7 +733,7 @@ RingPlan ring_plan(const moe_norm_config& c, int nin, int regs) {
     auto room = [&](int n) { return std::min(200 * 1024, 224 * 1024 / n - 3072); };
     while (per_sm > 1 && room(per_sm) < 3 * stage) --per_sm;
     p.stages = std::min(MAX_STAGES, room(per_sm) / stage);
-    if (p.stages < 2) { p.stages = 0; return p; }
+    if (p.stages < 3) { p.stages = 0; return p; }   // the backward works on two at a time
     p.smem = (size_t)p.stages * stage;
     p.grid = (int)std::min<int64_t>(c.T, (int64_t)per_sm * num_sms());
     return p;
