@@ -272,7 +272,8 @@ def test_long_batches_of_every_form(form, dt):
 @pytest.mark.gpu
 @pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("T,d", [(304, 8), (3000, 16), (5000, 264), (303, 1024), (305, 2816),
-                                 (700, 4096), (640, 4104), (700, 8192), (320, 16384)])
+                                 (700, 4096), (640, 4104), (700, 8192), (320, 16384), (305, 1),
+                                 (311, 3), (333, 7), (1001, 33), (1237, 1001), (400, 4097), (305, 8191)])
 def test_long_batches_of_every_width(T, d, dt):
     check(T, d, dt, (1, 1, 1, "channel"), seed=d)
     check(T, d, dt, (1, 1, 1, "full"), seed=d)

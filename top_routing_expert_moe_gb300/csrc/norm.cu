@@ -86,8 +86,8 @@ __device__ __forceinline__ void row_sums6(float (&s)[6], float* buf) {
 }
 
 // ---------------------------------------------------------------- rows read directly
-// For rows of no whole 16 bytes (VEC = 1), short batches and very wide rows.  A
-// thread's share: vectors tid, tid + threads, ... of VEC elements, EPT in all.
+// For short batches and very wide rows.  A thread's share: vectors tid, tid +
+// threads, ... of VEC elements (1 for rows of no whole 16 bytes), EPT in all.
 template <typename T, int VEC>
 __device__ __forceinline__ void load_vec(const T* p, int c, int nvec, float (&v)[VEC]) {
 #pragma unroll
@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(MAXT) block_norm_bwd_kernel(const NormArgs a) 
 }
 
 // ---------------------------------------------------------------- rows through a ring
-// Long batches of 16-byte rows.  A CTA is one row wide (8 elements a thread) and
+// Long batches.  A CTA is one row wide (8 elements a thread) and
 // persistent; its rows' tensors arrive by bulk copies in a ring of shared-memory
 // stages, so loads run ahead of the two dependent phases of a row (sums, then
 // outputs) that kept registers and memory waiting on each other; the vectors
@@ -314,6 +314,11 @@ __global__ void __launch_bounds__(MAXT) block_norm_bwd_kernel(const NormArgs a) 
 // after the bounded wait (recorded; the outputs are then undefined).
 constexpr int RE = 8;                      // elements of a row per thread
 constexpr int MAX_STAGES = 8;
+
+// bytes of a staged row: whole 16s, around any shift
+__host__ __device__ inline uint32_t row_pitch(uint32_t row_bytes) {
+    return row_bytes % 16 == 0 ? row_bytes : (row_bytes + 30) / 16 * 16;
+}
 
 struct RingArgs {
     NormArgs n;
@@ -355,13 +360,23 @@ __device__ __forceinline__ float sum2(f2 a) {
 }
 constexpr int RP = RE / 2;                 // pairs a thread
 
-// A thread's 8 elements of a staged row; fp32 rows as two halves, so that the
-// 16-byte accesses of neighbouring threads stay neighbours.
+// A thread's 8 elements of a row.  WIDE (rows of whole 16 bytes): one 16-byte
+// piece of bf16, or one of each half of an fp32 row, so that neighbouring threads'
+// accesses stay neighbours.  Otherwise elements tid, tid + threads, ...
 template <typename T>
 __device__ __forceinline__ int part_of(int half) { return (threadIdx.x + half * blockDim.x) * (16 / (int)sizeof(T)); }
-template <typename T>
+template <typename T, bool WIDE>
 __device__ __forceinline__ void take(const T* p, int d, f2 (&v)[RP]) {
-    if constexpr (sizeof(T) == 2) {
+    if constexpr (!WIDE) {
+        float f[RE];
+#pragma unroll
+        for (int j = 0; j < RE; ++j) {
+            const int c = threadIdx.x + j * blockDim.x;
+            f[j] = c < d ? to_f<T>(p[c]) : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < RP; ++i) v[i] = pk(f[2 * i], f[2 * i + 1]);
+    } else if constexpr (sizeof(T) == 2) {
         // threads past the row's end read its last elements; sums and stores leave them out
         const uint4 u = *reinterpret_cast<const uint4*>(p + min((int)threadIdx.x * RE, d - RE));
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
@@ -377,32 +392,44 @@ __device__ __forceinline__ void take(const T* p, int d, f2 (&v)[RP]) {
         }
     }
 }
-// whether this thread's share counts in sums (fp32 shares past the end are zeros)
-template <typename T>
-__device__ __forceinline__ float live(int d) { return sizeof(T) == 4 || (int)threadIdx.x * RE < d ? 1.f : 0.f; }
-template <typename T>
+// whether this thread's share counts in sums (other shares past the end are zeros)
+template <typename T, bool WIDE>
+__device__ __forceinline__ float live(int d) { return !WIDE || sizeof(T) == 4 || (int)threadIdx.x * RE < d ? 1.f : 0.f; }
+template <typename T, bool WIDE>
 __device__ __forceinline__ void give(T* p, int d, const f2 (&v)[RP]) {
-    constexpr int V = 16 / sizeof(T);
+    if constexpr (!WIDE) {
 #pragma unroll
-    for (int h = 0; h < RE / V; ++h) {
-        const int c = part_of<T>(h);
-        float f[V];
+        for (int i = 0; i < RP; ++i) {
+            float lo, hi;
+            unpk(v[i], lo, hi);
+            const int c = threadIdx.x + 2 * i * blockDim.x;
+            if (c < d) p[c] = from_f<T>(lo);
+            if (c + (int)blockDim.x < d) p[c + blockDim.x] = from_f<T>(hi);
+        }
+    } else {
+        constexpr int V = 16 / sizeof(T);
 #pragma unroll
-        for (int j = 0; j < V / 2; ++j) unpk(v[h * V / 2 + j], f[2 * j], f[2 * j + 1]);
-        if (c < d) store16_f<T>(p + c, f);
+        for (int h = 0; h < RE / V; ++h) {
+            const int c = part_of<T>(h);
+            float f[V];
+#pragma unroll
+            for (int j = 0; j < V / 2; ++j) unpk(v[h * V / 2 + j], f[2 * j], f[2 * j + 1]);
+            if (c < d) store16_f<T>(p + c, f);
+        }
     }
 }
 // the fp32 channel vector's share that goes with it
-template <typename T>
+template <typename T, bool WIDE>
 __device__ __forceinline__ void channel(const float* p, int d, f2 (&v)[RP]) {
-    constexpr int V = 16 / sizeof(T);
+    constexpr int V = WIDE ? 16 / sizeof(T) : 1;
+    float f[RE];
 #pragma unroll
-    for (int h = 0; h < RE / V; ++h) {
-        const int c = part_of<T>(h);
-#pragma unroll
-        for (int j = 0; j < V; j += 2)
-            v[(h * V + j) / 2] = c < d ? pk(__ldg(p + c + j), __ldg(p + c + j + 1)) : both(0.f);
+    for (int j = 0; j < RE; ++j) {
+        const int c = WIDE ? part_of<T>(j / V) + j % V : threadIdx.x + j * blockDim.x;
+        f[j] = c < d ? __ldg(p + c) : 0.f;
     }
+#pragma unroll
+    for (int i = 0; i < RP; ++i) v[i] = pk(f[2 * i], f[2 * i + 1]);
 }
 __device__ __forceinline__ void fill(f2 (&v)[RP], float x) {
 #pragma unroll
@@ -419,21 +446,41 @@ __device__ __forceinline__ float dot2(const f2 (&a)[RP], const f2 (&b)[RP]) {
 // `phase` follow the row being worked on.  One warp watches the barriers: it waits
 // for the next row's stage before it joins the current row's last reduction, whose
 // CTA barrier then tells the others.
-struct RowRing {
-    uint32_t base, bar0, row_bytes, stage_bytes;
+//
+// A copy starts and ends on 16 bytes.  A row that does not is copied with the bytes
+// around it and read at its shift; the batch's last bytes, where that would pass
+// the tensor's end, are stored by the copying thread itself (a barrier follows
+// before they are read).
+template <bool WIDE> struct RowRing {
+    uint32_t base, bar0, row_bytes, pitch, stage_bytes;
     int stages, slot = 0;
     uint32_t phase = 0;
     volatile int* abort_flag;
 
-    __device__ __forceinline__ void issue(const RingArgs& a, int64_t row, int s) const {
-        mbar_expect_tx(bar0 + s * 8, stage_bytes);
-        for (int j = 0; j < a.nin; ++j)
-            bulk_load(base + s * stage_bytes + j * row_bytes,
-                      static_cast<const uint8_t*>(a.in[j]) + (size_t)row * row_bytes, row_bytes, bar0 + s * 8);
+    __device__ __forceinline__ uint32_t shift(int64_t row) const { return (uint32_t)((uint64_t)row * row_bytes) & 15u; }
+    __device__ __forceinline__ void issue(const RingArgs& a, uint8_t* smem, int64_t row, int s) const {
+        if constexpr (WIDE) {
+            mbar_expect_tx(bar0 + s * 8, stage_bytes);
+            for (int j = 0; j < a.nin; ++j)
+                bulk_load(base + s * stage_bytes + j * pitch, static_cast<const uint8_t*>(a.in[j]) + (size_t)row * row_bytes,
+                          row_bytes, bar0 + s * 8);
+            return;
+        }
+        const uint64_t at = (uint64_t)row * row_bytes, from = at & ~15ull, all = (uint64_t)a.n.T * row_bytes;
+        uint64_t to = (at + row_bytes + 15) & ~15ull;
+        if (to > all) to = all & ~15ull;                 // (the batch's end: below)
+        const uint32_t bytes = (uint32_t)(to - from), tail = (uint32_t)(at + row_bytes > to ? at + row_bytes - to : 0);
+        mbar_expect_tx(bar0 + s * 8, bytes * a.nin);
+        for (int j = 0; j < a.nin; ++j) {
+            const uint8_t* src = static_cast<const uint8_t*>(a.in[j]);
+            const uint32_t off = s * stage_bytes + j * pitch;
+            if (bytes) bulk_load(base + off, src + from, bytes, bar0 + s * 8);
+            for (uint32_t i = 0; i < tail; ++i) smem[off + bytes + i] = src[to + i];
+        }
     }
-    __device__ __forceinline__ void start(const RingArgs& a) const {
+    __device__ __forceinline__ void start(const RingArgs& a, uint8_t* smem) const {
         int64_t row = blockIdx.x;
-        for (int i = 0; i < stages && row < a.n.T; ++i, row += gridDim.x) issue(a, row, i);
+        for (int i = 0; i < stages && row < a.n.T; ++i, row += gridDim.x) issue(a, smem, row, i);
     }
     __device__ __forceinline__ void wait(const RingArgs& a, int s, uint32_t ph) const {
         mbar_wait(bar0 + s * 8, ph, abort_flag, a.status);
@@ -445,9 +492,9 @@ struct RowRing {
             wait(a, ahead(k), slot + k >= stages ? phase ^ 1u : phase);
     }
     // after it, by one thread: the stage of the current row t takes a later row
-    __device__ __forceinline__ void refill(const RingArgs& a, int64_t t) const {
+    __device__ __forceinline__ void refill(const RingArgs& a, uint8_t* smem, int64_t t) const {
         const int64_t row = t + (int64_t)stages * gridDim.x;
-        if (row < a.n.T && !*abort_flag) issue(a, row, slot);
+        if (row < a.n.T && !*abort_flag) issue(a, smem, row, slot);
     }
     __device__ __forceinline__ void next() {
         if (++slot == stages) {
@@ -469,11 +516,12 @@ struct RowRing {
     const NormArgs& n = a.n;                                                                    \
     const int d = n.d;                                                                          \
     const float invd = 1.f / (float)d;                                                          \
-    RowRing ring;                                                                               \
+    RowRing<WIDE> ring;                                                                          \
     ring.base = smem_u32(ring_smem);                                                            \
     ring.bar0 = smem_u32(bars);                                                                 \
     ring.row_bytes = (uint32_t)(d * sizeof(T));                                                 \
-    ring.stage_bytes = ring.row_bytes * a.nin;                                                  \
+    ring.pitch = row_pitch(ring.row_bytes);                                                     \
+    ring.stage_bytes = ring.pitch * a.nin;                                                      \
     ring.stages = a.stages;                                                                     \
     ring.abort_flag = &abort_s;                                                                 \
     if (threadIdx.x == 0) {                                                                     \
@@ -484,37 +532,39 @@ struct RowRing {
     __syncthreads();                                                                            \
     pdl_wait();                                                                                 \
     pdl_trigger();                                                                              \
-    if (threadIdx.x == 0) ring.start(a);                                                        \
+    if (threadIdx.x == 0) ring.start(a, ring_smem);                                             \
+    __syncthreads();                                                                            \
     ring.wait(a, 0, 0)
 
 // in: x, u (leave), gate (full)
-template <typename T, int MAXT>
+template <typename T, bool WIDE, int MAXT>
 __global__ void __launch_bounds__(MAXT) block_norm_ring_kernel(const __grid_constant__ RingArgs a) {
     __shared__ float buf[2][32];
     NORM_RING_SETUP();
-    const float on = live<T>(d);
+    const float on = live<T, WIDE>(d);
     f2 wq[RP], wz[RP];                     // g w_post, w_pre
     fill(wq, 1.f);
-    if (n.post) channel<T>(n.w_post, d, wq);
+    if (n.post) channel<T, WIDE>(n.w_post, d, wq);
     if (n.gmode == MOE_GATE_CHANNEL) {
-        channel<T>(static_cast<const float*>(n.gate), d, wz);
+        channel<T, WIDE>(static_cast<const float*>(n.gate), d, wz);
 #pragma unroll
         for (int i = 0; i < RP; ++i) wq[i] = wq[i] * wz[i];
     }
-    if (n.enter) channel<T>(n.w_pre, d, wz);
+    if (n.enter) channel<T, WIDE>(n.w_pre, d, wz);
     for (int64_t t = blockIdx.x; t < n.T; t += gridDim.x, ring.next()) {
-        const T* st = reinterpret_cast<const T*>(ring_smem + ring.slot * ring.stage_bytes);
+        const uint8_t* st = ring_smem + ring.slot * ring.stage_bytes + (WIDE ? 0u : ring.shift(t));
+        auto in = [&](int j) { return reinterpret_cast<const T*>(st + j * ring.pitch); };
         const size_t o = (size_t)t * d;
         float tok = n.ob;
         if (n.gmode == MOE_GATE_TOKEN) tok *= __ldg(static_cast<const float*>(n.gate) + t);
         f2 y[RP], u[RP];
-        take<T>(st, d, y);
+        take<T, WIDE>(in(0), d, y);
         if (n.leave) {
-            take<T>(st + d, d, u);
+            take<T, WIDE>(in(1), d, u);
             const float s = n.post ? on * dot2(u, u) : 0.f;
             if (n.gmode == MOE_GATE_FULL) {
                 f2 g[RP];
-                take<T>(st + 2 * d, d, g);
+                take<T, WIDE>(in(2), d, g);
 #pragma unroll
                 for (int i = 0; i < RP; ++i) u[i] = u[i] * g[i];
             }
@@ -522,7 +572,7 @@ __global__ void __launch_bounds__(MAXT) block_norm_ring_kernel(const __grid_cons
             const f2 c = both(tok), ra = both(n.ra);
 #pragma unroll
             for (int i = 0; i < RP; ++i) y[i] = fma2(c * wq[i], u[i], ra * y[i]);
-            give<T>(static_cast<T*>(n.x_out) + o, d, y);
+            give<T, WIDE>(static_cast<T*>(n.x_out) + o, d, y);
         }
         if (n.enter) {
             const float s = on * dot2(y, y);
@@ -530,7 +580,7 @@ __global__ void __launch_bounds__(MAXT) block_norm_ring_kernel(const __grid_cons
             const f2 r = both(rsqrtf(row_sum(s, buf[1]) * invd + n.eps));
 #pragma unroll
             for (int i = 0; i < RP; ++i) y[i] = y[i] * (r * wz[i]);
-            give<T>(static_cast<T*>(n.z) + o, d, y);
+            give<T, WIDE>(static_cast<T*>(n.z) + o, d, y);
         }
         // both buffers alternate with two norms; otherwise a barrier keeps a row's sums
         // (and with no norm at all its stage) from the next row
@@ -538,13 +588,13 @@ __global__ void __launch_bounds__(MAXT) block_norm_ring_kernel(const __grid_cons
             if (!n.enter) ring.wait_next(a, t);
             __syncthreads();
         }
-        if (threadIdx.x == 0) ring.refill(a, t);
+        if (threadIdx.x == 0) ring.refill(a, ring_smem, t);
     }
     if (threadIdx.x == 0 && *ring.abort_flag) ring.drain();
 }
 
 // in: x_out, dz (enter), dx_out (if given), u (post or gate), gate (full)
-template <typename T, int MAXT>
+template <typename T, bool WIDE, int MAXT>
 __global__ void __launch_bounds__(MAXT) block_norm_bwd_ring_kernel(const __grid_constant__ RingArgs a) {
     __shared__ float buf[2][32 * 8];
     NORM_RING_SETUP();
@@ -556,37 +606,38 @@ __global__ void __launch_bounds__(MAXT) block_norm_bwd_ring_kernel(const __grid_
     fill(wq, 1.f);
     fill(wg, 1.f);
     fill(wz, 1.f);
-    if (n.post) channel<T>(n.w_post, d, wq);
-    if (n.enter) channel<T>(n.w_pre, d, wz);
-    if (n.gmode == MOE_GATE_CHANNEL) channel<T>(static_cast<const float*>(n.gate), d, wg);
+    if (n.post) channel<T, WIDE>(n.w_post, d, wq);
+    if (n.enter) channel<T, WIDE>(n.w_pre, d, wz);
+    if (n.gmode == MOE_GATE_CHANNEL) channel<T, WIDE>(static_cast<const float*>(n.gate), d, wg);
     const bool need_u = n.leave && (n.post || n.gmode != MOE_GATE_NONE);
-    // the tensors' places in a stage, in elements
-    const int p_dz = d, p_dx = n.enter ? 2 * d : 0, p_u = p_dx + (n.dx_out ? d : 0), p_g = p_u + d;
-    const float on = live<T>(d);
+    // the tensors' places in a stage
+    const int p_dz = 1, p_dx = n.enter ? 2 : 0, p_u = p_dx + (n.dx_out ? 1 : 0), p_g = p_u + 1;
+    const float on = live<T, WIDE>(d);
     // A row's tensors, from its stage.  They are taken twice, for the sums and for the
     // outputs: between the two lies a barrier, and the next row's sums come before it.
-    auto row = [&](int slot, f2 (&y)[RP], f2 (&dz)[RP], f2 (&G)[RP], f2 (&u)[RP], f2 (&g)[RP]) {
-        const T* st = reinterpret_cast<const T*>(ring_smem + slot * ring.stage_bytes);
-        if (n.dx_out) take<T>(st + p_dx, d, G);
+    auto row = [&](int slot, int64_t t, f2 (&y)[RP], f2 (&dz)[RP], f2 (&G)[RP], f2 (&u)[RP], f2 (&g)[RP]) {
+        const uint8_t* st = ring_smem + slot * ring.stage_bytes + (WIDE ? 0u : ring.shift(t));
+        auto in = [&](int j) { return reinterpret_cast<const T*>(st + j * ring.pitch); };
+        if (n.dx_out) take<T, WIDE>(in(p_dx), d, G);
         else fill(G, 0.f);
         if (n.enter) {
-            take<T>(st, d, y);
-            take<T>(st + p_dz, d, dz);
+            take<T, WIDE>(in(0), d, y);
+            take<T, WIDE>(in(p_dz), d, dz);
         } else {
             fill(y, 0.f);
             fill(dz, 0.f);
         }
-        if (need_u) take<T>(st + p_u, d, u);
+        if (need_u) take<T, WIDE>(in(p_u), d, u);
         else fill(u, 0.f);
-        if (n.gmode == MOE_GATE_FULL) take<T>(st + p_g, d, g);
+        if (n.gmode == MOE_GATE_FULL) take<T, WIDE>(in(p_g), d, g);
         else
 #pragma unroll
             for (int i = 0; i < RP; ++i) g[i] = wg[i];
     };
     // this warp's part of y^2, a y, u^2, q u dx', q u a, q u y  (a = w_pre dz, q = g w_post)
-    auto sums = [&](int slot, float* to) {
+    auto sums = [&](int slot, int64_t t, float* to) {
         f2 y[RP], dz[RP], G[RP], u[RP], g[RP];
-        row(slot, y, dz, G, u, g);
+        row(slot, t, y, dz, G, u, g);
         f2 s1 = both(0.f), s3 = s1, s4 = s1, s5 = s1;
 #pragma unroll
         for (int i = 0; i < RP; ++i) {
@@ -603,18 +654,18 @@ __global__ void __launch_bounds__(MAXT) block_norm_bwd_ring_kernel(const __grid_
         put_sums6(warp_sums6(s), to);
     };
     int par = 0;
-    if (blockIdx.x < n.T) sums(0, buf[0]);
+    if (blockIdx.x < n.T) sums(0, blockIdx.x, buf[0]);
     ring.wait_next(a, blockIdx.x);
     __syncthreads();
     for (int64_t t = blockIdx.x; t < n.T; t += gridDim.x, ring.next(), par ^= 1) {
-        if (t + gridDim.x < n.T) sums(ring.ahead(1), buf[par ^ 1]);
+        if (t + gridDim.x < n.T) sums(ring.ahead(1), t + gridDim.x, buf[par ^ 1]);
         const size_t o = (size_t)t * d;
         float tok = n.ob;
         if (n.gmode == MOE_GATE_TOKEN) tok *= __ldg(static_cast<const float*>(n.gate) + t);
         float s[6];
         get_sums6(s, buf[par]);
         f2 y[RP], G[RP], u[RP], dz[RP], g[RP], out[RP];   // (b and a token gate are in tok)
-        row(ring.slot, y, dz, G, u, g);
+        row(ring.slot, t, y, dz, G, u, g);
         float r = 0.f, ca = 0.f;
         if (n.enter) {
             r = rsqrtf(s[0] * invd + n.eps);
@@ -631,7 +682,7 @@ __global__ void __launch_bounds__(MAXT) block_norm_bwd_ring_kernel(const __grid_
             const f2 ra = both(n.ra);
 #pragma unroll
             for (int i = 0; i < RP; ++i) out[i] = ra * G[i];
-            give<T>(static_cast<T*>(n.dx) + o, d, out);
+            give<T, WIDE>(static_cast<T*>(n.dx) + o, d, out);
             const float S = s[3] + r * s[4] - ca * s[5];
             const float ru = n.post ? rsqrtf(s[2] * invd + n.eps) : 1.f;
             if (n.gmode == MOE_GATE_TOKEN && threadIdx.x == 0) static_cast<float*>(n.dgate)[t] = n.ob * ru * S;
@@ -641,7 +692,7 @@ __global__ void __launch_bounds__(MAXT) block_norm_bwd_ring_kernel(const __grid_
             if (n.gmode == MOE_GATE_FULL) {
 #pragma unroll
                 for (int i = 0; i < RP; ++i) out[i] = wq[i] * ((br * u[i]) * G[i]);
-                give<T>(static_cast<T*>(n.dgate) + o, d, out);
+                give<T, WIDE>(static_cast<T*>(n.dgate) + o, d, out);
             }
 #pragma unroll
             for (int i = 0; i < RP; ++i) {
@@ -650,29 +701,31 @@ __global__ void __launch_bounds__(MAXT) block_norm_bwd_ring_kernel(const __grid_
                 acc_g[i] = fma2(wq[i], h, acc_g[i]);
                 out[i] = fma2(cu, u[i], (g[i] * wq[i]) * tG);
             }
-            give<T>(static_cast<T*>(n.du) + o, d, out);
+            give<T, WIDE>(static_cast<T*>(n.du) + o, d, out);
         } else {
-            give<T>(static_cast<T*>(n.dx) + o, d, G);
+            give<T, WIDE>(static_cast<T*>(n.dx) + o, d, G);
         }
         // the next row's sums are there, its successor's stage has arrived, and this row's
         // stage is free
         ring.wait_next(a, t, 2);
         __syncthreads();
-        if (threadIdx.x == 0) ring.refill(a, t);
+        if (threadIdx.x == 0) ring.refill(a, ring_smem, t);
     }
     auto flush = [&](int which, const f2 (&acc)[RP]) {
-        constexpr int V = 16 / sizeof(T);
+        constexpr int V = WIDE ? 16 / sizeof(T) : 1;
         float* dst = n.part + ((size_t)which * gridDim.x + blockIdx.x) * d;
 #pragma unroll
-        for (int h = 0; h < RE / V; ++h) {
-            const int c = part_of<T>(h);
-            if (c < d)
-#pragma unroll
-                for (int j = 0; j < V; j += 2) {
-                    float lo, hi;
-                    unpk(acc[(h * V + j) / 2], lo, hi);
-                    *reinterpret_cast<float2*>(dst + c + j) = make_float2(lo, hi);
-                }
+        for (int i = 0; i < RP; ++i) {
+            float lo, hi;
+            unpk(acc[i], lo, hi);
+            if constexpr (WIDE) {
+                const int c = part_of<T>(2 * i / V) + 2 * i % V;
+                if (c < d) *reinterpret_cast<float2*>(dst + c) = make_float2(lo, hi);
+            } else {
+                const int c = threadIdx.x + 2 * i * blockDim.x;
+                if (c < d) dst[c] = lo;
+                if (c + (int)blockDim.x < d) dst[c + blockDim.x] = hi;
+            }
         }
     };
     if (n.enter) flush(0, acc_pre);
@@ -717,16 +770,16 @@ dim3 norm_block(const moe_norm_config& c) {
 bool wide_rows(const moe_norm_config& c) { return (c.d * (c.dtype == MOE_DTYPE_BF16 ? 2 : 4)) % 16 == 0; }
 
 // The ring's launch: threads, stages and CTAs, or none (0 stages) where the direct
-// kernels serve: rows of no whole 16 bytes, rows too wide for two stages, and
-// batches of fewer than RING_ROWS rows an SM, where filling a ring is all there is.
+// kernels serve: rows too wide for three stages, and batches of fewer than RING_ROWS
+// rows an SM, where filling a ring is all there is.
 constexpr int RING_ROWS = 2;
 struct RingPlan { int threads, stages, grid; size_t smem; };
 RingPlan ring_plan(const moe_norm_config& c, int nin, int regs) {
     RingPlan p = {0, 0, 0, 0};
     const int es = c.dtype == MOE_DTYPE_BF16 ? 2 : 4;
     p.threads = ((c.d + RE - 1) / RE + 31) / 32 * 32;
-    if (!wide_rows(c) || p.threads > 1024 || c.T < (int64_t)RING_ROWS * num_sms()) return p;
-    const int stage = nin * c.d * es;
+    if (p.threads > 1024 || c.T < (int64_t)RING_ROWS * num_sms()) return p;
+    const int stage = nin * (int)row_pitch(c.d * es);
     // CTAs an SM by registers and threads, fewer where they would not have three stages
     // each (228 KB an SM, 3 KB of it a CTA's fixed part)
     int per_sm = std::max(1, std::min(std::min(32, 65536 / (regs * p.threads)), 2048 / p.threads));
@@ -735,7 +788,9 @@ RingPlan ring_plan(const moe_norm_config& c, int nin, int regs) {
     p.stages = std::min(MAX_STAGES, room(per_sm) / stage);
     if (p.stages < 3) { p.stages = 0; return p; }   // the backward works on two at a time
     p.smem = (size_t)p.stages * stage;
-    p.grid = (int)std::min<int64_t>(c.T, (int64_t)per_sm * num_sms());
+    // four rows a CTA, at least, once every SM has one: a CTA's rows share its set-up and,
+    // in the backward, one row of partial sums
+    p.grid = (int)std::min<int64_t>((int64_t)per_sm * num_sms(), std::max<int64_t>(num_sms(), c.T / 4));
     return p;
 }
 int fwd_inputs(const moe_norm_config& c) { return 1 + c.leave + (c.gate == MOE_GATE_FULL); }
@@ -757,25 +812,30 @@ int bwd_grid(const moe_norm_config& c) {
     return (int)std::min<int64_t>((c.T + rows - 1) / rows, (int64_t)num_sms() * per_sm);
 }
 
-template <typename T>
+template <typename T, bool WIDE>
 int launch_fwd_ring(const RingPlan& p, const RingArgs& r, cudaStream_t st) {
     static bool done[2][64] = {};
     const bool big = p.threads > 512;
-    if (const int e = big ? smem_attr_once(block_norm_ring_kernel<T, 1024>, 200 * 1024, done[0])
-                          : smem_attr_once(block_norm_ring_kernel<T, 512>, 200 * 1024, done[1])) return e;
-    if (big) MOE_LAUNCH((block_norm_ring_kernel<T, 1024>), p.grid, p.threads, p.smem, st, r);
-    else MOE_LAUNCH((block_norm_ring_kernel<T, 512>), p.grid, p.threads, p.smem, st, r);
+    if (const int e = big ? smem_attr_once(block_norm_ring_kernel<T, WIDE, 1024>, 200 * 1024, done[0])
+                          : smem_attr_once(block_norm_ring_kernel<T, WIDE, 512>, 200 * 1024, done[1])) return e;
+    if (big) MOE_LAUNCH((block_norm_ring_kernel<T, WIDE, 1024>), p.grid, p.threads, p.smem, st, r);
+    else MOE_LAUNCH((block_norm_ring_kernel<T, WIDE, 512>), p.grid, p.threads, p.smem, st, r);
     return MOE_OK;
 }
-template <typename T>
-int launch_bwd_ring(const RingPlan& p, const RingArgs& r, cudaStream_t st) {
-    static bool done[2][64] = {};
-    const bool big = p.threads > 512;
-    if (const int e = big ? smem_attr_once(block_norm_bwd_ring_kernel<T, 1024>, 200 * 1024, done[0])
-                          : smem_attr_once(block_norm_bwd_ring_kernel<T, 512>, 200 * 1024, done[1])) return e;
-    if (big) MOE_LAUNCH((block_norm_bwd_ring_kernel<T, 1024>), p.grid, p.threads, p.smem, st, r);
-    else MOE_LAUNCH((block_norm_bwd_ring_kernel<T, 512>), p.grid, p.threads, p.smem, st, r);
+template <typename T, bool WIDE, int MAXT>
+int launch_bwd_ring_t(const RingPlan& p, const RingArgs& r, cudaStream_t st) {
+    static bool done[64] = {};
+    if (const int e = smem_attr_once(block_norm_bwd_ring_kernel<T, WIDE, MAXT>, 200 * 1024, done)) return e;
+    MOE_LAUNCH((block_norm_bwd_ring_kernel<T, WIDE, MAXT>), p.grid, p.threads, p.smem, st, r);
     return MOE_OK;
+}
+// the fewer the threads, the more registers each may have
+template <typename T, bool WIDE>
+int launch_bwd_ring(const RingPlan& p, const RingArgs& r, cudaStream_t st) {
+    return p.threads <= 512   ? launch_bwd_ring_t<T, WIDE, 512>(p, r, st)
+           : p.threads <= 640 ? launch_bwd_ring_t<T, WIDE, 640>(p, r, st)
+           : p.threads <= 768 ? launch_bwd_ring_t<T, WIDE, 768>(p, r, st)
+                              : launch_bwd_ring_t<T, WIDE, 1024>(p, r, st);
 }
 
 template <typename T, int VEC>
@@ -789,7 +849,7 @@ int launch_fwd(const moe_norm_config& c, const NormArgs& a, cudaStream_t st) {
         if (c.gate == MOE_GATE_FULL) r.in[r.nin++] = a.gate;
         r.stages = p.stages;
         r.status = device_status_ptr();
-        return launch_fwd_ring<T>(p, r, st);
+        return launch_fwd_ring<T, (VEC > 1)>(p, r, st);
     }
     const dim3 b = norm_block(c);
     const int grid = (int)std::min<int64_t>(((int64_t)c.T + b.y - 1) / b.y, (int64_t)num_sms() * 64);
@@ -814,7 +874,7 @@ int launch_bwd(const moe_norm_config& c, const NormArgs& a, float* dwpre, float*
         if (c.gate == MOE_GATE_FULL) q.in[q.nin++] = a.gate;
         q.stages = p.stages;
         q.status = device_status_ptr();
-        if (const int e = launch_bwd_ring<T>(p, q, st)) return e;
+        if (const int e = (launch_bwd_ring<T, (VEC > 1)>(p, q, st))) return e;
     } else if (direct_ept(c) == 16) {
         MOE_LAUNCH((block_norm_bwd_kernel<T, VEC, 16, 1024>), grid, b, smem, st, a);
     } else if (b.x <= 256) {
