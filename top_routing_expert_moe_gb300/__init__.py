@@ -424,12 +424,11 @@ class MoELayer:
                   self.counts, self.stats, self.ws, stream)
         moe_permute(c, x, self.topk_idx, self.x_perm, self.perm_token, self.slot_of, self.kept,
                     self.offsets, self.stats, self.ws, stream)
-        used = self.offsets[c.E:]
-        mx4_quantize(self.x_perm, used, xq, stream)
+        _quantize_segments(self.x_perm, self.offsets, c.E, xq, stream)
         moe_mx4_grouped_product(first, xq.codes, xq.scales, self.offsets, up.codes, up.scales,
                                 gate.codes if gate else None, gate.scales if gate else None,
                                 self.act, stream)
-        mx4_quantize(self.act, used, aq, stream)
+        _quantize_segments(self.act, self.offsets, c.E, aq, stream)
         moe_mx4_grouped_product(second, aq.codes, aq.scales, self.offsets, down.codes, down.scales,
                                 None, None, self.y_perm, stream)
         moe_combine(c, self.y_perm, self.slot_of, self.gate, self.out, stream)
@@ -488,3 +487,4 @@ class MoELayer:
 
 # the operators around the layer (imported last: they use the helpers above)
 from .block import *  # noqa: E402,F401,F403
+from .block import _quantize_segments  # noqa: E402

@@ -191,6 +191,7 @@ class BalanceLoss:
         if rc != 0:
             raise _moe.MoEError(rc, "moe_check_balance_config")
         self.cfg, dev = cfg, torch.device(device)
+        self._logits, self._topk, self._offsets = (cfg.T, cfg.E), (cfg.T, cfg.k), (cfg.S + 1,)
         e = lambda *s, dtype=torch.float32: torch.empty(*s, dtype=dtype, device=dev)  # noqa: E731
         self.loss = e(3)
         self.counts = e(cfg.S, cfg.E, dtype=torch.int32)
@@ -202,9 +203,9 @@ class BalanceLoss:
 
     def forward(self, logits, topk_idx, seq_offsets=None, stream=None):
         c = self.cfg
-        _checked(logits, (c.T, c.E), torch.float32, "logits")
-        _checked(topk_idx, (c.T, c.k), torch.int32, "topk_idx")
-        _checked(seq_offsets, (c.S + 1,), torch.int32, "seq_offsets")
+        _checked(logits, self._logits, torch.float32, "logits")
+        _checked(topk_idx, self._topk, torch.int32, "topk_idx")
+        _checked(seq_offsets, self._offsets, torch.int32, "seq_offsets")
         moe_balance_loss(c, logits, topk_idx, seq_offsets, self.loss, self.counts, self.pbar,
                          self.grad_w, self.ws, stream)
         self._inputs = (logits, topk_idx, seq_offsets)
@@ -245,11 +246,14 @@ def moe_mx4_dequantize(dtype, sets, rows, K, codes, scales, out, stream=None):
     _call("moe_mx4_dequantize", dtype, sets, rows, K, _p(codes), _p(scales), _p(out), _s(stream))
 
 
-def _mx4_dtype(t: torch.Tensor) -> int:
-    try:
-        return {torch.bfloat16: _moe.BF16, torch.float32: _moe.F32}[t.dtype]
-    except KeyError:
-        raise ValueError(f"expected bfloat16 or float32, got {t.dtype}") from None
+_MX4_DTYPES = {torch.bfloat16: _moe.BF16, torch.float32: _moe.F32}
+
+
+def _mx4_dtype(dtype) -> int:
+    code = _MX4_DTYPES.get(dtype)
+    if code is None:
+        raise ValueError(f"expected bfloat16 or float32, got {dtype}")
+    return code
 
 
 class MX4Tensor:
@@ -257,19 +261,24 @@ class MX4Tensor:
     (two to a byte) and ``scales`` (tiles, see include/moe.h)."""
 
     def __init__(self, shape, device="cuda"):
-        *sets, rows, K = shape
-        if len(sets) > 1:
+        shape = tuple(shape)
+        if len(shape) not in (2, 3):
             raise ValueError("expected [rows, K] or [E, rows, K]")
-        self.shape = tuple(shape)
-        n = sets[0] if sets else 1
-        self.codes = torch.empty(*shape[:-1], K // 2, dtype=torch.uint8, device=device)
-        self.scales = torch.empty(n * mx4_scale_bytes(rows, K), dtype=torch.uint8, device=device)
+        sets, (rows, K) = (shape[0] if len(shape) == 3 else 1), shape[-2:]
+        if rows < 1 or K < 1 or K % 32:
+            mx4_scale_bytes(rows, K)                 # raises
+        self.shape = shape
+        # moe_mx4_scale_bytes, without the call
+        n = sets * ((rows + 127) // 128) * ((K + 127) // 128) * 512
+        self.codes = torch.empty((*shape[:-1], K // 2), dtype=torch.uint8, device=device)
+        self.scales = torch.empty(n, dtype=torch.uint8, device=device)
 
     def dequantize(self, dtype=torch.bfloat16, stream=None):
+        code = _mx4_dtype(dtype)
         out = torch.empty(self.shape, dtype=dtype, device=self.codes.device)
         sets = self.shape[0] if len(self.shape) == 3 else 1
-        moe_mx4_dequantize(_mx4_dtype(out), sets, self.shape[-2], self.shape[-1], self.codes,
-                           self.scales, out, stream)
+        moe_mx4_dequantize(code, sets, self.shape[-2], self.shape[-1], self.codes, self.scales, out,
+                           stream)
         return out
 
 
@@ -278,14 +287,21 @@ def mx4_quantize(x, rows_used=None, out=None, stream=None) -> MX4Tensor:
     tensor.  ``rows_used``: one int32 on the device, rows from it on are left out."""
     if x.dim() != 2:
         raise ValueError("x: expected [rows, K]")
+    code = _mx4_dtype(x.dtype)
     if out is None:
         out = MX4Tensor(x.shape, x.device)
-    elif out.shape != tuple(x.shape):
+    elif out.shape != x.shape:
         raise ValueError(f"out: expected {tuple(x.shape)}, got {out.shape}")
     if rows_used is not None and (rows_used.numel() != 1 or rows_used.dtype != torch.int32):
         raise ValueError("rows_used must be one int32")
-    moe_mx4_quantize(_mx4_dtype(x), x.shape[0], x.shape[1], x, rows_used, out.codes, out.scales, stream)
+    moe_mx4_quantize(code, x.shape[0], x.shape[1], x, rows_used, out.codes, out.scales, stream)
     return out
+
+
+def _quantize_segments(x, offsets, E, out, stream):
+    """mx4_quantize of the rows below offsets[E] (a view of it would cost more than the call)."""
+    _call("moe_mx4_quantize", _mx4_dtype(x.dtype), x.shape[0], x.shape[1], _p(x), _p(offsets) + 4 * E,
+          _p(out.codes), _p(out.scales), _s(stream))
 
 
 def mx4_quantize_weight(W, stream=None) -> MX4Tensor:
@@ -293,8 +309,9 @@ def mx4_quantize_weight(W, stream=None) -> MX4Tensor:
     if W.dim() != 3:
         raise ValueError("W: expected [E, K, N]")
     E, K, N = W.shape
+    code = _mx4_dtype(W.dtype)
     out = MX4Tensor((E, N, K), W.device)
-    moe_mx4_quantize_weight(_mx4_dtype(W), E, K, N, W, out.codes, out.scales, stream)
+    moe_mx4_quantize_weight(code, E, K, N, W, out.codes, out.scales, stream)
     return out
 
 
@@ -331,7 +348,9 @@ class MX4Product:
         if rc != 0:
             raise _moe.MoEError(rc, "moe_check_mx4_product_config")
         self.cfg = cfg
-        self.xq = MX4Tensor((cfg.rows, cfg.K), device)
+        self._x, self._offsets, self._w = (cfg.rows, cfg.K), (cfg.E + 1,), (cfg.E, cfg.N, cfg.K)
+        self._dual = cfg.act == MX4_ACT_SWIGLU
+        self.xq = MX4Tensor(self._x, device)
         self.out = torch.empty(cfg.rows, cfg.N, dtype=cfg.torch_dtype, device=device)
 
     def forward(self, x, offsets, w: MX4Tensor, wg: MX4Tensor | None = None, stream=None):
@@ -339,15 +358,15 @@ class MX4Product:
         or fp32, offsets [E + 1] int32 as from moe_permute, w (and the gate wg for
         SwiGLU) [E, N, K]."""
         c = self.cfg
-        if tuple(x.shape) != (c.rows, c.K):
-            raise ValueError(f"x: expected {(c.rows, c.K)}, got {tuple(x.shape)}")
-        _checked(offsets, (c.E + 1,), torch.int32, "offsets")
-        if (wg is not None) != (c.act == MX4_ACT_SWIGLU):
+        if x.shape != self._x:
+            raise ValueError(f"x: expected {self._x}, got {tuple(x.shape)}")
+        _checked(offsets, self._offsets, torch.int32, "offsets")
+        if (wg is not None) != self._dual:
             raise ValueError("wg is required iff act is MX4_ACT_SWIGLU")
         for t, n in ((w, "w"), (wg, "wg")):
-            if t is not None and t.shape != (c.E, c.N, c.K):
-                raise ValueError(f"{n}: expected {(c.E, c.N, c.K)}, got {t.shape}")
-        mx4_quantize(x, offsets[c.E:], self.xq, stream)
+            if t is not None and t.shape != self._w:
+                raise ValueError(f"{n}: expected {self._w}, got {t.shape}")
+        _quantize_segments(x, offsets, c.E, self.xq, stream)
         moe_mx4_grouped_product(c, self.xq.codes, self.xq.scales, offsets, w.codes, w.scales,
                                 wg.codes if wg else None, wg.scales if wg else None, self.out, stream)
         return self.out

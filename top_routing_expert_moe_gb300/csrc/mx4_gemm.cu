@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) mx4_grouped_kernel(const __grid_c
         bool ok = live;
         for (int tix = unit; ok && tix < total; tix += nunits, ++tcount) {
             // the previous tile's epilogue is past the columns that both accumulators hold
-            if (!wait_bar<CG>(smem_u32(tempty), ((uint32_t)tcount & 1u) ^ 1u, abort_flag, P.status)) break;
+            if (!wait_bar<1>(smem_u32(tempty), ((uint32_t)tcount & 1u) ^ 1u, abort_flag, P.status)) break;
             tc_fence_after();
             const uint32_t dt = tm + (tcount & 1 ? ACC1 : 0);
             for (int kb = 0; kb < nk; ++kb) {
@@ -554,7 +554,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) mx4_grouped_kernel(const __grid_c
             const bool valid = (int)rank < t.valid;
             const int row = t.m0 + (int)rank * BM + qd * 32;
             const int col0 = t.nb * (dual ? 128 : BN);
-            const bool got = warp_wait<CG>(smem_u32(tfull), (uint32_t)tcount & 1u, abort_flag, P.status);
+            const bool got = warp_wait<1>(smem_u32(tfull), (uint32_t)tcount & 1u, abort_flag, P.status);
             if (!got) break;
             tc_fence_after();
             const uint32_t ta = tmem + (buf ? ACC1 : 0) + ((uint32_t)(qd * 32) << 16);
