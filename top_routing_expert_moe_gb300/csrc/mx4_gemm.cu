@@ -5,7 +5,7 @@
 //   32 elements along i;  out = u, silu(u), or silu(g) u with g from a second W.
 //
 // A persistent kernel like the bf16 grouped GEMM (gemm_tc.cu).  A CTA pair takes
-// 256 rows x 256 accumulator columns (a single CTA 128 x 256 where segments are
+// 256 rows x 256 accumulator columns (a single CTA 128 x 128 where segments are
 // short), warp-specialised:
 //   warp 0       TMA producer: per stage of 256 elements, 128 bytes a row, this CTA's
 //                128 rows of x and its 128 rows of W (for SwiGLU the even CTA's are
@@ -44,7 +44,6 @@ namespace moe {
 namespace {
 
 constexpr int BM = 128;                    // rows per CTA
-constexpr int BN = 256;                    // accumulator columns per tile (SwiGLU: 128 gate + 128 up)
 constexpr int BKB = 128;                   // bytes of a row per stage: 256 elements
 constexpr int A_BYTES = BM * BKB;
 constexpr int SF_TILE = 512;               // scale bytes of 128 rows x 128 elements
@@ -56,14 +55,14 @@ constexpr int NTHREADS = 64 + 32 * (NUM_EPI_WARPS + NUM_SF_WARPS);
 constexpr int STAGING_BYTES = NUM_EPI_WARPS * 4096;
 constexpr int CTRL_BYTES = 1024;
 constexpr int TMEM_COLS = 512;
-constexpr int ACC1 = 128;                  // second accumulator's first column (columns 128-255 overlap)
+constexpr int ACC1 = 128;                  // second accumulator's first column (a pair's overlap in 128-255)
 constexpr int SF_COL = 384, SF_COLS = 24;  // buffers of 24 columns: 8 of x's scales, 16 of W's
 constexpr int RASTER_ROWS = 4096;          // rows of x that pass over an expert's weights together
 
 template <int CG> struct Ring {            // CG CTAs a tile: stages and their bytes per CTA
-    static constexpr int B_ROWS = BN / CG;
-    static constexpr int BYTES = A_BYTES + B_ROWS * BKB;
-    static constexpr int STAGES = CG == 1 ? 3 : 5;
+    static constexpr int BN = 128 * CG;    // accumulator columns (SwiGLU: half gate, half up)
+    static constexpr int BYTES = A_BYTES + 128 * BKB;
+    static constexpr int STAGES = 5;
     static constexpr int SF_BUFS = STAGES;               // see the scale warps
     static constexpr int SMEM = 1024 + STAGES * BYTES + STAGING_BYTES + SF_SLOTS * SF_SLOT + CTRL_BYTES;
 };
@@ -241,7 +240,8 @@ __device__ __forceinline__ Mx4Tile decode(const int* offs, const int* prefix, in
 template <int CG, bool F32, bool DUAL>
 __global__ void __launch_bounds__(NTHREADS, 1) mx4_grouped_kernel(const __grid_constant__ Mx4Params P) {
     using R = Ring<CG>;
-    constexpr int S = R::STAGES, SB = R::SF_BUFS;
+    constexpr int S = R::STAGES, SB = R::SF_BUFS, BN = R::BN;
+    constexpr int OUT = DUAL ? BN / 2 : BN;              // output columns of a tile
     extern __shared__ uint8_t smem_raw[];
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sf_smem = base + S * R::BYTES + STAGING_BYTES;
@@ -338,15 +338,15 @@ __global__ void __launch_bounds__(NTHREADS, 1) mx4_grouped_kernel(const __grid_c
                     else tma_load3_pair(m, dst, bar, c0, c1, c2);
                 };
                 ld(&P.tmA, st, kb * BKB, am, 0);
-                // 128 rows of W at a time: box rows of the weight maps
-                if (dual) {
-                    if (CG == 1 || rank == 0) ld(&P.tmB0, st + A_BYTES, kb * BKB, t.nb * 128, t.e);
-                    if (CG == 1 || rank == 1)
-                        ld(&P.tmB1, st + A_BYTES + (CG == 1 ? 128 * BKB : 0), kb * BKB, t.nb * 128, t.e);
+                // this CTA's 128 rows of W: a pair's halves are gate and up, or columns;
+                // one CTA has 64 of each
+                if (dual && CG == 1) {
+                    ld(&P.tmB0, st + A_BYTES, kb * BKB, t.nb * OUT, t.e);
+                    ld(&P.tmB1, st + A_BYTES + 64 * BKB, kb * BKB, t.nb * OUT, t.e);
+                } else if (dual) {
+                    ld(rank ? &P.tmB1 : &P.tmB0, st + A_BYTES, kb * BKB, t.nb * OUT, t.e);
                 } else {
-                    for (int h = 0; h < 2 / CG; ++h)
-                        ld(&P.tmB0, st + A_BYTES + h * 128 * BKB, kb * BKB,
-                           t.nb * BN + (CG == 1 ? h : (int)rank) * 128, t.e);
+                    ld(&P.tmB0, st + A_BYTES, kb * BKB, t.nb * OUT + (int)rank * 128, t.e);
                 }
             }
         }
@@ -423,16 +423,19 @@ __global__ void __launch_bounds__(NTHREADS, 1) mx4_grouped_kernel(const __grid_c
         // first two warps the second k tile's W halves
         int f_tix = unit, f_kb = 0, f_slot = 0;         // the next stage to copy
         const uint4 *pa = nullptr, *pb = nullptr;       // its tile's first words (k tile 0), null past the end
+        uint32_t upper = 0, uppers = 0;                 // one CTA, SwiGLU: a tile is the upper or the lower 64
+                                                        // rows of W's tile; a bit per slot
         auto locate = [&]() {
             if (f_tix >= total) return;
             const Mx4Tile t = decode<CG>(offs, prefix, P.E, P.n_blocks, f_tix);
             const int ra = t.m0 / BM + (int)rank;
             auto wt = [&](int h) -> const uint4* {      // half h of the accumulator's columns
-                const int r = dual ? t.nb : t.nb * 2 + h;
-                return r < nt ? (dual && h ? P.sb1 : P.sb0) + ((int64_t)t.e * nt + r) * kt * 32 + lane : nullptr;
+                const int r = dual ? t.nb * OUT / 128 : t.nb * CG + h;
+                return (dual || h < CG) && r < nt ? (dual && h ? P.sb1 : P.sb0) + ((int64_t)t.e * nt + r) * kt * 32 + lane : nullptr;
             };
             pa = w >= 2 ? wt(w - 2) : ra < at ? P.sa + (int64_t)ra * kt * 32 + lane : nullptr;
             pb = w < 2 ? wt(w) : nullptr;
+            upper = t.nb & 1;
         };
         locate();
         auto copy = [&]() {                             // one group a stage, empty ones past the last
@@ -446,6 +449,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) mx4_grouped_kernel(const __grid_c
                 };
                 piece(pa, f_kb * 2 + (w == 1), w);
                 if (w < 2) piece(pb, f_kb * 2 + 1, 4 + w);
+                uppers = (uppers & ~(1u << f_slot)) | upper << f_slot;
                 f_slot = f_slot + 1 == SF_SLOTS ? 0 : f_slot + 1;
                 if (++f_kb == nk) {
                     f_kb = 0;
@@ -468,6 +472,14 @@ __global__ void __launch_bounds__(NTHREADS, 1) mx4_grouped_kernel(const __grid_c
             for (int k = 0; k < 2; ++k) a[k] = *reinterpret_cast<const uint4*>(t + k * SF_TILE);
 #pragma unroll
             for (int k = 0; k < 4; ++k) b[k] = *reinterpret_cast<const uint4*>(t + (2 + k) * SF_TILE);
+            if (dual && CG == 1) {                      // rows 0-63: the gate's, 64-127: up's
+                const bool up = uppers >> slot & 1;
+#pragma unroll
+                for (int k = 0; k < 4; k += 2) {
+                    const uint4 g = b[k], u = b[k + 1];
+                    b[k] = up ? make_uint4(g.z, g.w, u.z, u.w) : make_uint4(g.x, g.y, u.x, u.y);
+                }
+            }
             copy();      // into the slot that the previous stage's reads, before the barrier, left
             ok = ok && warp_wait<1>(smem_u32(&empty[buf]), ph, abort_flag, P.status);
             if (ok) {    // (a warp that gave up still joins the barriers above)
@@ -553,26 +565,56 @@ __global__ void __launch_bounds__(NTHREADS, 1) mx4_grouped_kernel(const __grid_c
             const int buf = tcount & 1;
             const bool valid = (int)rank < t.valid;
             const int row = t.m0 + (int)rank * BM + qd * 32;
-            const int col0 = t.nb * (dual ? 128 : BN);
+            const int col0 = t.nb * OUT;
             const bool got = warp_wait<1>(smem_u32(tfull), (uint32_t)tcount & 1u, abort_flag, P.status);
             if (!got) break;
             tc_fence_after();
             const uint32_t ta = tmem + (buf ? ACC1 : 0) + ((uint32_t)(qd * 32) << 16);
-            // Columns 128-255 of tensor memory belong to both accumulators (the first's
-            // upper half, the second's lower): each warp takes its 64 of them to
-            // registers first, and releases them to the next tile's MMAs.
             float v[2][32];
+            auto release = [&]() {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if constexpr (CG == 1) mbar_arrive(bar_te);
+                    else arrive_pair(bar_te);
+                }
+            };
+            if constexpr (CG == 1) {
+                // 128 columns: 64 a warp, or for SwiGLU the gate's 64 and up's by one warp
+                const bool work = !DUAL || half == 0;
+                if (work) {
+                    const uint32_t cols = ta + (DUAL ? 0 : half * 64);
+                    tmem_ld32(cols, v[0]);
+                    tmem_ld32(cols + 32, v[1]);
+                    tmem_wait_ld();
+                    if constexpr (DUAL) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            float o[16], (&w)[32] = v[i >> 1];
+                            const int k = (i & 1) * 16;
+                            tmem_ld16(cols + 64 + 16 * i, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) w[k + j] = act(w[k + j]) * o[j];
+                        }
+                    } else if (silu) {
+#pragma unroll
+                        for (int i = 0; i < 64; ++i) v[i >> 5][i & 31] = act(v[i >> 5][i & 31]);
+                    }
+                }
+                release();
+                if (work) store(v, col0 + (DUAL ? 0 : half * 64), row, valid);
+                continue;
+            }
+            // A pair.  Columns 128-255 of tensor memory belong to both accumulators (the
+            // first's upper half, the second's lower): each warp takes its 64 of them to
+            // registers first, and releases them to the next tile's MMAs.
             const int c = half * 64;
             const uint32_t shared_cols = ta + (buf ? 0 : 128) + c, own_cols = ta + (buf ? 128 : 0) + c;
             tmem_ld32(shared_cols, v[0]);
             tmem_ld32(shared_cols + 32, v[1]);
             tmem_wait_ld();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                if constexpr (CG == 1) mbar_arrive(bar_te);
-                else arrive_pair(bar_te);
-            }
+            release();
             if constexpr (DUAL) {                       // gate: columns 0-127, up: 128-255
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {           // 16 columns: registers are short
@@ -620,11 +662,11 @@ __global__ void __launch_bounds__(NTHREADS, 1) mx4_grouped_kernel(const __grid_c
         if (_r != MOE_OK) return _r; \
     } while (0)
 
-// codes [sets, rows, K / 2]: boxes of 128 bytes x 128 rows
-int codes_map(CUtensorMap* m, const void* p, int64_t rows, int sets, int K) {
+// codes [sets, rows, K / 2]: boxes of 128 bytes x `box_rows` rows
+int codes_map(CUtensorMap* m, const void* p, int64_t rows, int sets, int K, int box_rows) {
     const uint64_t dims[3] = {(uint64_t)K / 2, (uint64_t)rows, (uint64_t)sets};
     const uint64_t st[2] = {(uint64_t)K / 2, (uint64_t)K / 2 * rows};
-    const uint32_t box[3] = {BKB, BM, 1};
+    const uint32_t box[3] = {BKB, (uint32_t)box_rows, 1};
     return encode_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, p, 3, dims, st, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 template <int CG, bool F32, bool DUAL>
@@ -672,10 +714,17 @@ int launch_mx4_product(const moe_mx4_product_config& c, const void* xq, const vo
     Mx4Params P;
     memset(&P, 0, sizeof(P));
     const bool dual = c.act == MOE_MX4_ACT_SWIGLU;
-    MX4_TRY(codes_map(&P.tmA, xq, c.rows, 1, c.K));
+    // A pair's tile is 256 rows x 256 columns: it pays where an expert has two 128-row
+    // blocks or more (2048 rows of 8 experts, K = 4096, N = 14336, SwiGLU: 96 us against
+    // 116); with fewer half the pair idles.  A single CTA takes 128 x 128: it serves
+    // short segments, where W's bytes bound it and more, smaller tiles spread them
+    // evenly.  The host knows the rows' bound only, 127 of it an expert's padding.
+    const bool pair = c.rows >= (int64_t)(256 + 127) * c.E;
+    const int w_rows = dual && !pair ? 64 : 128;
+    MX4_TRY(codes_map(&P.tmA, xq, c.rows, 1, c.K, BM));
     // the accumulator's first half is the gate's for SwiGLU
-    MX4_TRY(codes_map(&P.tmB0, dual ? gq : wq, c.N, c.E, c.K));
-    if (dual) MX4_TRY(codes_map(&P.tmB1, wq, c.N, c.E, c.K));
+    MX4_TRY(codes_map(&P.tmB0, dual ? gq : wq, c.N, c.E, c.K, w_rows));
+    if (dual) MX4_TRY(codes_map(&P.tmB1, wq, c.N, c.E, c.K, w_rows));
     P.sa = static_cast<const uint4*>(xs);
     P.sb0 = static_cast<const uint4*>(dual ? gs : ws);
     P.sb1 = static_cast<const uint4*>(ws);
@@ -690,12 +739,9 @@ int launch_mx4_product(const moe_mx4_product_config& c, const void* xq, const vo
     P.status = device_status_ptr();
     P.rows = c.rows;
     P.E = c.E; P.K = c.K; P.N = c.N; P.act = c.act;
-    P.n_blocks = dual ? (c.N + 127) / 128 : (c.N + BN - 1) / BN;
-    // A pair's tile is 256 rows: it pays where an expert has two 128-row blocks or more
-    // (each CTA then reads half of W's tile): 4096 rows of 8 experts, K = 4096, N = 14336
-    // SwiGLU 163 us against 200; with one block an expert half the pair idles: 1024 rows
-    // 94 against 87 us.  The host knows the rows' bound only, 127 of it an expert's padding.
-    return c.rows >= (int64_t)(256 + 127) * c.E ? launch_mx4<2>(c, P, st) : launch_mx4<1>(c, P, st);
+    const int cols = (pair ? 256 : 128) / (dual ? 2 : 1);       // output columns of a tile
+    P.n_blocks = (c.N + cols - 1) / cols;
+    return pair ? launch_mx4<2>(c, P, st) : launch_mx4<1>(c, P, st);
 }
 
 }  // namespace moe
