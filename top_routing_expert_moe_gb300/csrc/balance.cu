@@ -59,6 +59,19 @@ __device__ __forceinline__ int seq_of(const BalArgs& a, int t) {
     return lo;
 }
 
+// The same for the whole CTA at once: the offsets at or before t are counted in
+// parallel (one memory latency instead of log2(S)) where they are few.
+__device__ __forceinline__ int cta_seq_of(const BalArgs& a, int t) {
+    if (!a.seq) return 0;
+    if (a.S > 8 * THREADS) return seq_of(a, t);
+    int n = 0;
+    for (int s0 = 0; s0 < a.S; s0 += THREADS) {
+        const int s = s0 + threadIdx.x;
+        n += __syncthreads_count(s < a.S && seq_at(a, s) <= t);
+    }
+    return max(n, 1) - 1;
+}
+
 template <int G>
 __device__ __forceinline__ float group_max(float v) {
 #pragma unroll
@@ -150,7 +163,15 @@ __global__ void __launch_bounds__(THREADS) balance_partial_kernel(const BalArgs 
             }
     }
     int t = t0;
-    for (int s = a.seq ? seq_of(a, t0) : 0; t < t1; ++s) {
+    // a token's logits are loaded while the one before is worked on
+    float nxt[R];
+    int32_t nxt_pick = -1;
+    auto fetch = [&](int tt) {
+        L::load(a.logits + (size_t)tt * a.E, a.E, gl, tt < t1, nxt);
+        nxt_pick = tt < t1 ? __ldg(a.topk + (size_t)tt * a.k) : -1;
+    };
+    fetch(t0 + grp);
+    for (int s = cta_seq_of(a, t0); t < t1; ++s) {
         const int end = min(t1, a.seq ? seq_at(a, s + 1) : a.T);
         if (end <= t && s + 1 < a.S) continue;       // (its record is not read)
         const int stop = s + 1 >= a.S ? t1 : end;
@@ -163,9 +184,12 @@ __global__ void __launch_bounds__(THREADS) balance_partial_kernel(const BalArgs 
             const int tt = base + grp;
             const bool in = tt < stop;
             float p[R];
-            L::load(a.logits + (size_t)tt * a.E, a.E, gl, in, p);
+#pragma unroll
+            for (int i = 0; i < R; ++i) p[i] = nxt[i];
             const int32_t* pick = a.topk + (size_t)tt * a.k;
-            const bool on = in && __ldg(pick) >= 0;
+            const bool on = in && nxt_pick >= 0;
+            // the pass's tokens past a sequence's end are its successor's first pass
+            fetch((base + TOK < stop ? base + TOK : stop) + grp);
             const float lse = softmax_row<G, R>(p, on, a.inv_tau * LOG2E);
             if (on) {
                 if (isnan(lse)) set_status(a.status, MOE_ERR_NONFINITE);
@@ -325,14 +349,23 @@ __global__ void __launch_bounds__(THREADS) balance_bwd_kernel(const BalArgs a) {
     const float up = (a.dloss ? __ldg(a.dloss) : 1.f) * a.inv_tau;
     const int t0 = blockIdx.x * a.chunk, t1 = min(a.T, t0 + a.chunk);
     // the sequence of this group's token, its end and its weights; they ascend with t
-    int s = a.seq ? seq_of(a, min(t0 + grp, a.T - 1)) : 0, end = -1;
-    float w[R], cz = 0.f;
+    int end = -1;
+    float w[R], cz = 0.f, nxt[R];
+    int32_t nxt_pick = -1;
+    auto fetch = [&](int tt) {
+        L::load(a.logits + (size_t)tt * a.E, a.E, gl, tt < t1, nxt);
+        nxt_pick = tt < t1 ? __ldg(a.topk + (size_t)tt * a.k) : -1;
+    };
+    fetch(t0 + grp);
+    int s = cta_seq_of(a, t0);
     for (int base = t0; base < t1; base += TOK) {
         const int t = base + grp;
         const bool in = t < t1;
         float p[R];
-        L::load(a.logits + (size_t)t * a.E, a.E, gl, in, p);
-        const bool on = in && __ldg(a.topk + (size_t)t * a.k) >= 0;
+#pragma unroll
+        for (int i = 0; i < R; ++i) p[i] = nxt[i];
+        const bool on = nxt_pick >= 0;
+        fetch(t + TOK);
         if (in && t >= end) {
             while (s + 1 < a.S && seq_at(a, s + 1) <= t) ++s;
             end = s + 1 < a.S ? seq_at(a, s + 1) : a.T;
