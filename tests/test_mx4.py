@@ -271,6 +271,16 @@ def test_product_segments(counts):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("counts", [[1], [2, 0, 1], [0, 0, 0, 5], [3, 1]])
+@pytest.mark.parametrize("K,N", [(2048, 64), (2080, 136), (4096, 640), (4128, 128), (6048, 1000)])
+@pytest.mark.parametrize("act,out_dt", [("none", torch.float32), ("silu", torch.bfloat16),
+                                        ("swiglu", torch.bfloat16), ("swiglu", torch.float32)])
+def test_product_of_few_rows_over_long_depths(K, N, counts, act, out_dt):
+    """Few tiles: clusters of two or four CTAs share a tile's depth."""
+    product_case(counts, K, N, act, out_dt, seed=K + N, slack=127 * len(counts) - sum(-c % 128 for c in counts))
+
+
+@pytest.mark.gpu
 def test_product_many_tiles_of_each_unit():
     """More tiles than the GPU holds at once, so that accumulators alternate."""
     product_case([4000, 3000], 320, 2560, "none", torch.float32)

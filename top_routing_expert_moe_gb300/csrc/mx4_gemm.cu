@@ -76,6 +76,8 @@ struct Mx4Params {
     int* status;
     int64_t rows;
     int E, K, N, n_blocks, act;
+    int ways;                              // CTAs of a cluster that may share a tile's K (single CTAs only)
+    int max_tiles;                         // their grid: tiles that rows of this number can make
 };
 
 __device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr) {
@@ -258,9 +260,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) mx4_grouped_kernel(const __grid_c
     int* prefix = offs + 66;                             // [E + 1]
 
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-    const uint32_t rank = CG == 1 ? 0u : cluster_rank();
+    const uint32_t rank = CG == 1 ? 0u : cluster_rank();   // within the pair
     const bool leader = rank == 0;
-    const int unit = (int)blockIdx.x / CG, nunits = (int)gridDim.x / CG;
     constexpr bool dual = DUAL;            // SwiGLU: gate and up
 
     if (tid == 0) {
@@ -274,11 +275,10 @@ __global__ void __launch_bounds__(NTHREADS, 1) mx4_grouped_kernel(const __grid_c
         mbar_init(smem_u32(drain), 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        const CUtensorMap* maps[4] = {&P.tmA, &P.tmB0, &P.tmO, &P.tmB1};
+        for (int i = 0; i < (dual ? 4 : 3); ++i)
+            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(maps[i])) : "memory");
     }
-    if constexpr (CG == 2) cluster_sync_all();
-    pdl_wait();
-    pdl_trigger();
-    if (tid < P.E + 1) offs[tid] = P.offsets[tid];
     if (warp == 1) {
         if constexpr (CG == 1) {
             asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
@@ -290,41 +290,74 @@ __global__ void __launch_bounds__(NTHREADS, 1) mx4_grouped_kernel(const __grid_c
             asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
         }
     }
+    if constexpr (CG == 2) cluster_sync_all();   // both CTAs' barriers exist before any cross-CTA use
+    pdl_wait();
+    pdl_trigger();
+    if (warp == 0) {
+        // Each lane two segments: their tiles, and the tiles before them.  Segments start
+        // at multiples of 128 rows and lie in 0..rows, so that no tile's box has a
+        // negative coordinate; others are recorded and nothing is computed.
+        int lo[2], hi[2], n[2], before = 0;
+        bool ok = true;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int e = lane + 32 * i;
+            lo[i] = e < P.E ? P.offsets[e] : 0;
+            hi[i] = e < P.E ? P.offsets[e + 1] : 0;
+        }
+        const bool pending = lane == 0 && timeout_pending(P.status);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            ok = ok && lo[i] >= 0 && hi[i] >= lo[i] && hi[i] <= P.rows && lo[i] % BM == 0 && hi[i] % BM == 0;
+            n[i] = (((hi[i] - lo[i]) / BM + CG - 1) / CG) * P.n_blocks;
+        }
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok && lane == 0) set_status(P.status, MOE_ERR_DEVICE_BOUNDS);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int e = lane + 32 * i;
+            int sum = ok ? n[i] : 0;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, sum, o);
+                if (lane >= o) sum += v;
+            }
+            if (e < P.E) {
+                offs[e] = lo[i];
+                prefix[e] = before + sum - (ok ? n[i] : 0);
+            }
+            if (e == P.E - 1) {
+                offs[P.E] = hi[i];
+                prefix[P.E] = before + sum;
+            }
+            before += __shfl_sync(0xffffffffu, sum, 31);
+        }
+        // a timeout recorded earlier on this device (not yet read by the host): skip the work
+        if (pending) *abort_flag = 1;
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (tid == 0) {
-        // segments start at multiples of 128 rows and lie in 0..rows: no tile's box
-        // has a negative coordinate; others are recorded and nothing is computed
-        bool ok = offs[0] >= 0 && offs[P.E] <= P.rows;
-        for (int e = 0; e <= P.E; ++e) ok = ok && offs[e] % BM == 0 && (e == 0 || offs[e] >= offs[e - 1]);
-        if (!ok) set_status(P.status, MOE_ERR_DEVICE_BOUNDS);
-        int acc = 0;
-        for (int e = 0; e < P.E; ++e) {
-            prefix[e] = acc;
-            if (ok) acc += ((offs[e + 1] - offs[e]) / BM + CG - 1) / CG * P.n_blocks;
-        }
-        prefix[P.E] = acc;
-        if (timeout_pending(P.status)) *abort_flag = 1;
-    }
-    __syncthreads();
     const uint32_t tmem = *tmem_slot;
     const int total = prefix[P.E];
     const uint32_t smem0 = smem_u32(base);
     const bool live = *abort_flag == 0;
     const int nk = (P.K / 2 + BKB - 1) / BKB;            // stages of a tile
+    // Few tiles: the CTAs of a cluster each take a share of one tile's stages, and the
+    // first adds the others' sums.  Every CTA then has one tile at most, so the ring
+    // is free to hold its sums once they are formed.
+    const bool split = CG == 1 && P.ways > 1 && total * P.ways <= (int)gridDim.x;
+    const int share = split ? (int)cluster_rank() : 0, ways = split ? P.ways : 1;
+    const int unit = (int)blockIdx.x / (CG * ways), nunits = (int)gridDim.x / (CG * ways);
+    const int kb0 = nk * share / ways, kb1 = nk * (share + 1) / ways;
 
     if (warp == 0 && lane == 0) {
         // ------------------------------------------------ TMA producer (each CTA)
-        const CUtensorMap* maps[4] = {&P.tmA, &P.tmB0, &P.tmO, &P.tmB1};
-        for (int i = 0; i < (dual ? 4 : 3); ++i)
-            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(maps[i])) : "memory");
         int it = 0;
         bool ok = live;
         for (int tix = unit; ok && tix < total; tix += nunits) {
             const Mx4Tile t = decode<CG>(offs, prefix, P.E, P.n_blocks, tix);
             const int am = t.m0 + (int)rank * BM;
-            for (int kb = 0; kb < nk; ++kb, ++it) {
+            for (int kb = kb0; kb < kb1; ++kb, ++it) {
                 const int s = it % S;
                 if (!wait_bar<1>(smem_u32(&empty[s]), ((uint32_t)(it / S) & 1u) ^ 1u, abort_flag, P.status)) {
                     ok = false;
@@ -371,7 +404,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) mx4_grouped_kernel(const __grid_c
             if (!wait_bar<1>(smem_u32(tempty), ((uint32_t)tcount & 1u) ^ 1u, abort_flag, P.status)) break;
             tc_fence_after();
             const uint32_t dt = tm + (tcount & 1 ? ACC1 : 0);
-            for (int kb = 0; kb < nk; ++kb) {
+            for (int kb = kb0; kb < kb1; ++kb) {
                 if (!wait_bar<1>(smem_u32(&full[s]), ph, abort_flag, P.status) ||
                     !wait_bar<1>(smem_u32(&sfull[s]), ph, abort_flag, P.status)) {
                     ok = false;
@@ -387,7 +420,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) mx4_grouped_kernel(const __grid_c
                     for (int ks = 0; ks < 4; ++ks)
                         if (ks < steps)
                             mma_mx4<CG>(dt, al + ks * 2, bl + ks * 2, hi, ks & 1 ? id1 : id0, sf + (ks >> 1) * 4,
-                                        sf + 8 + (ks >> 1) * 8, kb > 0 || ks > 0);
+                                        sf + 8 + (ks >> 1) * 8, kb > kb0 || ks > 0);
                     commit_all<CG>(smem_u32(&empty[s]));
                 }
                 __syncwarp();
@@ -418,10 +451,10 @@ __global__ void __launch_bounds__(NTHREADS, 1) mx4_grouped_kernel(const __grid_c
         const uint32_t bar0 = CG == 1 ? smem_u32(&sfull[0]) : mapa_shared(smem_u32(&sfull[0]), 0);
         const uint32_t sf0 = smem_u32(sf_smem) + lane * 16;
         const int kt = (P.K + 127) / 128, nt = (P.N + 127) / 128, at = (int)((P.rows + BM - 1) / BM);
-        const int stages = unit < total ? ((total - 1 - unit) / nunits + 1) * nk : 0;
+        const int stages = unit < total ? ((total - 1 - unit) / nunits + 1) * (kb1 - kb0) : 0;
         // this warp's tiles: w (0, 1: x's; 2, 3: the first k tile's W halves), and for the
         // first two warps the second k tile's W halves
-        int f_tix = unit, f_kb = 0, f_slot = 0;         // the next stage to copy
+        int f_tix = unit, f_kb = kb0, f_slot = 0;         // the next stage to copy
         const uint4 *pa = nullptr, *pb = nullptr;       // its tile's first words (k tile 0), null past the end
         uint32_t upper = 0, uppers = 0;                 // one CTA, SwiGLU: a tile is the upper or the lower 64
                                                         // rows of W's tile; a bit per slot
@@ -433,26 +466,33 @@ __global__ void __launch_bounds__(NTHREADS, 1) mx4_grouped_kernel(const __grid_c
                 const int r = dual ? t.nb * OUT / 128 : t.nb * CG + h;
                 return (dual || h < CG) && r < nt ? (dual && h ? P.sb1 : P.sb0) + ((int64_t)t.e * nt + r) * kt * 32 + lane : nullptr;
             };
+            // (w == 1 and the second piece take the stage's second k tile)
             pa = w >= 2 ? wt(w - 2) : ra < at ? P.sa + (int64_t)ra * kt * 32 + lane : nullptr;
             pb = w < 2 ? wt(w) : nullptr;
+            if (pa) pa += (kb0 * 2 + (w == 1)) * 32;
+            if (pb) pb += (kb0 * 2 + 1) * 32;
             upper = t.nb & 1;
         };
         locate();
+        const uint32_t dst_a = sf0 + w * SF_TILE, dst_b = sf0 + (4 + w) * SF_TILE;
+        const bool odd = kt & 1;
         auto copy = [&]() {                             // one group a stage, empty ones past the last
             if (f_tix < total) {
-                auto piece = [&](const uint4* p, int k, int tile) {
-                    const bool on = p && k < kt;
-                    const uint4* src = on ? p + k * 32 : P.sa;
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sf0 + f_slot * SF_SLOT + tile * SF_TILE),
-                                 "l"(src), "r"(on ? 16 : 0)
+                const bool second = !odd || f_kb + 1 < nk;    // the stage has a second k tile
+                const bool on_a = pa && (second || w != 1), on_b = pb && second;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst_a + f_slot * SF_SLOT),
+                             "l"(on_a ? pa : P.sa), "r"(on_a ? 16 : 0)
+                             : "memory");
+                if (w < 2)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst_b + f_slot * SF_SLOT),
+                                 "l"(on_b ? pb : P.sa), "r"(on_b ? 16 : 0)
                                  : "memory");
-                };
-                piece(pa, f_kb * 2 + (w == 1), w);
-                if (w < 2) piece(pb, f_kb * 2 + 1, 4 + w);
-                uppers = (uppers & ~(1u << f_slot)) | upper << f_slot;
+                if (pa) pa += 64;
+                if (pb) pb += 64;
+                if (dual && CG == 1) uppers = (uppers & ~(1u << f_slot)) | upper << f_slot;
                 f_slot = f_slot + 1 == SF_SLOTS ? 0 : f_slot + 1;
-                if (++f_kb == nk) {
-                    f_kb = 0;
+                if (++f_kb == kb1) {
+                    f_kb = kb0;
                     f_tix += nunits;
                     locate();
                 }
@@ -559,8 +599,44 @@ __global__ void __launch_bounds__(NTHREADS, 1) mx4_grouped_kernel(const __grid_c
                 send(col, row);
             }
         };
+        // a cluster's sums: 64 columns of a lane quarter's rows, by lane, in pieces of 16 bytes
+        const uint32_t sums = smem0 + (uint32_t)(qd * 2) * 8192 + lane * 16;
+        if (split && share > 0) {
+            if (unit < total && warp_wait<1>(smem_u32(tfull), 0, abort_flag, P.status)) {
+                tc_fence_after();
+                const uint32_t ta = tmem + ((uint32_t)(qd * 32) << 16) + half * 64;
+                float v[2][32];
+                tmem_ld32(ta, v[0]);
+                tmem_ld32(ta + 32, v[1]);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float* x = v[i >> 3] + (i & 7) * 4;
+                    asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(sums + half * 8192 + i * 512), "f"(x[0]),
+                                 "f"(x[1]), "f"(x[2]), "f"(x[3])
+                                 : "memory");
+                }
+            }
+            cluster_sync_all();                          // the sums are there
+        }
+        // adds 16 columns from 4 p on of half h's 64 of the other CTAs' sums, in order; their
+        // loads are issued together, as each takes a trip to the other SM
+        auto add_shares = [&](float* x, int h, int p) {
+            for (int q = 1; q < ways; ++q) {
+                const uint32_t from = mapa_shared(sums + h * 8192 + p * 512, (uint32_t)q);
+                float f[16];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                 : "=f"(f[4 * i]), "=f"(f[4 * i + 1]), "=f"(f[4 * i + 2]), "=f"(f[4 * i + 3])
+                                 : "r"(from + i * 512));
+#pragma unroll
+                for (int i = 0; i < 16; ++i) x[i] += f[i];
+            }
+        };
         int tcount = 0;
-        for (int tix = unit; tix < total; tix += nunits, ++tcount) {
+        bool joined = false;
+        for (int tix = unit; share == 0 && tix < total; tix += nunits, ++tcount) {
             const Mx4Tile t = decode<CG>(offs, prefix, P.E, P.n_blocks, tix);
             const int buf = tcount & 1;
             const bool valid = (int)rank < t.valid;
@@ -569,6 +645,10 @@ __global__ void __launch_bounds__(NTHREADS, 1) mx4_grouped_kernel(const __grid_c
             const bool got = warp_wait<1>(smem_u32(tfull), (uint32_t)tcount & 1u, abort_flag, P.status);
             if (!got) break;
             tc_fence_after();
+            if (split) {
+                cluster_sync_all();                      // the others' sums are there
+                joined = true;
+            }
             const uint32_t ta = tmem + (buf ? ACC1 : 0) + ((uint32_t)(qd * 32) << 16);
             float v[2][32];
             auto release = [&]() {
@@ -587,6 +667,9 @@ __global__ void __launch_bounds__(NTHREADS, 1) mx4_grouped_kernel(const __grid_c
                     tmem_ld32(cols, v[0]);
                     tmem_ld32(cols + 32, v[1]);
                     tmem_wait_ld();
+                    if (split)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) add_shares(v[i >> 1] + (i & 1) * 16, DUAL ? 0 : half, 4 * i);
                     if constexpr (DUAL) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
@@ -594,6 +677,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) mx4_grouped_kernel(const __grid_c
                             const int k = (i & 1) * 16;
                             tmem_ld16(cols + 64 + 16 * i, o);
                             tmem_wait_ld();
+                            if (split) add_shares(o, 1, 4 * i);
 #pragma unroll
                             for (int j = 0; j < 16; ++j) w[k + j] = act(w[k + j]) * o[j];
                         }
@@ -641,7 +725,15 @@ __global__ void __launch_bounds__(NTHREADS, 1) mx4_grouped_kernel(const __grid_c
                 }
             }
         }
+        if (split && share == 0 && !joined) cluster_sync_all();   // (no tile, or given up)
         if (lane == 0) bulk_wait_all();
+    }
+    // a cluster that shares a tile meets twice, every warp of it: when the sums are
+    // there (the epilogue's warps did so above), and when they have been read
+    if (split) {
+        __syncwarp();
+        if (warp < 2 || warp >= 2 + NUM_EPI_WARPS) cluster_sync_all();
+        cluster_sync_all();
     }
     tc_fence_before();
     __syncthreads();
@@ -675,8 +767,9 @@ int launch_mx4_t(const moe_mx4_product_config& c, const Mx4Params& P, cudaStream
     if (const int r = smem_attr_once(mx4_grouped_kernel<CG, F32, DUAL>, Ring<CG>::SMEM, attr_done)) return r;
     const int64_t mt = (c.rows / BM + CG - 1) / CG + (CG - 1) * c.E;   // a segment may round up
     const int64_t units = std::max<int64_t>(1, std::min<int64_t>(mt * P.n_blocks, num_sms() / CG));
+    const int cluster = CG == 2 ? 2 : P.ways;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(CG * units));
+    cfg.gridDim = dim3((unsigned)(P.ways > 1 ? P.ways * P.max_tiles : CG * units));
     cfg.blockDim = dim3(NTHREADS);
     cfg.dynamicSmemBytes = Ring<CG>::SMEM;
     cfg.stream = st;
@@ -684,11 +777,11 @@ int launch_mx4_t(const moe_mx4_product_config& c, const Mx4Params& P, cudaStream
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = CG;
+    attr[1].val.clusterDim.x = cluster;
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = CG == 2 ? 2 : 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     void* args[] = {const_cast<Mx4Params*>(&P)};
     const cudaError_t e = cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(mx4_grouped_kernel<CG, F32, DUAL>), args);
     note_launch();
@@ -741,6 +834,14 @@ int launch_mx4_product(const moe_mx4_product_config& c, const void* xq, const vo
     P.E = c.E; P.K = c.K; P.N = c.N; P.act = c.act;
     const int cols = (pair ? 256 : 128) / (dual ? 2 : 1);       // output columns of a tile
     P.n_blocks = (c.N + cols - 1) / cols;
+    // Few tiles (a token or two in decoding): two or four CTAs share a tile's K, if each
+    // then has four stages or more.  256 rows of 2 experts, K = 14336, N = 4096 (64
+    // tiles): 18 us against 24.  Tiles are bounded by the rows that are not padding.
+    const int64_t real = std::max<int64_t>(1, c.rows - 127 * (int64_t)c.E);
+    const int64_t tiles = (real / BM + std::min<int64_t>(c.E, real)) * P.n_blocks;
+    const int nk = (c.K / 2 + BKB - 1) / BKB;
+    P.ways = pair ? 1 : nk >= 16 && tiles * 4 <= num_sms() ? 4 : nk >= 8 && tiles * 2 <= num_sms() ? 2 : 1;
+    P.max_tiles = (int)std::min<int64_t>(tiles, num_sms());
     return pair ? launch_mx4<2>(c, P, st) : launch_mx4<1>(c, P, st);
 }
 
