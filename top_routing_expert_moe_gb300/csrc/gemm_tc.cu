@@ -674,20 +674,6 @@ int encode_bf16_map(CUtensorMap* m, const void* ptr, uint64_t d0, uint64_t d1, u
     return r == CUDA_SUCCESS ? MOE_OK : MOE_ERR_CUDA;
 }
 
-int encode_map(CUtensorMap* m, CUtensorMapDataType type, const void* ptr, int rank, const uint64_t* dims,
-               const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle swizzle) {
-    EncodeTiledFn fn = encode_fn();
-    if (!fn) return MOE_ERR_CUDA;
-    cuuint64_t d[5], st[4];
-    cuuint32_t b[5], es[5] = {1, 1, 1, 1, 1};
-    for (int i = 0; i < rank; ++i) { d[i] = dims[i]; b[i] = box[i]; }
-    for (int i = 0; i + 1 < rank; ++i) st[i] = strides[i];
-    CUresult r = fn(m, type, (cuuint32_t)rank, const_cast<void*>(ptr), d, st, b, es,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? MOE_OK : MOE_ERR_CUDA;
-}
-
 namespace {
 
 // bf16 map of rank 3 or 4 with 128-byte swizzle: dims[0] contiguous, strides[i] the

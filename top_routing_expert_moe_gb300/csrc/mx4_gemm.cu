@@ -34,6 +34,7 @@
 
 #include <algorithm>
 #include <cstring>
+#include <mutex>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -754,12 +755,43 @@ __global__ void __launch_bounds__(NTHREADS, 1) mx4_grouped_kernel(const __grid_c
         if (_r != MOE_OK) return _r; \
     } while (0)
 
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_fn() {
+    static EncodeTiledFn fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiledFn>(p);
+    });
+    return fn;
+}
+// 3-D map with 128-byte swizzle: dims[0] contiguous, strides[i] the byte stride of dims[i + 1]
+int encode_map(CUtensorMap* m, CUtensorMapDataType type, const void* ptr, const uint64_t (&dims)[3],
+               const uint64_t (&strides)[2], const uint32_t (&box)[3]) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return MOE_ERR_CUDA;
+    const cuuint64_t d[3] = {dims[0], dims[1], dims[2]}, st[2] = {strides[0], strides[1]};
+    const cuuint32_t b[3] = {box[0], box[1], box[2]}, es[3] = {1, 1, 1};
+    return fn(m, type, 3, const_cast<void*>(ptr), d, st, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? MOE_OK
+               : MOE_ERR_CUDA;
+}
+
 // codes [sets, rows, K / 2]: boxes of 128 bytes x `box_rows` rows
 int codes_map(CUtensorMap* m, const void* p, int64_t rows, int sets, int K, int box_rows) {
     const uint64_t dims[3] = {(uint64_t)K / 2, (uint64_t)rows, (uint64_t)sets};
     const uint64_t st[2] = {(uint64_t)K / 2, (uint64_t)K / 2 * rows};
     const uint32_t box[3] = {BKB, (uint32_t)box_rows, 1};
-    return encode_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, p, 3, dims, st, box, CU_TENSOR_MAP_SWIZZLE_128B);
+    return encode_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, p, dims, st, box);
 }
 template <int CG, bool F32, bool DUAL>
 int launch_mx4_t(const moe_mx4_product_config& c, const Mx4Params& P, cudaStream_t st) {
@@ -826,8 +858,8 @@ int launch_mx4_product(const moe_mx4_product_config& c, const void* xq, const vo
     const uint64_t dims[3] = {(uint64_t)c.N, (uint64_t)c.rows, 1};
     const uint64_t strides[2] = {c.N * es, c.N * es * c.rows};
     const uint32_t box[3] = {(uint32_t)(128 / es), 32, 1};
-    MX4_TRY(encode_map(&P.tmO, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, out, 3,
-                       dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B));
+    MX4_TRY(encode_map(&P.tmO, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, out, dims,
+                       strides, box));
     P.offsets = offsets;
     P.status = device_status_ptr();
     P.rows = c.rows;

@@ -14,11 +14,6 @@ int encode_bf16_map(CUtensorMap* m, const void* ptr, uint64_t d0, uint64_t d1, u
                     uint64_t s1, uint64_t s2, uint32_t b0, uint32_t b1,
                     CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B);
 
-// map of any element type and rank <= 5 (host; gemm_tc.cu): dims[0] contiguous,
-// strides[i] the byte stride of dims[i + 1]
-int encode_map(CUtensorMap* m, CUtensorMapDataType type, const void* ptr, int rank, const uint64_t* dims,
-               const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle swizzle);
-
 constexpr unsigned long long WAIT_NS = 4000000000ull;   // bounded waits give up after 4 s
 constexpr unsigned long long DRAIN_NS = 500000000ull;   // draining gives up after 0.5 s
 
