@@ -312,6 +312,10 @@ __global__ void __launch_bounds__(MAXT) block_norm_bwd_kernel(const NormArgs a) 
 // reduction of its row has passed (every thread has taken its share), so that
 // barrier doubles as the ring's release.  A copy that never arrives is given up
 // after the bounded wait (recorded; the outputs are then undefined).
+//
+// 65536 x 4096 bf16, both norms, channel gate: forward 355 us (6.05 TB/s, 0.90 of the
+// copy rate; the direct kernel 526), backward 763 us (4.2 TB/s; 1750), which issues on
+// 56 % of the slots of its 16 warps an SM.
 constexpr int RE = 8;                      // elements of a row per thread
 constexpr int MAX_STAGES = 8;
 
@@ -770,15 +774,26 @@ dim3 norm_block(const moe_norm_config& c) {
 bool wide_rows(const moe_norm_config& c) { return (c.d * (c.dtype == MOE_DTYPE_BF16 ? 2 : 4)) % 16 == 0; }
 
 // The ring's launch: threads, stages and CTAs, or none (0 stages) where the direct
-// kernels serve: rows too wide for three stages, and batches of fewer than RING_ROWS
-// rows an SM, where filling a ring is all there is.
-constexpr int RING_ROWS = 2;
+// kernels serve.  Those win while a batch is short, when filling a ring is most of the
+// work (us, direct and ring, bf16 rows):
+//   forward    1216 x 1024   4.2  6.7    16384 x 512  15.6 16.8    16384 x 1024  34.7 29.4
+//   backward    304 x 1024   8.6  9.0     4864 x 512  18.4 19.0    16384 x 512   51.0 35.8
+//               152 x 4096  15.9 13.9    16384 x 256  25.1 25.8    65536 x 64    55.7 60.9
+// Rows of no whole 16 bytes take the ring as soon as every SM has one (608 x 1001: 7.9
+// and 7.6 forward, 28.8 and 12.5 backward).  Rows too wide for three stages never do.
+bool ring_pays(const moe_norm_config& c, bool backward) {
+    const int64_t n = (int64_t)c.T * c.d;
+    if (c.T < num_sms()) return false;
+    if (!wide_rows(c)) return true;
+    if (!backward) return n >= (10 << 20);
+    return c.d >= 1024 || (c.d >= 128 && n >= (4 << 20));
+}
 struct RingPlan { int threads, stages, grid; size_t smem; };
-RingPlan ring_plan(const moe_norm_config& c, int nin, int regs) {
+RingPlan ring_plan(const moe_norm_config& c, int nin, int regs, bool backward) {
     RingPlan p = {0, 0, 0, 0};
     const int es = c.dtype == MOE_DTYPE_BF16 ? 2 : 4;
     p.threads = ((c.d + RE - 1) / RE + 31) / 32 * 32;
-    if (p.threads > 1024 || c.T < (int64_t)RING_ROWS * num_sms()) return p;
+    if (p.threads > 1024 || !ring_pays(c, backward)) return p;
     const int stage = nin * (int)row_pitch(c.d * es);
     // CTAs an SM by registers and threads, fewer where they would not have three stages
     // each (228 KB an SM, 3 KB of it a CTA's fixed part)
@@ -790,7 +805,7 @@ RingPlan ring_plan(const moe_norm_config& c, int nin, int regs) {
     p.smem = (size_t)p.stages * stage;
     // four rows a CTA, at least, once every SM has one: a CTA's rows share its set-up and,
     // in the backward, one row of partial sums
-    p.grid = (int)std::min<int64_t>((int64_t)per_sm * num_sms(), std::max<int64_t>(num_sms(), c.T / 4));
+    p.grid = (int)std::min<int64_t>(std::min<int64_t>(c.T, (int64_t)per_sm * num_sms()), std::max<int64_t>(num_sms(), c.T / 4));
     return p;
 }
 int fwd_inputs(const moe_norm_config& c) { return 1 + c.leave + (c.gate == MOE_GATE_FULL); }
@@ -798,7 +813,7 @@ bool bwd_needs_u(const moe_norm_config& c) { return c.leave && (c.post_norm || c
 int bwd_inputs(const moe_norm_config& c) {   // with dx_out
     return 1 + 2 * c.enter + bwd_needs_u(c) + (c.gate == MOE_GATE_FULL);
 }
-RingPlan bwd_ring(const moe_norm_config& c) { return ring_plan(c, bwd_inputs(c), 128); }
+RingPlan bwd_ring(const moe_norm_config& c) { return ring_plan(c, bwd_inputs(c), 128, true); }
 
 // CTAs of the backward: as many as the GPU holds, none with less than a row
 int bwd_grid(const moe_norm_config& c) {
@@ -840,7 +855,7 @@ int launch_bwd_ring(const RingPlan& p, const RingArgs& r, cudaStream_t st) {
 
 template <typename T, int VEC>
 int launch_fwd(const moe_norm_config& c, const NormArgs& a, cudaStream_t st) {
-    const RingPlan p = ring_plan(c, fwd_inputs(c), 64);
+    const RingPlan p = ring_plan(c, fwd_inputs(c), 64, false);
     if (p.stages) {
         RingArgs r = {};
         r.n = a;
@@ -879,6 +894,8 @@ int launch_bwd(const moe_norm_config& c, const NormArgs& a, float* dwpre, float*
         MOE_LAUNCH((block_norm_bwd_kernel<T, VEC, 16, 1024>), grid, b, smem, st, a);
     } else if (b.x <= 256) {
         MOE_LAUNCH((block_norm_bwd_kernel<T, VEC, 8, 256>), grid, b, smem, st, a);
+    } else if (b.x <= 512) {
+        MOE_LAUNCH((block_norm_bwd_kernel<T, VEC, 8, 512>), grid, b, smem, st, a);
     } else {
         MOE_LAUNCH((block_norm_bwd_kernel<T, VEC, 8, 1024>), grid, b, smem, st, a);
     }
