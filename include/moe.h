@@ -452,7 +452,7 @@ MOE_API int moe_mx4_quantize(int32_t dtype, int64_t rows, int32_t K, const void*
 
 /* Weights: W [E,K,N] with blocks along K -> codes [E,N,K/2] (each expert's
  * matrix transposed) and E scale sets of moe_mx4_scale_bytes(N, K) bytes.
- * K a multiple of 32, N of 8.                                                */
+ * K a multiple of 32, N of 8, at most 2^21.                                   */
 MOE_API int moe_mx4_quantize_weight(int32_t dtype, int32_t E, int32_t K, int32_t N, const void* W,
                                     void* codes, void* scales, moe_stream_t stream);
 

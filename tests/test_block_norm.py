@@ -102,7 +102,7 @@ def backward64(v, y, leave, post, enter, gate):
         return g, m
     g["dx"], m["dx"] = RA * G, RA * mG
     u = f["u"]
-    ru = 1 / torch.sqrt((u * u).mean(-1, keepdim=True) + EPS) if post else torch.ones(1, 1).double()
+    ru = 1 / torch.sqrt((u * u).mean(-1, keepdim=True) + EPS) if post else torch.ones(1, 1, device=u.device).double()
     n = u * ru * (f["w_post"] if post else 1)
     gt = 1 if gate == "none" else f["gate"][:, None] if gate == "token" else f["gate"]
     dn, mdn = OB * gt * G, (OB * gt * mG).abs() if gate != "none" else OB * mG
@@ -277,6 +277,30 @@ def test_long_batches_of_every_form(form, dt):
 def test_long_batches_of_every_width(T, d, dt):
     check(T, d, dt, (1, 1, 1, "channel"), seed=d)
     check(T, d, dt, (1, 1, 1, "full"), seed=d)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("form", [(0, 0, 1, "none"), (1, 0, 0, "token"), (1, 1, 0, "channel"), (1, 0, 1, "full"),
+                                  (1, 1, 1, "channel"), (1, 1, 1, "full"), (1, 1, 1, "token")])
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,d", [(20600, 520), (2700, 4104), (1300, 8192)])
+def test_batches_of_more_than_ten_million_elements(T, d, dt, form):
+    """Both passes of aligned rows through the ring, against the formulas in 64 bits on the GPU."""
+    v = make(T, d, dt, *form, seed=T)
+    n = moe.BlockNorm(config(T, d, dt, *form))
+    c = {k: t.cuda() for k, t in v.items()}
+    args = {k: c[k] for k in ("u", "w_pre", "w_post", "gate") if k in c}
+    x_out, z = n.forward(c["x"], **args)
+    y, my, z64, mz = (None if t is None else t.cpu() for t in forward64(c, *form))
+    if form[0]:
+        near(x_out, y, my, 64, "x_out")
+    if form[2]:
+        near(z, z64, mz, 64, "z")
+    g = n.backward(x_out, dx_out=c["dx_out"], dz=c.get("dz"), **args)
+    g64, m64 = backward64(c, x_out, *form)
+    for k in g64:
+        near(g[k], g64[k].cpu(), m64[k].cpu(), 64 + (T if g64[k].shape == (d,) else 0), k)
+    assert moe.last_device_status() == 0
 
 
 @pytest.mark.gpu

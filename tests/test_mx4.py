@@ -100,7 +100,9 @@ def test_refusals():
     assert moe.check_mx4_product_config(moe.MX4ProductConfig(**ok)) == moe.OK
     for b in (dict(rows=0), dict(K=0), dict(N=0), dict(E=0), dict(act=3), dict(out_dtype=2)):
         assert moe.check_mx4_product_config(moe.MX4ProductConfig(**{**ok, **b})) == moe.ERR_INVALID_ARG, b
-    for b in (dict(K=40), dict(N=12), dict(E=65)):
+    assert lib.moe_mx4_quantize_weight(moe.F32, 1, 32, 2 ** 21 + 8, p, p, p, None) == moe.ERR_UNSUPPORTED
+    assert lib.moe_mx4_dequantize(moe.F32, 2 ** 20, 2 ** 20, 32, p, p, p, None) == moe.ERR_UNSUPPORTED
+    for b in (dict(K=40), dict(N=12), dict(E=65), dict(N=2 ** 21 + 8), dict(rows=2 ** 30, N=2 ** 15)):
         assert moe.check_mx4_product_config(moe.MX4ProductConfig(**{**ok, **b})) == moe.ERR_UNSUPPORTED, b
     plain, dual = moe.MX4ProductConfig(**ok), moe.MX4ProductConfig(act=moe.MX4_ACT_SWIGLU, **ok)
     for i in range(8):

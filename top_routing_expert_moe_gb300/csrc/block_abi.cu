@@ -142,7 +142,8 @@ int moe_mx4_quantize_weight(int32_t dtype, int32_t E, int32_t K, int32_t N, cons
     if (!is_dtype(dtype) || E < 1) return MOE_ERR_INVALID_ARG;
     const int r = mx4_shape(N, K);
     if (r) return r;
-    if (N % 8 || N > (1 << 22) || E > 65535) return MOE_ERR_UNSUPPORTED;
+    // (the launch's grid: 64-column tiles and experts)
+    if (N % 8 || N > (1 << 21) || E > 65535) return MOE_ERR_UNSUPPORTED;
     if (!ok_ptr(W) || !ok_ptr(codes) || !ok_ptr(scales)) return MOE_ERR_INVALID_ARG;
     return launch_mx4_quantize_weight(dtype, E, K, N, W, codes, scales, (cudaStream_t)stream);
 }
@@ -152,6 +153,7 @@ int moe_mx4_dequantize(int32_t dtype, int32_t sets, int64_t rows, int32_t K, con
     if (!is_dtype(dtype) || sets < 1) return MOE_ERR_INVALID_ARG;
     const int r = mx4_shape(rows, K);
     if (r) return r;
+    if ((rows + 127) / 128 * sets > (1 << 26)) return MOE_ERR_UNSUPPORTED;   // 32-bit tile counts
     if (!ok_ptr(codes) || !ok_ptr(scales) || !ok_ptr(out)) return MOE_ERR_INVALID_ARG;
     return launch_mx4_dequantize(dtype, sets, rows, K, codes, scales, out, (cudaStream_t)stream);
 }
@@ -161,7 +163,9 @@ int moe_check_mx4_product_config(const moe_mx4_product_config* c) {
     if (c->act < MOE_MX4_ACT_NONE || c->act > MOE_MX4_ACT_SWIGLU) return MOE_ERR_INVALID_ARG;
     const int r = mx4_shape(c->rows, c->K);
     if (r) return r;
-    if (c->N % 8 || c->N > (1 << 22) || c->E > 64 || c->rows > (1 << 30)) return MOE_ERR_UNSUPPORTED;
+    if (c->N % 8 || c->N > (1 << 21) || c->E > 64 || c->rows > (1 << 30)) return MOE_ERR_UNSUPPORTED;
+    // 32-bit tile counts, at the smallest tile's 64 columns
+    if ((c->rows / 128 + c->E) * (((int64_t)c->N + 63) / 64) > (1LL << 30)) return MOE_ERR_UNSUPPORTED;
     return MOE_OK;
 }
 
