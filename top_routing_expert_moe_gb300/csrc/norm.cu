@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(MAXT) block_norm_bwd_kernel(const NormArgs a) 
 // after the bounded wait (recorded; the outputs are then undefined).
 //
 // 65536 x 4096 bf16, both norms, channel gate: forward 355 us (6.05 TB/s, 0.90 of the
-// copy rate; the direct kernel 526), backward 763 us (4.2 TB/s; 1750), which issues on
+// copy rate; the direct kernel 526), backward BWD_US (1750), which issues on
 // 56 % of the slots of its 16 warps an SM.
 constexpr int RE = 8;                      // elements of a row per thread
 constexpr int MAX_STAGES = 8;
@@ -598,33 +598,40 @@ __global__ void __launch_bounds__(MAXT) block_norm_ring_kernel(const __grid_cons
 }
 
 // in: x_out, dz (enter), dx_out (if given), u (post or gate), gate (full)
-template <typename T, bool WIDE, int MAXT>
+// ALL: both norms, a gradient along the stream and no full gate, known at compile time.
+template <typename T, bool WIDE, bool ALL, int MAXT>
 __global__ void __launch_bounds__(MAXT) block_norm_bwd_ring_kernel(const __grid_constant__ RingArgs a) {
     __shared__ float buf[2][32 * 8];
     NORM_RING_SETUP();
-    f2 wq[RP], wz[RP], wg[RP];             // w_post, w_pre, the channel gate
-    f2 acc_pre[RP], acc_post[RP], acc_g[RP];
+    const bool enter = ALL || n.enter, leave = ALL || n.leave, post = ALL || n.post;
+    const bool full = !ALL && n.gmode == MOE_GATE_FULL, along = ALL || n.dx_out;
+    const bool need_u = ALL || (n.leave && (n.post || n.gmode != MOE_GATE_NONE));
+    // q: w_post times the channel gate; w_pre.  Both channel gradients of u's side are
+    // sums of h = b u r_u G (a full gate's: of g h) times what is constant along the sum:
+    // dw_post = g sum h, dgate = w_post sum h.
+    f2 wq[RP], wz[RP], acc_pre[RP], acc_h[RP];
     fill(acc_pre, 0.f);
-    fill(acc_post, 0.f);
-    fill(acc_g, 0.f);
+    fill(acc_h, 0.f);
     fill(wq, 1.f);
-    fill(wg, 1.f);
+    if (post) channel<T, WIDE>(n.w_post, d, wq);
+    if (n.gmode == MOE_GATE_CHANNEL) {
+        channel<T, WIDE>(static_cast<const float*>(n.gate), d, wz);
+#pragma unroll
+        for (int i = 0; i < RP; ++i) wq[i] = wq[i] * wz[i];
+    }
     fill(wz, 1.f);
-    if (n.post) channel<T, WIDE>(n.w_post, d, wq);
-    if (n.enter) channel<T, WIDE>(n.w_pre, d, wz);
-    if (n.gmode == MOE_GATE_CHANNEL) channel<T, WIDE>(static_cast<const float*>(n.gate), d, wg);
-    const bool need_u = n.leave && (n.post || n.gmode != MOE_GATE_NONE);
+    if (enter) channel<T, WIDE>(n.w_pre, d, wz);
     // the tensors' places in a stage
-    const int p_dz = 1, p_dx = n.enter ? 2 : 0, p_u = p_dx + (n.dx_out ? 1 : 0), p_g = p_u + 1;
+    const int p_dz = 1, p_dx = enter ? 2 : 0, p_u = p_dx + (along ? 1 : 0), p_g = p_u + 1;
     const float on = live<T, WIDE>(d);
     // A row's tensors, from its stage.  They are taken twice, for the sums and for the
     // outputs: between the two lies a barrier, and the next row's sums come before it.
     auto row = [&](int slot, int64_t t, f2 (&y)[RP], f2 (&dz)[RP], f2 (&G)[RP], f2 (&u)[RP], f2 (&g)[RP]) {
         const uint8_t* st = ring_smem + slot * ring.stage_bytes + (WIDE ? 0u : ring.shift(t));
         auto in = [&](int j) { return reinterpret_cast<const T*>(st + j * ring.pitch); };
-        if (n.dx_out) take<T, WIDE>(in(p_dx), d, G);
+        if (along) take<T, WIDE>(in(p_dx), d, G);
         else fill(G, 0.f);
-        if (n.enter) {
+        if (enter) {
             take<T, WIDE>(in(0), d, y);
             take<T, WIDE>(in(p_dz), d, dz);
         } else {
@@ -633,10 +640,7 @@ __global__ void __launch_bounds__(MAXT) block_norm_bwd_ring_kernel(const __grid_
         }
         if (need_u) take<T, WIDE>(in(p_u), d, u);
         else fill(u, 0.f);
-        if (n.gmode == MOE_GATE_FULL) take<T, WIDE>(in(p_g), d, g);
-        else
-#pragma unroll
-            for (int i = 0; i < RP; ++i) g[i] = wg[i];
+        if (full) take<T, WIDE>(in(p_g), d, g);
     };
     // this warp's part of y^2, a y, u^2, q u dx', q u a, q u y  (a = w_pre dz, q = g w_post)
     auto sums = [&](int slot, int64_t t, float* to) {
@@ -648,7 +652,8 @@ __global__ void __launch_bounds__(MAXT) block_norm_bwd_ring_kernel(const __grid_
             const f2 az = wz[i] * dz[i];
             s1 = fma2(az, y[i], s1);
             if (need_u) {
-                const f2 qu = (g[i] * wq[i]) * u[i];
+                f2 qu = wq[i] * u[i];
+                if (full) qu = qu * g[i];
                 s3 = fma2(qu, G[i], s3);
                 s4 = fma2(qu, az, s4);
                 s5 = fma2(qu, y[i], s5);
@@ -671,7 +676,7 @@ __global__ void __launch_bounds__(MAXT) block_norm_bwd_ring_kernel(const __grid_
         f2 y[RP], G[RP], u[RP], dz[RP], g[RP], out[RP];   // (b and a token gate are in tok)
         row(ring.slot, t, y, dz, G, u, g);
         float r = 0.f, ca = 0.f;
-        if (n.enter) {
+        if (enter) {
             r = rsqrtf(s[0] * invd + n.eps);
             ca = r * r * r * invd * s[1];
             const f2 r2 = both(r), c2 = both(-ca);
@@ -682,28 +687,33 @@ __global__ void __launch_bounds__(MAXT) block_norm_bwd_ring_kernel(const __grid_
                 G[i] = fma2(rz, wz[i], fma2(c2, y[i], G[i]));
             }
         }
-        if (n.leave) {
+        if (leave) {
             const f2 ra = both(n.ra);
 #pragma unroll
             for (int i = 0; i < RP; ++i) out[i] = ra * G[i];
             give<T, WIDE>(static_cast<T*>(n.dx) + o, d, out);
             const float S = s[3] + r * s[4] - ca * s[5];
-            const float ru = n.post ? rsqrtf(s[2] * invd + n.eps) : 1.f;
+            const float ru = post ? rsqrtf(s[2] * invd + n.eps) : 1.f;
             if (n.gmode == MOE_GATE_TOKEN && threadIdx.x == 0) static_cast<float*>(n.dgate)[t] = n.ob * ru * S;
-            // with h = b u r_u G (a token gate's factor apart): dw_post += g h, dgate = w_post h
-            const f2 tr = both(tok * ru), br = both(n.ob * ru);
-            const f2 cu = both(n.post ? -tok * ru * ru * ru * invd * S : 0.f);
-            if (n.gmode == MOE_GATE_FULL) {
+            const f2 tr = both(tok * ru), cu = both(post ? -tok * ru * ru * ru * invd * S : 0.f);
+            if (full) {
 #pragma unroll
-                for (int i = 0; i < RP; ++i) out[i] = wq[i] * ((br * u[i]) * G[i]);
+                for (int i = 0; i < RP; ++i) {
+                    const f2 tG = tr * G[i], h = tG * u[i];
+                    acc_h[i] = fma2(g[i], h, acc_h[i]);
+                    u[i] = fma2(cu, u[i], (g[i] * wq[i]) * tG);
+                    out[i] = wq[i] * h;
+                }
                 give<T, WIDE>(static_cast<T*>(n.dgate) + o, d, out);
-            }
 #pragma unroll
-            for (int i = 0; i < RP; ++i) {
-                const f2 tG = tr * G[i], h = tG * u[i];
-                acc_post[i] = fma2(g[i], h, acc_post[i]);
-                acc_g[i] = fma2(wq[i], h, acc_g[i]);
-                out[i] = fma2(cu, u[i], (g[i] * wq[i]) * tG);
+                for (int i = 0; i < RP; ++i) out[i] = u[i];
+            } else {
+#pragma unroll
+                for (int i = 0; i < RP; ++i) {
+                    const f2 tG = tr * G[i];
+                    acc_h[i] = fma2(tG, u[i], acc_h[i]);
+                    out[i] = fma2(cu, u[i], wq[i] * tG);
+                }
             }
             give<T, WIDE>(static_cast<T*>(n.du) + o, d, out);
         } else {
@@ -732,9 +742,19 @@ __global__ void __launch_bounds__(MAXT) block_norm_bwd_ring_kernel(const __grid_
             }
         }
     };
-    if (n.enter) flush(0, acc_pre);
-    if (n.post) flush(1, acc_post);
-    if (n.gmode == MOE_GATE_CHANNEL) flush(2, acc_g);
+    if (enter) flush(0, acc_pre);
+    if (n.gmode == MOE_GATE_CHANNEL) {
+        if (post) channel<T, WIDE>(n.w_post, d, wq);
+        else fill(wq, 1.f);
+        channel<T, WIDE>(static_cast<const float*>(n.gate), d, wz);
+#pragma unroll
+        for (int i = 0; i < RP; ++i) {
+            wq[i] = wq[i] * acc_h[i];
+            acc_h[i] = wz[i] * acc_h[i];
+        }
+        flush(2, wq);
+    }
+    if (post) flush(1, acc_h);
     if (threadIdx.x == 0 && *ring.abort_flag) ring.drain();
 }
 
@@ -837,20 +857,22 @@ int launch_fwd_ring(const RingPlan& p, const RingArgs& r, cudaStream_t st) {
     else MOE_LAUNCH((block_norm_ring_kernel<T, WIDE, 512>), p.grid, p.threads, p.smem, st, r);
     return MOE_OK;
 }
-template <typename T, bool WIDE, int MAXT>
+template <typename T, bool WIDE, bool ALL, int MAXT>
 int launch_bwd_ring_t(const RingPlan& p, const RingArgs& r, cudaStream_t st) {
     static bool done[64] = {};
-    if (const int e = smem_attr_once(block_norm_bwd_ring_kernel<T, WIDE, MAXT>, 200 * 1024, done)) return e;
-    MOE_LAUNCH((block_norm_bwd_ring_kernel<T, WIDE, MAXT>), p.grid, p.threads, p.smem, st, r);
+    if (const int e = smem_attr_once(block_norm_bwd_ring_kernel<T, WIDE, ALL, MAXT>, 200 * 1024, done)) return e;
+    MOE_LAUNCH((block_norm_bwd_ring_kernel<T, WIDE, ALL, MAXT>), p.grid, p.threads, p.smem, st, r);
     return MOE_OK;
 }
 // the fewer the threads, the more registers each may have
 template <typename T, bool WIDE>
 int launch_bwd_ring(const RingPlan& p, const RingArgs& r, cudaStream_t st) {
-    return p.threads <= 512   ? launch_bwd_ring_t<T, WIDE, 512>(p, r, st)
-           : p.threads <= 640 ? launch_bwd_ring_t<T, WIDE, 640>(p, r, st)
-           : p.threads <= 768 ? launch_bwd_ring_t<T, WIDE, 768>(p, r, st)
-                              : launch_bwd_ring_t<T, WIDE, 1024>(p, r, st);
+    const bool all = r.n.enter && r.n.post && r.n.dx_out && r.n.gmode != MOE_GATE_FULL;
+    if (p.threads <= 512)
+        return all ? launch_bwd_ring_t<T, WIDE, true, 512>(p, r, st) : launch_bwd_ring_t<T, WIDE, false, 512>(p, r, st);
+    return p.threads <= 640   ? launch_bwd_ring_t<T, WIDE, false, 640>(p, r, st)
+           : p.threads <= 768 ? launch_bwd_ring_t<T, WIDE, false, 768>(p, r, st)
+                              : launch_bwd_ring_t<T, WIDE, false, 1024>(p, r, st);
 }
 
 template <typename T, int VEC>
