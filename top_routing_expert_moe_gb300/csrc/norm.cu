@@ -313,9 +313,8 @@ __global__ void __launch_bounds__(MAXT) block_norm_bwd_kernel(const NormArgs a) 
 // barrier doubles as the ring's release.  A copy that never arrives is given up
 // after the bounded wait (recorded; the outputs are then undefined).
 //
-// 65536 x 4096 bf16, both norms, channel gate: forward 355 us (6.05 TB/s, 0.90 of the
-// copy rate; the direct kernel 526), backward BWD_US (1750), which issues on
-// 56 % of the slots of its 16 warps an SM.
+// 65536 x 4096 bf16, both norms, channel gate: forward 339 us (6.3 TB/s, 0.95 of the
+// copy rate; the direct kernel 526), backward 550 us (5.9 TB/s, 0.87; 1750).
 constexpr int RE = 8;                      // elements of a row per thread
 constexpr int MAX_STAGES = 8;
 
@@ -446,6 +445,32 @@ __device__ __forceinline__ float dot2(const f2 (&a)[RP], const f2 (&b)[RP]) {
     return sum2(s);
 }
 
+// The parts of a pass, known at compile time for the usual forms: registers and
+// issue slots that the other parts would take are what these kernels are short of
+// (both norms, backward: 711 us with run-time flags, 550 so; 8192 wide 618 and 275).
+enum Form {
+    FORM_ANY,        // by the run-time flags
+    FORM_BOTH,       // leave with its norm, enter; a gate that is not full; dx_out given
+    FORM_ADD,        // leave without norm or gate, enter; dx_out given
+    FORM_ENTER,      // enter alone; dx_out given
+    FORM_LEAVE,      // leave with its norm, no enter; a gate that is not full
+};
+struct Parts { bool leave, post, enter, full, along; };
+template <int FORM>
+__device__ __forceinline__ Parts parts_of(const NormArgs& n) {
+    if constexpr (FORM == FORM_BOTH) return {true, true, true, false, true};
+    if constexpr (FORM == FORM_ADD) return {true, false, true, false, true};
+    if constexpr (FORM == FORM_ENTER) return {false, false, true, false, true};
+    if constexpr (FORM == FORM_LEAVE) return {true, true, false, false, true};
+    return {n.leave != 0, n.post != 0, n.enter != 0, n.gmode == MOE_GATE_FULL, n.dx_out != nullptr};
+}
+inline Form form_of(const NormArgs& n, bool backward) {
+    if (n.gmode == MOE_GATE_FULL || (backward && !n.dx_out)) return FORM_ANY;
+    if (n.leave && n.post) return n.enter ? FORM_BOTH : FORM_LEAVE;
+    if (!n.leave) return FORM_ENTER;
+    return n.enter && n.gmode == MOE_GATE_NONE ? FORM_ADD : FORM_ANY;
+}
+
 // Rows blockIdx.x + i gridDim.x pass through the stages in turn.  `slot` and
 // `phase` follow the row being worked on.  One warp watches the barriers: it waits
 // for the next row's stage before it joins the current row's last reduction, whose
@@ -541,44 +566,46 @@ template <bool WIDE> struct RowRing {
     ring.wait(a, 0, 0)
 
 // in: x, u (leave), gate (full)
-template <typename T, bool WIDE, int MAXT>
+template <typename T, bool WIDE, int FORM, int MAXT>
 __global__ void __launch_bounds__(MAXT) block_norm_ring_kernel(const __grid_constant__ RingArgs a) {
     __shared__ float buf[2][32];
     NORM_RING_SETUP();
+    const Parts p = parts_of<FORM>(n);
+    const int gmode = FORM == FORM_ADD || FORM == FORM_ENTER ? MOE_GATE_NONE : n.gmode;
     const float on = live<T, WIDE>(d);
     f2 wq[RP], wz[RP];                     // g w_post, w_pre
     fill(wq, 1.f);
-    if (n.post) channel<T, WIDE>(n.w_post, d, wq);
-    if (n.gmode == MOE_GATE_CHANNEL) {
+    if (p.post) channel<T, WIDE>(n.w_post, d, wq);
+    if (gmode == MOE_GATE_CHANNEL) {
         channel<T, WIDE>(static_cast<const float*>(n.gate), d, wz);
 #pragma unroll
         for (int i = 0; i < RP; ++i) wq[i] = wq[i] * wz[i];
     }
-    if (n.enter) channel<T, WIDE>(n.w_pre, d, wz);
+    if (p.enter) channel<T, WIDE>(n.w_pre, d, wz);
     for (int64_t t = blockIdx.x; t < n.T; t += gridDim.x, ring.next()) {
         const uint8_t* st = ring_smem + ring.slot * ring.stage_bytes + (WIDE ? 0u : ring.shift(t));
         auto in = [&](int j) { return reinterpret_cast<const T*>(st + j * ring.pitch); };
         const size_t o = (size_t)t * d;
         float tok = n.ob;
-        if (n.gmode == MOE_GATE_TOKEN) tok *= __ldg(static_cast<const float*>(n.gate) + t);
+        if (gmode == MOE_GATE_TOKEN) tok *= __ldg(static_cast<const float*>(n.gate) + t);
         f2 y[RP], u[RP];
         take<T, WIDE>(in(0), d, y);
-        if (n.leave) {
+        if (p.leave) {
             take<T, WIDE>(in(1), d, u);
-            const float s = n.post ? on * dot2(u, u) : 0.f;
-            if (n.gmode == MOE_GATE_FULL) {
+            const float s = p.post ? on * dot2(u, u) : 0.f;
+            if (p.full) {
                 f2 g[RP];
                 take<T, WIDE>(in(2), d, g);
 #pragma unroll
                 for (int i = 0; i < RP; ++i) u[i] = u[i] * g[i];
             }
-            if (n.post) tok *= rsqrtf(row_sum(s, buf[0]) * invd + n.eps);
+            if (p.post) tok *= rsqrtf(row_sum(s, buf[0]) * invd + n.eps);
             const f2 c = both(tok), ra = both(n.ra);
 #pragma unroll
             for (int i = 0; i < RP; ++i) y[i] = fma2(c * wq[i], u[i], ra * y[i]);
             give<T, WIDE>(static_cast<T*>(n.x_out) + o, d, y);
         }
-        if (n.enter) {
+        if (p.enter) {
             const float s = on * dot2(y, y);
             ring.wait_next(a, t);
             const f2 r = both(rsqrtf(row_sum(s, buf[1]) * invd + n.eps));
@@ -588,8 +615,8 @@ __global__ void __launch_bounds__(MAXT) block_norm_ring_kernel(const __grid_cons
         }
         // both buffers alternate with two norms; otherwise a barrier keeps a row's sums
         // (and with no norm at all its stage) from the next row
-        if (!(n.post && n.enter) || blockDim.x <= 32) {
-            if (!n.enter) ring.wait_next(a, t);
+        if (!(p.post && p.enter) || blockDim.x <= 32) {
+            if (!p.enter) ring.wait_next(a, t);
             __syncthreads();
         }
         if (threadIdx.x == 0) ring.refill(a, ring_smem, t);
@@ -598,14 +625,14 @@ __global__ void __launch_bounds__(MAXT) block_norm_ring_kernel(const __grid_cons
 }
 
 // in: x_out, dz (enter), dx_out (if given), u (post or gate), gate (full)
-// ALL: both norms, a gradient along the stream and no full gate, known at compile time.
-template <typename T, bool WIDE, bool ALL, int MAXT>
+template <typename T, bool WIDE, int FORM, int MAXT>
 __global__ void __launch_bounds__(MAXT) block_norm_bwd_ring_kernel(const __grid_constant__ RingArgs a) {
     __shared__ float buf[2][32 * 8];
     NORM_RING_SETUP();
-    const bool enter = ALL || n.enter, leave = ALL || n.leave, post = ALL || n.post;
-    const bool full = !ALL && n.gmode == MOE_GATE_FULL, along = ALL || n.dx_out;
-    const bool need_u = ALL || (n.leave && (n.post || n.gmode != MOE_GATE_NONE));
+    const Parts p = parts_of<FORM>(n);
+    const bool enter = p.enter, leave = p.leave, post = p.post, full = p.full, along = p.along;
+    const int gmode = FORM == FORM_ADD || FORM == FORM_ENTER ? MOE_GATE_NONE : n.gmode;
+    const bool need_u = leave && (post || gmode != MOE_GATE_NONE);
     // q: w_post times the channel gate; w_pre.  Both channel gradients of u's side are
     // sums of h = b u r_u G (a full gate's: of g h) times what is constant along the sum:
     // dw_post = g sum h, dgate = w_post sum h.
@@ -614,7 +641,7 @@ __global__ void __launch_bounds__(MAXT) block_norm_bwd_ring_kernel(const __grid_
     fill(acc_h, 0.f);
     fill(wq, 1.f);
     if (post) channel<T, WIDE>(n.w_post, d, wq);
-    if (n.gmode == MOE_GATE_CHANNEL) {
+    if (gmode == MOE_GATE_CHANNEL) {
         channel<T, WIDE>(static_cast<const float*>(n.gate), d, wz);
 #pragma unroll
         for (int i = 0; i < RP; ++i) wq[i] = wq[i] * wz[i];
@@ -670,7 +697,7 @@ __global__ void __launch_bounds__(MAXT) block_norm_bwd_ring_kernel(const __grid_
         if (t + gridDim.x < n.T) sums(ring.ahead(1), t + gridDim.x, buf[par ^ 1]);
         const size_t o = (size_t)t * d;
         float tok = n.ob;
-        if (n.gmode == MOE_GATE_TOKEN) tok *= __ldg(static_cast<const float*>(n.gate) + t);
+        if (gmode == MOE_GATE_TOKEN) tok *= __ldg(static_cast<const float*>(n.gate) + t);
         float s[6];
         get_sums6(s, buf[par]);
         f2 y[RP], G[RP], u[RP], dz[RP], g[RP], out[RP];   // (b and a token gate are in tok)
@@ -694,7 +721,7 @@ __global__ void __launch_bounds__(MAXT) block_norm_bwd_ring_kernel(const __grid_
             give<T, WIDE>(static_cast<T*>(n.dx) + o, d, out);
             const float S = s[3] + r * s[4] - ca * s[5];
             const float ru = post ? rsqrtf(s[2] * invd + n.eps) : 1.f;
-            if (n.gmode == MOE_GATE_TOKEN && threadIdx.x == 0) static_cast<float*>(n.dgate)[t] = n.ob * ru * S;
+            if (gmode == MOE_GATE_TOKEN && threadIdx.x == 0) static_cast<float*>(n.dgate)[t] = n.ob * ru * S;
             const f2 tr = both(tok * ru), cu = both(post ? -tok * ru * ru * ru * invd * S : 0.f);
             if (full) {
 #pragma unroll
@@ -743,7 +770,7 @@ __global__ void __launch_bounds__(MAXT) block_norm_bwd_ring_kernel(const __grid_
         }
     };
     if (enter) flush(0, acc_pre);
-    if (n.gmode == MOE_GATE_CHANNEL) {
+    if (gmode == MOE_GATE_CHANNEL) {
         if (post) channel<T, WIDE>(n.w_post, d, wq);
         else fill(wq, 1.f);
         channel<T, WIDE>(static_cast<const float*>(n.gate), d, wz);
@@ -833,7 +860,16 @@ bool bwd_needs_u(const moe_norm_config& c) { return c.leave && (c.post_norm || c
 int bwd_inputs(const moe_norm_config& c) {   // with dx_out
     return 1 + 2 * c.enter + bwd_needs_u(c) + (c.gate == MOE_GATE_FULL);
 }
-RingPlan bwd_ring(const moe_norm_config& c) { return ring_plan(c, bwd_inputs(c), 128, true); }
+// (the workspace is sized by this plan, so it does not look at which gradients are given:
+// a call without dx_out only has more CTAs than its registers let run at once)
+RingPlan bwd_ring(const moe_norm_config& c) {
+    int regs = 128;
+    if (c.gate != MOE_GATE_FULL) {
+        if (c.leave && c.post_norm) regs = c.enter ? 100 : 64;
+        else if (!c.leave || (c.enter && c.gate == MOE_GATE_NONE)) regs = 64;
+    }
+    return ring_plan(c, bwd_inputs(c), regs, true);
+}
 
 // CTAs of the backward: as many as the GPU holds, none with less than a row
 int bwd_grid(const moe_norm_config& c) {
@@ -847,37 +883,51 @@ int bwd_grid(const moe_norm_config& c) {
     return (int)std::min<int64_t>((c.T + rows - 1) / rows, (int64_t)num_sms() * per_sm);
 }
 
-template <typename T, bool WIDE>
-int launch_fwd_ring(const RingPlan& p, const RingArgs& r, cudaStream_t st) {
-    static bool done[2][64] = {};
-    const bool big = p.threads > 512;
-    if (const int e = big ? smem_attr_once(block_norm_ring_kernel<T, WIDE, 1024>, 200 * 1024, done[0])
-                          : smem_attr_once(block_norm_ring_kernel<T, WIDE, 512>, 200 * 1024, done[1])) return e;
-    if (big) MOE_LAUNCH((block_norm_ring_kernel<T, WIDE, 1024>), p.grid, p.threads, p.smem, st, r);
-    else MOE_LAUNCH((block_norm_ring_kernel<T, WIDE, 512>), p.grid, p.threads, p.smem, st, r);
+template <typename T, bool WIDE, int FORM, int MAXT>
+int launch_fwd_ring_t(const RingPlan& p, const RingArgs& r, cudaStream_t st) {
+    static bool done[64] = {};
+    if (const int e = smem_attr_once(block_norm_ring_kernel<T, WIDE, FORM, MAXT>, 200 * 1024, done)) return e;
+    MOE_LAUNCH((block_norm_ring_kernel<T, WIDE, FORM, MAXT>), p.grid, p.threads, p.smem, st, r);
     return MOE_OK;
 }
-template <typename T, bool WIDE, bool ALL, int MAXT>
+// (64 registers are enough for any width)
+template <typename T, bool WIDE>
+int launch_fwd_ring(const RingPlan& p, const RingArgs& r, cudaStream_t st) {
+    switch (form_of(r.n, false)) {
+        case FORM_BOTH: return launch_fwd_ring_t<T, WIDE, FORM_BOTH, 1024>(p, r, st);
+        case FORM_ADD: return launch_fwd_ring_t<T, WIDE, FORM_ADD, 1024>(p, r, st);
+        case FORM_ENTER: return launch_fwd_ring_t<T, WIDE, FORM_ENTER, 1024>(p, r, st);
+        default: return launch_fwd_ring_t<T, WIDE, FORM_ANY, 1024>(p, r, st);
+    }
+}
+template <typename T, bool WIDE, int FORM, int MAXT>
 int launch_bwd_ring_t(const RingPlan& p, const RingArgs& r, cudaStream_t st) {
     static bool done[64] = {};
-    if (const int e = smem_attr_once(block_norm_bwd_ring_kernel<T, WIDE, ALL, MAXT>, 200 * 1024, done)) return e;
-    MOE_LAUNCH((block_norm_bwd_ring_kernel<T, WIDE, ALL, MAXT>), p.grid, p.threads, p.smem, st, r);
+    if (const int e = smem_attr_once(block_norm_bwd_ring_kernel<T, WIDE, FORM, MAXT>, 200 * 1024, done)) return e;
+    MOE_LAUNCH((block_norm_bwd_ring_kernel<T, WIDE, FORM, MAXT>), p.grid, p.threads, p.smem, st, r);
     return MOE_OK;
 }
 // the fewer the threads, the more registers each may have
+template <typename T, bool WIDE, int FORM>
+int launch_bwd_ring_f(const RingPlan& p, const RingArgs& r, cudaStream_t st) {
+    return p.threads <= 512   ? launch_bwd_ring_t<T, WIDE, FORM, 512>(p, r, st)
+           : p.threads <= 768 ? launch_bwd_ring_t<T, WIDE, FORM, 768>(p, r, st)
+                              : launch_bwd_ring_t<T, WIDE, FORM, 1024>(p, r, st);
+}
 template <typename T, bool WIDE>
 int launch_bwd_ring(const RingPlan& p, const RingArgs& r, cudaStream_t st) {
-    const bool all = r.n.enter && r.n.post && r.n.dx_out && r.n.gmode != MOE_GATE_FULL;
-    if (p.threads <= 512)
-        return all ? launch_bwd_ring_t<T, WIDE, true, 512>(p, r, st) : launch_bwd_ring_t<T, WIDE, false, 512>(p, r, st);
-    return p.threads <= 640   ? launch_bwd_ring_t<T, WIDE, false, 640>(p, r, st)
-           : p.threads <= 768 ? launch_bwd_ring_t<T, WIDE, false, 768>(p, r, st)
-                              : launch_bwd_ring_t<T, WIDE, false, 1024>(p, r, st);
+    switch (form_of(r.n, true)) {
+        case FORM_BOTH: return launch_bwd_ring_f<T, WIDE, FORM_BOTH>(p, r, st);
+        case FORM_ADD: return launch_bwd_ring_f<T, WIDE, FORM_ADD>(p, r, st);
+        case FORM_ENTER: return launch_bwd_ring_f<T, WIDE, FORM_ENTER>(p, r, st);
+        case FORM_LEAVE: return launch_bwd_ring_f<T, WIDE, FORM_LEAVE>(p, r, st);
+        default: return launch_bwd_ring_f<T, WIDE, FORM_ANY>(p, r, st);
+    }
 }
 
 template <typename T, int VEC>
 int launch_fwd(const moe_norm_config& c, const NormArgs& a, cudaStream_t st) {
-    const RingPlan p = ring_plan(c, fwd_inputs(c), 64, false);
+    const RingPlan p = ring_plan(c, fwd_inputs(c), c.leave ? 64 : 32, false);
     if (p.stages) {
         RingArgs r = {};
         r.n = a;
