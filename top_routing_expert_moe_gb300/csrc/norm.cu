@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(MAXT) block_norm_bwd_kernel(const NormArgs a) 
 // barrier doubles as the ring's release.  A copy that never arrives is given up
 // after the bounded wait (recorded; the outputs are then undefined).
 //
-// 65536 x 4096 bf16, both norms, channel gate: forward 339 us (6.3 TB/s, 0.95 of the
+// 65536 x 4096 bf16, both norms, channel gate: forward 334 us (6.4 TB/s, 0.96 of the
 // copy rate; the direct kernel 526), backward 550 us (5.9 TB/s, 0.87; 1750).
 constexpr int RE = 8;                      // elements of a row per thread
 constexpr int MAX_STAGES = 8;
@@ -582,7 +582,12 @@ __global__ void __launch_bounds__(MAXT) block_norm_ring_kernel(const __grid_cons
         for (int i = 0; i < RP; ++i) wq[i] = wq[i] * wz[i];
     }
     if (p.enter) channel<T, WIDE>(n.w_pre, d, wz);
-    for (int64_t t = blockIdx.x; t < n.T; t += gridDim.x, ring.next()) {
+    // Two norms alternate their buffers, entering alone alternates from row to row, so a
+    // row's last reduction is the only barrier that is needed after it.  Leaving with one
+    // norm or none meets once more (plain addition and norm, 65536 x 4096: 357 us, without
+    // that barrier 386; entering alone 197 with it, 186 without).
+    int par = 0;
+    for (int64_t t = blockIdx.x; t < n.T; t += gridDim.x, ring.next(), par ^= 1) {
         const uint8_t* st = ring_smem + ring.slot * ring.stage_bytes + (WIDE ? 0u : ring.shift(t));
         auto in = [&](int j) { return reinterpret_cast<const T*>(st + j * ring.pitch); };
         const size_t o = (size_t)t * d;
@@ -599,7 +604,9 @@ __global__ void __launch_bounds__(MAXT) block_norm_ring_kernel(const __grid_cons
 #pragma unroll
                 for (int i = 0; i < RP; ++i) u[i] = u[i] * g[i];
             }
-            if (p.post) tok *= rsqrtf(row_sum(s, buf[0]) * invd + n.eps);
+            if (p.post) {
+                tok *= rsqrtf(row_sum(s, buf[0]) * invd + n.eps);
+            }
             const f2 c = both(tok), ra = both(n.ra);
 #pragma unroll
             for (int i = 0; i < RP; ++i) y[i] = fma2(c * wq[i], u[i], ra * y[i]);
@@ -608,17 +615,16 @@ __global__ void __launch_bounds__(MAXT) block_norm_ring_kernel(const __grid_cons
         if (p.enter) {
             const float s = on * dot2(y, y);
             ring.wait_next(a, t);
-            const f2 r = both(rsqrtf(row_sum(s, buf[1]) * invd + n.eps));
+            const f2 r = both(rsqrtf(row_sum(s, buf[p.leave ? 1 : par]) * invd + n.eps));
 #pragma unroll
             for (int i = 0; i < RP; ++i) y[i] = y[i] * (r * wz[i]);
             give<T, WIDE>(static_cast<T*>(n.z) + o, d, y);
         }
-        // both buffers alternate with two norms; otherwise a barrier keeps a row's sums
-        // (and with no norm at all its stage) from the next row
-        if (!(p.post && p.enter) || blockDim.x <= 32) {
+        if (p.leave && !(p.post && p.enter)) {
             if (!p.enter) ring.wait_next(a, t);
             __syncthreads();
         }
+        if (blockDim.x <= 32) __syncwarp();
         if (threadIdx.x == 0) ring.refill(a, ring_smem, t);
     }
     if (threadIdx.x == 0 && *ring.abort_flag) ring.drain();
@@ -890,14 +896,18 @@ int launch_fwd_ring_t(const RingPlan& p, const RingArgs& r, cudaStream_t st) {
     MOE_LAUNCH((block_norm_ring_kernel<T, WIDE, FORM, MAXT>), p.grid, p.threads, p.smem, st, r);
     return MOE_OK;
 }
-// (64 registers are enough for any width)
+template <typename T, bool WIDE, int FORM>
+int launch_fwd_ring_f(const RingPlan& p, const RingArgs& r, cudaStream_t st) {
+    return p.threads <= 512 ? launch_fwd_ring_t<T, WIDE, FORM, 512>(p, r, st)
+                            : launch_fwd_ring_t<T, WIDE, FORM, 1024>(p, r, st);
+}
 template <typename T, bool WIDE>
 int launch_fwd_ring(const RingPlan& p, const RingArgs& r, cudaStream_t st) {
     switch (form_of(r.n, false)) {
-        case FORM_BOTH: return launch_fwd_ring_t<T, WIDE, FORM_BOTH, 1024>(p, r, st);
-        case FORM_ADD: return launch_fwd_ring_t<T, WIDE, FORM_ADD, 1024>(p, r, st);
-        case FORM_ENTER: return launch_fwd_ring_t<T, WIDE, FORM_ENTER, 1024>(p, r, st);
-        default: return launch_fwd_ring_t<T, WIDE, FORM_ANY, 1024>(p, r, st);
+        case FORM_BOTH: return launch_fwd_ring_f<T, WIDE, FORM_BOTH>(p, r, st);
+        case FORM_ADD: return launch_fwd_ring_f<T, WIDE, FORM_ADD>(p, r, st);
+        case FORM_ENTER: return launch_fwd_ring_f<T, WIDE, FORM_ENTER>(p, r, st);
+        default: return launch_fwd_ring_f<T, WIDE, FORM_ANY>(p, r, st);
     }
 }
 template <typename T, bool WIDE, int FORM, int MAXT>
@@ -927,7 +937,7 @@ int launch_bwd_ring(const RingPlan& p, const RingArgs& r, cudaStream_t st) {
 
 template <typename T, int VEC>
 int launch_fwd(const moe_norm_config& c, const NormArgs& a, cudaStream_t st) {
-    const RingPlan p = ring_plan(c, fwd_inputs(c), c.leave ? 64 : 32, false);
+    const RingPlan p = ring_plan(c, fwd_inputs(c), c.post_norm || c.gate != MOE_GATE_NONE ? 64 : 40, false);
     if (p.stages) {
         RingArgs r = {};
         r.n = a;
