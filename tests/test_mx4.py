@@ -290,6 +290,15 @@ def test_product_many_tiles_of_each_unit():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("K", [32, 96, 224, 288, 1056])
+@pytest.mark.parametrize("N,act,out_dt", [(136, "none", torch.float32), (392, "silu", torch.bfloat16),
+                                          (1000, "swiglu", torch.bfloat16), (264, "swiglu", torch.float32)])
+def test_product_long_segments_at_odd_sizes(K, N, act, out_dt):
+    """Segments of two row blocks or more go to CTA pairs; odd numbers of blocks leave one idle."""
+    product_case([700, 0, 130, 1500], K, N, act, out_dt, seed=K + N)
+
+
+@pytest.mark.gpu
 def test_product_no_rows_writes_nothing():
     cfg = moe.MX4ProductConfig(rows=256, K=64, N=64, E=2)
     m = moe.MX4Product(cfg)
