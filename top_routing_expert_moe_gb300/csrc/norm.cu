@@ -850,7 +850,7 @@ RingPlan ring_plan(const moe_norm_config& c, int nin, int regs, bool backward) {
     // CTAs an SM by registers and threads, fewer where they would not have three stages
     // each (228 KB an SM, 3 KB of it a CTA's fixed part)
     int per_sm = std::max(1, std::min(std::min(32, 65536 / (regs * p.threads)), 2048 / p.threads));
-    auto room = [&](int n) { return std::min(200 * 1024, 224 * 1024 / n - 3072); };
+    auto room = [&](int n) { return std::min(200 * 1024, 224 * 1024 / n - 3 * 1024); };
     while (per_sm > 1 && room(per_sm) < 3 * stage) --per_sm;
     p.stages = std::min(MAX_STAGES, room(per_sm) / stage);
     if (p.stages < 3) { p.stages = 0; return p; }   // the backward works on two at a time
