@@ -16,6 +16,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "ring_cursor.h"
 #include "tma.cuh"
 
 namespace moe {
@@ -470,8 +471,8 @@ inline Form form_of(const NormArgs& n, bool backward) {
     return n.enter && n.gmode == MOE_GATE_NONE ? FORM_ADD : FORM_ANY;
 }
 
-// Rows blockIdx.x + i gridDim.x pass through the stages in turn.  `slot` and
-// `phase` follow the row being worked on.  One warp watches the barriers: it waits
+// Rows blockIdx.x + i gridDim.x pass through the stages in turn; the cursor follows
+// the row being worked on.  One warp watches the barriers: it waits
 // for the next row's stage before it joins the current row's last reduction, whose
 // CTA barrier then tells the others.
 //
@@ -479,11 +480,10 @@ inline Form form_of(const NormArgs& n, bool backward) {
 // around it and read at its shift; the batch's last bytes, where that would pass
 // the tensor's end, are stored by the copying thread itself (a barrier follows
 // before they are read).
-template <bool WIDE> struct RowRing {
+template <bool WIDE> struct RowRing : RingCursor {
     uint32_t base, bar0, row_bytes, pitch, stage_bytes;
-    int stages, slot = 0;
-    uint32_t phase = 0;
     volatile int* abort_flag;
+    volatile uint32_t* stop;               // rows from it on are not sent for
 
     __device__ __forceinline__ uint32_t shift(int64_t row) const { return (uint32_t)((uint64_t)row * row_bytes) & 15u; }
     __device__ __forceinline__ void issue(const RingArgs& a, uint8_t* smem, int64_t row, int s) const {
@@ -510,30 +510,27 @@ template <bool WIDE> struct RowRing {
         int64_t row = blockIdx.x;
         for (int i = 0; i < stages && row < a.n.T; ++i, row += gridDim.x) issue(a, smem, row, i);
     }
-    __device__ __forceinline__ void wait(const RingArgs& a, int s, uint32_t ph) const {
-        mbar_wait(bar0 + s * 8, ph, abort_flag, a.status);
+    // While row t is worked on.  The thread that sends for rows stops where a wait of its
+    // own gave up: the next would have been t's successor in t's stage.
+    __device__ __forceinline__ void wait(const RingArgs& a, int64_t t, int s, uint32_t ph) const {
+        if (!mbar_wait(bar0 + s * 8, ph, abort_flag, a.status) && threadIdx.x == 0)
+            atomicMin(const_cast<uint32_t*>(stop), (uint32_t)t + stages * gridDim.x);
     }
-    __device__ __forceinline__ int ahead(int k) const { return slot + k >= stages ? slot + k - stages : slot + k; }
     // before the row's last barrier: the stage of the k-th row after it (k < stages)
     __device__ __forceinline__ void wait_next(const RingArgs& a, int64_t t, int k = 1) const {
         if (threadIdx.x < 32 && t + (int64_t)k * gridDim.x < a.n.T)
-            wait(a, ahead(k), slot + k >= stages ? phase ^ 1u : phase);
+            wait(a, t, ahead(k), phase_ahead(k));
     }
     // after it, by one thread: the stage of the current row t takes a later row
     __device__ __forceinline__ void refill(const RingArgs& a, uint8_t* smem, int64_t t) const {
         const int64_t row = t + (int64_t)stages * gridDim.x;
-        if (row < a.n.T && !*abort_flag) issue(a, smem, row, slot);
+        if (row < *stop) issue(a, smem, row, slot);
     }
-    __device__ __forceinline__ void next() {
-        if (++slot == stages) {
-            slot = 0;
-            phase ^= 1u;
-        }
-    }
-    // after an aborted wait: no copy is in flight when the CTA ends (a stage's last
-    // phase is the current one or the one before)
+    // after an aborted wait: no copy is in flight when the CTA ends.  (The cursor has gone
+    // on over the rows that were not sent for.)
     __device__ __forceinline__ void drain() const {
-        for (int s = 0; s < stages; ++s) mbar_drain(bar0 + s * 8, s < slot ? phase ^ 1u : phase);
+        const uint32_t sent = (*stop - blockIdx.x + gridDim.x - 1) / gridDim.x;
+        for (uint32_t s = 0; s < (uint32_t)stages && s < sent; ++s) mbar_drain(bar0 + s * 8, last_parity(sent, stages, s));
     }
 };
 
@@ -541,6 +538,7 @@ template <bool WIDE> struct RowRing {
     extern __shared__ __align__(128) uint8_t ring_smem[];                                       \
     __shared__ __align__(8) uint64_t bars[MAX_STAGES];                                          \
     __shared__ int abort_s;                                                                     \
+    __shared__ uint32_t stop_s;                                                                 \
     const NormArgs& n = a.n;                                                                    \
     const int d = n.d;                                                                          \
     const float invd = 1.f / (float)d;                                                          \
@@ -552,9 +550,11 @@ template <bool WIDE> struct RowRing {
     ring.stage_bytes = ring.pitch * a.nin;                                                      \
     ring.stages = a.stages;                                                                     \
     ring.abort_flag = &abort_s;                                                                 \
+    ring.stop = &stop_s;                                                                        \
     if (threadIdx.x == 0) {                                                                     \
         for (int i = 0; i < a.stages; ++i) mbar_init(ring.bar0 + i * 8, 1);                     \
         abort_s = 0;                                                                            \
+        stop_s = n.T;                                                                           \
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");                      \
     }                                                                                           \
     __syncthreads();                                                                            \
@@ -562,7 +562,7 @@ template <bool WIDE> struct RowRing {
     pdl_trigger();                                                                              \
     if (threadIdx.x == 0) ring.start(a, ring_smem);                                             \
     __syncthreads();                                                                            \
-    ring.wait(a, 0, 0)
+    ring.wait(a, blockIdx.x, 0, 0)
 
 // in: x, u (leave), gate (full)
 template <typename T, bool WIDE, int FORM, int MAXT>
