@@ -179,7 +179,7 @@ __device__ __forceinline__ void commit_local(uint32_t bar) {
         asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
                      : "memory");
 }
-// Bounded wait (CG = 2: acquire at cluster scope), as mbar_wait, but the clock and the
+// Bounded wait of one thread (CG = 2: acquire at cluster scope), as mbar_wait, but the clock and the
 // flags are looked at every 1024 tries only: a stage of these kernels lasts no longer
 // than one look at them.
 template <int CG>
@@ -200,6 +200,10 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
         }
     }
 }
+// The lanes of a warp that all look may differ when a wait gives up (one sees the phase,
+// another the abort flag), and a warp that parted there would not meet again: they go on
+// together or not at all.
+__device__ __forceinline__ bool agreed(bool got) { return __all_sync(0xffffffffu, got); }
 // a whole warp waits: one lane looks
 template <int CG>
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {
@@ -402,17 +406,14 @@ __global__ void __launch_bounds__(NTHREADS, 1) mx4_grouped_kernel(const __grid_c
         bool ok = live;
         for (int tix = unit; ok && tix < total; tix += nunits, ++tcount) {
             // the previous tile's epilogue is past the columns that both accumulators hold
-            if (!wait_bar<1>(smem_u32(tempty), ((uint32_t)tcount & 1u) ^ 1u, abort_flag, P.status)) break;
+            if (!agreed(wait_bar<1>(smem_u32(tempty), ((uint32_t)tcount & 1u) ^ 1u, abort_flag, P.status))) break;
             tc_fence_after();
             const uint32_t dt = tm + (tcount & 1 ? ACC1 : 0);
             for (int kb = kb0; kb < kb1; ++kb) {
-                if (!wait_bar<1>(smem_u32(&full[s]), ph, abort_flag, P.status) ||
-                    !wait_bar<1>(smem_u32(&sfull[s]), ph, abort_flag, P.status)) {
-                    ok = false;
-                    break;
-                }
+                ok = agreed(wait_bar<1>(smem_u32(&full[s]), ph, abort_flag, P.status) &&
+                            wait_bar<1>(smem_u32(&sfull[s]), ph, abort_flag, P.status));
+                if (!ok) break;
                 tc_fence_after();
-                __syncwarp();
                 if (elected) {
                     const uint32_t al = a_lo + s * (R::BYTES >> 4), bl = b_lo + s * (R::BYTES >> 4);
                     const uint32_t sf = tm + SF_COL + s * SF_COLS;
