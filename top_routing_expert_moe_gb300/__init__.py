@@ -15,6 +15,7 @@ CPU fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -206,6 +207,15 @@ def _s(stream):
     return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
+_HERE = contextlib.nullcontext()
+
+
+def _on(stream):
+    """Context for what a call allocates: under the stream that it works on, since a
+    block is handed out and taken back in the order of the stream it was taken under."""
+    return _HERE if stream is None else torch.cuda.stream(stream)
+
+
 def _call(name, *args):
     rc = getattr(_lib or load_library(), name)(*args)
     if rc != 0:
@@ -333,7 +343,8 @@ def moe_backward_aux(cfg, x, W_r, W_up, W_gate, W_down, logits, topk_idx, gate, 
 # ----------------------------------------------------------------- convenience layer
 class MoELayer:
     """Owns the routing cache, permuted buffers and workspace of one layer
-    configuration (all torch-allocated once) and chains the entry points.
+    configuration (all torch-allocated once) and chains the entry points.  What the
+    first call of a kind allocates belongs to the stream that it is given.
     With cfg.f_shared > 0, forward() takes the shared experts' weights
     (``shared=(W_up_s, W_down_s, W_gate_s or None)``) and backward() also
     returns their gradients (dW_up_s, dW_gate_s, dW_down_s)."""
@@ -414,7 +425,9 @@ class MoELayer:
             raise ValueError("the experts' shapes are not this layer's")
         if self._mx4 is None:
             R, dev = self.rows_cap, self.out.device
-            self._mx4 = (MX4Tensor((R, c.d), dev), MX4Tensor((R, c.f), dev),
+            with _on(stream):
+                rows = MX4Tensor((R, c.d), dev), MX4Tensor((R, c.f), dev)
+            self._mx4 = (*rows,
                          MX4ProductConfig(R, c.d, c.f, c.E, MX4_ACT_SWIGLU if c.ffn == SWIGLU else MX4_ACT_SILU),
                          MX4ProductConfig(R, c.f, c.d, c.E))
         xq, aq, first, second = self._mx4
@@ -473,7 +486,8 @@ class MoELayer:
         if self._inputs is None:
             raise RuntimeError("backward() needs a forward() first")
         x, W_r, W_up, W_gate, W_down, bias = self._inputs
-        g = self.grads()
+        with _on(stream):
+            g = self.grads()
         if dlogits_aux is not None and (tuple(dlogits_aux.shape) != (self.cfg.T, self.cfg.E) or
                                         dlogits_aux.dtype != torch.float32):
             raise ValueError("dlogits_aux must be a [T, E] fp32 tensor")

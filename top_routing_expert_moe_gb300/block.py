@@ -4,7 +4,10 @@ Residual-stream norms (``moe_block_norm``) and the router's per-sequence balance
 loss (``moe_balance_loss``), each with its backward, and microscaled 4-bit
 numbers with the experts' grouped product (``moe_mx4_*``).  As in the
 package's root, every function mirrors the C entry point of the same name and
-the classes own the output buffers and workspaces of one configuration.
+the classes own the output buffers and workspaces of one configuration.  What a
+call with ``stream`` allocates belongs to that stream: another stream that uses it
+waits for that one first, and tells the allocator (``record_stream``) before it is
+dropped.
 """
 from __future__ import annotations
 
@@ -25,7 +28,7 @@ __all__ = ["GATE_NONE", "GATE_CHANNEL", "GATE_TOKEN", "GATE_FULL", "NormConfig",
 
 GATE_NONE, GATE_CHANNEL, GATE_TOKEN, GATE_FULL = 0, 1, 2, 3
 
-_p, _s, _call = _moe._p, _moe._s, _moe._call
+_p, _s, _on, _call = _moe._p, _moe._s, _moe._on, _moe._call
 
 
 def _checked(t, shape, dtype, name):
@@ -143,7 +146,8 @@ class BlockNorm:
         stored stream x_out (x where the configuration does not leave a block),
         given those of x_out along the stream (None: zero) and of z."""
         self._check((("x_out", x_out), ("dx_out", dx_out), ("dz", dz), ("u", u)), w_pre, w_post, gate)
-        g = self.grads()
+        with _on(stream):
+            g = self.grads()
         moe_block_norm_backward(self.cfg, x_out, u, w_post, gate, w_pre, dx_out, dz, g["dx"],
                                 g["du"], g["dw_post"], g["dgate"], g["dw_pre"], self._ws, stream)
         return g
@@ -275,7 +279,8 @@ class MX4Tensor:
 
     def dequantize(self, dtype=torch.bfloat16, stream=None):
         code = _mx4_dtype(dtype)
-        out = torch.empty(self.shape, dtype=dtype, device=self.codes.device)
+        with _on(stream):
+            out = torch.empty(self.shape, dtype=dtype, device=self.codes.device)
         sets = self.shape[0] if len(self.shape) == 3 else 1
         moe_mx4_dequantize(code, sets, self.shape[-2], self.shape[-1], self.codes, self.scales, out,
                            stream)
@@ -289,7 +294,8 @@ def mx4_quantize(x, rows_used=None, out=None, stream=None) -> MX4Tensor:
         raise ValueError("x: expected [rows, K]")
     code = _mx4_dtype(x.dtype)
     if out is None:
-        out = MX4Tensor(x.shape, x.device)
+        with _on(stream):
+            out = MX4Tensor(x.shape, x.device)
     elif out.shape != x.shape:
         raise ValueError(f"out: expected {tuple(x.shape)}, got {out.shape}")
     if rows_used is not None and (rows_used.numel() != 1 or rows_used.dtype != torch.int32):
@@ -310,7 +316,8 @@ def mx4_quantize_weight(W, stream=None) -> MX4Tensor:
         raise ValueError("W: expected [E, K, N]")
     E, K, N = W.shape
     code = _mx4_dtype(W.dtype)
-    out = MX4Tensor((E, N, K), W.device)
+    with _on(stream):
+        out = MX4Tensor((E, N, K), W.device)
     moe_mx4_quantize_weight(code, E, K, N, W, out.codes, out.scales, stream)
     return out
 
