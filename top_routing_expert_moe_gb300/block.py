@@ -399,7 +399,9 @@ class MoEBlock:
     ``weights`` of forward(): w_in [d] fp32, W_r, W_up, W_down and, where the
     configuration has them, W_gate, bias, w_out [d] fp32, gate (see NormConfig),
     shared (as MoELayer.forward takes it).  backward() returns the gradients by
-    the same names with a "d" before (dx too)."""
+    the same names with a "d" before (dx too).  x may be the block's own last
+    output (weights shared along the depth): x' then goes to a second buffer, and
+    backward() is that of the last forward(), as always."""
 
     def __init__(self, cfg, post_norm=0, gate=GATE_NONE, eps=1e-6, res_scale=1.0, out_scale=1.0,
                  sequences=1, balance_coef=0.01, z_coef=0.0, device="cuda"):
@@ -410,7 +412,7 @@ class MoEBlock:
                                           eps=eps, res_scale=res_scale, out_scale=out_scale), device)
         self.balance = BalanceLoss(BalanceConfig(c.T, c.E, c.k, sequences, balance_coef, z_coef,
                                                  c.temperature), device)
-        self._saved = None
+        self._saved = self._other = None
 
     def forward(self, x, weights, seq_offsets=None, noise=None, token_mask=None, stream=None):
         """(x', loss [3]): the stream after the block and the router's losses."""
@@ -418,6 +420,12 @@ class MoEBlock:
         z = self.enter.forward(x, w_pre=w["w_in"], stream=stream)[1]
         u = self.layer.forward(z, w["W_r"], w["W_up"], w["W_down"], w.get("W_gate"), w.get("bias"),
                                noise, token_mask, stream, shared=w.get("shared"))
+        if x.data_ptr() == self.leave.x_out.data_ptr():
+            # backward() reads x, so x' may not be written over it
+            if self._other is None:
+                with _on(stream):
+                    self._other = torch.empty_like(x)
+            self.leave.x_out, self._other = self._other, self.leave.x_out
         x_out = self.leave.forward(x, u=u, w_post=w.get("w_out"), gate=w.get("gate"), stream=stream)[0]
         loss = self.balance.forward(self.layer.logits, self.layer.topk_idx, seq_offsets, stream)
         self._saved = (x, u, w)
