@@ -1,4 +1,5 @@
-"""A block that is run on its own output, as a weight-tied stack does."""
+"""A block that is run on its own output, as a weight-tied stack does, and one whose
+forward did not come to its end."""
 import pytest
 import torch
 
@@ -42,6 +43,18 @@ def test_the_saved_stream_is_not_written(monkeypatch):
     assert len(set(seen)) == 2                 # two buffers take turns
     fresh = torch.zeros_like(x)
     assert b.forward(fresh, w)[0].data_ptr() == b.forward(fresh, w)[0].data_ptr()
+
+
+def test_a_forward_that_raised_leaves_no_backward(monkeypatch):
+    b, w, _ = cpu_block(monkeypatch, post_norm=1)
+    x = torch.zeros(200, 128, dtype=torch.bfloat16)
+    w["w_out"] = torch.ones(128)
+    b.forward(x, w)
+    b.backward(x)
+    with pytest.raises(ValueError, match="w_post"):
+        b.forward(x, {**w, "w_out": torch.ones(127)})
+    with pytest.raises(RuntimeError, match="forward"):
+        b.backward(x)
 
 
 @pytest.mark.gpu

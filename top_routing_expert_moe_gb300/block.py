@@ -417,6 +417,7 @@ class MoEBlock:
     def forward(self, x, weights, seq_offsets=None, noise=None, token_mask=None, stream=None):
         """(x', loss [3]): the stream after the block and the router's losses."""
         w = weights
+        self._saved = None            # the layer's buffers are this forward's from here on
         z = self.enter.forward(x, w_pre=w["w_in"], stream=stream)[1]
         u = self.layer.forward(z, w["W_r"], w["W_up"], w["W_down"], w.get("W_gate"), w.get("bias"),
                                noise, token_mask, stream, shared=w.get("shared"))
@@ -434,9 +435,9 @@ class MoEBlock:
     def forward_mx4(self, x, weights, experts: MX4Experts, token_mask=None, stream=None):
         """x' with the experts in 4 bits (serving: no loss, no backward)."""
         w = weights
+        self._saved = None
         z = self.enter.forward(x, w_pre=w["w_in"], stream=stream)[1]
         u = self.layer.forward_mx4(z, w["W_r"], experts, w.get("bias"), token_mask=token_mask, stream=stream)
-        self._saved = None
         return self.leave.forward(x, u=u, w_post=w.get("w_out"), gate=w.get("gate"), stream=stream)[0]
 
     def backward(self, dx_out, dloss=None, stream=None):
