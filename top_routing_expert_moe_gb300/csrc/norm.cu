@@ -564,9 +564,17 @@ template <bool WIDE> struct RowRing : RingCursor {
     __syncthreads();                                                                            \
     ring.wait(a, blockIdx.x, 0, 0)
 
+// CTAs an SM that the registers have to leave room for (0: no bound), where the compiler's
+// own choice is not what the plan below counts on.  Entering alone at odd widths took 53
+// registers, a wave of CTAs more than the plan's 40 (20000 x 1001 fp32, 30.5 us; so 27.3).
+// Backwards of 513-768 threads have an SM to themselves, but were cut to 40 registers with
+// spills for a second CTA (16384 x 5120 bf16, addition 170 us, entering 147; 135 and 125).
+template <bool WIDE, int FORM, int MAXT> constexpr int FWD_CTAS = !WIDE && FORM == FORM_ENTER && MAXT == 512 ? 3 : 0;
+template <int FORM, int MAXT> constexpr int BWD_CTAS = (FORM == FORM_ADD || FORM == FORM_ENTER) && MAXT == 768 ? 1 : 0;
+
 // in: x, u (leave), gate (full)
 template <typename T, bool WIDE, int FORM, int MAXT>
-__global__ void __launch_bounds__(MAXT) block_norm_ring_kernel(const __grid_constant__ RingArgs a) {
+__global__ void __launch_bounds__(MAXT, (FWD_CTAS<WIDE, FORM, MAXT>)) block_norm_ring_kernel(const __grid_constant__ RingArgs a) {
     __shared__ float buf[2][32];
     NORM_RING_SETUP();
     const Parts p = parts_of<FORM>(n);
@@ -631,7 +639,7 @@ __global__ void __launch_bounds__(MAXT) block_norm_ring_kernel(const __grid_cons
 
 // in: x_out, dz (enter), dx_out (if given), u (post or gate), gate (full)
 template <typename T, bool WIDE, int FORM, int MAXT>
-__global__ void __launch_bounds__(MAXT) block_norm_bwd_ring_kernel(const __grid_constant__ RingArgs a) {
+__global__ void __launch_bounds__(MAXT, (BWD_CTAS<FORM, MAXT>)) block_norm_bwd_ring_kernel(const __grid_constant__ RingArgs a) {
     __shared__ float buf[2][32 * 8];
     NORM_RING_SETUP();
     const Parts p = parts_of<FORM>(n);
