@@ -395,9 +395,11 @@ __device__ __forceinline__ void take(const T* p, int d, f2 (&v)[RP]) {
         }
     }
 }
-// whether this thread's share counts in sums (other shares past the end are zeros)
+// This thread's share of a sum: its own, or none where it has read again what belongs
+// to others (other shares past the end are zeros).  Chosen, not multiplied by 0: the
+// elements read again may be infinite, or their squares.
 template <typename T, bool WIDE>
-__device__ __forceinline__ float live(int d) { return !WIDE || sizeof(T) == 4 || (int)threadIdx.x * RE < d ? 1.f : 0.f; }
+__device__ __forceinline__ bool live(int d) { return !WIDE || sizeof(T) == 4 || (int)threadIdx.x * RE < d; }
 template <typename T, bool WIDE>
 __device__ __forceinline__ void give(T* p, int d, const f2 (&v)[RP]) {
     if constexpr (!WIDE) {
@@ -579,7 +581,7 @@ __global__ void __launch_bounds__(MAXT, (FWD_CTAS<WIDE, FORM, MAXT>)) block_norm
     NORM_RING_SETUP();
     const Parts p = parts_of<FORM>(n);
     const int gmode = FORM == FORM_ADD || FORM == FORM_ENTER ? MOE_GATE_NONE : n.gmode;
-    const float on = live<T, WIDE>(d);
+    const bool on = live<T, WIDE>(d);
     f2 wq[RP], wz[RP];                     // g w_post, w_pre
     fill(wq, 1.f);
     if (p.post) channel<T, WIDE>(n.w_post, d, wq);
@@ -604,7 +606,7 @@ __global__ void __launch_bounds__(MAXT, (FWD_CTAS<WIDE, FORM, MAXT>)) block_norm
         take<T, WIDE>(in(0), d, y);
         if (p.leave) {
             take<T, WIDE>(in(1), d, u);
-            const float s = p.post ? on * dot2(u, u) : 0.f;
+            const float s = p.post && on ? dot2(u, u) : 0.f;
             if (p.full) {
                 f2 g[RP];
                 take<T, WIDE>(in(2), d, g);
@@ -620,7 +622,7 @@ __global__ void __launch_bounds__(MAXT, (FWD_CTAS<WIDE, FORM, MAXT>)) block_norm
             give<T, WIDE>(static_cast<T*>(n.x_out) + o, d, y);
         }
         if (p.enter) {
-            const float s = on * dot2(y, y);
+            const float s = on ? dot2(y, y) : 0.f;
             ring.wait_next(a, t);
             const f2 r = both(rsqrtf(row_sum(s, buf[p.leave ? 1 : par]) * invd + n.eps));
 #pragma unroll
@@ -663,7 +665,7 @@ __global__ void __launch_bounds__(MAXT, (BWD_CTAS<FORM, MAXT>)) block_norm_bwd_r
     if (enter) channel<T, WIDE>(n.w_pre, d, wz);
     // the tensors' places in a stage
     const int p_dz = 1, p_dx = enter ? 2 : 0, p_u = p_dx + (along ? 1 : 0), p_g = p_u + 1;
-    const float on = live<T, WIDE>(d);
+    const bool on = live<T, WIDE>(d);
     // A row's tensors, from its stage.  They are taken twice, for the sums and for the
     // outputs: between the two lies a barrier, and the next row's sums come before it.
     auto row = [&](int slot, int64_t t, f2 (&y)[RP], f2 (&dz)[RP], f2 (&G)[RP], f2 (&u)[RP], f2 (&g)[RP]) {
@@ -699,7 +701,9 @@ __global__ void __launch_bounds__(MAXT, (BWD_CTAS<FORM, MAXT>)) block_norm_bwd_r
                 s5 = fma2(qu, y[i], s5);
             }
         }
-        const float s[6] = {on * dot2(y, y), on * sum2(s1), on * dot2(u, u), on * sum2(s3), on * sum2(s4), on * sum2(s5)};
+        float s[6] = {dot2(y, y), sum2(s1), dot2(u, u), sum2(s3), sum2(s4), sum2(s5)};
+#pragma unroll
+        for (int i = 0; i < 6; ++i) s[i] = on ? s[i] : 0.f;
         put_sums6(warp_sums6(s), to);
     };
     int par = 0;
