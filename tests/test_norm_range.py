@@ -1,5 +1,6 @@
 """The residual stream's norms at the ends of fp32's range: a row's result must not
-depend on the kernel that its batch takes.
+depend on the kernel that its batch takes, nor lose its gradient where r^3 leaves
+the range that r itself is well inside.
 
 Rows whose squares overflow have an infinite sum, so r = 0 in every kernel: their
 finite elements give exactly 0 (z, n) or pass the rest through (x', dx).  The other
@@ -74,4 +75,29 @@ def test_overflowing_and_infinite_rows_leaving(T, d, dt):
     keep = torch.arange(T) != 4
     base.near(g["du"][keep.cuda()], g64["du"], m64["du"], 64, "du")
     base.near(g["dw_post"], g64["dw_post"], m64["dw_post"], 64 + T, "dw_post")
+    assert moe.last_device_status() == 0
+
+
+@pytest.mark.parametrize("form", [(0, 0, 1, "none"), (1, 0, 1, "none"), (1, 1, 0, "channel"),
+                                  (1, 1, 1, "token"), (1, 1, 1, "full")])
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,d", [(9, 256), (4400, 1000), (400, 1001)])
+def test_gradients_where_the_cube_of_r_leaves_the_range(T, d, dt, form, monkeypatch):
+    """Zero and tiny rows under a tiny eps (r = 1e15), rows of size 1e15."""
+    monkeypatch.setattr(base, "EPS", 1e-30)
+    v = base.make(T, d, dt, *form, seed=T)              # row 1 is zero
+    for t in (v[n] for n in ("x", "u") if n in v):
+        t[3] = (t[3].float() * 1e-16).to(dt)
+        t[4] = (t[4].float() * 1e15).to(dt)
+    n, c, args = norm_of(v, T, d, dt, form)
+    x_out, z = n.forward(c["x"], **args)
+    y, my, z64, mz = base.forward64(v, *form)
+    if form[0]:
+        base.near(x_out, y, my, 64, "x_out")
+    if form[2]:
+        base.near(z, z64, mz, 64, "z")
+    g = n.backward(x_out, dx_out=c["dx_out"], dz=c.get("dz"), **args)
+    g64, m64 = base.backward64(v, x_out.cpu(), *form)
+    for k in g64:
+        base.near(g[k], g64[k], m64[k], 64 + (T if g64[k].shape == (d,) else 0), k)
     assert moe.last_device_status() == 0

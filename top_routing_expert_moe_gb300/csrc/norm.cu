@@ -11,7 +11,8 @@
 //   du  = r_u q G - u (r_u^3/d) S,                            S   = sum q u G
 // S is linear in G, so it comes from the first pass's sums,
 //   S = sum q u dx' + r sum q u a - (r^3/d) A sum q u x',
-// and one reduction of six sums serves the whole row.
+// and one reduction of six sums serves the whole row.  r^3 is never formed by itself:
+// it leaves fp32's range where r passes 1e12 or 1e-13, and the row's sum brings it back.
 #include <algorithm>
 
 #include "common.cuh"
@@ -245,10 +246,10 @@ __global__ void __launch_bounds__(MAXT) block_norm_bwd_kernel(const NormArgs a) 
         }
         row_sums6(s, buf[par]);
         const float r = a.enter ? rsqrtf(s[0] * invd + a.eps) : 0.f;
-        const float ca = r * r * r * invd * s[1];
+        const float ca = r * (r * (r * (invd * s[1])));
         const float S = s[3] + r * s[4] - ca * s[5];         // sum q u G, without tok
         const float ru = a.post ? rsqrtf(s[2] * invd + a.eps) : 1.f;
-        const float cu = a.post ? tok * ru * ru * ru * invd * S : 0.f;
+        const float cu = a.post ? tok * ru * (ru * (ru * (invd * S))) : 0.f;
         if (a.gmode == MOE_GATE_TOKEN && threadIdx.x == 0)
             static_cast<float*>(a.dgate)[t] = a.ob * ru * S;
 #pragma unroll
@@ -722,7 +723,7 @@ __global__ void __launch_bounds__(MAXT, (BWD_CTAS<FORM, MAXT>)) block_norm_bwd_r
         float r = 0.f, ca = 0.f;
         if (enter) {
             r = rsqrtf(s[0] * invd + n.eps);
-            ca = r * r * r * invd * s[1];
+            ca = r * (r * (r * (invd * s[1])));
             const f2 r2 = both(r), c2 = both(-ca);
 #pragma unroll
             for (int i = 0; i < RP; ++i) {
@@ -739,7 +740,7 @@ __global__ void __launch_bounds__(MAXT, (BWD_CTAS<FORM, MAXT>)) block_norm_bwd_r
             const float S = s[3] + r * s[4] - ca * s[5];
             const float ru = post ? rsqrtf(s[2] * invd + n.eps) : 1.f;
             if (gmode == MOE_GATE_TOKEN && threadIdx.x == 0) static_cast<float*>(n.dgate)[t] = n.ob * ru * S;
-            const f2 tr = both(tok * ru), cu = both(post ? -tok * ru * ru * ru * invd * S : 0.f);
+            const f2 tr = both(tok * ru), cu = both(post ? -tok * ru * (ru * (ru * (invd * S))) : 0.f);
             if (full) {
 #pragma unroll
                 for (int i = 0; i < RP; ++i) {
