@@ -379,7 +379,9 @@ MOE_API int moe_block_norm_backward(const moe_norm_config* cfg, const void* x_ou
  * Counts carry no gradient.  A logit of -inf is an expert masked for that token
  * (p = 0); a routed token whose logits are all -inf adds nothing but its counts
  * and n.  NaN or +inf in a routed token's logits is recorded as
- * MOE_ERR_NONFINITE; masked tokens' logits are not looked at.                 */
+ * MOE_ERR_NONFINITE; masked tokens' logits are not looked at.  Any finite logit
+ * is a number: only lse_t^2 may pass fp32, which makes z infinite (z is 0 where
+ * z_coef is).                                                                */
 typedef struct {
     int32_t T;            /* tokens                                           */
     int32_t E;            /* experts, 1..256                                  */

@@ -119,30 +119,32 @@ template <int G, int R, int W> struct Row {
     }
 };
 
-// Softmax of one token's logits over its G lanes, in place, in powers of two
-// (k2 = log2(e) / tau); returns lse (-inf, with p = 0, where every logit is -inf or
-// the token is masked; NaN where one is NaN or +inf).
+// Softmax of one token's logits over its G lanes, in place, in powers of two.  The
+// maximum is subtracted before anything is rounded: the difference of near logits is
+// exact, so the error of p goes by the distance from the maximum and not by the
+// logits' size, and no finite logit leaves the range.  Returns lse (0, with p = 0,
+// where every logit is -inf or the token is masked; NaN where one is NaN or +inf).
 template <int G, int R>
-__device__ __forceinline__ float softmax_row(float (&p)[R], bool on, float k2) {
+__device__ __forceinline__ float softmax_row(float (&p)[R], bool on, float inv_tau) {
     float m = -INFINITY;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-        p[i] = on ? p[i] * k2 : -INFINITY;
+        p[i] = on ? p[i] : -INFINITY;
         m = fmaxf(m, p[i]);
     }
     m = group_max<G>(m);
     float z = 0.f;
-    const float mm = m == -INFINITY ? 0.f : m;
+    const float mm = m == -INFINITY ? 0.f : m, k2 = inv_tau * LOG2E;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p[i]) : "f"(p[i] - mm));   // 2 ulp
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p[i]) : "f"((p[i] - mm) * k2));   // 2 ulp
         z += p[i];
     }
     z = group_sum<G>(z);
     const float iz = z == 0.f ? 0.f : __fdividef(1.f, z);   // (1 <= z <= E, or NaN)
 #pragma unroll
     for (int i = 0; i < R; ++i) p[i] *= iz;
-    return z == 0.f ? -INFINITY : (m + __log2f(z)) * 0.69314718f;
+    return z == 0.f ? 0.f : m * inv_tau + __logf(z);
 }
 
 template <int G, int R, int W>
@@ -195,14 +197,14 @@ __global__ void __launch_bounds__(THREADS) balance_partial_kernel(const BalArgs 
             const bool on = in && nxt_pick >= 0;
             // the pass's tokens past a sequence's end are its successor's first pass
             fetch((base + TOK < stop ? base + TOK : stop) + grp);
-            const float lse = softmax_row<G, R>(p, on, a.inv_tau * LOG2E);
+            const float lse = softmax_row<G, R>(p, on, a.inv_tau);
             if (on) {
                 if (isnan(lse)) set_status(a.status, MOE_ERR_NONFINITE);
 #pragma unroll
                 for (int i = 0; i < R; ++i) sum[i] += p[i];
                 if (gl == 0) {
                     n += 1.f;
-                    zz += lse == -INFINITY ? 0.f : lse * lse;
+                    zz += lse * lse;
                 }
             }
             if (in)
@@ -333,7 +335,8 @@ __global__ void __launch_bounds__(SEQ_THREADS) balance_sequence_kernel(const Bal
     }
     const float ns = fmaxf(v[1], 1.f), nt = fmaxf(v[2], 1.f);
     if (tid == 0) {
-        const float b = a.bcoef * v[0] / ns, z = a.zcoef * v[3] / nt;
+        // (lse^2 of the largest logits is infinite; without a z loss that is no matter)
+        const float b = a.bcoef * v[0] / ns, z = a.zcoef == 0.f ? 0.f : a.zcoef * v[3] / nt;
         a.loss[0] = b + z;
         a.loss[1] = b;
         a.loss[2] = z;
@@ -380,12 +383,12 @@ __global__ void __launch_bounds__(THREADS) balance_bwd_kernel(const BalArgs a) {
 #pragma unroll
             for (int i = 0; i < R; ++i) w[i] = L::expert(gl, i) < a.E ? cb * __ldg(gw + L::expert(gl, i)) : 0.f;
         }
-        const float lse = softmax_row<G, R>(p, on, a.inv_tau * LOG2E);
+        const float lse = softmax_row<G, R>(p, on, a.inv_tau);
         float dot = 0.f;
 #pragma unroll
         for (int i = 0; i < R; ++i) dot = fmaf(on ? w[i] : 0.f, p[i], dot);
         dot = group_sum<G>(dot);
-        const float zl = lse == -INFINITY ? 0.f : cz * lse;
+        const float zl = cz == 0.f ? 0.f : cz * lse;
 #pragma unroll
         for (int i = 0; i < R; ++i) p[i] = on ? up * (p[i] * (w[i] - dot + zl)) : 0.f;
         if (in) L::store(a.dlogits + (size_t)t * a.E, a.E, gl, p);
