@@ -403,7 +403,9 @@ MOE_API int moe_balance_workspace_size(const moe_balance_config* cfg, size_t* by
  * counts [S,E] int32; pbar [S,E] fp32 (0 for a sequence without tokens);
  * grad_w [S,E+2] fp32 = what the backward needs of each sequence.
  * Offsets out of order or outside 0..T, and expert indices outside -1..E-1,
- * are recorded as MOE_ERR_DEVICE_BOUNDS and clamped or left out.             */
+ * are recorded as MOE_ERR_DEVICE_BOUNDS.  Offsets are clamped to 0..T; where they
+ * descend all the same every output is 0 (and so is the backward's dlogits); such
+ * indices are left out.                                                       */
 MOE_API int moe_balance_loss(const moe_balance_config* cfg, const float* logits,
                              const int32_t* topk_idx, const int32_t* seq_offsets, float* loss,
                              int32_t* counts, float* pbar, float* grad_w, void* ws,

@@ -58,3 +58,18 @@ def test_the_z_loss_of_the_lowest_values_is_infinite_not_a_masked_row():
     assert ((dl - want[3]).abs() <= 4 * base.C * want[4] + 1e-30).all()
     assert not torch.equal(want[2], clean[2])           # the row counts in P
     assert moe.last_device_status() == 0
+
+
+@pytest.mark.parametrize("offs", [[0, 200, 100, 300], [0, 250, 20, 260, 300], [0, 300, 0, 300]])
+def test_descending_offsets_leave_every_output_zero(offs):
+    """Recorded, and nothing of what the workspace held before shows."""
+    logits, topk, _ = base.make(300, 8, 2, 1, masked=False)
+    o = torch.tensor(offs, dtype=torch.int32)
+    for fill in (0, 63, 127):
+        b = moe.BalanceLoss(moe.BalanceConfig(T=300, E=8, k=2, S=len(offs) - 1, balance_coef=1.0, z_coef=1.0))
+        b.ws.fill_(fill)
+        loss = b.forward(logits.cuda(), topk.cuda(), o.cuda())
+        dl = b.backward()
+        for t in (loss, b.counts, b.pbar, dl):
+            assert not t.any()
+        assert moe.last_device_status() == moe.ERR_DEVICE_BOUNDS

@@ -41,14 +41,15 @@ struct BalArgs {
     const float *grad_w, *dloss;
     float *rec, *seqsum, *loss, *pbar, *gw, *dlogits;
     int32_t* counts;
-    unsigned* ticket;
+    unsigned* ticket;                                // [0] CTAs done, [1] the offsets descend
     int* status;
     int T, E, k, S, chunk;                           // tokens of a CTA
     float bcoef, zcoef, inv_tau;
 };
 
-// sequence s's first token, with offsets that are out of order or range clamped
-// (the forward records that); without offsets one sequence
+// sequence s's first token, with offsets out of range clamped (the forward records
+// that, and where they still descend leaves every output zero); without offsets one
+// sequence
 __device__ __forceinline__ int seq_at(const BalArgs& a, int s) {
     if (s <= 0) return 0;
     if (s >= a.S) return a.T;
@@ -161,13 +162,21 @@ __global__ void __launch_bounds__(THREADS) balance_partial_kernel(const BalArgs 
     const int b = blockIdx.x;
     const int t0 = b * a.chunk, t1 = min(a.T, t0 + a.chunk);
     if (b == 0) {
-        if (tid == 0) *a.ticket = 0;
+        int down = 0;
         if (a.seq)                                   // offsets: ascending from 0 to T
             for (int s = tid; s <= a.S; s += THREADS) {
                 const int v = a.seq[s], nx = s < a.S ? a.seq[s + 1] : a.T;
                 if (v > nx || v < 0 || (s == 0 && v != 0) || (s == a.S && v != a.T))
                     set_status(a.status, MOE_ERR_DEVICE_BOUNDS);
+                // (pairs of chunks and sequences are then no staircase, and records that
+                // the next kernel would read are not written)
+                if (s < a.S && seq_at(a, s) > seq_at(a, s + 1)) down = 1;
             }
+        down = __syncthreads_or(down);
+        if (tid == 0) {
+            a.ticket[0] = 0;
+            a.ticket[1] = down;
+        }
     }
     int t = t0;
     // a token's logits are loaded while the one before is worked on
@@ -258,9 +267,10 @@ __global__ void __launch_bounds__(SEQ_THREADS) balance_sequence_kernel(const Bal
     pdl_wait();
     pdl_trigger();
     const int s = blockIdx.x, E = a.E, W = E + 2, tid = threadIdx.x;
+    const unsigned down = __ldcg(a.ticket + 1);
     const int beg = a.seq ? seq_at(a, s) : 0;
     const int end = s + 1 >= a.S ? a.T : seq_at(a, s + 1);
-    const int b0 = beg / a.chunk, b1 = end > beg ? (end - 1) / a.chunk : b0 - 1;
+    const int b0 = beg / a.chunk, b1 = end > beg && !down ? (end - 1) / a.chunk : b0 - 1;
     extern __shared__ float sd[];                    // [P][W] sums, then [P][E] counts
     const int P = seq_groups(E);
     int* sc = reinterpret_cast<int*>(sd + P * W);
@@ -343,7 +353,7 @@ __global__ void __launch_bounds__(SEQ_THREADS) balance_sequence_kernel(const Bal
     }
     for (int i = tid; i < a.S; i += SEQ_THREADS) {
         a.gw[(size_t)i * W + E] = a.bcoef / ns;
-        a.gw[(size_t)i * W + E + 1] = 2.f * a.zcoef / nt;
+        a.gw[(size_t)i * W + E + 1] = down ? 0.f : 2.f * a.zcoef / nt;
     }
 }
 
