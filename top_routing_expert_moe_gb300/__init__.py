@@ -204,7 +204,10 @@ def _s(stream):
     """Handle of the stream, or of the current device's current stream."""
     if stream is not None:
         return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    try:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    except AttributeError:       # private names, a microsecond quicker than the public call
+        return torch.cuda.current_stream().cuda_stream
 
 
 _HERE = contextlib.nullcontext()
