@@ -471,7 +471,10 @@ MOE_API int moe_mx4_dequantize(int32_t dtype, int32_t sets, int64_t rows, int32_
 #define MOE_MX4_ACT_SWIGLU 2
 
 typedef struct {
-    int64_t rows;      /* rows of x and out (the segments' upper bound)        */
+    int64_t rows;      /* rows of x and out (the segments' upper bound; the
+                          launch is sized for moe_rows_capacity's, which holds
+                          127 rows of padding an expert: a bound with less is
+                          right too, but may use fewer SMs)                     */
     int32_t K;         /* reduction width, a multiple of 32                    */
     int32_t N;         /* output width, a multiple of 8                        */
     int32_t E;         /* experts, 1..64                                       */

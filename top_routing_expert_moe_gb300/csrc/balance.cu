@@ -13,7 +13,7 @@
 // sums run in a fixed order (no float atomics); counts use integer atomics in
 // shared memory, whose order does not matter.
 //
-// T = 65536, E = 64, k = 8, 37 sequences: 20 us a pass as a graph, of them about 8 the
+// T = 65536, E = 64, k = 8, 37 sequences: 21 us a pass as a graph, of them about 8 the
 // partial sums, 4 the sequences, 7 the backward; the logits' two passes and dlogits
 // are 5 us of HBM.  Latency bounds it (each kernel's dependent loads, then half of
 // the issue slots for the softmax).  32 lanes a token and 256-token chunks took 80 us.

@@ -8,8 +8,8 @@
 // conversion instruction): the results do not depend on any order.
 //
 // Memory-bound: 2 (or 4) bytes read, 17/32 written an element.  65536 x 4096 bf16 rows
-// 107 us (6.2 TB/s), back to values 115 us (5.7 TB/s); weights of 8 x 2048 x 4096 32 us
-// (5.3 TB/s).  Decoding each code by its bits and finding each element's place by
+// 106 us (6.4 TB/s), back to values 117 us (5.8 TB/s); fp32 178 us (6.8 TB/s) and 261 us
+// (4.7); weights of 8 x 2048 x 4096 31 us (5.5 TB/s).  Decoding each code by its bits and finding each element's place by
 // division took 296 us where byte tables and the quantiser's split take 115.
 #include <algorithm>
 

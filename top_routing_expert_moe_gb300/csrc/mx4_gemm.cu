@@ -78,7 +78,7 @@ struct Mx4Params {
     int64_t rows;
     int E, K, N, n_blocks, act;
     int ways;                              // CTAs of a cluster that may share a tile's K (single CTAs only)
-    int max_tiles;                         // their grid: tiles that rows of this number can make
+    int max_tiles;                         // their grid: tiles of the rows that are not padding
 };
 
 __device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr) {
@@ -844,7 +844,8 @@ int launch_mx4_product(const moe_mx4_product_config& c, const void* xq, const vo
     // blocks or more (2048 rows of 8 experts, K = 4096, N = 14336, SwiGLU: 96 us against
     // 116); with fewer half the pair idles.  A single CTA takes 128 x 128: it serves
     // short segments, where W's bytes bound it and more, smaller tiles spread them
-    // evenly.  The host knows the rows' bound only, 127 of it an expert's padding.
+    // evenly.  The host knows the rows' bound only, and takes 127 of it for each expert's
+    // padding, which is what moe_permute's bound holds.
     const bool pair = c.rows >= (int64_t)(256 + 127) * c.E;
     const int w_rows = dual && !pair ? 64 : 128;
     MX4_TRY(codes_map(&P.tmA, xq, c.rows, 1, c.K, BM));
@@ -869,7 +870,9 @@ int launch_mx4_product(const moe_mx4_product_config& c, const void* xq, const vo
     P.n_blocks = (c.N + cols - 1) / cols;
     // Few tiles (a token or two in decoding): two or four CTAs share a tile's K, if each
     // then has four stages or more.  256 rows of 2 experts, K = 14336, N = 4096 (64
-    // tiles): 18 us against 24.  Tiles are bounded by the rows that are not padding.
+    // tiles): 18 us against 24.  Tiles are counted from the rows that are not padding: a
+    // bound without padding makes more of them than that, and the few CTAs take them in turn
+    // (8064 rows of 64 experts, all real, K = 4096, N = 1024: 101 us; 16128 rows 47).
     const int64_t real = std::max<int64_t>(1, c.rows - 127 * (int64_t)c.E);
     const int64_t tiles = (real / BM + std::min<int64_t>(c.E, real)) * P.n_blocks;
     const int nk = (c.K / 2 + BKB - 1) / BKB;

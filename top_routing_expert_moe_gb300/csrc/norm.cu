@@ -314,8 +314,9 @@ __global__ void __launch_bounds__(MAXT) block_norm_bwd_kernel(const NormArgs a) 
 // be filled again.  A copy that never arrives is given up after the bounded wait
 // (recorded; the outputs are then undefined).
 //
-// 65536 x 4096 bf16, both norms, channel gate: forward 334 us (6.4 TB/s, 0.96 of the
-// copy rate; the direct kernel 526), backward 550 us (5.9 TB/s, 0.87; 1750).
+// 65536 x 4096 bf16, both norms, channel gate: forward 324 us (6.6 TB/s, 0.99 of the
+// copy rate; the direct kernel 526), backward 531 us (6.1 TB/s, 0.91; 1750).
+// 65536 x 2048 fp32: 343 us (6.3 TB/s) and 472 us (6.8 TB/s).
 constexpr int RE = 8;                      // elements of a row per thread
 constexpr int MAX_STAGES = 8;
 
@@ -450,7 +451,9 @@ __device__ __forceinline__ float dot2(const f2 (&a)[RP], const f2 (&b)[RP]) {
 
 // The parts of a pass, known at compile time for the usual forms: registers and
 // issue slots that the other parts would take are what these kernels are short of
-// (both norms, backward: 711 us with run-time flags, 550 so; 8192 wide 618 and 275).
+// (65536 x 4096, both norms, backward: 702 us with run-time flags, 531 so; 16384 x 8192
+// 596 and 274).  A full gate stays with the flags: 449 us forward, 773 backward (5.6
+// TB/s); above 512 threads its backward spills (16384 x 8192: 885 us, 2.4 TB/s).
 enum Form {
     FORM_ANY,        // by the run-time flags
     FORM_BOTH,       // leave with its norm, enter; a gate that is not full; dx_out given
@@ -594,8 +597,8 @@ __global__ void __launch_bounds__(MAXT, (FWD_CTAS<WIDE, FORM, MAXT>)) block_norm
     if (p.enter) channel<T, WIDE>(n.w_pre, d, wz);
     // Two norms alternate their buffers, entering alone alternates from row to row, so a
     // row's last reduction is the only barrier that is needed after it.  Leaving with one
-    // norm or none meets once more (plain addition and norm, 65536 x 4096: 357 us, without
-    // that barrier 386; entering alone 197 with it, 186 without).
+    // norm or none meets once more (when it was chosen, 65536 x 4096: plain addition and norm
+    // 357 us, without that barrier 386; entering alone 197 with it, 186 without).
     int par = 0;
     for (int64_t t = blockIdx.x; t < n.T; t += gridDim.x, ring.next(), par ^= 1) {
         const uint8_t* st = ring_smem + ring.slot * ring.stage_bytes + (WIDE ? 0u : ring.shift(t));
@@ -840,12 +843,16 @@ bool wide_rows(const moe_norm_config& c) { return (c.d * (c.dtype == MOE_DTYPE_B
 
 // The ring's launch: threads, stages and CTAs, or none (0 stages) where the direct
 // kernels serve.  Those win while a batch is short, when filling a ring is most of the
-// work (us, direct and ring, bf16 rows):
-//   forward    1216 x 1024   4.2  6.7    16384 x 512  15.6 16.8    16384 x 1024  34.7 29.4
-//   backward    304 x 1024   8.6  9.0     4864 x 512  18.4 19.0    16384 x 512   51.0 35.8
-//               152 x 4096  15.9 13.9    16384 x 256  25.1 25.8    65536 x 64    55.7 60.9
-// Rows of no whole 16 bytes take the ring as soon as every SM has one (608 x 1001: 7.9
-// and 7.6 forward, 28.8 and 12.5 backward).  Rows too wide for three stages never do.
+// work (us as a graph, direct and ring, bf16 rows, both norms and a channel gate):
+//   forward    1216 x 1024   3.6  5.9    16384 x 512  14.9 15.3    16384 x 1024  34.1 27.4
+//   backward    304 x 1024   8.0  8.3     4864 x 512  17.8 17.3    16384 x 512   49.2 29.9
+//               152 x 4096  14.8 13.0    16384 x 256  24.4 25.1    65536 x 64    55.4 46.0
+// Rows of no whole 16 bytes take the ring as soon as every SM has one (608 x 1001: 7.1
+// and 6.2 forward, 27.9 and 10.9 backward).  Rows too wide for three stages never do.
+// The rule goes by elements alone, and is on the careful side at its edges: wide rows just
+// below the forward's bound (2432 x 4096: 22.6 direct, 16.4) and narrow ones in the backward
+// (65536 x 64 above) would gain from the ring; entering alone at 16384 x 512 would not
+// (10.7, 11.8).
 bool ring_pays(const moe_norm_config& c, bool backward) {
     const int64_t n = (int64_t)c.T * c.d;
     if (c.T < num_sms()) return false;
