@@ -498,6 +498,53 @@ MOE_API int moe_mx4_grouped_product(const moe_mx4_product_config* cfg, const voi
                                     const void* wg_codes, const void* wg_scales, void* out,
                                     moe_stream_t stream);
 
+/* ---- microscaled 8-bit numbers ----
+ * A block of 32 consecutive elements of a row shares one power-of-two scale.  With
+ * amax the block's largest magnitude:
+ *   scale byte s (value 2^(s-127)): the smallest s >= 0 with amax <= 448 2^(s-127);
+ *                  255 where the block holds an infinity or NaN (value NaN)
+ *   code  = x 2^(127-s) to the nearest e4m3 number, ties to the even code (448 is the
+ *           largest, so nothing is clipped); 0 in a block of byte 255
+ * Codes: one byte an element, [rows,K].  Scales: [rows,P], P = moe_mx8_scale_pitch(K),
+ * byte i/32 of a row for its element i; a row's bytes from K/32 on stand for nothing
+ * and may hold anything.  Expert weights are [E,N,K], each expert's matrix transposed:
+ * E N rows of K.                                                             */
+/* Bytes of a row of scales: K/32 rounded up to a multiple of 16. */
+MOE_API int moe_mx8_scale_pitch(int32_t K, int32_t* pitch);
+
+/* Rows: x [rows,K] (dtype MOE_DTYPE_*), K a multiple of 32 -> codes [rows,K], scales.
+ * rows_used: one int32 on the device (moe_permute's offsets + E), or NULL for all:
+ * rows from it on are neither read nor written.                              */
+MOE_API int moe_mx8_quantize(int32_t dtype, int64_t rows, int32_t K, const void* x,
+                             const int32_t* rows_used, void* codes, void* scales,
+                             moe_stream_t stream);
+
+/* Weights: W [E,K,N] with blocks along K -> codes [E,N,K], scales [E,N,P].
+ * K a multiple of 32, N of 8, at most 2^21.                                   */
+MOE_API int moe_mx8_quantize_weight(int32_t dtype, int32_t E, int32_t K, int32_t N, const void* W,
+                                    void* codes, void* scales, moe_stream_t stream);
+
+/* The values that codes and scales stand for: out [rows,K] in dtype.  Exact in fp32, and
+ * in bf16 but for values below 2^-126, which are rounded; 2^128, to which magnitudes
+ * within 2^-5 of it are rounded, is infinite in both.                        */
+MOE_API int moe_mx8_dequantize(int32_t dtype, int64_t rows, int32_t K, const void* codes,
+                               const void* scales, void* out, moe_stream_t stream);
+
+/* moe_permute for rows in 8 bits, without padding: expert e's rows are
+ * offsets[e]..offsets[e+1], all of them real (pad_m and the layer's type are not looked
+ * at; d a multiple of 32).  rows_cap = moe_mx8_rows_capacity().
+ *   in : codes [T,d], scales [T,P], topk_idx [T,k]
+ *   out: codes_perm [rows_cap,d], scales_perm [rows_cap,P] (rows from offsets[E] on are
+ *        left as they were), perm_token [rows_cap], slot_of [T,k], kept [E],
+ *        offsets [E+1]; stats (may be NULL) as moe_permute's
+ *   ws:  moe_permute_mx8_workspace_size() bytes                              */
+MOE_API int moe_mx8_rows_capacity(const moe_config* cfg, int64_t* rows);   /* min(T*k, E*C) */
+MOE_API int moe_permute_mx8_workspace_size(const moe_config* cfg, size_t* bytes);
+MOE_API int moe_permute_mx8(const moe_config* cfg, const void* codes, const void* scales,
+                            const int32_t* topk_idx, void* codes_perm, void* scales_perm,
+                            int32_t* perm_token, int32_t* slot_of, int32_t* kept, int32_t* offsets,
+                            float* stats, void* ws, moe_stream_t stream);
+
 /* ---- status and bookkeeping ---- */
 
 /* Text of a status code (static storage). */

@@ -154,6 +154,13 @@ _SIGS = {
                           + [ctypes.c_void_p] * 4,
     "moe_check_mx4_product_config": [ctypes.c_void_p],
     "moe_mx4_grouped_product": [ctypes.c_void_p] * 10,
+    "moe_mx8_scale_pitch": [ctypes.c_int32, ctypes.c_void_p],
+    "moe_mx8_quantize": [ctypes.c_int32, ctypes.c_int64, ctypes.c_int32] + [ctypes.c_void_p] * 5,
+    "moe_mx8_quantize_weight": [ctypes.c_int32] * 4 + [ctypes.c_void_p] * 4,
+    "moe_mx8_dequantize": [ctypes.c_int32, ctypes.c_int64, ctypes.c_int32] + [ctypes.c_void_p] * 4,
+    "moe_mx8_rows_capacity": [ctypes.c_void_p] * 2,
+    "moe_permute_mx8_workspace_size": [ctypes.c_void_p] * 2,
+    "moe_permute_mx8": [ctypes.c_void_p] * 13,
     "moe_last_device_status": [ctypes.c_void_p, ctypes.c_void_p],
     "moe_selftest_bounded_wait": [ctypes.c_ulonglong, ctypes.c_void_p],
 }
@@ -503,5 +510,6 @@ class MoELayer:
 
 
 # the operators around the layer (imported last: they use the helpers above)
+from .mx8 import *  # noqa: E402,F401,F403
 from .block import *  # noqa: E402,F401,F403
 from .block import _quantize_segments  # noqa: E402

@@ -22,6 +22,10 @@ int launch_route(const moe_config& c, const void* x, const void* Wr, const float
 
 // permute.cu
 size_t permute_ws_bytes(const moe_config& c);
+// tokens' places alone, segments padded to multiples of pad_m
+int launch_permute_index(const moe_config& c, int pad_m, const int32_t* topk, int32_t* perm_token,
+                         int32_t* slot_of, int32_t* kept, int32_t* offsets, float* stats, void* ws,
+                         cudaStream_t st);
 int launch_permute(const moe_config& c, const void* x, const int32_t* topk, void* x_perm,
                    int32_t* perm_token, int32_t* slot_of, int32_t* kept, int32_t* offsets,
                    float* stats, void* ws, cudaStream_t st);
@@ -80,5 +84,16 @@ int launch_mx4_dequantize(int dtype, int sets, int64_t rows, int K, const void* 
 int launch_mx4_product(const moe_mx4_product_config& c, const void* xq, const void* xs, const int32_t* offsets,
                        const void* wq, const void* ws, const void* gq, const void* gs, void* out,
                        cudaStream_t st);
+
+// mx8.cu, mx8_gemm.cu (microscaled 8-bit numbers)
+int launch_mx8_quantize(int dtype, int64_t rows, int K, const void* x, const int32_t* rows_used,
+                        void* codes, void* scales, cudaStream_t st);
+int launch_mx8_quantize_weight(int dtype, int E, int K, int N, const void* W, void* codes, void* scales,
+                               cudaStream_t st);
+int launch_mx8_dequantize(int dtype, int64_t rows, int K, const void* codes, const void* scales, void* out,
+                          cudaStream_t st);
+int launch_permute_mx8(const moe_config& c, const void* codes, const void* scales, const int32_t* topk,
+                       void* codes_perm, void* scales_perm, int32_t* perm_token, int32_t* slot_of,
+                       int32_t* kept, int32_t* offsets, float* stats, void* ws, cudaStream_t st);
 
 }  // namespace moe

@@ -1,0 +1,295 @@
+// mx8.cu -- microscaled 8-bit numbers (mx8.cuh): quantisation of rows and of expert
+// weights, the values that codes and scales stand for, and the permutation of 8-bit
+// rows into expert segments.
+//
+// Memory-bound: 2 (or 4) bytes read, 33/32 written an element, and back.
+#include <algorithm>
+
+#include "kernels.h"
+#include "mx8.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int ROW_THREADS = 256, ROW_UNROLL = 4;
+constexpr int ROW_VECS = ROW_THREADS * ROW_UNROLL;      // vectors of a CTA's turn
+
+// A CTA's turn: whole rows while they fit, else a part of one row.  Vector i of the
+// turn lies in row i / nvec of it (by a product: i and nvec stay below 2^11 then).
+struct Turns {
+    int64_t rows, turns;                                // rows, and turns of `per` of them
+    int nvec, per, parts;                               // vectors a row; rows a turn; turns a row
+    uint32_t magic;
+};
+Turns turns_of(int64_t rows, int nvec) {
+    Turns t;
+    t.rows = rows;
+    t.nvec = nvec;
+    t.per = std::max(1, ROW_VECS / nvec);
+    t.parts = nvec > ROW_VECS ? (nvec + ROW_VECS - 1) / ROW_VECS : 1;
+    t.turns = (rows + t.per - 1) / t.per * t.parts;
+    t.magic = (uint32_t)(((1ull << 32) + nvec - 1) / nvec);
+    return t;
+}
+// places of this thread's vectors in turn `u`: row and vector, row -1 past the end
+struct Place { int64_t row; int vec; };
+__device__ __forceinline__ Place place(const Turns& t, int64_t used, int64_t u, int j) {
+    const int i = threadIdx.x + j * ROW_THREADS;
+    Place p;
+    if (t.parts == 1) {
+        const int r = t.nvec == 1 ? i : (int)__umulhi((uint32_t)i, t.magic);
+        p.row = u * t.per + r;
+        p.vec = i - r * t.nvec;
+        if (r >= t.per) p.row = -1;
+    } else {
+        p.row = u / t.parts;
+        p.vec = (int)(u - p.row * t.parts) * ROW_VECS + i;
+        if (p.vec >= t.nvec) p.row = -1;
+    }
+    if (p.row >= used) p.row = -1;
+    return p;
+}
+int turn_grid(const Turns& t) { return (int)std::max<int64_t>(1, std::min<int64_t>(t.turns, (int64_t)num_sms() * 32)); }
+
+// 8 elements as loaded
+template <typename T> struct Eight;
+template <> struct Eight<__nv_bfloat16> {
+    uint4 w;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { w = __ldg(reinterpret_cast<const uint4*>(p)); }
+    __device__ __forceinline__ void zero() { w = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void values(float (&v)[8]) const {
+        const uint32_t a[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(a[i] << 16);
+            v[2 * i + 1] = __uint_as_float(a[i] & 0xffff0000u);
+        }
+    }
+};
+template <> struct Eight<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float* p) {
+        a = __ldg(reinterpret_cast<const float4*>(p));
+        b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    }
+    __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ void values(float (&v)[8]) const {
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    }
+};
+__device__ __forceinline__ uint32_t amax8(const float (&v)[8]) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, abs_bits(v[i]));
+    return m;
+}
+
+// Rows: 8 elements a thread, so four neighbouring lanes hold a block (rows are whole
+// blocks, so those lanes are of one row).
+template <typename T>
+__global__ void __launch_bounds__(ROW_THREADS) mx8_rows_kernel(const T* __restrict__ x, const Turns t, int K, int pitch,
+                                                               const int32_t* __restrict__ rows_used,
+                                                               uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
+    pdl_wait();
+    pdl_trigger();
+    int64_t used = t.rows;
+    if (rows_used) used = min(used, (int64_t)max(*rows_used, 0));
+    for (int64_t u = blockIdx.x; u < t.turns; u += gridDim.x) {
+        Place p[ROW_UNROLL];
+        Eight<T> raw[ROW_UNROLL];
+#pragma unroll
+        for (int j = 0; j < ROW_UNROLL; ++j) {
+            p[j] = place(t, used, u, j);
+            if (p[j].row >= 0) raw[j].load(x + p[j].row * K + p[j].vec * 8);
+            else raw[j].zero();
+        }
+#pragma unroll
+        for (int j = 0; j < ROW_UNROLL; ++j) {
+            float v[8];
+            raw[j].values(v);
+            uint32_t m = amax8(v);
+            m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+            m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+            const uint32_t s = mx8_scale_byte(m);
+            uint32_t w[2];
+            mx8_codes<8>(v, s, w);
+            if (p[j].row < 0) continue;
+            *reinterpret_cast<uint2*>(codes + p[j].row * K + p[j].vec * 8) = make_uint2(w[0], w[1]);
+            if ((threadIdx.x & 3) == 0) scales[p[j].row * pitch + p[j].vec / 4] = (uint8_t)s;
+        }
+    }
+}
+
+// 16 codes a thread: half a block
+template <typename T>
+__global__ void __launch_bounds__(ROW_THREADS) mx8_values_kernel(const uint8_t* __restrict__ codes,
+                                                                 const uint8_t* __restrict__ scales, const Turns t, int K,
+                                                                 int pitch, T* __restrict__ out) {
+    pdl_wait();
+    pdl_trigger();
+    for (int64_t u = blockIdx.x; u < t.turns; u += gridDim.x) {
+        Place p[ROW_UNROLL];
+        uint4 c[ROW_UNROLL];
+        uint32_t s[ROW_UNROLL];
+#pragma unroll
+        for (int j = 0; j < ROW_UNROLL; ++j) {
+            p[j] = place(t, t.rows, u, j);
+            if (p[j].row < 0) continue;
+            c[j] = __ldg(reinterpret_cast<const uint4*>(codes + p[j].row * K) + p[j].vec);
+            s[j] = __ldg(scales + p[j].row * pitch + p[j].vec / 2);
+        }
+#pragma unroll
+        for (int j = 0; j < ROW_UNROLL; ++j) {
+            if (p[j].row < 0) continue;
+            const float m = mx8_scale_value(s[j]);
+            const uint32_t w[4] = {c[j].x, c[j].y, c[j].z, c[j].w};
+            float v[16];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mx8_unpack4(w[i], v + 4 * i);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] *= m;
+            T* dst = out + p[j].row * K + p[j].vec * 16;
+            constexpr int V = Vec16<T>::N;
+#pragma unroll
+            for (int i = 0; i < 16; i += V) store16_f<T>(dst + i, v + i);
+        }
+    }
+}
+
+// Weights W [E, K, N] -> [E, N, K]: a CTA takes 128 k x 64 n through shared memory; a
+// thread forms one block (32 k) of one column.
+constexpr int WN = 64, W_THREADS = WN * 4;
+template <typename T>
+__global__ void __launch_bounds__(W_THREADS) mx8_weight_kernel(const T* __restrict__ W, int K, int N, int pitch,
+                                                               uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
+    pdl_wait();
+    pdl_trigger();
+    constexpr int V = 16 / sizeof(T);
+    __shared__ __align__(16) T sm[128][WN + V];
+    __shared__ __align__(16) uint8_t sc[WN][128 + 16];
+    __shared__ __align__(4) uint8_t sb[WN][4];
+    const int k0 = blockIdx.x * 128, n0 = blockIdx.y * WN, e = blockIdx.z;
+    const T* We = W + (size_t)e * K * N;
+#pragma unroll
+    for (int i = threadIdx.x; i < 128 * (WN / V); i += W_THREADS) {
+        const int k = i / (WN / V), c = i % (WN / V) * V;
+        uint4 u = make_uint4(0, 0, 0, 0);
+        if (k0 + k < K && n0 + c < N) u = __ldg(reinterpret_cast<const uint4*>(We + (size_t)(k0 + k) * N + n0 + c));
+        *reinterpret_cast<uint4*>(&sm[k][c]) = u;
+    }
+    __syncthreads();
+    const int n = threadIdx.x % WN, kb = threadIdx.x / WN;
+    float v[32];
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        v[i] = to_f<T>(sm[kb * 32 + i][n]);
+        m = max(m, abs_bits(v[i]));
+    }
+    const uint32_t s = mx8_scale_byte(m);
+    uint32_t w[8];
+    mx8_codes<32>(v, s, w);
+    *reinterpret_cast<uint4*>(&sc[n][kb * 32]) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4*>(&sc[n][kb * 32 + 16]) = make_uint4(w[4], w[5], w[6], w[7]);
+    sb[n][kb] = (uint8_t)s;
+    __syncthreads();
+    // eight neighbouring threads write a column's 128 codes
+#pragma unroll
+    for (int i = threadIdx.x; i < WN * 8; i += W_THREADS) {
+        const int c = i / 8, k = i % 8 * 16;
+        if (n0 + c < N && k0 + k < K)
+            *reinterpret_cast<uint4*>(codes + ((size_t)e * N + n0 + c) * K + k0 + k) = *reinterpret_cast<const uint4*>(&sc[c][k]);
+    }
+    // (the four bytes lie within the row's pitch, whose last may stand for no block)
+    if (threadIdx.x < WN && n0 + threadIdx.x < N)
+        *reinterpret_cast<uint32_t*>(scales + ((size_t)e * N + n0 + threadIdx.x) * pitch + k0 / 32) =
+            *reinterpret_cast<const uint32_t*>(sb[threadIdx.x]);
+}
+
+// Rows of 8-bit numbers to their places: a warp takes a token and writes each of its
+// slots, so a row is read once however many experts it goes to.
+__global__ void __launch_bounds__(256) mx8_scatter_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
+                                                          const int32_t* __restrict__ slot_of, int T, int k, int d, int pitch,
+                                                          uint8_t* __restrict__ codes_perm, uint8_t* __restrict__ scales_perm) {
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31, nc = d / 16, nv = nc + pitch / 16;
+    for (int t = blockIdx.x * 8 + (threadIdx.x >> 5); t < T; t += gridDim.x * 8) {
+        const int mine = lane < k ? slot_of[(size_t)t * k + lane] : -1;
+        const uint4* c = reinterpret_cast<const uint4*>(codes + (size_t)t * d);
+        const uint4* s = reinterpret_cast<const uint4*>(scales + (size_t)t * pitch);
+        for (int v0 = 0; v0 < nv; v0 += 128) {
+            uint4 r[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int v = v0 + i * 32 + lane;
+                if (v < nv) r[i] = __ldg(v < nc ? c + v : s + v - nc);
+            }
+            for (int j = 0; j < k; ++j) {
+                const int row = __shfl_sync(0xffffffffu, mine, j);
+                if (row < 0) continue;
+                uint4* dc = reinterpret_cast<uint4*>(codes_perm + (size_t)row * d);
+                uint4* ds = reinterpret_cast<uint4*>(scales_perm + (size_t)row * pitch);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int v = v0 + i * 32 + lane;
+                    if (v < nv) *(v < nc ? dc + v : ds + v - nc) = r[i];
+                }
+            }
+        }
+    }
+}
+
+template <typename T>
+int rows_t(int64_t rows, int K, const void* x, const int32_t* used, void* codes, void* scales, cudaStream_t st) {
+    const Turns t = turns_of(rows, K / 8);
+    MOE_LAUNCH(mx8_rows_kernel<T>, turn_grid(t), ROW_THREADS, 0, st, static_cast<const T*>(x), t, K, (int)mx8_pitch(K), used,
+               static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scales));
+    return MOE_OK;
+}
+template <typename T>
+int weight_t(int E, int K, int N, const void* W, void* codes, void* scales, cudaStream_t st) {
+    const dim3 grid((K + 127) / 128, (N + WN - 1) / WN, E);
+    MOE_LAUNCH(mx8_weight_kernel<T>, grid, W_THREADS, 0, st, static_cast<const T*>(W), K, N, (int)mx8_pitch(K),
+               static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scales));
+    return MOE_OK;
+}
+template <typename T>
+int values_t(int64_t rows, int K, const void* codes, const void* scales, void* out, cudaStream_t st) {
+    const Turns t = turns_of(rows, K / 16);
+    MOE_LAUNCH(mx8_values_kernel<T>, turn_grid(t), ROW_THREADS, 0, st, static_cast<const uint8_t*>(codes),
+               static_cast<const uint8_t*>(scales), t, K, (int)mx8_pitch(K), static_cast<T*>(out));
+    return MOE_OK;
+}
+
+}  // namespace
+
+int launch_mx8_quantize(int dtype, int64_t rows, int K, const void* x, const int32_t* rows_used, void* codes,
+                        void* scales, cudaStream_t st) {
+    return dtype == MOE_DTYPE_BF16 ? rows_t<__nv_bfloat16>(rows, K, x, rows_used, codes, scales, st)
+                                   : rows_t<float>(rows, K, x, rows_used, codes, scales, st);
+}
+int launch_mx8_quantize_weight(int dtype, int E, int K, int N, const void* W, void* codes, void* scales,
+                               cudaStream_t st) {
+    return dtype == MOE_DTYPE_BF16 ? weight_t<__nv_bfloat16>(E, K, N, W, codes, scales, st)
+                                   : weight_t<float>(E, K, N, W, codes, scales, st);
+}
+int launch_mx8_dequantize(int dtype, int64_t rows, int K, const void* codes, const void* scales, void* out,
+                          cudaStream_t st) {
+    return dtype == MOE_DTYPE_BF16 ? values_t<__nv_bfloat16>(rows, K, codes, scales, out, st)
+                                   : values_t<float>(rows, K, codes, scales, out, st);
+}
+int launch_permute_mx8(const moe_config& c, const void* codes, const void* scales, const int32_t* topk,
+                       void* codes_perm, void* scales_perm, int32_t* perm_token, int32_t* slot_of, int32_t* kept,
+                       int32_t* offsets, float* stats, void* ws, cudaStream_t st) {
+    if (const int r = launch_permute_index(c, 1, topk, perm_token, slot_of, kept, offsets, stats, ws, st)) return r;
+    const int grid = std::min((c.T + 7) / 8, num_sms() * 8);
+    MOE_LAUNCH(mx8_scatter_kernel, grid, 256, 0, st, static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(scales),
+               slot_of, c.T, c.k, c.d, (int)mx8_pitch(c.d), static_cast<uint8_t*>(codes_perm),
+               static_cast<uint8_t*>(scales_perm));
+    return MOE_OK;
+}
+
+}  // namespace moe

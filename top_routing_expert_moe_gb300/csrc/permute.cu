@@ -185,17 +185,27 @@ size_t permute_ws_bytes(const moe_config& c) {
     return align_up(ntiles * c.E * 4);
 }
 
-int launch_permute(const moe_config& c, const void* x, const int32_t* topk, void* x_perm,
-                   int32_t* perm_token, int32_t* slot_of, int32_t* kept, int32_t* offsets,
-                   float* stats, void* ws, cudaStream_t st)
+int launch_permute_index(const moe_config& c, int pad_m, const int32_t* topk, int32_t* perm_token,
+                         int32_t* slot_of, int32_t* kept, int32_t* offsets, float* stats, void* ws,
+                         cudaStream_t st)
 {
     const int ntiles = (c.T + PT_TOK - 1) / PT_TOK;
     int32_t* tile_counts = static_cast<int32_t*>(ws);
     const int C = capacity_of(c);
     MOE_LAUNCH(tile_hist_kernel, ntiles, PT_TOK, 0, st, topk, c.T, c.E, c.k, tile_counts,
                                                 device_status_ptr());
-    MOE_LAUNCH(scan_assign_kernel, ntiles, PT_TOK, 0, st, topk, c.T, c.E, c.k, C, c.pad_m, tile_counts,
+    MOE_LAUNCH(scan_assign_kernel, ntiles, PT_TOK, 0, st, topk, c.T, c.E, c.k, C, pad_m, tile_counts,
                ntiles, kept, offsets, slot_of, perm_token, stats);
+    return MOE_OK;
+}
+
+int launch_permute(const moe_config& c, const void* x, const int32_t* topk, void* x_perm,
+                   int32_t* perm_token, int32_t* slot_of, int32_t* kept, int32_t* offsets,
+                   float* stats, void* ws, cudaStream_t st)
+{
+    if (const int r = launch_permute_index(c, c.pad_m, topk, perm_token, slot_of, kept, offsets, stats,
+                                           ws, st))
+        return r;
     const int64_t rows = rows_cap_of(c);
     const int grid = (int)std::min<int64_t>((rows + 7) / 8, (int64_t)num_sms() * 8);
     if (c.dtype == MOE_DTYPE_BF16)

@@ -1,0 +1,168 @@
+"""The experts in 8 bits: binding of their C entry points.
+
+Microscaled 8-bit numbers (``moe_mx8_*``) and the permutation of rows held in them
+(``moe_permute_mx8``).  As in the package's root, every function mirrors the C entry
+point of the same name and the classes own the output buffers and workspaces of one
+configuration.  What a call with ``stream`` allocates belongs to that stream.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+import top_routing_expert_moe_gb300 as _moe
+
+__all__ = ["MX8Tensor", "mx8_scale_pitch", "moe_mx8_quantize", "moe_mx8_quantize_weight",
+           "moe_mx8_dequantize", "mx8_quantize", "mx8_quantize_weight", "mx8_rows_capacity",
+           "permute_mx8_workspace_size", "moe_permute_mx8", "MX8Dispatch"]
+
+_p, _s, _on, _call = _moe._p, _moe._s, _moe._on, _moe._call
+
+
+def _checked(t, shape, dtype, name):
+    """The tensor, after a check of its shape and type."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch tensor")
+    if t.shape != shape or t.dtype != dtype:
+        raise ValueError(f"{name}: expected {tuple(shape)} {dtype}, got {tuple(t.shape)} {t.dtype}")
+    return t
+
+
+def _checked8(t, shape, name):
+    if not isinstance(t, MX8Tensor):
+        raise TypeError(f"{name}: expected an MX8Tensor")
+    if t.shape != tuple(shape):
+        raise ValueError(f"{name}: expected {tuple(shape)}, got {t.shape}")
+    return t
+
+
+_DTYPES = {torch.bfloat16: _moe.BF16, torch.float32: _moe.F32}
+
+
+def _dtype(dtype) -> int:
+    code = _DTYPES.get(dtype)
+    if code is None:
+        raise ValueError(f"expected bfloat16 or float32, got {dtype}")
+    return code
+
+
+def mx8_scale_pitch(K: int) -> int:
+    v = ctypes.c_int32()
+    _call("moe_mx8_scale_pitch", K, ctypes.byref(v))
+    return v.value
+
+
+def moe_mx8_quantize(dtype, rows, K, x, rows_used, codes, scales, stream=None):
+    _call("moe_mx8_quantize", dtype, rows, K, _p(x), _p(rows_used), _p(codes), _p(scales), _s(stream))
+
+
+def moe_mx8_quantize_weight(dtype, E, K, N, W, codes, scales, stream=None):
+    _call("moe_mx8_quantize_weight", dtype, E, K, N, _p(W), _p(codes), _p(scales), _s(stream))
+
+
+def moe_mx8_dequantize(dtype, rows, K, codes, scales, out, stream=None):
+    _call("moe_mx8_dequantize", dtype, rows, K, _p(codes), _p(scales), _p(out), _s(stream))
+
+
+class MX8Tensor:
+    """8-bit numbers [rows, K] or, for expert weights, [E, rows, K]: ``codes`` (e4m3, as
+    bytes) of that shape and ``scales`` [..., pitch], one byte for 32 codes."""
+
+    def __init__(self, shape, device="cuda"):
+        shape = tuple(shape)
+        if len(shape) not in (2, 3):
+            raise ValueError("expected [rows, K] or [E, rows, K]")
+        K = shape[-1]
+        if min(shape) < 1 or K % 32:
+            mx8_scale_pitch(K)                       # raises for the width
+            raise ValueError(f"expected sizes of 1 or more, got {shape}")
+        self.shape = shape
+        # moe_mx8_scale_pitch, without the call
+        self.codes = torch.empty(shape, dtype=torch.uint8, device=device)
+        self.scales = torch.empty((*shape[:-1], (K // 32 + 15) // 16 * 16), dtype=torch.uint8, device=device)
+
+    def dequantize(self, dtype=torch.bfloat16, stream=None):
+        code = _dtype(dtype)
+        with _on(stream):
+            out = torch.empty(self.shape, dtype=dtype, device=self.codes.device)
+        K = self.shape[-1]
+        moe_mx8_dequantize(code, out.numel() // K, K, self.codes, self.scales, out, stream)
+        return out
+
+
+def mx8_quantize(x, rows_used=None, out=None, stream=None) -> MX8Tensor:
+    """Quantise rows x [rows, K] along K (K a multiple of 32) into ``out`` or a new
+    tensor.  ``rows_used``: one int32 on the device, rows from it on are left out."""
+    if x.dim() != 2:
+        raise ValueError("x: expected [rows, K]")
+    code = _dtype(x.dtype)
+    if out is None:
+        with _on(stream):
+            out = MX8Tensor(x.shape, x.device)
+    else:
+        _checked8(out, x.shape, "out")
+    if rows_used is not None and (rows_used.numel() != 1 or rows_used.dtype != torch.int32):
+        raise ValueError("rows_used must be one int32")
+    moe_mx8_quantize(code, x.shape[0], x.shape[1], x, rows_used, out.codes, out.scales, stream)
+    return out
+
+
+def mx8_quantize_weight(W, stream=None) -> MX8Tensor:
+    """Quantise expert weights W [E, K, N] along K: an MX8Tensor [E, N, K]."""
+    if W.dim() != 3:
+        raise ValueError("W: expected [E, K, N]")
+    E, K, N = W.shape
+    code = _dtype(W.dtype)
+    with _on(stream):
+        out = MX8Tensor((E, N, K), W.device)
+    moe_mx8_quantize_weight(code, E, K, N, W, out.codes, out.scales, stream)
+    return out
+
+
+# ----------------------------------------------------------------- permutation
+def mx8_rows_capacity(cfg) -> int:
+    v = ctypes.c_int64()
+    _call("moe_mx8_rows_capacity", ctypes.byref(cfg), ctypes.byref(v))
+    return v.value
+
+
+def permute_mx8_workspace_size(cfg) -> int:
+    v = ctypes.c_size_t()
+    _call("moe_permute_mx8_workspace_size", ctypes.byref(cfg), ctypes.byref(v))
+    return v.value
+
+
+def moe_permute_mx8(cfg, codes, scales, topk_idx, codes_perm, scales_perm, perm_token, slot_of, kept,
+                    offsets, stats, ws, stream=None):
+    _call("moe_permute_mx8", ctypes.byref(cfg), _p(codes), _p(scales), _p(topk_idx), _p(codes_perm),
+          _p(scales_perm), _p(perm_token), _p(slot_of), _p(kept), _p(offsets), _p(stats), _p(ws),
+          _s(stream))
+
+
+class MX8Dispatch:
+    """Rows in 8 bits to the experts that they go to: segments without padding,
+    ``offsets`` [E + 1], for ``MX8Product``.  Owns the permuted rows, ``perm_token``
+    (the token of each row), ``slot_of`` [T, k] (the row of each choice, -1 if dropped)
+    and ``kept`` [E]."""
+
+    def __init__(self, cfg, device="cuda"):
+        ws = permute_mx8_workspace_size(cfg)          # raises for a bad configuration
+        self.cfg, self.rows_cap = cfg, mx8_rows_capacity(cfg)
+        e = lambda *s, dtype=torch.int32: torch.empty(*s, dtype=dtype, device=device)  # noqa: E731
+        self.rows = MX8Tensor((self.rows_cap, cfg.d), device)
+        self.perm_token, self.slot_of = e(self.rows_cap), e(cfg.T, cfg.k)
+        self.kept, self.offsets = e(cfg.E), e(cfg.E + 1)
+        self.ws = e(max(ws, 256), dtype=torch.uint8)
+
+    def forward(self, x: MX8Tensor, topk_idx, stats=None, stream=None) -> MX8Tensor:
+        """The permuted rows of x [T, d] (those from offsets[E] on are left as they were)
+        for topk_idx [T, k] int32, -1 where a token takes part in nothing."""
+        c = self.cfg
+        _checked8(x, (c.T, c.d), "x")
+        _checked(topk_idx, (c.T, c.k), torch.int32, "topk_idx")
+        if stats is not None:
+            _checked(stats, (9 + c.E,), torch.float32, "stats")
+        moe_permute_mx8(c, x.codes, x.scales, topk_idx, self.rows.codes, self.rows.scales, self.perm_token,
+                        self.slot_of, self.kept, self.offsets, stats, self.ws, stream)
+        return self.rows
