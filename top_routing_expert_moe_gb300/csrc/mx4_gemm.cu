@@ -34,11 +34,10 @@
 
 #include <algorithm>
 #include <cstring>
-#include <mutex>
 
 #include "common.cuh"
 #include "kernels.h"
-#include "tma.cuh"
+#include "mx_tc.cuh"
 
 namespace moe {
 
@@ -81,52 +80,12 @@ struct Mx4Params {
     int max_tiles;                         // their grid: tiles of the rows that are not padding
 };
 
-__device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr) {
-    uint64_t d = (uint64_t)((saddr & 0x3FFFFu) >> 4);
-    d |= (uint64_t)1 << 16;                // leading offset: not used with one swizzle atom along K
-    d |= (uint64_t)(1024 >> 4) << 32;      // 8-row groups
-    d |= (uint64_t)1 << 46;                // descriptor version
-    d |= (uint64_t)2 << 61;                // 128-byte swizzle
-    return d;
-}
 // kind::mxf4: e2m1 x e2m1, scales of 8 exponent bits for 32 elements; `half` picks the
 // lower or upper two bytes of a scale word
 __device__ __forceinline__ uint32_t idesc_mx4(int M, int N, int half) {
     return ((uint32_t)(2 * half) << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | (1u << 23) |
            ((uint32_t)(M >> 7) << 27) | ((uint32_t)(2 * half) << 29);
 }
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* v) {
-    uint32_t r[16];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-          "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr));
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
-}
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
-    uint32_t r[32];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
-          "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
-          "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr));
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-}
-
 template <int CG>
 __device__ __forceinline__ void mma_mx4(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc,
                                         uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
@@ -141,90 +100,6 @@ __device__ __forceinline__ void mma_mx4(uint32_t d, uint32_t a_lo, uint32_t b_lo
             "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], da, db, %4, [%5], [%6], p;\n}" ::"r"(d),
             "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate));
 }
-__device__ __forceinline__ uint32_t elect_one() {
-    uint32_t p;
-    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(p));
-    return p;
-}
-// words of this warp's 32 lanes, from column taddr on
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint4 (&v)[2]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0].x),
-                 "r"(v[0].y), "r"(v[0].z), "r"(v[0].w), "r"(v[1].x), "r"(v[1].y), "r"(v[1].z), "r"(v[1].w)
-                 : "memory");
-}
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint4 (&v)[4]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-        "r"(v[0].x), "r"(v[0].y), "r"(v[0].z), "r"(v[0].w), "r"(v[1].x), "r"(v[1].y), "r"(v[1].z), "r"(v[1].w),
-        "r"(v[2].x), "r"(v[2].y), "r"(v[2].z), "r"(v[2].w), "r"(v[3].x), "r"(v[3].y), "r"(v[3].z), "r"(v[3].w)
-        : "memory");
-}
-template <int CG>
-__device__ __forceinline__ void commit_all(uint32_t bar) {
-    if constexpr (CG == 1)
-        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-                     : "memory");
-    else
-        asm volatile(
-            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-            "h"((uint16_t)0x3)
-            : "memory");
-}
-template <int CG>
-__device__ __forceinline__ void commit_local(uint32_t bar) {
-    if constexpr (CG == 1)
-        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-                     : "memory");
-    else
-        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-                     : "memory");
-}
-// Bounded wait of one thread (CG = 2: acquire at cluster scope), as mbar_wait, but the clock and the
-// flags are looked at every 1024 tries only: a stage of these kernels lasts no longer
-// than one look at them.
-template <int CG>
-__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {
-    unsigned long long t0 = 0;
-    for (uint32_t it = 1;; ++it) {
-        if (CG == 1 ? mbar_try(bar, parity) : mbar_try_cl(bar, parity)) return true;
-        if ((it & 1023) == 0) {
-            if (*abort_flag) return false;
-            const unsigned long long now = gtimer();
-            if (t0 == 0) t0 = now;
-            const bool late = now - t0 > WAIT_NS;
-            if (late) set_status(status, MOE_ERR_TIMEOUT);
-            if (late || timeout_pending(status)) {
-                *abort_flag = 1;
-                return false;
-            }
-        }
-    }
-}
-// The lanes of a warp that all look may differ when a wait gives up (one sees the phase,
-// another the abort flag), and a warp that parted there would not meet again: they go on
-// together or not at all.
-__device__ __forceinline__ bool agreed(bool got) { return __all_sync(0xffffffffu, got); }
-// a whole warp waits: one lane looks
-template <int CG>
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {
-    int got = 0;
-    if ((threadIdx.x & 31) == 0) got = wait_bar<CG>(bar, parity, abort_flag, status);
-    return __shfl_sync(0xffffffffu, got, 0) != 0;
-}
-// Arrival on the pair's even CTA.  What it announces (tensor memory written or read)
-// is ordered by the tcgen05 waits and fences around it, so it carries no release of
-// ordinary memory to the cluster, which costs more than a stage's MMAs.
-__device__ __forceinline__ void arrive_pair(uint32_t cluster_addr) {
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
-}
-template <int CG>
-__device__ __forceinline__ void drain_bar(uint32_t bar, uint32_t parity) {
-    if constexpr (CG == 1) mbar_drain(bar, parity);
-    else mbar_drain_cl(bar, parity);
-}
-
-__device__ __forceinline__ float silu_quick(float z) { return __fdividef(z, 1.0f + __expf(-z)); }
-
 // A tile is CG * 128 rows x BN accumulator columns; tiles run over experts, then
 // groups of RASTER_ROWS rows, columns, rows.
 struct Mx4Tile { int e, m0, nb, valid; };   // valid: 128-row blocks of the segment from m0 on
@@ -755,37 +630,6 @@ __global__ void __launch_bounds__(NTHREADS, 1) mx4_grouped_kernel(const __grid_c
         int _r = (x);                \
         if (_r != MOE_OK) return _r; \
     } while (0)
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-EncodeTiledFn encode_fn() {
-    static EncodeTiledFn fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(p);
-    });
-    return fn;
-}
-// 3-D map with 128-byte swizzle: dims[0] contiguous, strides[i] the byte stride of dims[i + 1]
-int encode_map(CUtensorMap* m, CUtensorMapDataType type, const void* ptr, const uint64_t (&dims)[3],
-               const uint64_t (&strides)[2], const uint32_t (&box)[3]) {
-    EncodeTiledFn fn = encode_fn();
-    if (!fn) return MOE_ERR_CUDA;
-    const cuuint64_t d[3] = {dims[0], dims[1], dims[2]}, st[2] = {strides[0], strides[1]};
-    const cuuint32_t b[3] = {box[0], box[1], box[2]}, es[3] = {1, 1, 1};
-    return fn(m, type, 3, const_cast<void*>(ptr), d, st, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
-               ? MOE_OK
-               : MOE_ERR_CUDA;
-}
 
 // codes [sets, rows, K / 2]: boxes of 128 bytes x `box_rows` rows
 int codes_map(CUtensorMap* m, const void* p, int64_t rows, int sets, int K, int box_rows) {
