@@ -545,6 +545,37 @@ MOE_API int moe_permute_mx8(const moe_config* cfg, const void* codes, const void
                             int32_t* perm_token, int32_t* slot_of, int32_t* kept, int32_t* offsets,
                             float* stats, void* ws, moe_stream_t stream);
 
+#define MOE_DTYPE_MX8 2    /* out_dtype below: codes and scales */
+#define MOE_MX8_ACT_NONE 0
+#define MOE_MX8_ACT_SILU 1
+#define MOE_MX8_ACT_SWIGLU 2
+
+typedef struct {
+    int64_t rows;      /* rows of x and out                                    */
+    int32_t K;         /* reduction width, a multiple of 32                    */
+    int32_t N;         /* output width, a multiple of 8 (MX8 output: of 32)    */
+    int32_t E;         /* experts, 1..64                                       */
+    int32_t act;       /* MOE_MX8_ACT_*                                        */
+    int32_t out_dtype; /* MOE_DTYPE_F32, MOE_DTYPE_BF16 or MOE_DTYPE_MX8       */
+} moe_mx8_product_config;
+
+MOE_API int moe_check_mx8_product_config(const moe_mx8_product_config* cfg);
+
+/* Grouped product over segments of any length, expert e's the rows offsets[e] to
+ * offsets[e+1] (device, ascending, within 0..rows; moe_permute_mx8's or moe_permute's):
+ *   u = Q(x) Q(W_e), fp32 accumulation;  out = u, silu(u), or silu(g) u with g = Q(x) Q(Wg_e)
+ *   x_codes/x_scales: 8-bit rows [rows,K]; w_*, wg_*: moe_mx8_quantize_weight of W, Wg
+ *   [E,K,N] (wg_* NULL but for SWIGLU); out [rows,N] by out_dtype; out_scales
+ *   [rows, moe_mx8_scale_pitch(N)] for MOE_DTYPE_MX8 (out then holds the codes of the
+ *   fp32 values), else NULL.  Rows of no segment are not written.
+ * Offsets that descend or leave 0..rows are recorded as MOE_ERR_DEVICE_BOUNDS, and
+ * nothing is written.                                                        */
+MOE_API int moe_mx8_grouped_product(const moe_mx8_product_config* cfg, const void* x_codes,
+                                    const void* x_scales, const int32_t* offsets,
+                                    const void* w_codes, const void* w_scales,
+                                    const void* wg_codes, const void* wg_scales, void* out,
+                                    void* out_scales, moe_stream_t stream);
+
 /* ---- status and bookkeeping ---- */
 
 /* Text of a status code (static storage). */

@@ -30,6 +30,21 @@ __device__ __forceinline__ float mx8_scale_value(uint32_t s) {
 }
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
+// bits of the largest magnitude of N (even) values: NaN's where one is, which is above
+// every number's; two values an instruction
+__device__ __forceinline__ float max3_abs(float a, float b, float c) {
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+template <int N>
+__device__ __forceinline__ uint32_t amax_bits(const float* v) {
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; i += 2) m = max3_abs(m, v[i], v[i + 1]);
+    return __float_as_uint(m);
+}
+
 // 4 scaled values -> 4 codes, the first in the low byte
 __device__ __forceinline__ uint32_t mx8_pack4(float a, float b, float c, float d) {
     uint32_t r;

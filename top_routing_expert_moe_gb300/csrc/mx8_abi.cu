@@ -11,6 +11,8 @@ namespace {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool ok_ptr(const void* p) { return p != nullptr && aligned16(p); }
+// a pointer that is there exactly when `on`
+bool ok_if(bool on, const void* p) { return on ? ok_ptr(p) : p == nullptr; }
 bool is_dtype(int v) { return v == MOE_DTYPE_F32 || v == MOE_DTYPE_BF16; }
 // a tensor of 8-bit numbers: rows, and a width that is whole blocks
 int mx8_shape(int64_t rows, int K) {
@@ -94,6 +96,34 @@ int moe_permute_mx8(const moe_config* c, const void* codes, const void* scales, 
         return MOE_ERR_INVALID_ARG;
     return launch_permute_mx8(*c, codes, scales, topk_idx, codes_perm, scales_perm, perm_token, slot_of, kept,
                               offsets, stats, ws, (cudaStream_t)stream);
+}
+
+int moe_check_mx8_product_config(const moe_mx8_product_config* c) {
+    if (!c || c->N < 1 || c->E < 1) return MOE_ERR_INVALID_ARG;
+    if (!is_dtype(c->out_dtype) && c->out_dtype != MOE_DTYPE_MX8) return MOE_ERR_INVALID_ARG;
+    if (c->act < MOE_MX8_ACT_NONE || c->act > MOE_MX8_ACT_SWIGLU) return MOE_ERR_INVALID_ARG;
+    const int r = mx8_shape(c->rows, c->K);
+    if (r) return r;
+    if (c->N % (c->out_dtype == MOE_DTYPE_MX8 ? 32 : 8) || c->N > (1 << 21) || c->E > 64 || c->rows > (1 << 30))
+        return MOE_ERR_UNSUPPORTED;
+    // 32-bit tile counts, at the smallest tile's 64 columns
+    if ((c->rows / 128 + c->E) * (((int64_t)c->N + 63) / 64) > (1LL << 30)) return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+
+int moe_mx8_grouped_product(const moe_mx8_product_config* c, const void* x_codes, const void* x_scales,
+                            const int32_t* offsets, const void* w_codes, const void* w_scales,
+                            const void* wg_codes, const void* wg_scales, void* out, void* out_scales,
+                            moe_stream_t stream) {
+    const int r = moe_check_mx8_product_config(c);
+    if (r) return r;
+    const bool dual = c->act == MOE_MX8_ACT_SWIGLU;
+    if (!ok_ptr(x_codes) || !ok_ptr(x_scales) || !ok_ptr(offsets) || !ok_ptr(w_codes) ||
+        !ok_ptr(w_scales) || !ok_if(dual, wg_codes) || !ok_if(dual, wg_scales) || !ok_ptr(out) ||
+        !ok_if(c->out_dtype == MOE_DTYPE_MX8, out_scales))
+        return MOE_ERR_INVALID_ARG;
+    return launch_mx8_product(*c, x_codes, x_scales, offsets, w_codes, w_scales, wg_codes, wg_scales, out,
+                              out_scales, (cudaStream_t)stream);
 }
 
 }  // extern "C"

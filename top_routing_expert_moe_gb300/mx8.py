@@ -1,7 +1,8 @@
 """The experts in 8 bits: binding of their C entry points.
 
-Microscaled 8-bit numbers (``moe_mx8_*``) and the permutation of rows held in them
-(``moe_permute_mx8``).  As in the package's root, every function mirrors the C entry
+Microscaled 8-bit numbers, the permutation of rows held in them
+(``moe_permute_mx8``) and the experts' grouped product over segments of any length
+(``moe_mx8_grouped_product``).  As in the package's root, every function mirrors the C entry
 point of the same name and the classes own the output buffers and workspaces of one
 configuration.  What a call with ``stream`` allocates belongs to that stream.
 """
@@ -15,7 +16,12 @@ import top_routing_expert_moe_gb300 as _moe
 
 __all__ = ["MX8Tensor", "mx8_scale_pitch", "moe_mx8_quantize", "moe_mx8_quantize_weight",
            "moe_mx8_dequantize", "mx8_quantize", "mx8_quantize_weight", "mx8_rows_capacity",
-           "permute_mx8_workspace_size", "moe_permute_mx8", "MX8Dispatch"]
+           "permute_mx8_workspace_size", "moe_permute_mx8", "MX8Dispatch", "MX8", "MX8_ACT_NONE",
+           "MX8_ACT_SILU", "MX8_ACT_SWIGLU", "MX8ProductConfig", "check_mx8_product_config",
+           "moe_mx8_grouped_product", "MX8Product", "MX8Experts"]
+
+MX8 = 2                                              # an output type beside F32 and BF16
+MX8_ACT_NONE, MX8_ACT_SILU, MX8_ACT_SWIGLU = 0, 1, 2
 
 _p, _s, _on, _call = _moe._p, _moe._s, _moe._on, _moe._call
 
@@ -166,3 +172,67 @@ class MX8Dispatch:
         moe_permute_mx8(c, x.codes, x.scales, topk_idx, self.rows.codes, self.rows.scales, self.perm_token,
                         self.slot_of, self.kept, self.offsets, stats, self.ws, stream)
         return self.rows
+
+
+# ----------------------------------------------------------------- product
+class MX8ProductConfig(ctypes.Structure):
+    """Mirror of ``moe_mx8_product_config`` (include/moe.h)."""
+    _fields_ = [("rows", ctypes.c_int64), ("K", ctypes.c_int32), ("N", ctypes.c_int32),
+                ("E", ctypes.c_int32), ("act", ctypes.c_int32), ("out_dtype", ctypes.c_int32)]
+
+    def __init__(self, rows, K, N, E, act=MX8_ACT_NONE, out_dtype=_moe.BF16):
+        super().__init__(rows, K, N, E, act, out_dtype)
+
+
+def check_mx8_product_config(cfg: MX8ProductConfig) -> int:
+    return _moe.load_library().moe_check_mx8_product_config(ctypes.byref(cfg))
+
+
+def moe_mx8_grouped_product(cfg, x_codes, x_scales, offsets, w_codes, w_scales, wg_codes, wg_scales,
+                            out, out_scales, stream=None):
+    _call("moe_mx8_grouped_product", ctypes.byref(cfg), _p(x_codes), _p(x_scales), _p(offsets),
+          _p(w_codes), _p(w_scales), _p(wg_codes), _p(wg_scales), _p(out), _p(out_scales), _s(stream))
+
+
+class MX8Product:
+    """out = act(x W_e) over expert segments of any length, x and W in 8 bits.  Owns the
+    output: a tensor, or an MX8Tensor where ``out_dtype`` is MX8."""
+
+    def __init__(self, cfg: MX8ProductConfig, device="cuda"):
+        rc = check_mx8_product_config(cfg)
+        if rc != 0:
+            raise _moe.MoEError(rc, "moe_check_mx8_product_config")
+        self.cfg = c = cfg
+        self._x, self._offsets, self._w = (c.rows, c.K), (c.E + 1,), (c.E, c.N, c.K)
+        self._dual = c.act == MX8_ACT_SWIGLU
+        if c.out_dtype == MX8:
+            self.out = MX8Tensor((c.rows, c.N), device)
+            self._out = self.out.codes, self.out.scales
+        else:
+            self.out = torch.empty(c.rows, c.N, device=device,
+                                   dtype=torch.bfloat16 if c.out_dtype == _moe.BF16 else torch.float32)
+            self._out = self.out, None
+
+    def forward(self, x: MX8Tensor, offsets, w: MX8Tensor, wg: MX8Tensor | None = None, stream=None):
+        """out [rows, N] (rows of no segment are not written); x [rows, K], offsets
+        [E + 1] int32 as from MX8Dispatch, w (and the gate wg for SwiGLU) [E, N, K]."""
+        _checked8(x, self._x, "x")
+        _checked(offsets, self._offsets, torch.int32, "offsets")
+        if (wg is not None) != self._dual:
+            raise ValueError("wg is required iff act is MX8_ACT_SWIGLU")
+        _checked8(w, self._w, "w")
+        if wg is not None:
+            _checked8(wg, self._w, "wg")
+        moe_mx8_grouped_product(self.cfg, x.codes, x.scales, offsets, w.codes, w.scales,
+                                wg.codes if wg else None, wg.scales if wg else None, *self._out, stream)
+        return self.out
+
+
+class MX8Experts:
+    """A layer's expert weights in 8 bits, for ``MoELayer.forward_mx8``: quantised once
+    from W_up, W_gate (SwiGLU) [E, d, f] and W_down [E, f, d]."""
+
+    def __init__(self, W_up, W_down, W_gate=None, stream=None):
+        self.up = mx8_quantize_weight(W_up, stream)
+        self.down = mx8_quantize_weight(W_down, stream)
+        self.gate = mx8_quantize_weight(W_gate, stream) if W_gate is not None else None
