@@ -545,6 +545,14 @@ MOE_API int moe_permute_mx8(const moe_config* cfg, const void* codes, const void
                             int32_t* perm_token, int32_t* slot_of, int32_t* kept, int32_t* offsets,
                             float* stats, void* ws, moe_stream_t stream);
 
+/* moe_block_norm (enter = 1, d a multiple of 32) with z in 8 bits: codes [T,d], scales
+ * [T,P], quantised from z before it is rounded to the storage type; z itself may be NULL
+ * (not wanted).  x_out may be x and z may be u, as there; no other overlap.     */
+MOE_API int moe_block_norm_mx8(const moe_norm_config* cfg, const void* x, const void* u,
+                               const float* w_post, const void* gate, const float* w_pre,
+                               void* x_out, void* z, void* codes, void* scales,
+                               moe_stream_t stream);
+
 #define MOE_DTYPE_MX8 2    /* out_dtype below: codes and scales */
 #define MOE_MX8_ACT_NONE 0
 #define MOE_MX8_ACT_SILU 1

@@ -161,6 +161,7 @@ _SIGS = {
     "moe_mx8_rows_capacity": [ctypes.c_void_p] * 2,
     "moe_permute_mx8_workspace_size": [ctypes.c_void_p] * 2,
     "moe_permute_mx8": [ctypes.c_void_p] * 13,
+    "moe_block_norm_mx8": [ctypes.c_void_p] * 11,
     "moe_check_mx8_product_config": [ctypes.c_void_p],
     "moe_mx8_grouped_product": [ctypes.c_void_p] * 11,
     "moe_last_device_status": [ctypes.c_void_p, ctypes.c_void_p],

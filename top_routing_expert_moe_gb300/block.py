@@ -16,9 +16,10 @@ import ctypes
 import torch
 
 import top_routing_expert_moe_gb300 as _moe
+from .mx8 import MX8Tensor
 
 __all__ = ["GATE_NONE", "GATE_CHANNEL", "GATE_TOKEN", "GATE_FULL", "NormConfig",
-           "check_norm_config", "norm_workspace_size", "moe_block_norm",
+           "check_norm_config", "norm_workspace_size", "moe_block_norm", "moe_block_norm_mx8",
            "moe_block_norm_backward", "BlockNorm", "BalanceConfig", "check_balance_config",
            "balance_workspace_size", "moe_balance_loss", "moe_balance_loss_backward",
            "BalanceLoss", "MX4_ACT_NONE", "MX4_ACT_SILU", "MX4_ACT_SWIGLU", "MX4Tensor",
@@ -82,6 +83,11 @@ def moe_block_norm(cfg, x, u, w_post, gate, w_pre, x_out, z, stream=None):
           _p(x_out), _p(z), _s(stream))
 
 
+def moe_block_norm_mx8(cfg, x, u, w_post, gate, w_pre, x_out, z, codes, scales, stream=None):
+    _call("moe_block_norm_mx8", ctypes.byref(cfg), _p(x), _p(u), _p(w_post), _p(gate), _p(w_pre),
+          _p(x_out), _p(z), _p(codes), _p(scales), _s(stream))
+
+
 def moe_block_norm_backward(cfg, x_out, u, w_post, gate, w_pre, dx_out, dz, dx, du, dw_post, dgate,
                             dw_pre, ws, stream=None):
     _call("moe_block_norm_backward", ctypes.byref(cfg), _p(x_out), _p(u), _p(w_post), _p(gate),
@@ -106,7 +112,7 @@ class BlockNorm:
             torch.empty(*s, dtype=dtype, device=self.device) if on else None)
         self.x_out = e(c.leave, c.T, c.d)
         self.z = e(c.enter, c.T, c.d)
-        self._grads = self._ws = None
+        self.z8 = self._grads = self._ws = None
 
     def _check(self, rows, w_pre, w_post, gate):
         for n, t in rows:
@@ -124,6 +130,21 @@ class BlockNorm:
         self._check((("x", x), ("u", u)), w_pre, w_post, gate)
         moe_block_norm(self.cfg, x, u, w_post, gate, w_pre, self.x_out, self.z, stream)
         return (self.x_out if self._leave else x), self.z
+
+    def forward_mx8(self, x, u=None, w_pre=None, w_post=None, gate=None, keep_z=True, stream=None):
+        """(x_out, z8, z): forward() with the normalised copy in 8 bits, an MX8Tensor, and
+        beside it z itself (None unless ``keep_z``).  Needs ``enter`` and a width of whole
+        32s; the backward is that of the unquantised z."""
+        c = self.cfg
+        if not c.enter:
+            raise ValueError("forward_mx8 needs a configuration that enters a block")
+        self._check((("x", x), ("u", u)), w_pre, w_post, gate)
+        if self.z8 is None:
+            with _on(stream):
+                self.z8 = MX8Tensor((c.T, c.d), self.device)
+        z = self.z if keep_z else None
+        moe_block_norm_mx8(c, x, u, w_post, gate, w_pre, self.x_out, z, self.z8.codes, self.z8.scales, stream)
+        return (self.x_out if self._leave else x), self.z8, z
 
     def grads(self):
         if self._grads is None:

@@ -65,6 +65,11 @@ int launch_block_norm_backward(const moe_norm_config& c, const void* x_out, cons
                                const void* dx_out, const void* dz, void* dx, void* du,
                                float* dw_post, void* dgate, float* dw_pre, void* ws, cudaStream_t st);
 
+// norm_mx8.cu (z in 8 bits, and z itself unless NULL)
+int launch_block_norm_mx8(const moe_norm_config& c, const void* x, const void* u, const float* w_post,
+                          const void* gate, const float* w_pre, void* x_out, void* z, void* codes,
+                          void* scales, cudaStream_t st);
+
 // balance.cu (per-sequence balance loss and z loss)
 size_t balance_ws_bytes(const moe_balance_config& c);
 int launch_balance_loss(const moe_balance_config& c, const float* logits, const int32_t* topk,

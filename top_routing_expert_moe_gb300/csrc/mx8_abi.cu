@@ -98,6 +98,20 @@ int moe_permute_mx8(const moe_config* c, const void* codes, const void* scales, 
                               offsets, stats, ws, (cudaStream_t)stream);
 }
 
+int moe_block_norm_mx8(const moe_norm_config* c, const void* x, const void* u, const float* w_post,
+                       const void* gate, const float* w_pre, void* x_out, void* z, void* codes,
+                       void* scales, moe_stream_t stream) {
+    const int r = moe_check_norm_config(c);
+    if (r) return r;
+    if (!c->enter) return MOE_ERR_INVALID_ARG;
+    if (c->d % 32) return MOE_ERR_UNSUPPORTED;
+    if (!ok_ptr(x) || !ok_if(c->leave, u) || !ok_if(c->post_norm, w_post) ||
+        !ok_if(c->gate != MOE_GATE_NONE, gate) || !ok_ptr(w_pre) || !ok_if(c->leave, x_out) ||
+        !aligned16(z) || !ok_ptr(codes) || !ok_ptr(scales))
+        return MOE_ERR_INVALID_ARG;
+    return launch_block_norm_mx8(*c, x, u, w_post, gate, w_pre, x_out, z, codes, scales, (cudaStream_t)stream);
+}
+
 int moe_check_mx8_product_config(const moe_mx8_product_config* c) {
     if (!c || c->N < 1 || c->E < 1) return MOE_ERR_INVALID_ARG;
     if (!is_dtype(c->out_dtype) && c->out_dtype != MOE_DTYPE_MX8) return MOE_ERR_INVALID_ARG;
