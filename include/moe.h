@@ -584,6 +584,39 @@ MOE_API int moe_mx8_grouped_product(const moe_mx8_product_config* cfg, const voi
                                     const void* wg_codes, const void* wg_scales, void* out,
                                     void* out_scales, moe_stream_t stream);
 
+/* ---- activations kept in 8 bits ----
+ * moe_grouped_ffn with the hidden rows h (SwiGLU: g, u) kept for the backward in 8-bit
+ * numbers, a quarter of what h_saved and act take (SiLU; SwiGLU a third), for the bf16
+ * layer without shared experts.  The forward computes with the unrounded h, as
+ * moe_grouped_ffn does; act is scratch that need not outlive it.  The backward sees the
+ * kept values alone: with h^ (g^, u^) what the codes stand for it forms
+ * act = silu(h^) (silu(g^) u^) again, into act, and
+ *   dW_down = act^T dy, dh = dact silu'(h^) (dg, du likewise), dW_up, dW_gate, dx as
+ * moe_grouped_ffn_backward does from these.
+ *   h_codes [nh,rows_cap,f], h_scales [nh,rows_cap,P], P = moe_mx8_scale_pitch(f); the
+ *   other arguments as there.                                                */
+MOE_API int moe_grouped_ffn_mx8(const moe_config* cfg, const void* x_perm, const int32_t* offsets,
+                                const void* W_up, const void* W_gate, const void* W_down,
+                                void* h_codes, void* h_scales, void* act, void* y_perm, void* ws,
+                                moe_stream_t stream);
+MOE_API int moe_grouped_ffn_backward_mx8(const moe_config* cfg, const void* x_perm,
+                                         const int32_t* offsets, const void* W_up,
+                                         const void* W_gate, const void* W_down,
+                                         const void* h_codes, const void* h_scales, void* act,
+                                         const void* dy_perm, void* dh, void* dx_perm, void* dW_up,
+                                         void* dW_gate, void* dW_down, void* ws,
+                                         moe_stream_t stream);
+
+/* moe_backward_aux from activations kept so (act: scratch [rows_cap,f]). */
+MOE_API int moe_backward_mx8(const moe_config* cfg, const void* x, const void* W_r, const void* W_up,
+                     const void* W_gate, const void* W_down, const float* logits,
+                     const int32_t* topk_idx, const float* gate, const int32_t* slot_of,
+                     const int32_t* perm_token, const int32_t* offsets, const void* x_perm,
+                     const void* h_codes, const void* h_scales, void* act, const void* y_perm,
+                     const float* stats, const float* dlogits_aux, const void* dout, void* dx,
+                     void* dW_r, float* dbias, void* dW_up, void* dW_gate, void* dW_down, void* ws,
+                     moe_stream_t stream);
+
 /* ---- status and bookkeeping ---- */
 
 /* Text of a status code (static storage). */

@@ -162,6 +162,9 @@ _SIGS = {
     "moe_permute_mx8_workspace_size": [ctypes.c_void_p] * 2,
     "moe_permute_mx8": [ctypes.c_void_p] * 13,
     "moe_block_norm_mx8": [ctypes.c_void_p] * 11,
+    "moe_grouped_ffn_mx8": [ctypes.c_void_p] * 12,
+    "moe_grouped_ffn_backward_mx8": [ctypes.c_void_p] * 17,
+    "moe_backward_mx8": [ctypes.c_void_p] * 28,
     "moe_check_mx8_product_config": [ctypes.c_void_p],
     "moe_mx8_grouped_product": [ctypes.c_void_p] * 11,
     "moe_last_device_status": [ctypes.c_void_p, ctypes.c_void_p],
@@ -406,8 +409,14 @@ class MoELayer:
                             act=self.act_shared, y=self.y_shared)
 
     def forward(self, x, W_r, W_up, W_down, W_gate=None, bias=None, noise=None, token_mask=None,
-                stream=None, shared=None):
+                stream=None, shared=None, checkpoint=None):
+        """The layer's output [T, d] (its own buffer).  With ``checkpoint`` (a MoECheckpoint) what
+        the backward needs is kept there, the activations in 8 bits, and nothing of it in the
+        layer: one layer then serves a model's every depth, each with a checkpoint of its own.
+        x and the weights are to stay as they are until that backward."""
         c = self.cfg
+        if checkpoint is not None:
+            return self._forward_kept(checkpoint, x, W_r, W_up, W_down, W_gate, bias, noise, token_mask, stream)
         if (c.f_shared > 0) != (shared is not None):
             raise ValueError("shared-expert weights are required iff cfg.f_shared > 0")
         if shared is not None:
@@ -424,6 +433,34 @@ class MoELayer:
         moe_combine(c, self.y_perm, self.slot_of, self.gate, self.out, stream, shared=sh)
         self._inputs = (x, W_r, W_up, W_gate, W_down, bias)
         return self.out
+
+    def _forward_kept(self, k, x, W_r, W_up, W_down, W_gate, bias, noise, token_mask, stream):
+        c = self.cfg
+        k.check(c)
+        self._inputs = k.inputs = None
+        moe_route(c, x, W_r, bias, noise, token_mask, k.logits, k.topk_idx, k.gate, k.counts, k.stats, self.ws,
+                  stream)
+        moe_permute(c, x, k.topk_idx, self.x_perm, k.perm_token, k.slot_of, k.kept, k.offsets, k.stats, self.ws,
+                    stream)
+        moe_grouped_ffn_mx8(c, self.x_perm, k.offsets, W_up, W_gate, W_down, k.h.codes, k.h.scales, self.act,
+                            self.y_perm, self.ws, stream)
+        k.keep_y(self.y_perm, stream)
+        moe_combine(c, self.y_perm, k.slot_of, k.gate, self.out, stream)
+        k.inputs = (x, W_r, W_up, W_gate, W_down, bias)
+        return self.out
+
+    def _backward_kept(self, k, dout, stream, dlogits_aux, g):
+        c = self.cfg
+        x, W_r, W_up, W_gate, W_down, bias = k.inputs
+        # the same rows as in the forward: the permutation goes by the kept choices alone
+        moe_permute(c, x, k.topk_idx, self.x_perm, k.perm_token, k.slot_of, k.kept, k.offsets, None, self.ws,
+                    stream)
+        k.y_into(self.y_perm, stream)
+        moe_backward_mx8(c, x, W_r, W_up, W_gate, W_down, k.logits, k.topk_idx, k.gate, k.slot_of, k.perm_token,
+                         k.offsets, self.x_perm, k.h.codes, k.h.scales, self.act, self.y_perm, k.stats,
+                         dlogits_aux, dout, g["dx"], g["dW_r"], g["dbias"] if bias is not None else None,
+                         g["dW_up"], g["dW_gate"], g["dW_down"], self.ws, stream)
+        return g
 
     def forward_mx4(self, x, W_r, experts, bias=None, noise=None, token_mask=None, stream=None):
         """The forward with both GEMMs' operands in microscaled 4-bit numbers:
@@ -493,17 +530,24 @@ class MoELayer:
                             act=self.act_shared, y=self.y_shared, dout=dout, dh=dh, dx=dx,
                             dW_up=g["dW_up_s"], dW_gate=g["dW_gate_s"], dW_down=g["dW_down_s"])
 
-    def backward(self, dout, stream=None, dlogits_aux=None):
-        """Gradients of the last forward.  ``dlogits_aux`` [T, E] fp32: a further
-        gradient on the router logits (a balance loss's), added to the router's own."""
-        if self._inputs is None:
+    def backward(self, dout, stream=None, dlogits_aux=None, checkpoint=None):
+        """Gradients of the last forward, or of the forward that ``checkpoint`` was given to
+        (its activations as their 8-bit numbers stand for them).  ``dlogits_aux`` [T, E] fp32:
+        a further gradient on the router logits (a balance loss's), added to the router's own."""
+        if checkpoint is not None:
+            checkpoint.check(self.cfg)
+        if (self._inputs if checkpoint is None else checkpoint.inputs) is None:
             raise RuntimeError("backward() needs a forward() first")
-        x, W_r, W_up, W_gate, W_down, bias = self._inputs
         with _on(stream):
             g = self.grads()
         if dlogits_aux is not None and (tuple(dlogits_aux.shape) != (self.cfg.T, self.cfg.E) or
                                         dlogits_aux.dtype != torch.float32):
             raise ValueError("dlogits_aux must be a [T, E] fp32 tensor")
+        if checkpoint is not None:
+            # what the last plain forward left in the layer's buffers goes
+            self._inputs = None
+            return self._backward_kept(checkpoint, dout, stream, dlogits_aux, g)
+        x, W_r, W_up, W_gate, W_down, bias = self._inputs
         moe_backward_aux(self.cfg, x, W_r, W_up, W_gate, W_down, self.logits, self.topk_idx,
                          self.gate, self.slot_of, self.perm_token, self.offsets, self.x_perm,
                          self.h_saved, self.act, self.y_perm, self.stats, dlogits_aux, dout,

@@ -50,6 +50,7 @@
 #include "common.cuh"
 #include "gemm_tc.h"
 #include "kernels.h"
+#include "mx8.cuh"
 #include "tma.cuh"
 
 namespace moe {
@@ -78,6 +79,9 @@ constexpr int RASTER_GM = 32;
 constexpr int SPLIT_MIN_WAVES = 16;   // "many waves of tiles": a launch this long is split by tile length
 
 enum Epi { EPI_STORE = 0, EPI_SILU_FWD = 1, EPI_SWIGLU_FWD = 2, EPI_SILU_BWD = 3, EPI_SWIGLU_BWD = 4 };
+// With h (g, u) kept in 8 bits the same four read and write it so (kernels of KEEP8; EPI_STORE
+// is the other kernels'): the forward writes codes in h's place, the backward forms
+// the activation again from them and writes it for the weight gradient of W_down.
 enum Sched { SCHED_ROWS = 0, SCHED_KSEG = 1 };
 
 // One GEMM problem of a launch.  A launch runs up to MAX_PROBLEMS independent
@@ -94,6 +98,10 @@ struct TcProblem {
     __nv_bfloat16* out2;
     const __nv_bfloat16* in0;
     const __nv_bfloat16* in1;
+    CUtensorMap tmC[2];     // KEEP8: codes of h (or g, u), boxes of 32 rows x 32 columns, 32-byte swizzle
+    uint8_t* codes[2];
+    uint8_t* scales[2];
+    int sc_pitch;
     long long out_estride;  // SCHED_KSEG: elements between experts' outputs
     int sched;
     int n_blocks;           // N / bn
@@ -273,7 +281,7 @@ __device__ __forceinline__ void mma_commit_local(uint32_t bar) {
 // completions are multicast to both CTAs' "empty" and "accumulator full"
 // barriers, and both CTAs' epilogue warps release an accumulator on the even
 // CTA's "accumulator empty" barrier.  Each CTA drains its own 128 TMEM lanes.
-template <int CG>
+template <int CG, bool KEEP8>
 __global__ void __launch_bounds__(NTHREADS, 1) tc_grouped_gemm_kernel(const __grid_constant__ TcParams P)
 {
     constexpr int S = CG == 1 ? 2 : 3;                       // ring stages
@@ -364,6 +372,10 @@ __global__ void __launch_bounds__(NTHREADS, 1) tc_grouped_gemm_kernel(const __gr
             for (int i = 0; i < 3; ++i)
                 if (outs[i])
                     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&q.tmO[i])) : "memory");
+            if constexpr (KEEP8)
+                if (q.epi == EPI_SILU_FWD || q.epi == EPI_SWIGLU_FWD)
+                    for (int i = 0; i < 1 + q.dual; ++i)
+                        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&q.tmC[i])) : "memory");
         }
         int it = 0;
         bool ok = start_live;
@@ -524,6 +536,28 @@ __global__ void __launch_bounds__(NTHREADS, 1) tc_grouped_gemm_kernel(const __gr
             }
             ++nst;
         };
+        // 32 columns of this lane's row in 8 bits: a block
+        auto put8 = [&](const TcProblem& q, int i, const float* v, int c0, int c1, long long row) {
+            uint8_t* buf = stg + (nst & 1) * 2048;
+            if (nst >= 2) {
+                if (lane == 0) bulk_wait_read<1>();
+                __syncwarp();
+            }
+            const uint32_t s = mx8_scale_byte(amax_bits<32>(v));
+            uint32_t w[8];
+            mx8_codes<32>(v, s, w);
+            const int x = ((lane >> 2) & 1) << 4;         // 32-byte swizzle
+            *reinterpret_cast<uint4*>(buf + lane * 32 + x) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(buf + lane * 32 + (x ^ 16)) = make_uint4(w[4], w[5], w[6], w[7]);
+            q.scales[i][row * q.sc_pitch + c0 / 32] = (uint8_t)s;
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                tma_store3(&q.tmC[i], smem_u32(buf), c0, c1, 0);
+                bulk_commit();
+            }
+            ++nst;
+        };
         int tcount = 0;
         for (int tix = unit; tix < total; tix += nunits, ++tcount) {
             Tile t;
@@ -552,7 +586,25 @@ __global__ void __launch_bounds__(NTHREADS, 1) tc_grouped_gemm_kernel(const __gr
                     for (int j = 0; j < 4; ++j) nxt[1][j] = p1[j];
                 }
             };
-            if (valid && n_in) fetch(c_lo);
+            // the same of what is kept in 8 bits
+            uint4 nxt8[2][2];
+            uint32_t nxs[2];
+            auto fetch8 = [&](int c) {
+                const long long at = row * q.ldo + t.n0 + c * 32, sat = row * q.sc_pitch + (t.n0 + c * 32) / 32;
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    if (i < n_in) {
+                        const uint4* p = reinterpret_cast<const uint4*>(q.codes[i] + at);
+                        nxt8[i][0] = p[0];
+                        nxt8[i][1] = p[1];
+                        nxs[i] = q.scales[i][sat];
+                    }
+            };
+            if constexpr (KEEP8) {
+                if (valid && n_in) fetch8(c_lo);
+            } else {
+                if (valid && n_in) fetch(c_lo);
+            }
             // every lane takes the same decision (the box stores below sync the warp)
             const bool got = __all_sync(0xffffffffu,
                                         CG == 1 ? mbar_wait(smem_u32(&tfull[acc]), aph, abort_flag, P.status)
@@ -566,6 +618,58 @@ __global__ void __launch_bounds__(NTHREADS, 1) tc_grouped_gemm_kernel(const __gr
             for (int c = c_lo; valid && c < c_hi; ++c) {
                 const int bcol = t.n0 + c * 32;
                 float v[32];
+                if constexpr (KEEP8) {
+                    tmem_ld32(taddr + c * 32, v);
+                    if (q.epi == EPI_SWIGLU_FWD) {
+                        float u[32];
+                        tmem_ld32(taddr + 128 + c * 32, u);
+                        tmem_wait_ld();
+                        put8(q, 0, v, bcol, brow, row);
+                        put8(q, 1, u, bcol, brow, row);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = silu_fast(v[i]) * u[i];
+                        put(&q.tmO[0], v, bcol, brow, 0);
+                    } else if (q.epi == EPI_SILU_FWD) {
+                        tmem_wait_ld();
+                        put8(q, 0, v, bcol, brow, row);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = silu_fast(v[i]);
+                        put(&q.tmO[0], v, bcol, brow, 0);
+                    } else {
+                        // v = dact; dh (or dg, du) and the activation at the kept values
+                        uint32_t w[2][8];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                const uint4 x = nxt8[i][j];
+                                w[i][4 * j] = x.x; w[i][4 * j + 1] = x.y; w[i][4 * j + 2] = x.z; w[i][4 * j + 3] = x.w;
+                            }
+                        const float sc0 = mx8_scale_value(nxs[0]), sc1 = n_in == 2 ? mx8_scale_value(nxs[1]) : 0.f;
+                        if (c + 1 < c_hi) fetch8(c + 1);
+                        tmem_wait_ld();
+                        float a[32], o[32];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            float g[4], u[4];
+                            mx8_unpack4(w[0][k], g);
+                            if (n_in == 2) mx8_unpack4(w[1][k], u);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const int i = 4 * k + j;
+                                const float z = g[j] * sc0, x = n_in == 2 ? u[j] * sc1 : 1.f;
+                                const float sg = __fdividef(1.0f, 1.0f + __expf(-z));   // sigmoid(z), once
+                                a[i] = z * sg * x;
+                                o[i] = v[i] * x * (sg * (1.0f + z * (1.0f - sg)));
+                                v[i] *= z * sg;
+                            }
+                        }
+                        put(&q.tmO[0], o, bcol, brow, 0);                       // dh, or dg
+                        if (n_in == 2) put(&q.tmO[1], v, bcol, brow, 0);        // du
+                        put(&q.tmO[2], a, bcol, brow, 0);
+                    }
+                    continue;
+                }
                 if (t.nk == 0) {
 #pragma unroll
                     for (int i = 0; i < 32; ++i) v[i] = 0.f;
@@ -693,6 +797,18 @@ int make_map_nd(CUtensorMap* m, const void* ptr, int rank, const uint64_t* dims,
     return r == CUDA_SUCCESS ? MOE_OK : MOE_ERR_CUDA;
 }
 
+// [rows, cols] bytes, boxes of 32 rows x 32 columns, 32-byte swizzle
+int encode_u8_map(CUtensorMap* m, const void* ptr, int cols, int64_t rows) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return MOE_ERR_CUDA;
+    const cuuint64_t d[3] = {(cuuint64_t)cols, (cuuint64_t)rows, 1}, st[2] = {(cuuint64_t)cols, (cuuint64_t)cols * rows};
+    const cuuint32_t b[3] = {32, 32, 1}, es[3] = {1, 1, 1};
+    const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(ptr), d, st, b, es,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_32B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? MOE_OK : MOE_ERR_CUDA;
+}
+
 // activations [rows_cap, cols] as the block view {64, rows_cap, cols / 64} (64-column
 // blocks 128 B apart).  K-major share: box {64, 128 rows, 2 k-blocks}; MN-major share:
 // box {64, 128 k-rows, blocks 64-column blocks}.  Shared memory: the box's blocks one
@@ -743,7 +859,7 @@ int max_pairs() {
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
     if (!done[dev]) {
         done[dev] = true;
-        if (cudaFuncSetAttribute(tc_grouped_gemm_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        if (cudaFuncSetAttribute(tc_grouped_gemm_kernel<2, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  SMEM_BYTES) != cudaSuccess) {
             (void)cudaGetLastError();
             return 0;
@@ -760,7 +876,7 @@ int max_pairs() {
         cfg.attrs = attr;
         cfg.numAttrs = 1;
         int n = 0;
-        if (cudaOccupancyMaxActiveClusters(&n, tc_grouped_gemm_kernel<2>, &cfg) != cudaSuccess) {
+        if (cudaOccupancyMaxActiveClusters(&n, tc_grouped_gemm_kernel<2, false>, &cfg) != cudaSuccess) {
             (void)cudaGetLastError();
             n = 0;
         }
@@ -769,14 +885,18 @@ int max_pairs() {
     return cached[dev];
 }
 
+template <bool KEEP8 = false>
 int launch_tc(const moe_config& c, const int32_t* offsets, const TcProblem* probs, int nprob,
               cudaStream_t st) {
     static bool attr_done[64] = {};
     int dev = 0;
     MOE_CUDA_TRY(cudaGetDevice(&dev));
     if (dev < 64 && !attr_done[dev]) {
-        MOE_CUDA_TRY(cudaFuncSetAttribute(tc_grouped_gemm_kernel<1>,
+        MOE_CUDA_TRY(cudaFuncSetAttribute(tc_grouped_gemm_kernel<1, KEEP8>,
                                           cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES));
+        if (KEEP8)                        // (max_pairs() does so for the others)
+            MOE_CUDA_TRY(cudaFuncSetAttribute(tc_grouped_gemm_kernel<2, KEEP8>,
+                                              cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES));
         attr_done[dev] = true;
     }
     if (nprob < 1 || nprob > MAX_PROBLEMS) return MOE_ERR_INVALID_ARG;
@@ -807,7 +927,7 @@ int launch_tc(const moe_config& c, const int32_t* offsets, const TcProblem* prob
         cfg.attrs = attr;
         cfg.numAttrs = 2;
         void* args[] = {&P};
-        const cudaError_t e = cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(tc_grouped_gemm_kernel<2>), args);
+        const cudaError_t e = cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(tc_grouped_gemm_kernel<2, KEEP8>), args);
         note_launch();
         if (e != cudaSuccess) {
             (void)cudaGetLastError();
@@ -818,7 +938,7 @@ int launch_tc(const moe_config& c, const int32_t* offsets, const TcProblem* prob
     int64_t tiles = 0;
     for (int i = 0; i < nprob; ++i) tiles += max_tiles(c, probs[i], 1);
     const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(tiles, num_sms()));
-    MOE_LAUNCH_PARAM(tc_grouped_gemm_kernel<1>, grid, NTHREADS, SMEM_BYTES, st, P);
+    MOE_LAUNCH_PARAM((tc_grouped_gemm_kernel<1, KEEP8>), grid, NTHREADS, SMEM_BYTES, st, P);
     return MOE_OK;
 }
 
@@ -931,6 +1051,7 @@ int wgrad_problem(TcProblem& q, const Family& F, const void* A, int64_t a_rows, 
 }
 
 // GEMM1 with the activation fused: h|g,u = x W_up|W_gate; act = silu(h) | silu(g) u
+// (h NULL: it is kept in 8 bits, and act is the only output in 16)
 int gemm1_problem(TcProblem& q, const moe_config& c, const Family& F, void* h, void* act) {
     using bf = __nv_bfloat16;
     const int d = c.d, f = F.f;
@@ -944,15 +1065,20 @@ int gemm1_problem(TcProblem& q, const moe_config& c, const Family& F, void* h, v
         MOE_TRY(weight_map(&q.tmB0, F.Wg, F.E, d, f, true, 2));
         MOE_TRY(weight_map(&q.tmB1, F.Wu, F.E, d, f, true, 2));
         q.epi = EPI_SWIGLU_FWD;
-        q.out0 = static_cast<bf*>(h);
-        q.out1 = static_cast<bf*>(h) + F.rows * f;
-        q.out2 = static_cast<bf*>(act);
+        if (h) {
+            q.out0 = static_cast<bf*>(h);
+            q.out1 = static_cast<bf*>(h) + F.rows * f;
+            q.out2 = static_cast<bf*>(act);
+        }
     } else {
         MOE_TRY(weight_map(&q.tmB0, F.Wu, F.E, d, f, true, q.bn / cta_group() / 64));
         q.epi = EPI_SILU_FWD;
-        q.out0 = static_cast<bf*>(h);
-        q.out1 = static_cast<bf*>(act);
+        if (h) {
+            q.out0 = static_cast<bf*>(h);
+            q.out1 = static_cast<bf*>(act);
+        }
     }
+    if (!h) q.out0 = static_cast<bf*>(act);
     return out_maps_rows(q, F.rows);
 }
 
@@ -967,17 +1093,19 @@ int gemm2_problem(TcProblem& q, const moe_config& c, const Family& F, const void
 }
 
 // dgrad2 with the activation derivative fused: dact = dy W_down^T -> dh (SiLU) or dg, du (SwiGLU)
+// (h NULL: it was kept in 8 bits; act is then formed again, else NULL)
 int dgrad2_problem(TcProblem& q, const moe_config& c, const Family& F, const void* dy,
-                   int64_t dy_rows, const void* h, void* dh) {
+                   int64_t dy_rows, const void* h, void* dh, void* act = nullptr) {
     using bf = __nv_bfloat16;
     const int f = F.f;
     MOE_TRY(rows_problem(q, F, dy, dy_rows, c.d, f));
     MOE_TRY(weight_map(&q.tmB0, F.Wd, F.E, f, c.d, false, q.bn / cta_group()));
     q.in0 = static_cast<const bf*>(h);
     q.out0 = static_cast<bf*>(dh);
+    q.out2 = static_cast<bf*>(act);
     if (c.ffn == MOE_FFN_SWIGLU) {
         q.epi = EPI_SWIGLU_BWD;
-        q.in1 = static_cast<const bf*>(h) + F.rows * f;
+        if (h) q.in1 = static_cast<const bf*>(h) + F.rows * f;
         q.out1 = static_cast<bf*>(dh) + F.rows * f;
     } else {
         q.epi = EPI_SILU_BWD;
@@ -1001,6 +1129,17 @@ int dgrad1_problem(TcProblem& q, const moe_config& c, const Family& F, const voi
     q.epi = EPI_STORE;
     q.out0 = static_cast<bf*>(dx);
     return out_maps_rows(q, F.rows);
+}
+
+// codes and scales of h [nh, rows, f] as a problem's outputs (or, its codes, inputs)
+int keep8_fields(TcProblem& q, const moe_config& c, const Family& F, void* codes, void* scales) {
+    q.sc_pitch = (int)mx8_pitch(F.f);
+    for (int i = 0; i < (c.ffn == MOE_FFN_SWIGLU ? 2 : 1); ++i) {
+        q.codes[i] = static_cast<uint8_t*>(codes) + (int64_t)i * F.rows * F.f;
+        q.scales[i] = static_cast<uint8_t*>(scales) + (int64_t)i * F.rows * q.sc_pitch;
+        MOE_TRY(encode_u8_map(&q.tmC[i], q.codes[i], F.f, F.rows));
+    }
+    return MOE_OK;
 }
 
 // weight gradients: dW_down = act^T dy; dW_up = x^T dh (du); dW_gate = x^T dg
@@ -1087,6 +1226,51 @@ int tc_ffn_backward(const moe_config& c, const void* x_perm, const int32_t* offs
     };
     MOE_TRY(second(R, dh, dW_up, dW_gate, dx_perm));
     if (sh) MOE_TRY(second(shared_family(c, *sh), sh->dh, sh->dW_up, sh->dW_gate, sh->dx));
+    return launch_tc_classes(c, offsets, q, n, st);
+}
+
+int tc_ffn_forward_keep8(const moe_config& c, const void* x_perm, const int32_t* offsets,
+                         const void* W_up, const void* W_gate, const void* W_down, void* h_codes,
+                         void* h_scales, void* act, void* y_perm, cudaStream_t st)
+{
+    const Family R = routed_family(c, x_perm, W_up, W_gate, W_down);
+    TcProblem q = new_problem();
+    MOE_TRY(gemm1_problem(q, c, R, nullptr, act));
+    MOE_TRY(keep8_fields(q, c, R, h_codes, h_scales));
+    MOE_TRY(launch_tc<true>(c, offsets, &q, 1, st));
+    q = new_problem();
+    MOE_TRY(gemm2_problem(q, c, R, act, y_perm));
+    return launch_tc(c, offsets, &q, 1, st);
+}
+
+int tc_ffn_backward_keep8(const moe_config& c, const void* x_perm, const int32_t* offsets,
+                          const void* W_up, const void* W_gate, const void* W_down, const void* h_codes,
+                          const void* h_scales, void* act, const void* dy_perm, void* dh, void* dx_perm,
+                          void* dW_up, void* dW_gate, void* dW_down, cudaStream_t st)
+{
+    using bf = __nv_bfloat16;
+    const bool sw = c.ffn == MOE_FFN_SWIGLU;
+    const Family R = routed_family(c, x_perm, W_up, W_gate, W_down);
+    // launch 1: dact = dy W_down^T, and from the kept values dh (dg, du) and the activation
+    TcProblem q[MAX_PROBLEMS];
+    q[0] = new_problem();
+    MOE_TRY(dgrad2_problem(q[0], c, R, dy_perm, R.rows, nullptr, dh, act));
+    MOE_TRY(keep8_fields(q[0], c, R, const_cast<void*>(h_codes), const_cast<void*>(h_scales)));
+    MOE_TRY(launch_tc<true>(c, offsets, q, 1, st));
+    // launch 2: dW_down = act^T dy  ||  dW_up = x^T dh (du)  ||  [dW_gate = x^T dg]  ||  dx
+    const bf* dh0 = static_cast<const bf*>(dh);
+    const bf* dh1 = sw ? dh0 + R.rows * R.f : nullptr;
+    int n = 0;
+    q[n] = new_problem();
+    MOE_TRY(wgrads_down(q[n++], c, R, act, dy_perm, R.rows, dW_down));
+    q[n] = new_problem();
+    MOE_TRY(wgrad_problem(q[n++], R, R.x, R.x_rows, c.d, sw ? dh1 : dh0, R.rows, R.f, dW_up));
+    if (sw) {
+        q[n] = new_problem();
+        MOE_TRY(wgrad_problem(q[n++], R, R.x, R.x_rows, c.d, dh0, R.rows, R.f, dW_gate));
+    }
+    q[n] = new_problem();
+    MOE_TRY(dgrad1_problem(q[n++], c, R, dh, dx_perm));
     return launch_tc_classes(c, offsets, q, n, st);
 }
 

@@ -6,6 +6,7 @@
 #include <mutex>
 
 #include "common.cuh"
+#include "gemm_tc.h"
 #include "kernels.h"
 
 namespace moe {
@@ -143,6 +144,48 @@ int router_backward(const moe_config* c, const void* x, const void* W_r, const f
     return launch_router_backward(*c, x, W_r, logits, topk_idx, gate, slot_of, dgate, dx_perm,
                                   shared ? shared->dx : nullptr, stats, dl_aux, dx, dW_r, dbias,
                                   dlogits, ws, (cudaStream_t)stream);
+}
+
+// the bf16 layer's routed experts can keep their hidden rows in 8 bits
+int keep8_config(const moe_config* c) {
+    const int r = moe_check_config(c);
+    if (r) return r;
+    return c->dtype != MOE_DTYPE_BF16 || c->f_shared > 0 ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+
+// combine backward, the experts' (ffn), router backward; intermediates in ws
+template <typename Ffn>
+int whole_backward(const moe_config* c, const void* x, const void* W_r, const float* logits,
+                   const int32_t* topk_idx, const float* gate, const int32_t* slot_of,
+                   const int32_t* perm_token, const int32_t* offsets, const moe_shared_ffn* shared,
+                   const void* dout, const void* y_perm,
+                   const float* stats, const float* dlogits_aux, void* dx, void* dW_r, float* dbias, void* ws,
+                   moe_stream_t stream, const Ffn& ffn) {
+    int r = moe_check_config(c);
+    if (r) return r;
+    if (!ok_ptr(ws)) return MOE_ERR_INVALID_ARG;
+    if ((c->f_shared > 0) != (shared != nullptr)) return MOE_ERR_INVALID_ARG;
+    const BwdLayout L = bwd_layout(*c);
+    uint8_t* w = static_cast<uint8_t*>(ws);
+    void* dy = w + L.dy;
+    float* dgate = reinterpret_cast<float*>(w + L.dgate);
+    void* dh = w + L.dh;
+    void* dxp = w + L.dxp;
+    float* dlogits = reinterpret_cast<float*>(w + L.dlogits);
+    void* rest = w + L.rest;
+    moe_shared_ffn sh;
+    if (shared) {                     // the shared FFN's dy is the layer's dout (weight 1)
+        sh = *shared;
+        sh.dout = dout;
+        if (!sh.dh) sh.dh = w + L.sdh;
+        if (!sh.dx) sh.dx = w + L.sdx;
+    }
+    const moe_shared_ffn* shp = shared ? &sh : nullptr;
+    if ((r = moe_combine_backward(c, dout, y_perm, gate, slot_of, perm_token, offsets, dy, dgate, stream)))
+        return r;
+    if ((r = ffn(dy, dh, dxp, shp, rest))) return r;
+    return router_backward(c, x, W_r, logits, topk_idx, gate, slot_of, dgate, dxp, shp, stats,
+                           dlogits_aux, dx, dW_r, dbias, dlogits, rest, stream);
 }
 
 }  // namespace
@@ -303,6 +346,39 @@ int moe_router_backward(const moe_config* c, const void* x, const void* W_r, con
                            nullptr, dx, dW_r, dbias, dlogits, ws, stream);
 }
 
+int moe_grouped_ffn_mx8(const moe_config* c, const void* x_perm, const int32_t* offsets, const void* W_up,
+                        const void* W_gate, const void* W_down, void* h_codes, void* h_scales, void* act,
+                        void* y_perm, void* ws, moe_stream_t stream) {
+    const int r = keep8_config(c);
+    if (r) return r;
+    const bool sw = c->ffn == MOE_FFN_SWIGLU;
+    if (!ok_ptr(x_perm) || !ok_ptr(offsets) || !ok_ptr(W_up) || !ok_ptr(W_down) ||
+        (sw ? !ok_ptr(W_gate) : !ok_opt(W_gate)) || !ok_ptr(h_codes) || !ok_ptr(h_scales) || !ok_ptr(act) ||
+        !ok_ptr(y_perm) || !ok_opt(ws))
+        return MOE_ERR_INVALID_ARG;
+    if (ffn_ws_bytes(*c) > 0 && !ws) return MOE_ERR_INVALID_ARG;
+    return tc_ffn_forward_keep8(*c, x_perm, offsets, W_up, W_gate, W_down, h_codes, h_scales, act, y_perm,
+                                (cudaStream_t)stream);
+}
+
+int moe_grouped_ffn_backward_mx8(const moe_config* c, const void* x_perm, const int32_t* offsets,
+                                 const void* W_up, const void* W_gate, const void* W_down,
+                                 const void* h_codes, const void* h_scales, void* act, const void* dy_perm,
+                                 void* dh, void* dx_perm, void* dW_up, void* dW_gate, void* dW_down,
+                                 void* ws, moe_stream_t stream) {
+    const int r = keep8_config(c);
+    if (r) return r;
+    const bool sw = c->ffn == MOE_FFN_SWIGLU;
+    if (!ok_ptr(x_perm) || !ok_ptr(offsets) || !ok_ptr(W_up) || !ok_ptr(W_down) ||
+        (sw ? !ok_ptr(W_gate) : !ok_opt(W_gate)) || !ok_ptr(h_codes) || !ok_ptr(h_scales) || !ok_ptr(act) ||
+        !ok_ptr(dy_perm) || !ok_ptr(dh) || !ok_ptr(dx_perm) || !ok_ptr(dW_up) ||
+        (sw ? !ok_ptr(dW_gate) : !ok_opt(dW_gate)) || !ok_ptr(dW_down) || !ok_opt(ws))
+        return MOE_ERR_INVALID_ARG;
+    if (ffn_ws_bytes(*c) > 0 && !ws) return MOE_ERR_INVALID_ARG;
+    return tc_ffn_backward_keep8(*c, x_perm, offsets, W_up, W_gate, W_down, h_codes, h_scales, act, dy_perm, dh,
+                                 dx_perm, dW_up, dW_gate, dW_down, (cudaStream_t)stream);
+}
+
 int moe_backward_aux(const moe_config* c, const void* x, const void* W_r, const void* W_up,
                  const void* W_gate, const void* W_down, const float* logits,
                  const int32_t* topk_idx, const float* gate, const int32_t* slot_of,
@@ -311,33 +387,30 @@ int moe_backward_aux(const moe_config* c, const void* x, const void* W_r, const 
                  const float* dlogits_aux, const void* dout, void* dx, void* dW_r, float* dbias,
                  void* dW_up, void* dW_gate, void* dW_down, const moe_shared_ffn* shared, void* ws,
                  moe_stream_t stream) {
-    int r = moe_check_config(c);
-    if (r) return r;
-    if (!ok_ptr(ws)) return MOE_ERR_INVALID_ARG;
-    if ((c->f_shared > 0) != (shared != nullptr)) return MOE_ERR_INVALID_ARG;
-    const BwdLayout L = bwd_layout(*c);
-    uint8_t* w = static_cast<uint8_t*>(ws);
-    void* dy = w + L.dy;
-    float* dgate = reinterpret_cast<float*>(w + L.dgate);
-    void* dh = w + L.dh;
-    void* dxp = w + L.dxp;
-    float* dlogits = reinterpret_cast<float*>(w + L.dlogits);
-    void* rest = w + L.rest;
-    moe_shared_ffn sh;
-    if (shared) {                     // the shared FFN's dy is the layer's dout (weight 1)
-        sh = *shared;
-        sh.dout = dout;
-        if (!sh.dh) sh.dh = w + L.sdh;
-        if (!sh.dx) sh.dx = w + L.sdx;
-    }
-    const moe_shared_ffn* shp = shared ? &sh : nullptr;
-    if ((r = moe_combine_backward(c, dout, y_perm, gate, slot_of, perm_token, offsets, dy, dgate, stream)))
-        return r;
-    if ((r = moe_grouped_ffn_backward(c, x_perm, offsets, W_up, W_gate, W_down, h_saved, act, dy, dh,
-                                      dxp, dW_up, dW_gate, dW_down, shp, rest, stream)))
-        return r;
-    return router_backward(c, x, W_r, logits, topk_idx, gate, slot_of, dgate, dxp, shp, stats,
-                           dlogits_aux, dx, dW_r, dbias, dlogits, rest, stream);
+    return whole_backward(c, x, W_r, logits, topk_idx, gate, slot_of, perm_token, offsets, shared, dout,
+                          y_perm, stats, dlogits_aux, dx, dW_r, dbias, ws, stream,
+                          [&](const void* dy, void* dh, void* dxp, const moe_shared_ffn* sh, void* rest) {
+                              return moe_grouped_ffn_backward(c, x_perm, offsets, W_up, W_gate, W_down, h_saved,
+                                                              act, dy, dh, dxp, dW_up, dW_gate, dW_down, sh,
+                                                              rest, stream);
+                          });
+}
+
+int moe_backward_mx8(const moe_config* c, const void* x, const void* W_r, const void* W_up,
+                     const void* W_gate, const void* W_down, const float* logits, const int32_t* topk_idx,
+                     const float* gate, const int32_t* slot_of, const int32_t* perm_token,
+                     const int32_t* offsets, const void* x_perm, const void* h_codes, const void* h_scales,
+                     void* act, const void* y_perm, const float* stats, const float* dlogits_aux,
+                     const void* dout, void* dx, void* dW_r, float* dbias, void* dW_up, void* dW_gate,
+                     void* dW_down, void* ws, moe_stream_t stream) {
+    if (const int r = keep8_config(c)) return r;
+    return whole_backward(c, x, W_r, logits, topk_idx, gate, slot_of, perm_token, offsets, nullptr, dout,
+                          y_perm, stats, dlogits_aux, dx, dW_r, dbias, ws, stream,
+                          [&](const void* dy, void* dh, void* dxp, const moe_shared_ffn*, void* rest) {
+                              return moe_grouped_ffn_backward_mx8(c, x_perm, offsets, W_up, W_gate, W_down,
+                                                                  h_codes, h_scales, act, dy, dh, dxp, dW_up,
+                                                                  dW_gate, dW_down, rest, stream);
+                          });
 }
 
 int moe_backward(const moe_config* c, const void* x, const void* W_r, const void* W_up,

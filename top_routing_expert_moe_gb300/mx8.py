@@ -1,8 +1,9 @@
 """The experts in 8 bits: binding of their C entry points.
 
 Microscaled 8-bit numbers, the permutation of rows held in them
-(``moe_permute_mx8``) and the experts' grouped product over segments of any length
-(``moe_mx8_grouped_product``).  As in the package's root, every function mirrors the C entry
+(``moe_permute_mx8``), the experts' grouped product over segments of any length
+(``moe_mx8_grouped_product``), and the experts' forward and backward with their
+activations kept in 8 bits (``moe_grouped_ffn_mx8``).  As in the package's root, every function mirrors the C entry
 point of the same name and the classes own the output buffers and workspaces of one
 configuration.  What a call with ``stream`` allocates belongs to that stream.
 """
@@ -18,7 +19,8 @@ __all__ = ["MX8Tensor", "mx8_scale_pitch", "moe_mx8_quantize", "moe_mx8_quantize
            "moe_mx8_dequantize", "mx8_quantize", "mx8_quantize_weight", "mx8_rows_capacity",
            "permute_mx8_workspace_size", "moe_permute_mx8", "MX8Dispatch", "MX8", "MX8_ACT_NONE",
            "MX8_ACT_SILU", "MX8_ACT_SWIGLU", "MX8ProductConfig", "check_mx8_product_config",
-           "moe_mx8_grouped_product", "MX8Product", "MX8Experts"]
+           "moe_mx8_grouped_product", "MX8Product", "MX8Experts", "moe_grouped_ffn_mx8",
+           "moe_grouped_ffn_backward_mx8", "moe_backward_mx8", "MoECheckpoint"]
 
 MX8 = 2                                              # an output type beside F32 and BF16
 MX8_ACT_NONE, MX8_ACT_SILU, MX8_ACT_SWIGLU = 0, 1, 2
@@ -236,3 +238,64 @@ class MX8Experts:
         self.up = mx8_quantize_weight(W_up, stream)
         self.down = mx8_quantize_weight(W_down, stream)
         self.gate = mx8_quantize_weight(W_gate, stream) if W_gate is not None else None
+
+
+# ----------------------------------------------------------------- activations kept in 8 bits
+def moe_grouped_ffn_mx8(cfg, x_perm, offsets, W_up, W_gate, W_down, h_codes, h_scales, act, y_perm, ws,
+                        stream=None):
+    _call("moe_grouped_ffn_mx8", ctypes.byref(cfg), _p(x_perm), _p(offsets), _p(W_up), _p(W_gate),
+          _p(W_down), _p(h_codes), _p(h_scales), _p(act), _p(y_perm), _p(ws), _s(stream))
+
+
+def moe_grouped_ffn_backward_mx8(cfg, x_perm, offsets, W_up, W_gate, W_down, h_codes, h_scales, act,
+                                 dy_perm, dh, dx_perm, dW_up, dW_gate, dW_down, ws, stream=None):
+    _call("moe_grouped_ffn_backward_mx8", ctypes.byref(cfg), _p(x_perm), _p(offsets), _p(W_up),
+          _p(W_gate), _p(W_down), _p(h_codes), _p(h_scales), _p(act), _p(dy_perm), _p(dh), _p(dx_perm),
+          _p(dW_up), _p(dW_gate), _p(dW_down), _p(ws), _s(stream))
+
+
+def moe_backward_mx8(cfg, x, W_r, W_up, W_gate, W_down, logits, topk_idx, gate, slot_of, perm_token,
+                     offsets, x_perm, h_codes, h_scales, act, y_perm, stats, dlogits_aux, dout, dx, dW_r,
+                     dbias, dW_up, dW_gate, dW_down, ws, stream=None):
+    _call("moe_backward_mx8", ctypes.byref(cfg), _p(x), _p(W_r), _p(W_up), _p(W_gate), _p(W_down),
+          _p(logits), _p(topk_idx), _p(gate), _p(slot_of), _p(perm_token), _p(offsets), _p(x_perm),
+          _p(h_codes), _p(h_scales), _p(act), _p(y_perm), _p(stats), _p(dlogits_aux), _p(dout), _p(dx),
+          _p(dW_r), _p(dbias), _p(dW_up), _p(dW_gate), _p(dW_down), _p(ws), _s(stream))
+
+
+class MoECheckpoint:
+    """What one forward of a ``MoELayer`` leaves for its backward, the experts' hidden rows
+    ``h`` and outputs ``y`` in 8 bits (a third of the 16-bit buffers' bytes, which the
+    layer then keeps once for all depths): for ``MoELayer.forward(..., checkpoint=c)`` and
+    ``backward(..., checkpoint=c)``.  bf16 layers without shared experts."""
+
+    def __init__(self, cfg, device="cuda"):
+        rc = _moe.check_config(cfg)
+        if rc != 0:
+            raise _moe.MoEError(rc, "moe_check_config")
+        c = cfg
+        if c.dtype != _moe.BF16 or c.f_shared > 0:
+            raise ValueError("a checkpoint needs a bf16 layer without shared experts")
+        self.cfg = c
+        R = _moe.rows_capacity(c)
+        e = lambda *s, dtype=torch.int32: torch.empty(*s, dtype=dtype, device=device)  # noqa: E731
+        f32 = torch.float32
+        self.h, self.y = MX8Tensor((c.nh, R, c.f), device), MX8Tensor((R, c.d), device)
+        self.logits, self.gate, self.stats = e(c.T, c.E, dtype=f32), e(c.T, c.k, dtype=f32), e(9 + c.E, dtype=f32)
+        self.topk_idx, self.slot_of, self.perm_token = e(c.T, c.k), e(c.T, c.k), e(R)
+        self.counts, self.kept, self.offsets = e(c.E), e(c.E), e(c.E + 1)
+        self.inputs = None
+
+    def check(self, cfg):
+        if bytes(cfg) != bytes(self.cfg):
+            raise ValueError(f"the checkpoint is of another layer: {self.cfg!r}")
+
+    def keep_y(self, y_perm, stream=None):
+        R, d = self.y.shape
+        # the rows below offsets[E] (a view of it would cost more than the call)
+        _call("moe_mx8_quantize", _moe.BF16, R, d, _p(y_perm), _p(self.offsets) + 4 * self.cfg.E,
+              _p(self.y.codes), _p(self.y.scales), _s(stream))
+
+    def y_into(self, y_perm, stream=None):
+        R, d = self.y.shape
+        moe_mx8_dequantize(_moe.BF16, R, d, self.y.codes, self.y.scales, y_perm, stream)
