@@ -399,7 +399,7 @@ class MoELayer:
         self._grads = None
         self._inputs = None
         self._shared_w = None
-        self._mx4 = None
+        self._mx4 = self._mx8 = None
 
     def _shared_fwd(self, x):
         if self.cfg.f_shared <= 0:
@@ -495,6 +495,37 @@ class MoELayer:
         moe_mx4_grouped_product(second, aq.codes, aq.scales, self.offsets, down.codes, down.scales,
                                 None, None, self.y_perm, stream)
         moe_combine(c, self.y_perm, self.slot_of, self.gate, self.out, stream)
+        return self.out
+
+    def forward_mx8(self, x, W_r, experts, bias=None, noise=None, token_mask=None, stream=None, x8=None):
+        """The forward with both GEMMs' operands in microscaled 8-bit numbers: ``experts`` (an
+        MX8Experts) holds the weights, ``x8`` (an MX8Tensor, quantised here if None) the rows,
+        whose 16-bit copy x the router reads; the hidden rows leave the first product in 8
+        bits.  Segments are not padded.  bf16 layers without shared experts; there is no
+        backward of it."""
+        c = self.cfg
+        if c.dtype != BF16 or c.f_shared > 0:
+            raise ValueError("forward_mx8 needs a bf16 layer without shared experts")
+        if (experts.gate is not None) != (c.ffn == SWIGLU):
+            raise ValueError("a gate matrix is required iff cfg.ffn is SWIGLU")
+        if experts.up.shape != (c.E, c.f, c.d) or experts.down.shape != (c.E, c.d, c.f):
+            raise ValueError("the experts' shapes are not this layer's")
+        if self._mx8 is None:
+            dev, rows = self.out.device, mx8_rows_capacity(c)
+            act = MX8_ACT_SWIGLU if c.ffn == SWIGLU else MX8_ACT_SILU
+            with _on(stream):
+                self._mx8 = (MX8Dispatch(c, dev), MX8Product(MX8ProductConfig(rows, c.d, c.f, c.E, act, MX8), dev),
+                             MX8Product(MX8ProductConfig(rows, c.f, c.d, c.E), dev), MX8Tensor((c.T, c.d), dev))
+        dispatch, first, second, own = self._mx8
+        if x8 is None:
+            x8 = mx8_quantize(x, out=own, stream=stream)
+        self._inputs = None
+        moe_route(c, x, W_r, bias, noise, token_mask, self.logits, self.topk_idx, self.gate,
+                  self.counts, self.stats, self.ws, stream)
+        rows = dispatch.forward(x8, self.topk_idx, self.stats, stream)
+        hidden = first.forward(rows, dispatch.offsets, experts.up, experts.gate, stream)
+        y = second.forward(hidden, dispatch.offsets, experts.down, stream=stream)
+        moe_combine(c, y, dispatch.slot_of, self.gate, self.out, stream)
         return self.out
 
     def grads(self):

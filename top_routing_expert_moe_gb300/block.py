@@ -461,6 +461,15 @@ class MoEBlock:
         u = self.layer.forward_mx4(z, w["W_r"], experts, w.get("bias"), token_mask=token_mask, stream=stream)
         return self.leave.forward(x, u=u, w_post=w.get("w_out"), gate=w.get("gate"), stream=stream)[0]
 
+    def forward_mx8(self, x, weights, experts, token_mask=None, stream=None):
+        """x' with the experts in 8 bits, an MX8Experts (serving: no loss, no backward): the
+        norm writes their rows in 8 bits beside the router's in 16."""
+        w = weights
+        self._saved = None
+        z8, z = self.enter.forward_mx8(x, w_pre=w["w_in"], stream=stream)[1:]
+        u = self.layer.forward_mx8(z, w["W_r"], experts, w.get("bias"), token_mask=token_mask, stream=stream, x8=z8)
+        return self.leave.forward(x, u=u, w_post=w.get("w_out"), gate=w.get("gate"), stream=stream)[0]
+
     def backward(self, dx_out, dloss=None, stream=None):
         """Gradients of <dx_out, x'> + dloss (balance + z) (dloss None: 1)."""
         if self._saved is None:
