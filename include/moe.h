@@ -507,8 +507,13 @@ MOE_API int moe_mx4_grouped_product(const moe_mx4_product_config* cfg, const voi
  *           largest, so nothing is clipped); 0 in a block of byte 255
  * Codes: one byte an element, [rows,K].  Scales: [rows,P], P = moe_mx8_scale_pitch(K),
  * byte i/32 of a row for its element i; a row's bytes from K/32 on stand for nothing
- * and may hold anything.  Expert weights are [E,N,K], each expert's matrix transposed:
- * E N rows of K.                                                             */
+ * and may hold anything.
+ * Expert weights W [E,K,N] are quantised along K and kept in blocks of 128 n x 128 k,
+ * as the experts' product reads them, codes 16384 bytes a block and scales 512:
+ *   block b = (e * ceil(N/128) + n/128) * ceil(K/128) + k/128
+ *   code of (e, n, k)  at b * 16384 + (n%128) * 128 + k%128
+ *   scale of (e, n, k) at b * 512 + (n%32) * 16 + (n%128)/32 * 4 + (k%128)/32
+ * with zeros past N and K.                                                   */
 /* Bytes of a row of scales: K/32 rounded up to a multiple of 16. */
 MOE_API int moe_mx8_scale_pitch(int32_t K, int32_t* pitch);
 
@@ -519,8 +524,8 @@ MOE_API int moe_mx8_quantize(int32_t dtype, int64_t rows, int32_t K, const void*
                              const int32_t* rows_used, void* codes, void* scales,
                              moe_stream_t stream);
 
-/* Weights: W [E,K,N] with blocks along K -> codes [E,N,K], scales [E,N,P].
- * K a multiple of 32, N of 8, at most 2^21.                                   */
+/* Weights: W [E,K,N], K a multiple of 32, N of 8, at most 2^21, at most 2^24 - 1 blocks. */
+MOE_API int moe_mx8_weight_bytes(int32_t E, int32_t K, int32_t N, size_t* codes, size_t* scales);
 MOE_API int moe_mx8_quantize_weight(int32_t dtype, int32_t E, int32_t K, int32_t N, const void* W,
                                     void* codes, void* scales, moe_stream_t stream);
 
@@ -529,6 +534,10 @@ MOE_API int moe_mx8_quantize_weight(int32_t dtype, int32_t E, int32_t K, int32_t
  * within 2^-5 of it are rounded, is infinite in both.                        */
 MOE_API int moe_mx8_dequantize(int32_t dtype, int64_t rows, int32_t K, const void* codes,
                                const void* scales, void* out, moe_stream_t stream);
+/* ... and of weights: out [E,N,K], each expert's matrix transposed. */
+MOE_API int moe_mx8_dequantize_weight(int32_t dtype, int32_t E, int32_t K, int32_t N,
+                                      const void* codes, const void* scales, void* out,
+                                      moe_stream_t stream);
 
 /* moe_permute for rows in 8 bits, without padding: expert e's rows are
  * offsets[e]..offsets[e+1], all of them real (pad_m and the layer's type are not looked

@@ -15,7 +15,7 @@ def test_refusals():
 
     class Experts:
         def __init__(self, up, down, gate=None):
-            self.up, self.down, self.gate = (moe.MX8Tensor(s, "cpu") if s else None for s in (up, down, gate))
+            self.up, self.down, self.gate = (moe.MX8Weight(s, "cpu") if s else None for s in (up, down, gate))
 
     with pytest.raises(ValueError, match="gate matrix"):
         layer.forward_mx8(x, x, Experts((2, 128, 128), (2, 128, 128), (2, 128, 128)))

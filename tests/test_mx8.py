@@ -48,6 +48,17 @@ def rows_of(T, K, dt, seed=0):
     return x.to(dt)
 
 
+def weight_blocks(code, byte):
+    """Codes [N, K] and scale bytes [N, K / 32] in the blocks' order (include/moe.h)."""
+    N, K = code.shape
+    nt, kt = (N + 127) // 128, (K + 127) // 128
+    c, s = torch.zeros(nt * 128, kt * 128, dtype=torch.uint8), torch.zeros(nt * 128, kt * 4, dtype=torch.uint8)
+    c[:N, :K], s[:N, :K // 32] = code, byte
+    # [nt, n, kt, k] -> [nt, kt, n, k];  [nt, n / 32, n % 32, kt, block] -> [nt, kt, n % 32, n / 32, block]
+    return (c.reshape(nt, 128, kt, 128).permute(0, 2, 1, 3).reshape(-1),
+            s.reshape(nt, 4, 32, kt, 4).permute(0, 3, 2, 1, 4).reshape(-1))
+
+
 def same(a, b):
     return torch.equal(a.nan_to_num(nan=12345.0), b.nan_to_num(nan=12345.0))
 
@@ -77,6 +88,19 @@ def test_pitch():
         assert moe.MX8Tensor((2, 3, K), "cpu").scales.shape == (2, 3, p)
 
 
+def test_weight_blocks():
+    N, K = 200, 160
+    byte = (torch.arange(N * 5).reshape(N, 5) % 251).to(torch.uint8)
+    code = (torch.arange(N * K).reshape(N, K) % 253).to(torch.uint8)
+    c, s = weight_blocks(code, byte)
+    assert (c.numel(), s.numel()) == moe.mx8_weight_bytes(1, K, N) == (4 * 16384, 4 * 512)
+    assert moe.mx8_weight_bytes(3, K, N) == (12 * 16384, 12 * 512)
+    for n, k in ((0, 0), (31, 100), (32, 127), (127, 128), (128, 31), (199, 159)):
+        b = n // 128 * 2 + k // 128
+        assert c[b * 16384 + n % 128 * 128 + k % 128] == code[n, k]
+        assert s[b * 512 + n % 32 * 16 + n % 128 // 32 * 4 + k % 128 // 32] == byte[n, k // 32]
+
+
 def test_refusals():
     lib, p, bad = moe.load_library(), ctypes.c_void_p(0x10000), ctypes.c_void_p(0x10008)
     n = ctypes.c_int32()
@@ -95,7 +119,13 @@ def test_refusals():
     assert lib.moe_mx8_quantize_weight(moe.F32, 2, 32, 12, p, p, p, None) == moe.ERR_UNSUPPORTED
     assert lib.moe_mx8_quantize_weight(moe.F32, 1, 32, 2 ** 21 + 8, p, p, p, None) == moe.ERR_UNSUPPORTED
     assert lib.moe_mx8_quantize_weight(moe.F32, 0, 32, 16, p, p, p, None) == moe.ERR_INVALID_ARG
+    assert lib.moe_mx8_quantize_weight(moe.F32, 2 ** 12, 2 ** 14, 2 ** 12, p, p, p, None) == moe.ERR_UNSUPPORTED
     assert lib.moe_mx8_dequantize(moe.F32, 4, 32, p, None, p, None) == moe.ERR_INVALID_ARG
+    assert lib.moe_mx8_dequantize_weight(moe.F32, 1, 32, 8, p, None, p, None) == moe.ERR_INVALID_ARG
+    assert lib.moe_mx8_dequantize_weight(7, 1, 32, 8, p, p, p, None) == moe.ERR_INVALID_ARG
+    assert lib.moe_mx8_dequantize_weight(moe.F32, 1, 32, 12, p, p, p, None) == moe.ERR_UNSUPPORTED
+    assert lib.moe_mx8_weight_bytes(1, 32, 8, None, None) == moe.ERR_INVALID_ARG
+    assert lib.moe_mx8_weight_bytes(0, 32, 8, p, p) == moe.ERR_INVALID_ARG
     cfg = moe.MoEConfig(T=8, d=128, f=128, E=2, k=1)
     for i in range(10):
         for v in (None, bad):
@@ -150,11 +180,14 @@ def test_rows(T, K, dt):
 def test_weights(E, K, N, dt):
     W = torch.stack([rows_of(N, K, dt, seed=e).t() for e in range(E)]).contiguous()
     q = moe.mx8_quantize_weight(W.cuda())
+    assert q.shape == (E, N, K)
+    codes, scales = q.codes.cpu().reshape(E, -1), q.scales.cpu().reshape(E, -1)
     for e in range(E):
         code, v, byte = quantize64(W[e].t())
-        assert torch.equal(q.codes[e].cpu(), code)
-        assert torch.equal(q.scales[e].cpu()[:, :K // 32], byte)
-        assert torch.equal(q.dequantize(torch.float32)[e].cpu(), v.float())
+        c, s = weight_blocks(code, byte)
+        assert torch.equal(codes[e], c) and torch.equal(scales[e], s)
+        for out in (torch.bfloat16, torch.float32):
+            assert torch.equal(q.dequantize(out)[e].cpu(), v.to(out))
 
 
 @pytest.mark.gpu
@@ -167,7 +200,9 @@ def test_infinities_and_nans_make_their_block_nan():
     # (3.4e38 stands for 2^128, which fp32 has no number for)
     assert same(q.dequantize(torch.float32).cpu(), v.float())
     W = moe.mx8_quantize_weight(x.t()[None].contiguous().cuda())
-    assert torch.equal(W.scales[0].cpu()[:, :4], byte) and torch.equal(W.codes[0].cpu(), code)
+    c, s = weight_blocks(code, byte)
+    assert torch.equal(W.scales.cpu(), s) and torch.equal(W.codes.cpu(), c)
+    assert same(W.dequantize(torch.float32)[0].cpu(), v.float())
 
 
 @pytest.mark.gpu

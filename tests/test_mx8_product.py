@@ -92,7 +92,7 @@ def test_refusals():
     for b in (dict(rows=0), dict(K=0), dict(N=0), dict(E=0), dict(act=3), dict(act=-1), dict(out_dtype=3)):
         assert moe.check_mx8_product_config(moe.MX8ProductConfig(**{**ok, **b})) == moe.ERR_INVALID_ARG, b
     for b in (dict(K=40), dict(N=12), dict(E=65), dict(N=2 ** 21 + 8), dict(rows=2 ** 30, N=2 ** 15),
-              dict(rows=2 ** 30 + 1), dict(out_dtype=moe.MX8)):
+              dict(rows=2 ** 30 + 1), dict(out_dtype=moe.MX8), dict(K=2 ** 20, N=2 ** 20)):
         assert moe.check_mx8_product_config(moe.MX8ProductConfig(**{**ok, **b})) == moe.ERR_UNSUPPORTED, b
     with pytest.raises(moe.MoEError):
         moe.MX8Product(moe.MX8ProductConfig(rows=4, K=33, N=8, E=1), "cpu")
@@ -111,7 +111,7 @@ def test_refusals():
     assert lib.moe_mx8_grouped_product(ctypes.byref(eight), p, p, p, p, p, None, None, p, None, None) == \
         moe.ERR_INVALID_ARG
     m = moe.MX8Product(plain, device="cpu")
-    x, w = moe.MX8Tensor((256, 64), "cpu"), moe.MX8Tensor((2, 16, 64), "cpu")
+    x, w = moe.MX8Tensor((256, 64), "cpu"), moe.MX8Weight((2, 16, 64), "cpu")
     offs = torch.zeros(3, dtype=torch.int32)
     with pytest.raises(TypeError, match="x: expected an MX8Tensor"):
         m.forward(torch.zeros(256, 64), offs, w)
@@ -122,9 +122,11 @@ def test_refusals():
     with pytest.raises(ValueError, match="wg is required"):
         m.forward(x, offs, w, w)
     with pytest.raises(ValueError, match="w: expected"):
-        m.forward(x, offs, moe.MX8Tensor((2, 32, 64), "cpu"))
+        m.forward(x, offs, moe.MX8Weight((2, 32, 64), "cpu"))
+    with pytest.raises(TypeError, match="w: expected an MX8Weight"):
+        m.forward(x, offs, moe.MX8Tensor((2, 16, 64), "cpu"))
     with pytest.raises(ValueError, match="wg: expected"):
-        moe.MX8Product(dual, device="cpu").forward(x, offs, w, moe.MX8Tensor((2, 32, 64), "cpu"))
+        moe.MX8Product(dual, device="cpu").forward(x, offs, w, moe.MX8Weight((2, 32, 64), "cpu"))
 
 
 # ----------------------------------------------------------------- GPU

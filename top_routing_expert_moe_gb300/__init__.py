@@ -157,6 +157,8 @@ _SIGS = {
     "moe_mx8_scale_pitch": [ctypes.c_int32, ctypes.c_void_p],
     "moe_mx8_quantize": [ctypes.c_int32, ctypes.c_int64, ctypes.c_int32] + [ctypes.c_void_p] * 5,
     "moe_mx8_quantize_weight": [ctypes.c_int32] * 4 + [ctypes.c_void_p] * 4,
+    "moe_mx8_weight_bytes": [ctypes.c_int32] * 3 + [ctypes.c_void_p] * 2,
+    "moe_mx8_dequantize_weight": [ctypes.c_int32] * 4 + [ctypes.c_void_p] * 4,
     "moe_mx8_dequantize": [ctypes.c_int32, ctypes.c_int64, ctypes.c_int32] + [ctypes.c_void_p] * 4,
     "moe_mx8_rows_capacity": [ctypes.c_void_p] * 2,
     "moe_permute_mx8_workspace_size": [ctypes.c_void_p] * 2,

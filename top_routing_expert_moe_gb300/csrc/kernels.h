@@ -97,6 +97,8 @@ int launch_mx8_quantize_weight(int dtype, int E, int K, int N, const void* W, vo
                                cudaStream_t st);
 int launch_mx8_dequantize(int dtype, int64_t rows, int K, const void* codes, const void* scales, void* out,
                           cudaStream_t st);
+int launch_mx8_dequantize_weight(int dtype, int E, int K, int N, const void* codes, const void* scales,
+                                 void* out, cudaStream_t st);
 int launch_mx8_product(const moe_mx8_product_config& c, const void* xq, const void* xs, const int32_t* offsets,
                        const void* wq, const void* ws, const void* gq, const void* gs, void* out,
                        void* out_scales, cudaStream_t st);

@@ -158,11 +158,12 @@ __global__ void __launch_bounds__(ROW_THREADS) mx8_values_kernel(const uint8_t* 
     }
 }
 
-// Weights W [E, K, N] -> [E, N, K]: a CTA takes 128 k x 64 n through shared memory; a
-// thread forms one block (32 k) of one column.
+// Weights W [E, K, N] -> blocks of 128 n x 128 k (the header's order): a CTA takes 128 k x
+// 64 n through shared memory and writes half a block, 8 KB in a row; a thread forms one
+// run of 32 k of one column.  Places past N or K hold zeros.
 constexpr int WN = 64, W_THREADS = WN * 4;
 template <typename T>
-__global__ void __launch_bounds__(W_THREADS) mx8_weight_kernel(const T* __restrict__ W, int K, int N, int pitch,
+__global__ void __launch_bounds__(W_THREADS) mx8_weight_kernel(const T* __restrict__ W, int K, int N,
                                                                uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
     pdl_wait();
     pdl_trigger();
@@ -195,17 +196,42 @@ __global__ void __launch_bounds__(W_THREADS) mx8_weight_kernel(const T* __restri
     *reinterpret_cast<uint4*>(&sc[n][kb * 32 + 16]) = make_uint4(w[4], w[5], w[6], w[7]);
     sb[n][kb] = (uint8_t)s;
     __syncthreads();
-    // eight neighbouring threads write a column's 128 codes
+    const size_t block = ((size_t)e * (gridDim.y / 2) + blockIdx.y / 2) * gridDim.x + blockIdx.x;
+    const int r0 = blockIdx.y % 2 * WN;                     // this half's first row
+    uint8_t* dst = codes + block * 16384 + r0 * 128;
 #pragma unroll
-    for (int i = threadIdx.x; i < WN * 8; i += W_THREADS) {
-        const int c = i / 8, k = i % 8 * 16;
-        if (n0 + c < N && k0 + k < K)
-            *reinterpret_cast<uint4*>(codes + ((size_t)e * N + n0 + c) * K + k0 + k) = *reinterpret_cast<const uint4*>(&sc[c][k]);
-    }
-    // (the four bytes lie within the row's pitch, whose last may stand for no block)
-    if (threadIdx.x < WN && n0 + threadIdx.x < N)
-        *reinterpret_cast<uint32_t*>(scales + ((size_t)e * N + n0 + threadIdx.x) * pitch + k0 / 32) =
+    for (int i = threadIdx.x; i < WN * 8; i += W_THREADS)
+        *reinterpret_cast<uint4*>(dst + i * 16) = *reinterpret_cast<const uint4*>(&sc[i / 8][i % 8 * 16]);
+    if (threadIdx.x < WN) {
+        const int r = r0 + threadIdx.x;
+        *reinterpret_cast<uint32_t*>(scales + block * 512 + r % 32 * 16 + r / 32 * 4) =
             *reinterpret_cast<const uint32_t*>(sb[threadIdx.x]);
+    }
+}
+
+// The values of weights: 16 codes a thread, out [E, N, K] written along K
+template <typename T>
+__global__ void __launch_bounds__(256) mx8_weight_values_kernel(const uint8_t* __restrict__ codes,
+                                                                const uint8_t* __restrict__ scales, int K, int N,
+                                                                T* __restrict__ out) {
+    pdl_wait();
+    pdl_trigger();
+    const int kt = (K + 127) / 128, nt = (N + 127) / 128, e = blockIdx.z;
+    const int k = (blockIdx.x % kt * 8 + (threadIdx.x & 7)) * 16, n = blockIdx.x / kt * 32 + (threadIdx.x >> 3);
+    if (k >= K || n >= N) return;
+    const size_t block = ((size_t)e * nt + n / 128) * kt + k / 128;
+    const int r = n % 128;
+    const uint4 c = __ldg(reinterpret_cast<const uint4*>(codes + block * 16384 + r * 128 + k % 128));
+    const float m = mx8_scale_value(__ldg(scales + block * 512 + r % 32 * 16 + r / 32 * 4 + k % 128 / 32));
+    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+    float v[16];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) mx8_unpack4(w[i], v + 4 * i);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] *= m;
+    T* dst = out + ((size_t)e * N + n) * K + k;
+#pragma unroll
+    for (int i = 0; i < 16; i += Vec16<T>::N) store16_f<T>(dst + i, v + i);
 }
 
 // Rows of 8-bit numbers to their places: a warp takes a token and writes each of its
@@ -251,9 +277,16 @@ int rows_t(int64_t rows, int K, const void* x, const int32_t* used, void* codes,
 }
 template <typename T>
 int weight_t(int E, int K, int N, const void* W, void* codes, void* scales, cudaStream_t st) {
-    const dim3 grid((K + 127) / 128, (N + WN - 1) / WN, E);
-    MOE_LAUNCH(mx8_weight_kernel<T>, grid, W_THREADS, 0, st, static_cast<const T*>(W), K, N, (int)mx8_pitch(K),
-               static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scales));
+    const dim3 grid((K + 127) / 128, (N + 127) / 128 * 2, E);
+    MOE_LAUNCH(mx8_weight_kernel<T>, grid, W_THREADS, 0, st, static_cast<const T*>(W), K, N, static_cast<uint8_t*>(codes),
+               static_cast<uint8_t*>(scales));
+    return MOE_OK;
+}
+template <typename T>
+int weight_values_t(int E, int K, int N, const void* codes, const void* scales, void* out, cudaStream_t st) {
+    const dim3 grid((K + 127) / 128 * ((N + 31) / 32), 1, E);
+    MOE_LAUNCH(mx8_weight_values_kernel<T>, grid, 256, 0, st, static_cast<const uint8_t*>(codes),
+               static_cast<const uint8_t*>(scales), K, N, static_cast<T*>(out));
     return MOE_OK;
 }
 template <typename T>
@@ -280,6 +313,11 @@ int launch_mx8_dequantize(int dtype, int64_t rows, int K, const void* codes, con
                           cudaStream_t st) {
     return dtype == MOE_DTYPE_BF16 ? values_t<__nv_bfloat16>(rows, K, codes, scales, out, st)
                                    : values_t<float>(rows, K, codes, scales, out, st);
+}
+int launch_mx8_dequantize_weight(int dtype, int E, int K, int N, const void* codes, const void* scales, void* out,
+                                 cudaStream_t st) {
+    return dtype == MOE_DTYPE_BF16 ? weight_values_t<__nv_bfloat16>(E, K, N, codes, scales, out, st)
+                                   : weight_values_t<float>(E, K, N, codes, scales, out, st);
 }
 int launch_permute_mx8(const moe_config& c, const void* codes, const void* scales, const int32_t* topk,
                        void* codes_perm, void* scales_perm, int32_t* perm_token, int32_t* slot_of, int32_t* kept,

@@ -19,6 +19,15 @@ int mx8_shape(int64_t rows, int K) {
     if (rows < 1 || K < 1) return MOE_ERR_INVALID_ARG;
     return K % 32 || K > (1 << 24) || rows > (1LL << 31) - 256 ? MOE_ERR_UNSUPPORTED : MOE_OK;
 }
+// expert weights: W's columns in whole 16-byte pieces, and the launches' grids (64-column
+// tiles, experts); 128-byte rows of all blocks counted in 31 bits
+int weight8_shape(int64_t E, int K, int N) {
+    if (E < 1 || N < 1) return MOE_ERR_INVALID_ARG;
+    const int r = mx8_shape(N, K);
+    if (r) return r;
+    if (N % 8 || N > (1 << 21) || E > 65535) return MOE_ERR_UNSUPPORTED;
+    return E * ((N + 127) / 128) * ((K + 127) / 128) > (1LL << 31) / 128 - 1 ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
 int64_t rows_cap8(const moe_config& c) { return std::min<int64_t>((int64_t)c.T * c.k, (int64_t)c.E * capacity_of(c)); }
 int permute8_config(const moe_config* c) {
     const int r = moe_check_config(c);
@@ -49,15 +58,32 @@ int moe_mx8_quantize(int32_t dtype, int64_t rows, int32_t K, const void* x, cons
     return launch_mx8_quantize(dtype, rows, K, x, rows_used, codes, scales, (cudaStream_t)stream);
 }
 
+int moe_mx8_weight_bytes(int32_t E, int32_t K, int32_t N, size_t* codes, size_t* scales) {
+    const int r = weight8_shape(E, K, N);
+    if (r) return r;
+    if (!codes || !scales) return MOE_ERR_INVALID_ARG;
+    const size_t blocks = (size_t)E * ((N + 127) / 128) * ((K + 127) / 128);
+    *codes = blocks * 16384;
+    *scales = blocks * 512;
+    return MOE_OK;
+}
+
 int moe_mx8_quantize_weight(int32_t dtype, int32_t E, int32_t K, int32_t N, const void* W,
                             void* codes, void* scales, moe_stream_t stream) {
-    if (!is_dtype(dtype) || E < 1) return MOE_ERR_INVALID_ARG;
-    const int r = mx8_shape(N, K);
+    if (!is_dtype(dtype)) return MOE_ERR_INVALID_ARG;
+    const int r = weight8_shape(E, K, N);
     if (r) return r;
-    // (the launch's grid: 64-column tiles and experts)
-    if (N % 8 || N > (1 << 21) || E > 65535) return MOE_ERR_UNSUPPORTED;
     if (!ok_ptr(W) || !ok_ptr(codes) || !ok_ptr(scales)) return MOE_ERR_INVALID_ARG;
     return launch_mx8_quantize_weight(dtype, E, K, N, W, codes, scales, (cudaStream_t)stream);
+}
+
+int moe_mx8_dequantize_weight(int32_t dtype, int32_t E, int32_t K, int32_t N, const void* codes,
+                              const void* scales, void* out, moe_stream_t stream) {
+    if (!is_dtype(dtype)) return MOE_ERR_INVALID_ARG;
+    const int r = weight8_shape(E, K, N);
+    if (r) return r;
+    if (!ok_ptr(codes) || !ok_ptr(scales) || !ok_ptr(out)) return MOE_ERR_INVALID_ARG;
+    return launch_mx8_dequantize_weight(dtype, E, K, N, codes, scales, out, (cudaStream_t)stream);
 }
 
 int moe_mx8_dequantize(int32_t dtype, int64_t rows, int32_t K, const void* codes, const void* scales,
@@ -120,6 +146,7 @@ int moe_check_mx8_product_config(const moe_mx8_product_config* c) {
     if (r) return r;
     if (c->N % (c->out_dtype == MOE_DTYPE_MX8 ? 32 : 8) || c->N > (1 << 21) || c->E > 64 || c->rows > (1 << 30))
         return MOE_ERR_UNSUPPORTED;
+    if (const int w = weight8_shape(c->E, c->K, c->N)) return w;
     // 32-bit tile counts, at the smallest tile's 64 columns
     if ((c->rows / 128 + c->E) * (((int64_t)c->N + 63) / 64) > (1LL << 30)) return MOE_ERR_UNSUPPORTED;
     return MOE_OK;

@@ -25,6 +25,16 @@
 // scale warps form the tile (row r's four bytes as word r / 32 of lane r % 32) from 16
 // bytes a row, four stages' worth, in registers.
 //
+// W is kept in blocks of 128 rows x 128 elements, 16 KB each, a row block's one after the
+// other along K, and its scales in the tensor cores' tiles of 512 bytes in the same order:
+// a stage's scales of W are whole sectors, where 16 bytes a row for four stages left
+// half of each unused (16384 rows, K = 4096, N = 14336, SwiGLU: 2460 us, by rows 2560).
+//
+// Few rows (decoding) are bound by W's bytes, and what they must not do is read x's few
+// lines from every CTA more often than they have to: 128 requests of every CTA for the
+// scales of one row, where only the segment's rows are asked for now, took 145 us
+// where the rest takes 69 (2 rows of each of 2 experts, K = 4096, N = 14336, SwiGLU).
+//
 // Tensor memory: two accumulators of 256 columns that overlap in 128, and buffers of 16
 // columns of scales.
 #include <algorithm>
@@ -50,6 +60,7 @@ constexpr int CTRL_BYTES = 1024;
 constexpr int TMEM_COLS = 512;
 constexpr int ACC1 = 128;                  // second accumulator's first column (a pair's overlap in 128-255)
 constexpr int SF_COL = 384, SF_COLS = 16;  // buffers: 4 columns of x's scales, from the 8th on 4 or 8 of W's
+constexpr int SF_QUAD = BM * 16;           // scale bytes of a quad: of 128 rows of x, or of a row block of W
 constexpr int SF_AHEAD = 2, SF_SLOTS = SF_AHEAD + 1;     // in quads
 constexpr int RASTER_ROWS = 4096;          // rows of x that pass over an expert's weights together
 
@@ -58,7 +69,7 @@ template <int CG> struct Ring {            // CG CTAs a tile: stages and their b
     static constexpr int BYTES = A_BYTES + 128 * BK;
     static constexpr int STAGES = 5;
     static constexpr int SF_BUFS = STAGES;               // see the scale warps
-    static constexpr int SF_SLOT = (BM + BN) * 16;       // a quad's: 16 bytes of each row of x and W
+    static constexpr int SF_SLOT = 3 * SF_QUAD;          // x, and one or two row blocks of W
     static constexpr int SMEM = 1024 + STAGES * BYTES + STAGING_BYTES + SF_SLOTS * SF_SLOT + CTRL_BYTES;
 };
 static_assert(Ring<1>::BYTES % 1024 == 0 && Ring<2>::BYTES % 1024 == 0, "128B swizzle atoms");
@@ -69,14 +80,16 @@ enum Out { OUT_F32, OUT_BF16, OUT_MX8 };
 
 struct Mx8Params {
     CUtensorMap tmA, tmB0, tmB1, tmO;
-    const uint8_t *sa, *sb0, *sb1;         // scales of x, and of the accumulator's two halves' W
+    const uint8_t *sa, *sb0, *sb1;         // scales of x (rows), and of the accumulator's two halves' W (tiles)
     uint8_t* out;
     uint8_t* out_scales;                   // OUT_MX8
     const int32_t* offsets;
     int* status;
     int64_t rows;
     int E, K, N, n_blocks, act;
-    int pitch, out_pitch;                  // bytes of a row of scales: of x and W, of out
+    int w_blocks;                          // W's row blocks an expert
+    int a_rows;                            // rows of x that a stage loads (one CTA: fewer where there are no more)
+    int pitch, out_pitch;                  // bytes of a row of scales: of x, of out
     int ways;                              // CTAs of a cluster that may share a tile's K (single CTAs only)
     int max_tiles;                         // their grid
 };
@@ -124,6 +137,13 @@ __device__ __forceinline__ Mx8Tile decode(const int* offs, const int* prefix, in
     const int r = local - grp * RG * n_blocks;
     const int m = first + r % gm;
     return {lo, offs[lo] + m * CG * BM, r / gm, offs[lo + 1]};
+}
+
+// W's row block that half h of the accumulator's columns multiplies by (SwiGLU: the half's
+// own matrix'); past the last block that one again, for columns that are not stored
+template <int CG, bool DUAL>
+__device__ __forceinline__ int w_block(const Mx8Params& P, int nb, int h) {
+    return min(DUAL ? (CG == 2 ? nb : nb >> 1) : nb * CG + h, P.w_blocks - 1);
 }
 
 template <int CG, int OT, bool DUAL>
@@ -244,6 +264,9 @@ __global__ void __launch_bounds__(NTHREADS, 1) mx8_grouped_kernel(const __grid_c
         for (int tix = unit; ok && tix < total; tix += nunits) {
             const Mx8Tile t = decode<CG>(offs, prefix, P.E, P.n_blocks, tix);
             const int am = t.m0 + (int)rank * BM;
+            // its first row of W's 128-byte rows in memory
+            const int wrow = (t.e * P.w_blocks + w_block<CG, DUAL>(P, t.nb, (int)rank)) * nk * 128 +
+                             (DUAL && CG == 1 ? (t.nb & 1) * 64 : 0);
             for (int kb = kb0; kb < kb1; ++kb, ++it) {
                 const int s = it % S;
                 if (!wait_bar<1>(smem_u32(&empty[s]), ((uint32_t)(it / S) & 1u) ^ 1u, abort_flag, P.status)) {
@@ -252,7 +275,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) mx8_grouped_kernel(const __grid_c
                 }
                 const uint32_t st = smem0 + s * R::BYTES;
                 const uint32_t bar = CG == 1 ? smem_u32(&full[s]) : mapa_shared(smem_u32(&full[s]), 0);
-                if (leader) mbar_expect_tx(smem_u32(&full[s]), CG * R::BYTES);   // every byte of a stage
+                if (leader) mbar_expect_tx(smem_u32(&full[s]), CG * (R::BYTES - A_BYTES + P.a_rows * BK));   // every byte of a stage
                 auto ld = [&](const CUtensorMap* m, uint32_t dst, int c0, int c1, int c2) {
                     if constexpr (CG == 1) tma_load3(m, dst, bar, c0, c1, c2);
                     else tma_load3_pair(m, dst, bar, c0, c1, c2);
@@ -261,12 +284,10 @@ __global__ void __launch_bounds__(NTHREADS, 1) mx8_grouped_kernel(const __grid_c
                 // this CTA's 128 rows of W: a pair's halves are gate and up, or columns;
                 // one CTA has 64 of each
                 if (DUAL && CG == 1) {
-                    ld(&P.tmB0, st + A_BYTES, kb * BK, t.nb * OUT, t.e);
-                    ld(&P.tmB1, st + A_BYTES + 64 * BK, kb * BK, t.nb * OUT, t.e);
-                } else if (DUAL) {
-                    ld(rank ? &P.tmB1 : &P.tmB0, st + A_BYTES, kb * BK, t.nb * OUT, t.e);
+                    ld(&P.tmB0, st + A_BYTES, 0, wrow + kb * 128, 0);
+                    ld(&P.tmB1, st + A_BYTES + 64 * BK, 0, wrow + kb * 128, 0);
                 } else {
-                    ld(&P.tmB0, st + A_BYTES, kb * BK, t.nb * OUT + (int)rank * 128, t.e);
+                    ld(DUAL && rank ? &P.tmB1 : &P.tmB0, st + A_BYTES, 0, wrow + kb * 128, 0);
                 }
             }
         }
@@ -324,14 +345,15 @@ __global__ void __launch_bounds__(NTHREADS, 1) mx8_grouped_kernel(const __grid_c
         __syncwarp();
     } else if (warp >= 2 + NUM_EPI_WARPS) {
         // ------------------------------------------------ scales (each CTA: its rows' and all columns')
-        // Thread i of the four warps copies 16 bytes of the scales of row i of x and of
-        // rows i (and 128 + i) of W: a quad, four stages.  Quads are copied SF_AHEAD
-        // ahead (cp.async).  Each warp then takes the words of every row to registers, as
-        // the MMA reads its scales from every lane quarter, and writes a stage's to its
-        // quarter of tensor memory.  A buffer there is free once the MMAs
+        // Thread i of the four warps copies 16 bytes of the scales of row i of x, and 16
+        // bytes of the four tiles of each row block of W: a quad, four stages.  Quads are
+        // copied SF_AHEAD ahead (cp.async).  Each warp then takes the words of every row to
+        // registers, as the MMA reads its scales from every lane quarter, and writes a
+        // stage's to its quarter of tensor memory.  A buffer there is free once the MMAs
         // SF_BUFS = STAGES stages back have read it, which is when that stage's "empty"
         // barrier completes.  (With more buffers than stages the barrier could pass that
         // phase and the next unseen.)
+        constexpr int NB = CG == 2 || DUAL ? 2 : 1;      // row blocks of W
         const int i = (warp - 2 - NUM_EPI_WARPS) * 32 + lane;
         const uint32_t ta = tmem + ((uint32_t)((warp & 3) * 32) << 16) + SF_COL;
         const uint32_t bar0 = CG == 1 ? smem_u32(&sfull[0]) : mapa_shared(smem_u32(&sfull[0]), 0);
@@ -340,29 +362,35 @@ __global__ void __launch_bounds__(NTHREADS, 1) mx8_grouped_kernel(const __grid_c
         const int q0 = kb0 / QUAD, q1 = (kb1 + QUAD - 1) / QUAD;
         const int quads = tiles * (q1 - q0);
         int f_tix = unit, f_q = q0, f_slot = 0;          // the next quad to copy
-        const uint8_t *pa = nullptr, *pb[CG] = {};       // its tile's rows, null past W's end
+        const uint8_t *pa = nullptr, *pb[NB] = {};       // its tile's first bytes
+        uint32_t upper = 0, uppers = 0;                  // one CTA, SwiGLU: a tile is the upper or the lower 64
+                                                         // rows of W's block; a bit per slot
         auto locate = [&]() {
             if (f_tix >= total) return;
             const Mx8Tile t = decode<CG>(offs, prefix, P.E, P.n_blocks, f_tix);
-            // (rows past the end of x are not stored: any scale will do)
-            pa = P.sa + (int64_t)min(t.m0 + (int)rank * BM + i, (int)P.rows - 1) * P.pitch;
+            // (the next segments' rows are not stored: any scale will do)
+            const int row = t.m0 + (int)rank * BM + i;
+            pa = row < t.end ? P.sa + (int64_t)row * P.pitch : nullptr;
 #pragma unroll
-            for (int h = 0; h < CG; ++h) {               // half h of the accumulator's columns
-                const bool up = DUAL && (CG == 2 ? h == 1 : i >= 64);
-                const int col = DUAL ? t.nb * OUT + (CG == 2 ? i : i & 63) : t.nb * OUT + h * 128 + i;
-                pb[h] = col < P.N ? (up ? P.sb1 : P.sb0) + ((int64_t)t.e * P.N + col) * P.pitch : nullptr;
-            }
+            for (int h = 0; h < NB; ++h)
+                pb[h] = (DUAL && h ? P.sb1 : P.sb0) +
+                        ((int64_t)t.e * P.w_blocks + w_block<CG, DUAL>(P, t.nb, h)) * nk * 512 + i * 16;
+            upper = t.nb & 1;
         };
         locate();
         auto copy = [&]() {                              // one group a quad, empty ones past the last
             if (f_tix < total) {
                 const uint32_t d = dst + f_slot * R::SF_SLOT;
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(pa + f_q * 16) : "memory");
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(pa ? pa + f_q * 16 : P.sa),
+                             "r"(pa ? 16 : 0)
+                             : "memory");
+                const bool in = f_q * QUAD + i / 32 < nk;    // the row block has this tile
 #pragma unroll
-                for (int h = 0; h < CG; ++h)
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d + (BM + h * 128) * 16),
-                                 "l"(pb[h] ? pb[h] + f_q * 16 : P.sa), "r"(pb[h] ? 16 : 0)
+                for (int h = 0; h < NB; ++h)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d + (1 + h) * SF_QUAD),
+                                 "l"(in ? pb[h] + f_q * SF_QUAD : P.sa), "r"(in ? 16 : 0)
                                  : "memory");
+                if (DUAL && CG == 1) uppers = (uppers & ~(1u << f_slot)) | upper << f_slot;
                 f_slot = f_slot + 1 == SF_SLOTS ? 0 : f_slot + 1;
                 if (++f_q == q1) {
                     f_q = q0;
@@ -379,12 +407,22 @@ __global__ void __launch_bounds__(NTHREADS, 1) mx8_grouped_kernel(const __grid_c
         for (int q = 0; q < quads; ++q) {
             asm volatile("cp.async.wait_group %0;" ::"n"(SF_AHEAD - 1) : "memory");
             asm volatile("bar.sync 1, 128;" ::: "memory");   // every thread's rows are there
-            uint4 a[4], b[4 * CG];
+            uint4 a[4], b[NB][QUAD];
             const uint8_t* t = sf_smem + slot * R::SF_SLOT + lane * 16;
 #pragma unroll
             for (int k = 0; k < 4; ++k) a[k] = *reinterpret_cast<const uint4*>(t + k * 512);
 #pragma unroll
-            for (int k = 0; k < 4 * CG; ++k) b[k] = *reinterpret_cast<const uint4*>(t + BM * 16 + k * 512);
+            for (int h = 0; h < NB; ++h)
+#pragma unroll
+                for (int k = 0; k < QUAD; ++k) b[h][k] = *reinterpret_cast<const uint4*>(t + (1 + h) * SF_QUAD + k * 512);
+            if (DUAL && CG == 1) {                       // rows 0-63: the gate's, 64-127: up's
+                const bool up = uppers >> slot & 1;
+#pragma unroll
+                for (int k = 0; k < QUAD; ++k) {
+                    const uint4 g = b[0][k], u = b[NB - 1][k];
+                    b[0][k] = up ? make_uint4(g.z, g.w, u.z, u.w) : make_uint4(g.x, g.y, u.x, u.y);
+                }
+            }
             copy();      // into the slot that the previous quad's reads, before the barrier, left
             const int n = min(QUAD, kb1 - kb);
             kb = kb + n == kb1 ? kb0 : kb + n;
@@ -398,7 +436,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) mx8_grouped_kernel(const __grid_c
                     tmem_st4(ta + buf * SF_COLS, w(a[0]), w(a[1]), w(a[2]), w(a[3]));
 #pragma unroll
                     for (int h = 0; h < CG; ++h)
-                        tmem_st4(ta + buf * SF_COLS + 8 + 4 * h, w(b[4 * h]), w(b[4 * h + 1]), w(b[4 * h + 2]), w(b[4 * h + 3]));
+                        tmem_st4(ta + buf * SF_COLS + 8 + 4 * h, b[h][st].x, b[h][st].y, b[h][st].z, b[h][st].w);
                     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                     tc_fence_before();
                     __syncwarp();
@@ -653,10 +691,10 @@ __global__ void __launch_bounds__(NTHREADS, 1) mx8_grouped_kernel(const __grid_c
         if (_r != MOE_OK) return _r; \
     } while (0)
 
-// codes [sets, rows, K]: boxes of 128 bytes x `box_rows` rows
-int codes_map(CUtensorMap* m, const void* p, int64_t rows, int sets, int K, int box_rows) {
-    const uint64_t dims[3] = {(uint64_t)K, (uint64_t)rows, (uint64_t)sets};
-    const uint64_t st[2] = {(uint64_t)K, (uint64_t)K * rows};
+// rows of `bytes`: boxes of 128 bytes x `box_rows` rows
+int codes_map(CUtensorMap* m, const void* p, int64_t rows, int bytes, int box_rows) {
+    const uint64_t dims[3] = {(uint64_t)bytes, (uint64_t)rows, 1};
+    const uint64_t st[2] = {(uint64_t)bytes, (uint64_t)bytes * rows};
     const uint32_t box[3] = {BK, (uint32_t)box_rows, 1};
     return encode_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, p, dims, st, box);
 }
@@ -716,10 +754,14 @@ int launch_mx8_product(const moe_mx8_product_config& c, const void* xq, const vo
     // where experts have more than 128 rows.  The host knows their sum only.
     const bool pair = c.rows >= (int64_t)256 * c.E;
     const int w_rows = dual && !pair ? 64 : 128;
-    MX8_TRY(codes_map(&P.tmA, xq, c.rows, 1, c.K, BM));
+    // (rows of x behind the last: what is left in shared memory serves as well)
+    P.a_rows = pair ? BM : (int)std::min<int64_t>(BM, (c.rows + 7) / 8 * 8);
+    MX8_TRY(codes_map(&P.tmA, xq, c.rows, c.K, P.a_rows));
     // the accumulator's first half is the gate's for SwiGLU
-    MX8_TRY(codes_map(&P.tmB0, dual ? gq : wq, c.N, c.E, c.K, w_rows));
-    if (dual) MX8_TRY(codes_map(&P.tmB1, wq, c.N, c.E, c.K, w_rows));
+    P.w_blocks = (c.N + 127) / 128;
+    const int64_t w_lines = (int64_t)c.E * P.w_blocks * ((c.K + BK - 1) / BK) * 128;
+    MX8_TRY(codes_map(&P.tmB0, dual ? gq : wq, w_lines, BK, w_rows));
+    if (dual) MX8_TRY(codes_map(&P.tmB1, wq, w_lines, BK, w_rows));
     P.sa = static_cast<const uint8_t*>(xs);
     P.sb0 = static_cast<const uint8_t*>(dual ? gs : ws);
     P.sb1 = static_cast<const uint8_t*>(ws);

@@ -15,7 +15,7 @@ import torch
 
 import top_routing_expert_moe_gb300 as _moe
 
-__all__ = ["MX8Tensor", "mx8_scale_pitch", "moe_mx8_quantize", "moe_mx8_quantize_weight",
+__all__ = ["MX8Tensor", "MX8Weight", "mx8_weight_bytes", "moe_mx8_dequantize_weight", "mx8_scale_pitch", "moe_mx8_quantize", "moe_mx8_quantize_weight",
            "moe_mx8_dequantize", "mx8_quantize", "mx8_quantize_weight", "mx8_rows_capacity",
            "permute_mx8_workspace_size", "moe_permute_mx8", "MX8Dispatch", "MX8", "MX8_ACT_NONE",
            "MX8_ACT_SILU", "MX8_ACT_SWIGLU", "MX8ProductConfig", "check_mx8_product_config",
@@ -37,9 +37,10 @@ def _checked(t, shape, dtype, name):
     return t
 
 
-def _checked8(t, shape, name):
-    if not isinstance(t, MX8Tensor):
-        raise TypeError(f"{name}: expected an MX8Tensor")
+def _checked8(t, shape, name, kind=None):
+    kind = kind or MX8Tensor
+    if not isinstance(t, kind):
+        raise TypeError(f"{name}: expected an {kind.__name__}")
     if t.shape != tuple(shape):
         raise ValueError(f"{name}: expected {tuple(shape)}, got {t.shape}")
     return t
@@ -73,14 +74,24 @@ def moe_mx8_dequantize(dtype, rows, K, codes, scales, out, stream=None):
     _call("moe_mx8_dequantize", dtype, rows, K, _p(codes), _p(scales), _p(out), _s(stream))
 
 
+def mx8_weight_bytes(E: int, K: int, N: int):
+    c, s = ctypes.c_size_t(), ctypes.c_size_t()
+    _call("moe_mx8_weight_bytes", E, K, N, ctypes.byref(c), ctypes.byref(s))
+    return c.value, s.value
+
+
+def moe_mx8_dequantize_weight(dtype, E, K, N, codes, scales, out, stream=None):
+    _call("moe_mx8_dequantize_weight", dtype, E, K, N, _p(codes), _p(scales), _p(out), _s(stream))
+
+
 class MX8Tensor:
-    """8-bit numbers [rows, K] or, for expert weights, [E, rows, K]: ``codes`` (e4m3, as
+    """Rows of 8-bit numbers, [rows, K] or sets of them [sets, rows, K]: ``codes`` (e4m3, as
     bytes) of that shape and ``scales`` [..., pitch], one byte for 32 codes."""
 
     def __init__(self, shape, device="cuda"):
         shape = tuple(shape)
         if len(shape) not in (2, 3):
-            raise ValueError("expected [rows, K] or [E, rows, K]")
+            raise ValueError("expected [rows, K] or [sets, rows, K]")
         K = shape[-1]
         if min(shape) < 1 or K % 32:
             mx8_scale_pitch(K)                       # raises for the width
@@ -96,6 +107,26 @@ class MX8Tensor:
             out = torch.empty(self.shape, dtype=dtype, device=self.codes.device)
         K = self.shape[-1]
         moe_mx8_dequantize(code, out.numel() // K, K, self.codes, self.scales, out, stream)
+        return out
+
+
+class MX8Weight:
+    """Expert weights [E, N, K] in 8 bits (each expert's matrix transposed): ``codes`` and
+    ``scales`` in blocks of 128 x 128, see include/moe.h."""
+
+    def __init__(self, shape, device="cuda"):
+        E, N, K = shape
+        codes, scales = mx8_weight_bytes(E, K, N)
+        self.shape = (E, N, K)
+        self.codes = torch.empty(codes, dtype=torch.uint8, device=device)
+        self.scales = torch.empty(scales, dtype=torch.uint8, device=device)
+
+    def dequantize(self, dtype=torch.bfloat16, stream=None):
+        E, N, K = self.shape
+        code = _dtype(dtype)
+        with _on(stream):
+            out = torch.empty(self.shape, dtype=dtype, device=self.codes.device)
+        moe_mx8_dequantize_weight(code, E, K, N, self.codes, self.scales, out, stream)
         return out
 
 
@@ -116,14 +147,14 @@ def mx8_quantize(x, rows_used=None, out=None, stream=None) -> MX8Tensor:
     return out
 
 
-def mx8_quantize_weight(W, stream=None) -> MX8Tensor:
-    """Quantise expert weights W [E, K, N] along K: an MX8Tensor [E, N, K]."""
+def mx8_quantize_weight(W, stream=None) -> MX8Weight:
+    """Quantise expert weights W [E, K, N] along K: an MX8Weight [E, N, K]."""
     if W.dim() != 3:
         raise ValueError("W: expected [E, K, N]")
     E, K, N = W.shape
     code = _dtype(W.dtype)
     with _on(stream):
-        out = MX8Tensor((E, N, K), W.device)
+        out = MX8Weight((E, N, K), W.device)
     moe_mx8_quantize_weight(code, E, K, N, W, out.codes, out.scales, stream)
     return out
 
@@ -215,16 +246,16 @@ class MX8Product:
                                    dtype=torch.bfloat16 if c.out_dtype == _moe.BF16 else torch.float32)
             self._out = self.out, None
 
-    def forward(self, x: MX8Tensor, offsets, w: MX8Tensor, wg: MX8Tensor | None = None, stream=None):
+    def forward(self, x: MX8Tensor, offsets, w: MX8Weight, wg: MX8Weight | None = None, stream=None):
         """out [rows, N] (rows of no segment are not written); x [rows, K], offsets
         [E + 1] int32 as from MX8Dispatch, w (and the gate wg for SwiGLU) [E, N, K]."""
         _checked8(x, self._x, "x")
         _checked(offsets, self._offsets, torch.int32, "offsets")
         if (wg is not None) != self._dual:
             raise ValueError("wg is required iff act is MX8_ACT_SWIGLU")
-        _checked8(w, self._w, "w")
+        _checked8(w, self._w, "w", MX8Weight)
         if wg is not None:
-            _checked8(wg, self._w, "wg")
+            _checked8(wg, self._w, "wg", MX8Weight)
         moe_mx8_grouped_product(self.cfg, x.codes, x.scales, offsets, w.codes, w.scales,
                                 wg.codes if wg else None, wg.scales if wg else None, *self._out, stream)
         return self.out
