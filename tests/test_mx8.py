@@ -234,7 +234,8 @@ def dispatch_reference(topk, E, C):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("T,d,E,k,cf", [(1, 128, 1, 1, 0.0), (2, 256, 8, 2, 0.0), (17, 1024, 4, 2, 0.0), (255, 128, 3, 3, 0.0),
-                                        (256, 256, 64, 8, 0.0), (257, 128, 5, 2, 0.6), (700, 384, 7, 3, 1.0),
+                                        (256, 256, 64, 8, 0.0), (256, 128, 64, 8, 0.5), (33, 2176, 64, 1, 0.0),
+                                        (200, 128, 5, 2, 0.6), (257, 128, 5, 2, 0.6), (700, 384, 7, 3, 1.0),
                                         (1500, 2176, 6, 4, 0.0)])
 def test_dispatch(T, d, E, k, cf):
     g = torch.Generator().manual_seed(T)
@@ -263,10 +264,12 @@ def test_dispatch(T, d, E, k, cf):
 
 
 @pytest.mark.gpu
-def test_dispatch_reports_and_drops_an_expert_out_of_range():
-    topk = torch.tensor([[0], [5], [1], [-7], [1]], dtype=torch.int32)
-    cfg = moe.MoEConfig(T=5, d=128, f=128, E=2, k=1)
+@pytest.mark.parametrize("more", [0, 300])
+def test_dispatch_reports_and_drops_an_expert_out_of_range(more):
+    topk = torch.tensor([[0], [5], [1], [-7], [1]] + [[-1]] * more, dtype=torch.int32)
+    cfg = moe.MoEConfig(T=5 + more, d=128, f=128, E=2, k=1)
     D = moe.MX8Dispatch(cfg)
-    D.forward(moe.mx8_quantize(rows_of(5, 128, torch.bfloat16).cuda()), topk.cuda())
+    D.forward(moe.mx8_quantize(rows_of(5 + more, 128, torch.bfloat16).cuda()), topk.cuda())
     assert moe.last_device_status() == moe.ERR_DEVICE_BOUNDS
-    assert D.slot_of.flatten().tolist() == [0, -1, 1, -1, 2] and D.offsets.tolist() == [0, 1, 3]
+    assert D.slot_of[:5].flatten().tolist() == [0, -1, 1, -1, 2] and D.offsets.tolist() == [0, 1, 3]
+    assert (D.slot_of[5:] == -1).all()

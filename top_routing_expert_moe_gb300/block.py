@@ -143,7 +143,8 @@ class BlockNorm:
             with _on(stream):
                 self.z8 = MX8Tensor((c.T, c.d), self.device)
         z = self.z if keep_z else None
-        moe_block_norm_mx8(c, x, u, w_post, gate, w_pre, self.x_out, z, self.z8.codes, self.z8.scales, stream)
+        _call("moe_block_norm_mx8", ctypes.byref(c), _p(x), _p(u), _p(w_post), _p(gate), _p(w_pre),
+              _p(self.x_out), _p(z), *self.z8.ptrs, _s(stream))
         return (self.x_out if self._leave else x), self.z8, z
 
     def grads(self):

@@ -122,38 +122,42 @@ __global__ void __launch_bounds__(ROW_THREADS) mx8_rows_kernel(const T* __restri
     }
 }
 
-// 16 codes a thread: half a block
+// Values: as many codes a thread as 16 bytes of the output hold, so that a warp's stores
+// lie side by side (32 bytes a thread, two stores: 16384 x 4096 to bf16 39 us, so 32)
 template <typename T>
 __global__ void __launch_bounds__(ROW_THREADS) mx8_values_kernel(const uint8_t* __restrict__ codes,
                                                                  const uint8_t* __restrict__ scales, const Turns t, int K,
                                                                  int pitch, T* __restrict__ out) {
     pdl_wait();
     pdl_trigger();
+    constexpr int V = Vec16<T>::N;
     for (int64_t u = blockIdx.x; u < t.turns; u += gridDim.x) {
         Place p[ROW_UNROLL];
-        uint4 c[ROW_UNROLL];
-        uint32_t s[ROW_UNROLL];
+        uint32_t c[ROW_UNROLL][V / 4], s[ROW_UNROLL];
 #pragma unroll
         for (int j = 0; j < ROW_UNROLL; ++j) {
             p[j] = place(t, t.rows, u, j);
             if (p[j].row < 0) continue;
-            c[j] = __ldg(reinterpret_cast<const uint4*>(codes + p[j].row * K) + p[j].vec);
-            s[j] = __ldg(scales + p[j].row * pitch + p[j].vec / 2);
+            const uint8_t* src = codes + p[j].row * K + p[j].vec * V;
+            if constexpr (V == 8) {
+                const uint2 w = __ldg(reinterpret_cast<const uint2*>(src));
+                c[j][0] = w.x;
+                c[j][1] = w.y;
+            } else {
+                c[j][0] = __ldg(reinterpret_cast<const uint32_t*>(src));
+            }
+            s[j] = __ldg(scales + p[j].row * pitch + p[j].vec / (32 / V));
         }
 #pragma unroll
         for (int j = 0; j < ROW_UNROLL; ++j) {
             if (p[j].row < 0) continue;
             const float m = mx8_scale_value(s[j]);
-            const uint32_t w[4] = {c[j].x, c[j].y, c[j].z, c[j].w};
-            float v[16];
+            float v[V];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) mx8_unpack4(w[i], v + 4 * i);
+            for (int i = 0; i < V / 4; ++i) mx8_unpack4(c[j][i], v + 4 * i);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] *= m;
-            T* dst = out + p[j].row * K + p[j].vec * 16;
-            constexpr int V = Vec16<T>::N;
-#pragma unroll
-            for (int i = 0; i < 16; i += V) store16_f<T>(dst + i, v + i);
+            for (int i = 0; i < V; ++i) v[i] *= m;
+            store16_f<T>(out + p[j].row * K + p[j].vec * V, v);
         }
     }
 }
@@ -268,6 +272,116 @@ __global__ void __launch_bounds__(256) mx8_scatter_kernel(const uint8_t* __restr
     }
 }
 
+// A batch of up to 256 tokens in one launch: every CTA finds all places by itself (a thread
+// a token; ranks by ballots, as in permute.cu), the first writes them down, and each
+// copies its tokens' rows.  Three launches for 17 tokens took 6.0 us.
+constexpr int FEW = 256;
+__global__ void __launch_bounds__(FEW) mx8_dispatch_few_kernel(
+    const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, const int32_t* __restrict__ topk, int T, int E,
+    int k, int C, int d, int pitch, uint8_t* __restrict__ codes_perm, uint8_t* __restrict__ scales_perm,
+    int32_t* __restrict__ perm_token, int32_t* __restrict__ slot_of, int32_t* __restrict__ kept,
+    int32_t* __restrict__ offsets, float* __restrict__ stats, int* status) {
+    pdl_wait();
+    pdl_trigger();
+    __shared__ int wcount[FEW / 32][64], s_off[65], s_slot[FEW][8];
+    const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+    const bool first = blockIdx.x == 0;
+    int sel[8], rank[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        sel[j] = t < T && j < k ? topk[t * k + j] : -1;
+        if (first && (sel[j] < -1 || sel[j] >= E)) set_status(status, MOE_ERR_DEVICE_BOUNDS);
+        rank[j] = 0;
+    }
+    const unsigned lt = (1u << lane) - 1u;
+    for (int e = 0; e < E; ++e) {
+        bool mine = false;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) mine |= sel[j] == e;
+        const unsigned bal = __ballot_sync(0xffffffffu, mine);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (sel[j] == e) rank[j] = __popc(bal & lt);
+        if (lane == 0) wcount[warp][e] = __popc(bal);
+    }
+    __syncthreads();
+    if (warp == 0) {                       // segments: two experts a lane
+        int n[2], total[2], before = 0;
+        long dropped = 0;
+        int kmax = 0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int e = lane + 32 * i;
+            total[i] = 0;
+            if (e < E)
+                for (int w = 0; w < FEW / 32; ++w) total[i] += wcount[w][e];
+            n[i] = min(total[i], C);
+            int sum = n[i];
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, sum, o);
+                if (lane >= o) sum += v;
+            }
+            if (e < E) s_off[e] = before + sum - n[i];
+            before += __shfl_sync(0xffffffffu, sum, 31);
+            dropped += total[i] - n[i];
+            kmax = max(kmax, n[i]);
+        }
+        if (lane == 0) s_off[E] = before;
+        if (first) {
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int e = lane + 32 * i;
+                if (e < E) {
+                    kept[e] = n[i];
+                    offsets[e] = s_off[e];
+                }
+            }
+            int drop = (int)dropped;
+            for (int o = 16; o > 0; o >>= 1) {
+                drop += __shfl_xor_sync(0xffffffffu, drop, o);
+                kmax = max(kmax, __shfl_xor_sync(0xffffffffu, kmax, o));
+            }
+            if (lane == 0) {
+                offsets[E] = before;
+                if (stats) {
+                    stats[MOE_STAT_DROPPED] = (float)drop;
+                    stats[MOE_STAT_MAX_OVER_MEAN_KEPT] = before > 0 ? (float)kmax / ((float)before / (float)E) : 0.f;
+                }
+            }
+        }
+    }
+    __syncthreads();
+    if (t < T)
+        for (int j = 0; j < k; ++j) {
+            int slot = -1;
+            if (sel[j] >= 0 && sel[j] < E) {
+                int r = rank[j];
+                for (int w = 0; w < warp; ++w) r += wcount[w][sel[j]];
+                if (r < C) slot = s_off[sel[j]] + r;
+            }
+            s_slot[t][j] = slot;
+            if (first) {
+                slot_of[t * k + j] = slot;
+                if (slot >= 0) perm_token[slot] = t;
+            }
+        }
+    __syncthreads();
+    const int nc = d / 16, nv = nc + pitch / 16;
+    for (int row = blockIdx.x; row < T; row += gridDim.x)
+        for (int v = t; v < nv; v += FEW) {
+            const bool code = v < nc;
+            const uint4 x = __ldg(code ? reinterpret_cast<const uint4*>(codes + (size_t)row * d) + v
+                                       : reinterpret_cast<const uint4*>(scales + (size_t)row * pitch) + v - nc);
+            for (int j = 0; j < k; ++j) {
+                const int to = s_slot[row][j];
+                if (to >= 0)
+                    *(code ? reinterpret_cast<uint4*>(codes_perm + (size_t)to * d) + v
+                           : reinterpret_cast<uint4*>(scales_perm + (size_t)to * pitch) + v - nc) = x;
+            }
+        }
+}
+
 template <typename T>
 int rows_t(int64_t rows, int K, const void* x, const int32_t* used, void* codes, void* scales, cudaStream_t st) {
     const Turns t = turns_of(rows, K / 8);
@@ -291,7 +405,7 @@ int weight_values_t(int E, int K, int N, const void* codes, const void* scales, 
 }
 template <typename T>
 int values_t(int64_t rows, int K, const void* codes, const void* scales, void* out, cudaStream_t st) {
-    const Turns t = turns_of(rows, K / 16);
+    const Turns t = turns_of(rows, K / Vec16<T>::N);
     MOE_LAUNCH(mx8_values_kernel<T>, turn_grid(t), ROW_THREADS, 0, st, static_cast<const uint8_t*>(codes),
                static_cast<const uint8_t*>(scales), t, K, (int)mx8_pitch(K), static_cast<T*>(out));
     return MOE_OK;
@@ -322,6 +436,13 @@ int launch_mx8_dequantize_weight(int dtype, int E, int K, int N, const void* cod
 int launch_permute_mx8(const moe_config& c, const void* codes, const void* scales, const int32_t* topk,
                        void* codes_perm, void* scales_perm, int32_t* perm_token, int32_t* slot_of, int32_t* kept,
                        int32_t* offsets, float* stats, void* ws, cudaStream_t st) {
+    if (c.T <= FEW) {
+        MOE_LAUNCH(mx8_dispatch_few_kernel, std::min(c.T, num_sms()), FEW, 0, st, static_cast<const uint8_t*>(codes),
+                   static_cast<const uint8_t*>(scales), topk, c.T, c.E, c.k, capacity_of(c), c.d, (int)mx8_pitch(c.d),
+                   static_cast<uint8_t*>(codes_perm), static_cast<uint8_t*>(scales_perm), perm_token, slot_of, kept,
+                   offsets, stats, device_status_ptr());
+        return MOE_OK;
+    }
     if (const int r = launch_permute_index(c, 1, topk, perm_token, slot_of, kept, offsets, stats, ws, st)) return r;
     const int grid = std::min((c.T + 7) / 8, num_sms() * 8);
     MOE_LAUNCH(mx8_scatter_kernel, grid, 256, 0, st, static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(scales),

@@ -46,6 +46,7 @@ def _checked8(t, shape, name, kind=None):
     return t
 
 
+_NONE = (None, None)
 _DTYPES = {torch.bfloat16: _moe.BF16, torch.float32: _moe.F32}
 
 
@@ -84,7 +85,28 @@ def moe_mx8_dequantize_weight(dtype, E, K, N, codes, scales, out, stream=None):
     _call("moe_mx8_dequantize_weight", dtype, E, K, N, _p(codes), _p(scales), _p(out), _s(stream))
 
 
-class MX8Tensor:
+class _Numbers:
+    """``codes`` and ``scales`` of a set of 8-bit numbers: buffers that it holds for good, so that
+    their addresses are looked up once."""
+
+    def _hold(self, codes, scales):
+        self._codes, self._scales = codes, scales
+        self._ptrs = (codes.data_ptr(), scales.data_ptr()) if codes.is_cuda else None
+
+    @property
+    def codes(self):
+        return self._codes
+
+    @property
+    def scales(self):
+        return self._scales
+
+    @property
+    def ptrs(self):
+        return self._ptrs or (_p(self._codes), _p(self._scales))     # (raises off the GPU)
+
+
+class MX8Tensor(_Numbers):
     """Rows of 8-bit numbers, [rows, K] or sets of them [sets, rows, K]: ``codes`` (e4m3, as
     bytes) of that shape and ``scales`` [..., pitch], one byte for 32 codes."""
 
@@ -97,20 +119,21 @@ class MX8Tensor:
             mx8_scale_pitch(K)                       # raises for the width
             raise ValueError(f"expected sizes of 1 or more, got {shape}")
         self.shape = shape
+        self._rows = shape[0] if len(shape) == 2 else shape[0] * shape[1]
         # moe_mx8_scale_pitch, without the call
-        self.codes = torch.empty(shape, dtype=torch.uint8, device=device)
-        self.scales = torch.empty((*shape[:-1], (K // 32 + 15) // 16 * 16), dtype=torch.uint8, device=device)
+        self._hold(torch.empty(shape, dtype=torch.uint8, device=device),
+                   torch.empty((*shape[:-1], (K // 32 + 15) // 16 * 16), dtype=torch.uint8, device=device))
 
     def dequantize(self, dtype=torch.bfloat16, stream=None):
         code = _dtype(dtype)
+        c, s = self.ptrs
         with _on(stream):
-            out = torch.empty(self.shape, dtype=dtype, device=self.codes.device)
-        K = self.shape[-1]
-        moe_mx8_dequantize(code, out.numel() // K, K, self.codes, self.scales, out, stream)
+            out = torch.empty(self.shape, dtype=dtype, device=self._codes.device)
+        _call("moe_mx8_dequantize", code, self._rows, self.shape[-1], c, s, out.data_ptr(), _s(stream))
         return out
 
 
-class MX8Weight:
+class MX8Weight(_Numbers):
     """Expert weights [E, N, K] in 8 bits (each expert's matrix transposed): ``codes`` and
     ``scales`` in blocks of 128 x 128, see include/moe.h."""
 
@@ -118,8 +141,8 @@ class MX8Weight:
         E, N, K = shape
         codes, scales = mx8_weight_bytes(E, K, N)
         self.shape = (E, N, K)
-        self.codes = torch.empty(codes, dtype=torch.uint8, device=device)
-        self.scales = torch.empty(scales, dtype=torch.uint8, device=device)
+        self._hold(torch.empty(codes, dtype=torch.uint8, device=device),
+                   torch.empty(scales, dtype=torch.uint8, device=device))
 
     def dequantize(self, dtype=torch.bfloat16, stream=None):
         E, N, K = self.shape
@@ -202,8 +225,8 @@ class MX8Dispatch:
         _checked(topk_idx, (c.T, c.k), torch.int32, "topk_idx")
         if stats is not None:
             _checked(stats, (9 + c.E,), torch.float32, "stats")
-        moe_permute_mx8(c, x.codes, x.scales, topk_idx, self.rows.codes, self.rows.scales, self.perm_token,
-                        self.slot_of, self.kept, self.offsets, stats, self.ws, stream)
+        _call("moe_permute_mx8", ctypes.byref(c), *x.ptrs, _p(topk_idx), *self.rows.ptrs, _p(self.perm_token),
+              _p(self.slot_of), _p(self.kept), _p(self.offsets), _p(stats), _p(self.ws), _s(stream))
         return self.rows
 
 
@@ -240,11 +263,9 @@ class MX8Product:
         self._dual = c.act == MX8_ACT_SWIGLU
         if c.out_dtype == MX8:
             self.out = MX8Tensor((c.rows, c.N), device)
-            self._out = self.out.codes, self.out.scales
         else:
             self.out = torch.empty(c.rows, c.N, device=device,
                                    dtype=torch.bfloat16 if c.out_dtype == _moe.BF16 else torch.float32)
-            self._out = self.out, None
 
     def forward(self, x: MX8Tensor, offsets, w: MX8Weight, wg: MX8Weight | None = None, stream=None):
         """out [rows, N] (rows of no segment are not written); x [rows, K], offsets
@@ -256,9 +277,10 @@ class MX8Product:
         _checked8(w, self._w, "w", MX8Weight)
         if wg is not None:
             _checked8(wg, self._w, "wg", MX8Weight)
-        moe_mx8_grouped_product(self.cfg, x.codes, x.scales, offsets, w.codes, w.scales,
-                                wg.codes if wg else None, wg.scales if wg else None, *self._out, stream)
-        return self.out
+        out = self.out
+        _call("moe_mx8_grouped_product", ctypes.byref(self.cfg), *x.ptrs, _p(offsets), *w.ptrs,
+              *(wg.ptrs if wg else _NONE), *(out.ptrs if self.cfg.out_dtype == MX8 else (_p(out), None)), _s(stream))
+        return out
 
 
 class MX8Experts:
