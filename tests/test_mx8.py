@@ -264,6 +264,28 @@ def test_dispatch(T, d, E, k, cf):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T", [4, 300])
+def test_dispatch_of_an_expert_that_a_token_names_twice(T):
+    """The token takes one row of the expert, and both of its slots point there."""
+    topk = torch.tensor([[0, 0], [1, 0], [1, 1], [0, 1]] + [[-1, -1]] * (T - 4), dtype=torch.int32)
+    D = moe.MX8Dispatch(moe.MoEConfig(T=T, d=128, f=128, E=2, k=2))
+    x = moe.mx8_quantize(rows_of(T, 128, torch.bfloat16).cuda())
+    rows = D.forward(x, topk.cuda())
+    assert D.slot_of[:4].tolist() == [[0, 0], [3, 1], [4, 4], [2, 5]]
+    token = D.perm_token.tolist()
+    assert (token[0], token[1], token[2], token[3], token[4], token[5]) == (0, 1, 3, 1, 2, 3)
+    assert torch.equal(rows.codes[:6], x.codes[torch.tensor(token[:6]).cuda()])
+    # and so does moe_permute, to segments of whole 128s
+    L = moe.MoELayer(moe.MoEConfig(T=T, d=128, f=128, E=2, k=2))
+    xb = x.dequantize()
+    L.perm_token.fill_(2 ** 30)
+    moe.moe_permute(L.cfg, xb, topk.cuda(), L.x_perm, L.perm_token, L.slot_of, L.kept, L.offsets, None, L.ws)
+    assert L.slot_of[:4].tolist() == [[0, 0], [128, 1], [129, 129], [2, 130]] and L.kept.tolist() == [3, 3]
+    assert L.perm_token[:4].tolist() == [0, 1, 3, -1] and L.perm_token[128:132].tolist() == [1, 2, 3, -1]
+    assert torch.equal(L.x_perm[:3], xb[[0, 1, 3]]) and (L.x_perm[3:128] == 0).all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("more", [0, 300])
 def test_dispatch_reports_and_drops_an_expert_out_of_range(more):
     topk = torch.tensor([[0], [5], [1], [-7], [1]] + [[-1]] * more, dtype=torch.int32)

@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(256) mx8_scatter_kernel(const uint8_t* __restr
 }
 
 // A batch of up to 256 tokens in one launch: every CTA finds all places by itself (a thread
-// a token; ranks by ballots, as in permute.cu), the first writes them down, and each
+// a token; ranks by lane masks, as in permute.cu), the first writes them down, and each
 // copies its tokens' rows.  Three launches for 17 tokens took 6.0 us.
 constexpr int FEW = 256;
 __global__ void __launch_bounds__(FEW) mx8_dispatch_few_kernel(
@@ -283,26 +283,18 @@ __global__ void __launch_bounds__(FEW) mx8_dispatch_few_kernel(
     int32_t* __restrict__ offsets, float* __restrict__ stats, int* status) {
     pdl_wait();
     pdl_trigger();
-    __shared__ int wcount[FEW / 32][64], s_off[65], s_slot[FEW][8];
+    __shared__ unsigned picks[FEW / 32][64];   // per warp and expert, the lanes whose token picks it
+    __shared__ int s_off[65], s_slot[FEW][8];
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
     const bool first = blockIdx.x == 0;
-    int sel[8], rank[8];
+    for (int i = t; i < FEW / 32 * 64; i += FEW) (&picks[0][0])[i] = 0;
+    __syncthreads();
+    int sel[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         sel[j] = t < T && j < k ? topk[t * k + j] : -1;
         if (first && (sel[j] < -1 || sel[j] >= E)) set_status(status, MOE_ERR_DEVICE_BOUNDS);
-        rank[j] = 0;
-    }
-    const unsigned lt = (1u << lane) - 1u;
-    for (int e = 0; e < E; ++e) {
-        bool mine = false;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) mine |= sel[j] == e;
-        const unsigned bal = __ballot_sync(0xffffffffu, mine);
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (sel[j] == e) rank[j] = __popc(bal & lt);
-        if (lane == 0) wcount[warp][e] = __popc(bal);
+        if (sel[j] >= 0 && sel[j] < E) atomicOr(&picks[warp][sel[j]], 1u << lane);
     }
     __syncthreads();
     if (warp == 0) {                       // segments: two experts a lane
@@ -314,7 +306,7 @@ __global__ void __launch_bounds__(FEW) mx8_dispatch_few_kernel(
             const int e = lane + 32 * i;
             total[i] = 0;
             if (e < E)
-                for (int w = 0; w < FEW / 32; ++w) total[i] += wcount[w][e];
+                for (int w = 0; w < FEW / 32; ++w) total[i] += __popc(picks[w][e]);
             n[i] = min(total[i], C);
             int sum = n[i];
             for (int o = 1; o < 32; o <<= 1) {
@@ -356,8 +348,8 @@ __global__ void __launch_bounds__(FEW) mx8_dispatch_few_kernel(
         for (int j = 0; j < k; ++j) {
             int slot = -1;
             if (sel[j] >= 0 && sel[j] < E) {
-                int r = rank[j];
-                for (int w = 0; w < warp; ++w) r += wcount[w][sel[j]];
+                int r = __popc(picks[warp][sel[j]] & ((1u << lane) - 1u));
+                for (int w = 0; w < warp; ++w) r += __popc(picks[w][sel[j]]);
                 if (r < C) slot = s_off[sel[j]] + r;
             }
             s_slot[t][j] = slot;
