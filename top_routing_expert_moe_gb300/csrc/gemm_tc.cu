@@ -537,7 +537,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) tc_grouped_gemm_kernel(const __gr
             ++nst;
         };
         // 32 columns of this lane's row in 8 bits: a block
-        auto put8 = [&](const TcProblem& q, int i, const float* v, int c0, int c1, long long row) {
+        // (its scale byte is returned)
+        auto put8 = [&](const CUtensorMap* m, const float* v, int c0, int c1) {
             uint8_t* buf = stg + (nst & 1) * 2048;
             if (nst >= 2) {
                 if (lane == 0) bulk_wait_read<1>();
@@ -549,14 +550,14 @@ __global__ void __launch_bounds__(NTHREADS, 1) tc_grouped_gemm_kernel(const __gr
             const int x = ((lane >> 2) & 1) << 4;         // 32-byte swizzle
             *reinterpret_cast<uint4*>(buf + lane * 32 + x) = make_uint4(w[0], w[1], w[2], w[3]);
             *reinterpret_cast<uint4*>(buf + lane * 32 + (x ^ 16)) = make_uint4(w[4], w[5], w[6], w[7]);
-            q.scales[i][row * q.sc_pitch + c0 / 32] = (uint8_t)s;
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-                tma_store3(&q.tmC[i], smem_u32(buf), c0, c1, 0);
+                tma_store3(m, smem_u32(buf), c0, c1, 0);
                 bulk_commit();
             }
             ++nst;
+            return s;
         };
         int tcount = 0;
         for (int tix = unit; tix < total; tix += nunits, ++tcount) {
@@ -586,22 +587,31 @@ __global__ void __launch_bounds__(NTHREADS, 1) tc_grouped_gemm_kernel(const __gr
                     for (int j = 0; j < 4; ++j) nxt[1][j] = p1[j];
                 }
             };
-            // the same of what is kept in 8 bits
+            // The same of what is kept in 8 bits.  The scale bytes of this warp's two or four
+            // chunks are neighbours: they are read, or written, as one word a row.
             uint4 nxt8[2][2];
-            uint32_t nxs[2];
+            uint32_t sw[2] = {0, 0};
+            const bool four = c_hi - c_lo == 4;
+            const long long sat = row * q.sc_pitch + t.n0 / 32 + c_lo;
             auto fetch8 = [&](int c) {
-                const long long at = row * q.ldo + t.n0 + c * 32, sat = row * q.sc_pitch + (t.n0 + c * 32) / 32;
+                const long long at = row * q.ldo + t.n0 + c * 32;
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
                     if (i < n_in) {
                         const uint4* p = reinterpret_cast<const uint4*>(q.codes[i] + at);
                         nxt8[i][0] = p[0];
                         nxt8[i][1] = p[1];
-                        nxs[i] = q.scales[i][sat];
                     }
             };
             if constexpr (KEEP8) {
-                if (valid && n_in) fetch8(c_lo);
+                if (valid && n_in) {
+                    fetch8(c_lo);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        if (i < n_in)
+                            sw[i] = four ? *reinterpret_cast<const uint32_t*>(q.scales[i] + sat)
+                                         : *reinterpret_cast<const uint16_t*>(q.scales[i] + sat);
+                }
             } else {
                 if (valid && n_in) fetch(c_lo);
             }
@@ -624,14 +634,14 @@ __global__ void __launch_bounds__(NTHREADS, 1) tc_grouped_gemm_kernel(const __gr
                         float u[32];
                         tmem_ld32(taddr + 128 + c * 32, u);
                         tmem_wait_ld();
-                        put8(q, 0, v, bcol, brow, row);
-                        put8(q, 1, u, bcol, brow, row);
+                        sw[0] |= put8(&q.tmC[0], v, bcol, brow) << (8 * (c - c_lo));
+                        sw[1] |= put8(&q.tmC[1], u, bcol, brow) << (8 * (c - c_lo));
 #pragma unroll
                         for (int i = 0; i < 32; ++i) v[i] = silu_fast(v[i]) * u[i];
                         put(&q.tmO[0], v, bcol, brow, 0);
                     } else if (q.epi == EPI_SILU_FWD) {
                         tmem_wait_ld();
-                        put8(q, 0, v, bcol, brow, row);
+                        sw[0] |= put8(&q.tmC[0], v, bcol, brow) << (8 * (c - c_lo));
 #pragma unroll
                         for (int i = 0; i < 32; ++i) v[i] = silu_fast(v[i]);
                         put(&q.tmO[0], v, bcol, brow, 0);
@@ -645,7 +655,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) tc_grouped_gemm_kernel(const __gr
                                 const uint4 x = nxt8[i][j];
                                 w[i][4 * j] = x.x; w[i][4 * j + 1] = x.y; w[i][4 * j + 2] = x.z; w[i][4 * j + 3] = x.w;
                             }
-                        const float sc0 = mx8_scale_value(nxs[0]), sc1 = n_in == 2 ? mx8_scale_value(nxs[1]) : 0.f;
+                        const int sh = 8 * (c - c_lo);
+                        const float sc0 = mx8_scale_value(sw[0] >> sh & 255u), sc1 = mx8_scale_value(sw[1] >> sh & 255u);
                         if (c + 1 < c_hi) fetch8(c + 1);
                         tmem_wait_ld();
                         float a[32], o[32];
@@ -716,6 +727,15 @@ __global__ void __launch_bounds__(NTHREADS, 1) tc_grouped_gemm_kernel(const __gr
                     put(&q.tmO[0], o, bcol, brow, bz);
                     put(&q.tmO[1], v, bcol, brow, bz);
                 }
+            }
+            if constexpr (KEEP8) {
+                if (valid && !n_in)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        if (i < 1 + q.dual) {
+                            if (four) *reinterpret_cast<uint32_t*>(q.scales[i] + sat) = sw[i];
+                            else *reinterpret_cast<uint16_t*>(q.scales[i] + sat) = (uint16_t)sw[i];
+                        }
             }
             tc_fence_before();
             __syncwarp();
