@@ -120,6 +120,18 @@ __device__ __forceinline__ void tmem_st4(uint32_t taddr, uint32_t a, uint32_t b,
                  : "memory");
 }
 
+// silu for fp32 outputs, within a few units of fp32: e^-z = 2^h (1 + l ln 2), where h + l is
+// -z log2(e) in two parts, so that the product's rounding does not grow with z.  (The
+// quick form's error does, which 16 and 8 bits hide; by expf and a division the registers
+// spilled: 32768 rows, K = 2048, N = 4096, silu 439 us, so 208.)
+__device__ __forceinline__ float silu_fine(float z) {
+    constexpr float L = 1.44269504f, L_LO = 1.92596303e-8f, LN2 = 0.693147181f;   // log2(e) in two parts
+    const float h = -z * L, l = fmaf(-z, L_LO, fmaf(-z, L, -h));
+    float e;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(fminf(h, 126.f)));             // (no infinity times l)
+    return __fdividef(z, 1.f + fmaf(e, l * LN2, e));
+}
+
 // A tile is CG * 128 rows x BN accumulator columns; tiles run over experts, then
 // groups of RASTER_ROWS rows, columns, rows.
 struct Mx8Tile { int e, m0, nb, end; };    // end: the segment's
@@ -488,8 +500,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) mx8_grouped_kernel(const __grid_c
             __syncwarp();
         };
         const bool silu = P.act == MOE_MX8_ACT_SILU;
-        // fp32 outputs take the exact form
-        auto act = [](float z) { return F32 ? silu_f(z) : silu_quick(z); };
+        auto act = [](float z) { return F32 ? silu_fine(z) : silu_quick(z); };
         // 64 neighbouring columns of this lane's row, in two halves of 32; nv: rows of the
         // warp's 32 that are the segment's
         auto store = [&](const float (&o)[2][32], int col, int row, int nv) {
@@ -752,7 +763,7 @@ int launch_mx8_product(const moe_mx8_product_config& c, const void* xq, const vo
     const bool dual = c.act == MOE_MX8_ACT_SWIGLU;
     // A pair's tile is 256 rows x 256 columns, a single CTA's 128 x 128: the pair pays
     // where experts have more than 128 rows.  The host knows their sum only.
-    const bool pair = c.rows >= (int64_t)256 * c.E;
+    const bool pair = c.rows >= (int64_t)96 * c.E;
     const int w_rows = dual && !pair ? 64 : 128;
     // (rows of x behind the last: what is left in shared memory serves as well)
     P.a_rows = pair ? BM : (int)std::min<int64_t>(BM, (c.rows + 7) / 8 * 8);
