@@ -761,8 +761,13 @@ int launch_mx8_product(const moe_mx8_product_config& c, const void* xq, const vo
     Mx8Params P;
     memset(&P, 0, sizeof(P));
     const bool dual = c.act == MOE_MX8_ACT_SWIGLU;
-    // A pair's tile is 256 rows x 256 columns, a single CTA's 128 x 128: the pair pays
-    // where experts have more than 128 rows.  The host knows their sum only.
+    // A pair's tile is 256 rows x 256 columns, a single CTA's 128 x 128, which loads twice
+    // the bytes for the same products: it serves where an expert has so few rows that W's
+    // bytes are all that counts.  The host knows the experts' rows together (8 of them, us,
+    // single and pair):     640 rows       768 rows       1024 rows
+    //   4096 -> 14336 SwiGLU  148  153       200  154       211  156
+    //   2048 -> 4096 silu      19  24         25  23         25  22
+    //   14336 -> 4096          82  93        110  89        109  91
     const bool pair = c.rows >= (int64_t)96 * c.E;
     const int w_rows = dual && !pair ? 64 : 128;
     // (rows of x behind the last: what is left in shared memory serves as well)

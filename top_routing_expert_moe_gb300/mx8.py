@@ -85,12 +85,20 @@ def moe_mx8_dequantize_weight(dtype, E, K, N, codes, scales, out, stream=None):
     _call("moe_mx8_dequantize_weight", dtype, E, K, N, _p(codes), _p(scales), _p(out), _s(stream))
 
 
+def _current_device() -> int:
+    try:
+        return torch._C._cuda_getDevice()
+    except AttributeError:       # a private name, a microsecond quicker than the public call
+        return torch.cuda.current_device()
+
+
 class _Numbers:
     """``codes`` and ``scales`` of a set of 8-bit numbers: buffers that it holds for good, so that
     their addresses are looked up once."""
 
     def _hold(self, codes, scales):
         self._codes, self._scales = codes, scales
+        self._device = codes.device
         self._ptrs = (codes.data_ptr(), scales.data_ptr()) if codes.is_cuda else None
 
     @property
@@ -103,7 +111,12 @@ class _Numbers:
 
     @property
     def ptrs(self):
-        return self._ptrs or (_p(self._codes), _p(self._scales))     # (raises off the GPU)
+        """Addresses of the codes and scales, for a call on the current device."""
+        if self._ptrs is None:
+            _p(self._codes)                          # raises: not on a GPU
+        if self._device.index != _current_device():
+            raise ValueError(f"the numbers are on {self._device}, which is not the current device")
+        return self._ptrs
 
 
 class MX8Tensor(_Numbers):
@@ -128,7 +141,7 @@ class MX8Tensor(_Numbers):
         code = _dtype(dtype)
         c, s = self.ptrs
         with _on(stream):
-            out = torch.empty(self.shape, dtype=dtype, device=self._codes.device)
+            out = torch.empty(self.shape, dtype=dtype, device=self._device)
         _call("moe_mx8_dequantize", code, self._rows, self.shape[-1], c, s, out.data_ptr(), _s(stream))
         return out
 
@@ -147,9 +160,10 @@ class MX8Weight(_Numbers):
     def dequantize(self, dtype=torch.bfloat16, stream=None):
         E, N, K = self.shape
         code = _dtype(dtype)
+        c, s = self.ptrs
         with _on(stream):
-            out = torch.empty(self.shape, dtype=dtype, device=self.codes.device)
-        moe_mx8_dequantize_weight(code, E, K, N, self.codes, self.scales, out, stream)
+            out = torch.empty(self.shape, dtype=dtype, device=self._device)
+        _call("moe_mx8_dequantize_weight", code, E, K, N, c, s, out.data_ptr(), _s(stream))
         return out
 
 
@@ -166,7 +180,7 @@ def mx8_quantize(x, rows_used=None, out=None, stream=None) -> MX8Tensor:
         _checked8(out, x.shape, "out")
     if rows_used is not None and (rows_used.numel() != 1 or rows_used.dtype != torch.int32):
         raise ValueError("rows_used must be one int32")
-    moe_mx8_quantize(code, x.shape[0], x.shape[1], x, rows_used, out.codes, out.scales, stream)
+    _call("moe_mx8_quantize", code, x.shape[0], x.shape[1], _p(x), _p(rows_used), *out.ptrs, _s(stream))
     return out
 
 
@@ -178,7 +192,7 @@ def mx8_quantize_weight(W, stream=None) -> MX8Weight:
     code = _dtype(W.dtype)
     with _on(stream):
         out = MX8Weight((E, N, K), W.device)
-    moe_mx8_quantize_weight(code, E, K, N, W, out.codes, out.scales, stream)
+    _call("moe_mx8_quantize_weight", code, E, K, N, _p(W), *out.ptrs, _s(stream))
     return out
 
 
@@ -347,8 +361,8 @@ class MoECheckpoint:
         R, d = self.y.shape
         # the rows below offsets[E] (a view of it would cost more than the call)
         _call("moe_mx8_quantize", _moe.BF16, R, d, _p(y_perm), _p(self.offsets) + 4 * self.cfg.E,
-              _p(self.y.codes), _p(self.y.scales), _s(stream))
+              *self.y.ptrs, _s(stream))
 
     def y_into(self, y_perm, stream=None):
         R, d = self.y.shape
-        moe_mx8_dequantize(_moe.BF16, R, d, self.y.codes, self.y.scales, y_perm, stream)
+        _call("moe_mx8_dequantize", _moe.BF16, R, d, *self.y.ptrs, _p(y_perm), _s(stream))
