@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(MAXT) block_norm_kernel(const NormArgs a) {
 // 65536 x 4096 bf16, both norms, channel gate: forward 324 us (6.6 TB/s, 0.99 of the
 // copy rate; the direct kernel 526), backward 531 us (6.1 TB/s, 0.91; 1750).
 // 65536 x 2048 fp32: 343 us (6.3 TB/s) and 472 us (6.8 TB/s).
-constexpr int RE = 8;                      // elements of a row per thread
+constexpr int RE = 8;                      // elements of a row per thread (see RE8 for z in 8 bits)
 constexpr int MAX_STAGES = 8;
 
 // bytes of a staged row: whole 16s, around any shift
@@ -212,48 +212,63 @@ __device__ __forceinline__ float sum2(f2 a) {
 }
 constexpr int RP = RE / 2;                 // pairs a thread
 
-// A thread's 8 elements of a row.  WIDE (rows of whole 16 bytes): one 16-byte
-// piece of bf16, or one of each half of an fp32 row, so that neighbouring threads'
-// accesses stay neighbours.  Otherwise elements tid, tid + threads, ...
+// With z in 8 bits too a row costs its threads more instructions, and the kernel is bound by
+// issuing them: twice the elements a thread halve what is once a row (the reductions, the
+// ring, addresses) for bf16.
+template <typename T> constexpr int RE8 = sizeof(T) == 2 ? 16 : RE;
+
+// A thread's 2 NP elements of a row.  WIDE (rows of whole 16 bytes): one 16-byte
+// piece of bf16, or one of each half of an fp32 row (or of a bf16 row where there are
+// 16 elements), so that neighbouring threads' accesses stay neighbours.  Otherwise
+// elements tid, tid + threads, ...
 template <typename T>
 __device__ __forceinline__ int part_of(int half) { return (threadIdx.x + half * blockDim.x) * (16 / (int)sizeof(T)); }
-template <typename T, bool WIDE>
-__device__ __forceinline__ void take(const T* p, int d, f2 (&v)[RP]) {
+template <typename T, bool WIDE, int NP>
+__device__ __forceinline__ void take(const T* p, int d, f2 (&v)[NP]) {
+    constexpr int V = 16 / sizeof(T);
     if constexpr (!WIDE) {
-        float f[RE];
+        float f[2 * NP];
 #pragma unroll
-        for (int j = 0; j < RE; ++j) {
+        for (int j = 0; j < 2 * NP; ++j) {
             const int c = threadIdx.x + j * blockDim.x;
             f[j] = c < d ? to_f<T>(p[c]) : 0.f;
         }
 #pragma unroll
-        for (int i = 0; i < RP; ++i) v[i] = pk(f[2 * i], f[2 * i + 1]);
-    } else if constexpr (sizeof(T) == 2) {
+        for (int i = 0; i < NP; ++i) v[i] = pk(f[2 * i], f[2 * i + 1]);
+    } else if constexpr (sizeof(T) == 2 && 2 * NP == V) {
         // threads past the row's end read its last elements; sums and stores leave them out
-        const uint4 u = *reinterpret_cast<const uint4*>(p + min((int)threadIdx.x * RE, d - RE));
+        const uint4 u = *reinterpret_cast<const uint4*>(p + min((int)threadIdx.x * V, d - V));
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-        for (int i = 0; i < RP; ++i) v[i] = pk(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+        for (int i = 0; i < NP; ++i) v[i] = pk(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
     } else {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < 2 * NP / V; ++h) {
             const int c = part_of<T>(h);
-            const float4 f = c < d ? *reinterpret_cast<const float4*>(p + c) : make_float4(0.f, 0.f, 0.f, 0.f);
-            v[2 * h] = pk(f.x, f.y);
-            v[2 * h + 1] = pk(f.z, f.w);
+            const uint4 u = c < d ? *reinterpret_cast<const uint4*>(p + c) : make_uint4(0, 0, 0, 0);
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int i = 0; i < V / 2; ++i) {
+                if constexpr (sizeof(T) == 2)
+                    v[h * V / 2 + i] = pk(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+                else v[h * V / 2 + i] = pk(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+            }
         }
     }
 }
 // This thread's share of a sum: its own, or none where it has read again what belongs
 // to others (other shares past the end are zeros).  Chosen, not multiplied by 0: the
 // elements read again may be infinite, or their squares.
-template <typename T, bool WIDE>
-__device__ __forceinline__ bool live(int d) { return !WIDE || sizeof(T) == 4 || (int)threadIdx.x * RE < d; }
-template <typename T, bool WIDE>
-__device__ __forceinline__ void give(T* p, int d, const f2 (&v)[RP]) {
+template <typename T, bool WIDE, int NP = RP>
+__device__ __forceinline__ bool live(int d) {
+    constexpr int V = 16 / sizeof(T);
+    return !WIDE || sizeof(T) == 4 || 2 * NP != V || (int)threadIdx.x * V < d;
+}
+template <typename T, bool WIDE, int NP>
+__device__ __forceinline__ void give(T* p, int d, const f2 (&v)[NP]) {
     if constexpr (!WIDE) {
 #pragma unroll
-        for (int i = 0; i < RP; ++i) {
+        for (int i = 0; i < NP; ++i) {
             float lo, hi;
             unpk(v[i], lo, hi);
             const int c = threadIdx.x + 2 * i * blockDim.x;
@@ -263,7 +278,7 @@ __device__ __forceinline__ void give(T* p, int d, const f2 (&v)[RP]) {
     } else {
         constexpr int V = 16 / sizeof(T);
 #pragma unroll
-        for (int h = 0; h < RE / V; ++h) {
+        for (int h = 0; h < 2 * NP / V; ++h) {
             const int c = part_of<T>(h);
             float f[V];
 #pragma unroll
@@ -273,11 +288,11 @@ __device__ __forceinline__ void give(T* p, int d, const f2 (&v)[RP]) {
     }
 }
 // in 8 bits, by the same split
-template <typename T>
-__device__ __forceinline__ void give_mx8(uint8_t* codes, uint8_t* scales, int d, const f2 (&v)[RP]) {
+template <typename T, int NP>
+__device__ __forceinline__ void give_mx8(uint8_t* codes, uint8_t* scales, int d, const f2 (&v)[NP]) {
     constexpr int V = 16 / sizeof(T);
 #pragma unroll
-    for (int h = 0; h < RE / V; ++h) {
+    for (int h = 0; h < 2 * NP / V; ++h) {
         float f[V];
 #pragma unroll
         for (int j = 0; j < V / 2; ++j) unpk(v[h * V / 2 + j], f[2 * j], f[2 * j + 1]);
@@ -285,26 +300,28 @@ __device__ __forceinline__ void give_mx8(uint8_t* codes, uint8_t* scales, int d,
     }
 }
 // the fp32 channel vector's share that goes with it
-template <typename T, bool WIDE>
-__device__ __forceinline__ void channel(const float* p, int d, f2 (&v)[RP]) {
+template <typename T, bool WIDE, int NP>
+__device__ __forceinline__ void channel(const float* p, int d, f2 (&v)[NP]) {
     constexpr int V = WIDE ? 16 / sizeof(T) : 1;
-    float f[RE];
+    float f[2 * NP];
 #pragma unroll
-    for (int j = 0; j < RE; ++j) {
+    for (int j = 0; j < 2 * NP; ++j) {
         const int c = WIDE ? part_of<T>(j / V) + j % V : threadIdx.x + j * blockDim.x;
         f[j] = c < d ? __ldg(p + c) : 0.f;
     }
 #pragma unroll
-    for (int i = 0; i < RP; ++i) v[i] = pk(f[2 * i], f[2 * i + 1]);
+    for (int i = 0; i < NP; ++i) v[i] = pk(f[2 * i], f[2 * i + 1]);
 }
-__device__ __forceinline__ void fill(f2 (&v)[RP], float x) {
+template <int NP>
+__device__ __forceinline__ void fill(f2 (&v)[NP], float x) {
 #pragma unroll
-    for (int i = 0; i < RP; ++i) v[i] = both(x);
+    for (int i = 0; i < NP; ++i) v[i] = both(x);
 }
-__device__ __forceinline__ float dot2(const f2 (&a)[RP], const f2 (&b)[RP]) {
+template <int NP>
+__device__ __forceinline__ float dot2(const f2 (&a)[NP], const f2 (&b)[NP]) {
     f2 s = a[0] * b[0];
 #pragma unroll
-    for (int i = 1; i < RP; ++i) s = fma2(a[i], b[i], s);
+    for (int i = 1; i < NP; ++i) s = fma2(a[i], b[i], s);
     return sum2(s);
 }
 
@@ -435,23 +452,28 @@ template <bool WIDE> struct RowRing : RingCursor {
 // Backwards of 513-768 threads have an SM to themselves, but were cut to 40 registers with
 // spills for a second CTA (16384 x 5120 bf16, addition 170 us, entering 147; 135 and 125).
 template <bool WIDE, int FORM, int MAXT> constexpr int FWD_CTAS = !WIDE && FORM == FORM_ENTER && MAXT == 512 ? 3 : 0;
+// With 16 elements a thread both norms want about 100 registers, where the compiler aimed
+// at 64 and spilled: two CTAs of 256 threads are what the plan counts on.
+template <int FORM, int MAXT> constexpr int FWD8_CTAS = FORM == FORM_BOTH || FORM == FORM_ANY ? (MAXT == 256 ? 2 : 1) : 0;
 template <int FORM, int MAXT> constexpr int BWD_CTAS = (FORM == FORM_ADD || FORM == FORM_ENTER) && MAXT == 768 ? 1 : 0;
 
 // in: x, u (leave), gate (full)
 template <typename T, bool WIDE, int FORM, int MAXT, bool Q8>
-__global__ void __launch_bounds__(MAXT, (FWD_CTAS<WIDE, FORM, MAXT>)) block_norm_ring_kernel(const __grid_constant__ RingArgs a) {
+__global__ void __launch_bounds__(MAXT, (Q8 && sizeof(T) == 2 ? FWD8_CTAS<FORM, MAXT> : FWD_CTAS<WIDE, FORM, MAXT>))
+block_norm_ring_kernel(const __grid_constant__ RingArgs a) {
     __shared__ float buf[2][32];
     NORM_RING_SETUP();
     const Parts p = parts_of<FORM>(n);
     const int gmode = FORM == FORM_ADD || FORM == FORM_ENTER ? MOE_GATE_NONE : n.gmode;
-    const bool on = live<T, WIDE>(d);
-    f2 wq[RP], wz[RP];                     // g w_post, w_pre
+    constexpr int NP = (Q8 ? RE8<T> : RE) / 2;
+    const bool on = live<T, WIDE, NP>(d);
+    f2 wq[NP], wz[NP];                     // g w_post, w_pre
     fill(wq, 1.f);
     if (p.post) channel<T, WIDE>(n.w_post, d, wq);
     if (gmode == MOE_GATE_CHANNEL) {
         channel<T, WIDE>(static_cast<const float*>(n.gate), d, wz);
 #pragma unroll
-        for (int i = 0; i < RP; ++i) wq[i] = wq[i] * wz[i];
+        for (int i = 0; i < NP; ++i) wq[i] = wq[i] * wz[i];
     }
     if (p.enter) channel<T, WIDE>(n.w_pre, d, wz);
     // Two norms alternate their buffers, entering alone alternates from row to row, so a
@@ -465,23 +487,23 @@ __global__ void __launch_bounds__(MAXT, (FWD_CTAS<WIDE, FORM, MAXT>)) block_norm
         const size_t o = (size_t)t * d;
         float tok = n.ob;
         if (gmode == MOE_GATE_TOKEN) tok *= __ldg(static_cast<const float*>(n.gate) + t);
-        f2 y[RP], u[RP];
+        f2 y[NP], u[NP];
         take<T, WIDE>(in(0), d, y);
         if (p.leave) {
             take<T, WIDE>(in(1), d, u);
             const float s = p.post && on ? dot2(u, u) : 0.f;
             if (p.full) {
-                f2 g[RP];
+                f2 g[NP];
                 take<T, WIDE>(in(2), d, g);
 #pragma unroll
-                for (int i = 0; i < RP; ++i) u[i] = u[i] * g[i];
+                for (int i = 0; i < NP; ++i) u[i] = u[i] * g[i];
             }
             if (p.post) {
                 tok *= rsqrtf(row_sum(s, buf[0]) * invd + n.eps);
             }
             const f2 c = both(tok), ra = both(n.ra);
 #pragma unroll
-            for (int i = 0; i < RP; ++i) y[i] = fma2(c * wq[i], u[i], ra * y[i]);
+            for (int i = 0; i < NP; ++i) y[i] = fma2(c * wq[i], u[i], ra * y[i]);
             give<T, WIDE>(static_cast<T*>(n.x_out) + o, d, y);
         }
         if (p.enter) {
@@ -489,7 +511,7 @@ __global__ void __launch_bounds__(MAXT, (FWD_CTAS<WIDE, FORM, MAXT>)) block_norm
             ring.wait_next(a, t);
             const f2 r = both(rsqrtf(row_sum(s, buf[p.leave ? 1 : par]) * invd + n.eps));
 #pragma unroll
-            for (int i = 0; i < RP; ++i) y[i] = y[i] * (r * wz[i]);
+            for (int i = 0; i < NP; ++i) y[i] = y[i] * (r * wz[i]);
             if constexpr (Q8) give_mx8<T>(n.codes + o, n.scales + (size_t)t * n.pitch, d, y);
             if (!Q8 || n.z) give<T, WIDE>(static_cast<T*>(n.z) + o, d, y);
         }
@@ -531,10 +553,10 @@ bool ring_pays(const moe_norm_config& c, bool backward) {
     return c.d >= 1024 || (c.d >= 128 && n >= (4 << 20));
 }
 struct RingPlan { int threads, stages, grid; size_t smem; };
-RingPlan ring_plan(const moe_norm_config& c, int nin, int regs, bool backward) {
+RingPlan ring_plan(const moe_norm_config& c, int nin, int regs, bool backward, int re = RE) {
     RingPlan p = {0, 0, 0, 0};
     const int es = c.dtype == MOE_DTYPE_BF16 ? 2 : 4;
-    p.threads = ((c.d + RE - 1) / RE + 31) / 32 * 32;
+    p.threads = ((c.d + re - 1) / re + 31) / 32 * 32;
     if (p.threads > 1024 || !ring_pays(c, backward)) return p;
     const int stage = nin * (int)row_pitch(c.d * es);
     // CTAs an SM by registers and threads, fewer where they would not have three stages
@@ -560,6 +582,8 @@ int launch_fwd_ring_t(const RingPlan& p, const RingArgs& r, cudaStream_t st) {
 }
 template <typename T, bool WIDE, int FORM, bool Q8>
 int launch_fwd_ring_f(const RingPlan& p, const RingArgs& r, cudaStream_t st) {
+    if constexpr (Q8 && sizeof(T) == 2)
+        if (p.threads <= 256) return launch_fwd_ring_t<T, WIDE, FORM, 256, Q8>(p, r, st);
     return p.threads <= 512 ? launch_fwd_ring_t<T, WIDE, FORM, 512, Q8>(p, r, st)
                             : launch_fwd_ring_t<T, WIDE, FORM, 1024, Q8>(p, r, st);
 }
@@ -574,8 +598,9 @@ int launch_fwd_ring(const RingPlan& p, const RingArgs& r, cudaStream_t st) {
 }
 template <typename T, int VEC, bool Q8 = false>
 int launch_fwd(const moe_norm_config& c, const NormArgs& a, cudaStream_t st) {
-    const int light = Q8 && c.d > 4096 ? 48 : 40;            // registers without a norm or gate of u
-    const RingPlan p = ring_plan(c, fwd_inputs(c), c.post_norm || c.gate != MOE_GATE_NONE ? 64 : light, false);
+    const bool heavy = c.post_norm || c.gate != MOE_GATE_NONE;
+    const int regs = Q8 ? (sizeof(T) == 2 ? (heavy ? 96 : 64) : heavy ? 64 : 48) : heavy ? 64 : 40;
+    const RingPlan p = ring_plan(c, fwd_inputs(c), regs, false, Q8 ? RE8<T> : RE);
     if (p.stages) {
         RingArgs r = {};
         r.n = a;
