@@ -266,3 +266,43 @@ def test_repeats_are_identical_on_other_streams_and_in_graphs():
     graph.replay()
     c = m.out.dequantize(torch.float32).clone()
     assert torch.equal(c, m.forward(x, o, w).dequantize(torch.float32)) and not torch.equal(a, c)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows", [40, 1000])
+def test_product_nan_rows_in_8_bits(rows):
+    """A row that is no number makes its own blocks so, and nothing else."""
+    g = torch.Generator().manual_seed(1)
+    x, W = torch.randn(rows, 96, generator=g), torch.randn(2, 96, 160, generator=g)
+    m = moe.MX8Product(moe.MX8ProductConfig(rows=rows, K=96, N=160, E=2, act=moe.MX8_ACT_SILU, out_dtype=moe.MX8))
+    w, o = moe.mx8_quantize_weight(W.cuda()), torch.tensor([0, 7, rows], dtype=torch.int32).cuda()
+    clean = m.forward(moe.mx8_quantize(x.cuda()), o, w).dequantize(torch.float32)
+    x[6, 1], x[7, 95] = float("nan"), float("inf")
+    out = m.forward(moe.mx8_quantize(x.cuda()), o, w)
+    got = out.dequantize(torch.float32)
+    assert (out.scales[6:8, :5] == 255).all() and (out.codes[6:8] == 0).all()
+    assert got[6:8].isnan().all()
+    keep = [i for i in range(rows) if i not in (6, 7)]
+    assert torch.equal(got[keep], clean[keep])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("act", ["silu", "swiglu"])
+@pytest.mark.parametrize("out", ["fp32", "bf16"])
+@pytest.mark.parametrize("rows", [64, 700])
+def test_activations_far_from_zero(act, out, rows):
+    """Gates of up to some thousands, where e^-z leaves fp32's range on either side."""
+    K, N = 64, 64
+    g = torch.Generator().manual_seed(5)
+    x = torch.randn(rows, K, generator=g) * torch.exp2(torch.randint(-8, 9, (rows, 1), generator=g).float())
+    W, Wg = torch.randn(1, K, N, generator=g), torch.randn(1, K, N, generator=g)
+    code, dt = OUTS[out]
+    m = moe.MX8Product(moe.MX8ProductConfig(rows=rows, K=K, N=N, E=1, act=ACTS.index(act), out_dtype=code))
+    o = torch.tensor([0, rows], dtype=torch.int32).cuda()
+    got = m.forward(moe.mx8_quantize(x.cuda()), o, moe.mx8_quantize_weight(W.cuda()),
+                    moe.mx8_quantize_weight(Wg.cuda()) if act == "swiglu" else None).cpu().double()
+    want, terms = product64(x, W, Wg, [0, rows], act)
+    assert want.abs().max() > 1000 and torch.isfinite(got).all()
+    # the quick form (bf16) has e^-z off by up to |z| 2^-24 of it, where |z| stays below 128 (0 beyond)
+    tol = torch.finfo(dt).eps / 2 * (1 + 2.0 ** -6) * want.abs() + terms + (128 * 2.0 ** -24 * want.abs() if out == "bf16" else 0)
+    assert ((got - want).abs() <= tol).all(), ((got - want).abs() / tol.clamp(min=1e-300)).max()

@@ -80,8 +80,12 @@ constexpr int SPLIT_MIN_WAVES = 16;   // "many waves of tiles": a launch this lo
 
 enum Epi { EPI_STORE = 0, EPI_SILU_FWD = 1, EPI_SWIGLU_FWD = 2, EPI_SILU_BWD = 3, EPI_SWIGLU_BWD = 4 };
 // With h (g, u) kept in 8 bits the same four read and write it so (kernels of KEEP8; EPI_STORE
-// is the other kernels'): the forward writes codes in h's place, the backward forms
-// the activation again from them and writes it for the weight gradient of W_down.
+// is the other kernels'): the forward writes codes in h's place, the backward forms the
+// activation again from them and writes it for the weight gradient of W_down.  A lane holds
+// 32 columns of a row at a time, which are a block.  32768 rows of 8 experts, d = 2048,
+// f = 4096, SwiGLU: forward 1026 us and backward 2112, with h and act in 16 bits 1066 and
+// 2152; 4096 rows of 4, 1024 x 2048, SiLU: 42 and 78 against 41 and 68, as dW_down waits for
+// the activation there and joins the second launch.
 enum Sched { SCHED_ROWS = 0, SCHED_KSEG = 1 };
 
 // One GEMM problem of a launch.  A launch runs up to MAX_PROBLEMS independent

@@ -37,6 +37,14 @@
 //
 // Tensor memory: two accumulators of 256 columns that overlap in 128, and buffers of 16
 // columns of scales.
+//
+// What bounds it.  Large products: the power cap.  32768 rows of 8 experts, K = 4096,
+// N = 14336, SwiGLU: 2480 us, 3.1 PFLOP/s at 1440 MHz and 1.37 kW, where the tensor pipe is
+// active 0.82 of the time; with operands of zeros, which draw less, the same launch holds
+// 2070 MHz and 4.0 PFLOP/s (1925 us).  There the MMAs alone take 1646 us, the loads add
+// 4 %, the stores 4 %, the hand-over of the accumulator 2 %, the scales nothing.  Few rows:
+// HBM, 6.8 TB/s of W (64 rows of 8 experts, the same product: 143 us).  In between the 256
+// rows of a tile that a segment does not fill (2048 rows: 232 us).
 #include <algorithm>
 #include <cstring>
 
