@@ -605,7 +605,8 @@ MOE_API int moe_mx8_grouped_product(const moe_mx8_product_config* cfg, const voi
  *   dW_down = act^T dy, dh = dact silu'(h^) (dg, du likewise), dW_up, dW_gate, dx as
  * moe_grouped_ffn_backward does from these.
  *   h_codes [nh,rows_cap,f], h_scales [nh,rows_cap,P], P = moe_mx8_scale_pitch(f); the
- *   other arguments as there.                                                */
+ *   other arguments as there.  h_codes, act and dh (in moe_backward_mx8: ws) are 32-byte
+ *   aligned.                                                                 */
 MOE_API int moe_grouped_ffn_mx8(const moe_config* cfg, const void* x_perm, const int32_t* offsets,
                                 const void* W_up, const void* W_gate, const void* W_down,
                                 void* h_codes, void* h_scales, void* act, void* y_perm, void* ws,

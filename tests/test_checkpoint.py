@@ -86,6 +86,19 @@ def test_refusals():
             args = [p] * 14
             args[i] = v
             assert lib.moe_grouped_ffn_backward_mx8(ctypes.byref(cfg), *args, p, None) == moe.ERR_INVALID_ARG, i
+    half = ctypes.c_void_p(0x10010)                          # 16-byte aligned
+    for i in (5, 7):
+        args = [p] * 9
+        args[i] = half
+        assert lib.moe_grouped_ffn_mx8(ctypes.byref(cfg), *args, p, None) == moe.ERR_INVALID_ARG, i
+    for i in (5, 7, 9):
+        args = [p] * 14
+        args[i] = half
+        assert lib.moe_grouped_ffn_backward_mx8(ctypes.byref(cfg), *args, p, None) == moe.ERR_INVALID_ARG, i
+    for i in (12, 14, 25):
+        args = [p] * 26
+        args[i] = half
+        assert lib.moe_backward_mx8(ctypes.byref(cfg), *args, None) == moe.ERR_INVALID_ARG, i
     for c in (moe.MoEConfig(T=8, d=128, f=128, E=2, k=1, dtype=moe.F32),
               moe.MoEConfig(T=8, d=128, f=128, E=2, k=1, f_shared=128)):
         assert lib.moe_grouped_ffn_mx8(ctypes.byref(c), *[p] * 10, None) == moe.ERR_UNSUPPORTED

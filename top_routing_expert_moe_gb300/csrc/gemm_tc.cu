@@ -102,8 +102,7 @@ struct TcProblem {
     __nv_bfloat16* out2;
     const __nv_bfloat16* in0;
     const __nv_bfloat16* in1;
-    CUtensorMap tmC[2];     // KEEP8: codes of h (or g, u), boxes of 32 rows x 32 columns, 32-byte swizzle
-    uint8_t* codes[2];
+    uint8_t* codes[2];      // KEEP8: codes of h (or g, u)
     uint8_t* scales[2];
     int sc_pitch;
     long long out_estride;  // SCHED_KSEG: elements between experts' outputs
@@ -376,10 +375,6 @@ __global__ void __launch_bounds__(NTHREADS, 1) tc_grouped_gemm_kernel(const __gr
             for (int i = 0; i < 3; ++i)
                 if (outs[i])
                     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&q.tmO[i])) : "memory");
-            if constexpr (KEEP8)
-                if (q.epi == EPI_SILU_FWD || q.epi == EPI_SWIGLU_FWD)
-                    for (int i = 0; i < 1 + q.dual; ++i)
-                        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&q.tmC[i])) : "memory");
         }
         int it = 0;
         bool ok = start_live;
@@ -540,27 +535,24 @@ __global__ void __launch_bounds__(NTHREADS, 1) tc_grouped_gemm_kernel(const __gr
             }
             ++nst;
         };
-        // 32 columns of this lane's row in 8 bits: a block
-        // (its scale byte is returned)
-        auto put8 = [&](const CUtensorMap* m, const float* v, int c0, int c1) {
-            uint8_t* buf = stg + (nst & 1) * 2048;
-            if (nst >= 2) {
-                if (lane == 0) bulk_wait_read<1>();
-                __syncwarp();
+        // KEEP8: 32 columns of this lane's row, straight from its registers.  A box through
+        // shared memory waits for the TMA unit, whose queue holds the producer's loads: with
+        // three boxes a chunk the backward's first launch (32768 x 4096 x 2048) took 411 us.
+        auto keep16 = [&](__nv_bfloat16* p, const float* v) {
+            uint32_t w[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                __nv_bfloat162 b2 = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+                w[i] = *reinterpret_cast<uint32_t*>(&b2);
             }
+            store32(p, w);
+            store32(p + 16, w + 8);
+        };
+        auto keep8 = [&](uint8_t* p, const float* v) {      // a block: its scale byte is returned
             const uint32_t s = mx8_scale_byte(amax_bits<32>(v));
             uint32_t w[8];
             mx8_codes<32>(v, s, w);
-            const int x = ((lane >> 2) & 1) << 4;         // 32-byte swizzle
-            *reinterpret_cast<uint4*>(buf + lane * 32 + x) = make_uint4(w[0], w[1], w[2], w[3]);
-            *reinterpret_cast<uint4*>(buf + lane * 32 + (x ^ 16)) = make_uint4(w[4], w[5], w[6], w[7]);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-                tma_store3(m, smem_u32(buf), c0, c1, 0);
-                bulk_commit();
-            }
-            ++nst;
+            store32(p, w);
             return s;
         };
         int tcount = 0;
@@ -593,7 +585,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) tc_grouped_gemm_kernel(const __gr
             };
             // The same of what is kept in 8 bits.  The scale bytes of this warp's two or four
             // chunks are neighbours: they are read, or written, as one word a row.
-            uint4 nxt8[2][2];
+            uint32_t nxt8[2][8];
             uint32_t sw[2] = {0, 0};
             const bool four = c_hi - c_lo == 4;
             const long long sat = row * q.sc_pitch + t.n0 / 32 + c_lo;
@@ -601,11 +593,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) tc_grouped_gemm_kernel(const __gr
                 const long long at = row * q.ldo + t.n0 + c * 32;
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
-                    if (i < n_in) {
-                        const uint4* p = reinterpret_cast<const uint4*>(q.codes[i] + at);
-                        nxt8[i][0] = p[0];
-                        nxt8[i][1] = p[1];
-                    }
+                    if (i < n_in) load32(q.codes[i] + at, nxt8[i]);
             };
             if constexpr (KEEP8) {
                 if (valid && n_in) {
@@ -634,31 +622,27 @@ __global__ void __launch_bounds__(NTHREADS, 1) tc_grouped_gemm_kernel(const __gr
                 float v[32];
                 if constexpr (KEEP8) {
                     tmem_ld32(taddr + c * 32, v);
+                    const long long at = row * q.ldo + bcol;
                     if (q.epi == EPI_SWIGLU_FWD) {
                         float u[32];
                         tmem_ld32(taddr + 128 + c * 32, u);
                         tmem_wait_ld();
-                        sw[0] |= put8(&q.tmC[0], v, bcol, brow) << (8 * (c - c_lo));
-                        sw[1] |= put8(&q.tmC[1], u, bcol, brow) << (8 * (c - c_lo));
+                        sw[0] |= keep8(q.codes[0] + at, v) << (8 * (c - c_lo));
+                        sw[1] |= keep8(q.codes[1] + at, u) << (8 * (c - c_lo));
 #pragma unroll
                         for (int i = 0; i < 32; ++i) v[i] = silu_fast(v[i]) * u[i];
-                        put(&q.tmO[0], v, bcol, brow, 0);
+                        keep16(q.out0 + at, v);
                     } else if (q.epi == EPI_SILU_FWD) {
                         tmem_wait_ld();
-                        sw[0] |= put8(&q.tmC[0], v, bcol, brow) << (8 * (c - c_lo));
+                        sw[0] |= keep8(q.codes[0] + at, v) << (8 * (c - c_lo));
 #pragma unroll
                         for (int i = 0; i < 32; ++i) v[i] = silu_fast(v[i]);
-                        put(&q.tmO[0], v, bcol, brow, 0);
+                        keep16(q.out0 + at, v);
                     } else {
                         // v = dact; dh (or dg, du) and the activation at the kept values
                         uint32_t w[2][8];
 #pragma unroll
-                        for (int i = 0; i < 2; ++i)
-#pragma unroll
-                            for (int j = 0; j < 2; ++j) {
-                                const uint4 x = nxt8[i][j];
-                                w[i][4 * j] = x.x; w[i][4 * j + 1] = x.y; w[i][4 * j + 2] = x.z; w[i][4 * j + 3] = x.w;
-                            }
+                        for (int j = 0; j < 8; ++j) { w[0][j] = nxt8[0][j]; w[1][j] = nxt8[1][j]; }
                         const int sh = 8 * (c - c_lo);
                         const float sc0 = mx8_scale_value(sw[0] >> sh & 255u), sc1 = mx8_scale_value(sw[1] >> sh & 255u);
                         if (c + 1 < c_hi) fetch8(c + 1);
@@ -679,9 +663,9 @@ __global__ void __launch_bounds__(NTHREADS, 1) tc_grouped_gemm_kernel(const __gr
                                 v[i] *= z * sg;
                             }
                         }
-                        put(&q.tmO[0], o, bcol, brow, 0);                       // dh, or dg
-                        if (n_in == 2) put(&q.tmO[1], v, bcol, brow, 0);        // du
-                        put(&q.tmO[2], a, bcol, brow, 0);
+                        keep16(q.out0 + at, o);                       // dh, or dg
+                        if (n_in == 2) keep16(q.out1 + at, v);        // du
+                        keep16(q.out2 + at, a);
                     }
                     continue;
                 }
@@ -818,18 +802,6 @@ int make_map_nd(CUtensorMap* m, const void* ptr, int rank, const uint64_t* dims,
     CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(ptr), d, st,
                     b, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? MOE_OK : MOE_ERR_CUDA;
-}
-
-// [rows, cols] bytes, boxes of 32 rows x 32 columns, 32-byte swizzle
-int encode_u8_map(CUtensorMap* m, const void* ptr, int cols, int64_t rows) {
-    EncodeTiledFn fn = encode_fn();
-    if (!fn) return MOE_ERR_CUDA;
-    const cuuint64_t d[3] = {(cuuint64_t)cols, (cuuint64_t)rows, 1}, st[2] = {(cuuint64_t)cols, (cuuint64_t)cols * rows};
-    const cuuint32_t b[3] = {32, 32, 1}, es[3] = {1, 1, 1};
-    const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(ptr), d, st, b, es,
-                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_32B,
-                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? MOE_OK : MOE_ERR_CUDA;
 }
 
@@ -1155,15 +1127,13 @@ int dgrad1_problem(TcProblem& q, const moe_config& c, const Family& F, const voi
     return out_maps_rows(q, F.rows);
 }
 
-// codes and scales of h [nh, rows, f] as a problem's outputs (or, its codes, inputs)
-int keep8_fields(TcProblem& q, const moe_config& c, const Family& F, void* codes, void* scales) {
+// codes and scales of h [nh, rows, f] as a problem's outputs or inputs
+void keep8_fields(TcProblem& q, const moe_config& c, const Family& F, void* codes, void* scales) {
     q.sc_pitch = (int)mx8_pitch(F.f);
     for (int i = 0; i < (c.ffn == MOE_FFN_SWIGLU ? 2 : 1); ++i) {
         q.codes[i] = static_cast<uint8_t*>(codes) + (int64_t)i * F.rows * F.f;
         q.scales[i] = static_cast<uint8_t*>(scales) + (int64_t)i * F.rows * q.sc_pitch;
-        MOE_TRY(encode_u8_map(&q.tmC[i], q.codes[i], F.f, F.rows));
     }
-    return MOE_OK;
 }
 
 // weight gradients: dW_down = act^T dy; dW_up = x^T dh (du); dW_gate = x^T dg
@@ -1260,7 +1230,7 @@ int tc_ffn_forward_keep8(const moe_config& c, const void* x_perm, const int32_t*
     const Family R = routed_family(c, x_perm, W_up, W_gate, W_down);
     TcProblem q = new_problem();
     MOE_TRY(gemm1_problem(q, c, R, nullptr, act));
-    MOE_TRY(keep8_fields(q, c, R, h_codes, h_scales));
+    keep8_fields(q, c, R, h_codes, h_scales);
     MOE_TRY(launch_tc<true>(c, offsets, &q, 1, st));
     q = new_problem();
     MOE_TRY(gemm2_problem(q, c, R, act, y_perm));
@@ -1279,7 +1249,7 @@ int tc_ffn_backward_keep8(const moe_config& c, const void* x_perm, const int32_t
     TcProblem q[MAX_PROBLEMS];
     q[0] = new_problem();
     MOE_TRY(dgrad2_problem(q[0], c, R, dy_perm, R.rows, nullptr, dh, act));
-    MOE_TRY(keep8_fields(q[0], c, R, const_cast<void*>(h_codes), const_cast<void*>(h_scales)));
+    keep8_fields(q[0], c, R, const_cast<void*>(h_codes), const_cast<void*>(h_scales));
     MOE_TRY(launch_tc<true>(c, offsets, q, 1, st));
     // launch 2: dW_down = act^T dy  ||  dW_up = x^T dh (du)  ||  [dW_gate = x^T dg]  ||  dx
     const bf* dh0 = static_cast<const bf*>(dh);

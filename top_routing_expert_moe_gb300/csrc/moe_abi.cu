@@ -74,6 +74,7 @@ namespace {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool ok_ptr(const void* p) { return p != nullptr && aligned16(p); }
+bool ok_ptr32(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 bool ok_opt(const void* p) { return p == nullptr || aligned16(p); }
 size_t esize(const moe_config& c) { return c.dtype == MOE_DTYPE_BF16 ? 2 : 4; }
 int nh_of(const moe_config& c) { return c.ffn == MOE_FFN_SWIGLU ? 2 : 1; }
@@ -353,7 +354,7 @@ int moe_grouped_ffn_mx8(const moe_config* c, const void* x_perm, const int32_t* 
     if (r) return r;
     const bool sw = c->ffn == MOE_FFN_SWIGLU;
     if (!ok_ptr(x_perm) || !ok_ptr(offsets) || !ok_ptr(W_up) || !ok_ptr(W_down) ||
-        (sw ? !ok_ptr(W_gate) : !ok_opt(W_gate)) || !ok_ptr(h_codes) || !ok_ptr(h_scales) || !ok_ptr(act) ||
+        (sw ? !ok_ptr(W_gate) : !ok_opt(W_gate)) || !ok_ptr32(h_codes) || !ok_ptr(h_scales) || !ok_ptr32(act) ||
         !ok_ptr(y_perm) || !ok_opt(ws))
         return MOE_ERR_INVALID_ARG;
     if (ffn_ws_bytes(*c) > 0 && !ws) return MOE_ERR_INVALID_ARG;
@@ -370,8 +371,8 @@ int moe_grouped_ffn_backward_mx8(const moe_config* c, const void* x_perm, const 
     if (r) return r;
     const bool sw = c->ffn == MOE_FFN_SWIGLU;
     if (!ok_ptr(x_perm) || !ok_ptr(offsets) || !ok_ptr(W_up) || !ok_ptr(W_down) ||
-        (sw ? !ok_ptr(W_gate) : !ok_opt(W_gate)) || !ok_ptr(h_codes) || !ok_ptr(h_scales) || !ok_ptr(act) ||
-        !ok_ptr(dy_perm) || !ok_ptr(dh) || !ok_ptr(dx_perm) || !ok_ptr(dW_up) ||
+        (sw ? !ok_ptr(W_gate) : !ok_opt(W_gate)) || !ok_ptr32(h_codes) || !ok_ptr(h_scales) || !ok_ptr32(act) ||
+        !ok_ptr(dy_perm) || !ok_ptr32(dh) || !ok_ptr(dx_perm) || !ok_ptr(dW_up) ||
         (sw ? !ok_ptr(dW_gate) : !ok_opt(dW_gate)) || !ok_ptr(dW_down) || !ok_opt(ws))
         return MOE_ERR_INVALID_ARG;
     if (ffn_ws_bytes(*c) > 0 && !ws) return MOE_ERR_INVALID_ARG;
@@ -404,6 +405,8 @@ int moe_backward_mx8(const moe_config* c, const void* x, const void* W_r, const 
                      const void* dout, void* dx, void* dW_r, float* dbias, void* dW_up, void* dW_gate,
                      void* dW_down, void* ws, moe_stream_t stream) {
     if (const int r = keep8_config(c)) return r;
+    // (checked before anything is launched)
+    if (!ok_ptr32(h_codes) || !ok_ptr(h_scales) || !ok_ptr32(act) || !ok_ptr32(ws)) return MOE_ERR_INVALID_ARG;
     return whole_backward(c, x, W_r, logits, topk_idx, gate, slot_of, perm_token, offsets, nullptr, dout,
                           y_perm, stats, dlogits_aux, dx, dW_r, dbias, ws, stream,
                           [&](const void* dy, void* dh, void* dxp, const moe_shared_ffn*, void* rest) {
