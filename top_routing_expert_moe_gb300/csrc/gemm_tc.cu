@@ -83,9 +83,11 @@ enum Epi { EPI_STORE = 0, EPI_SILU_FWD = 1, EPI_SWIGLU_FWD = 2, EPI_SILU_BWD = 3
 // is the other kernels'): the forward writes codes in h's place, the backward forms the
 // activation again from them and writes it for the weight gradient of W_down.  A lane holds
 // 32 columns of a row at a time, which are a block.  32768 rows of 8 experts, d = 2048,
-// f = 4096, SwiGLU: forward 1026 us and backward 2112, with h and act in 16 bits 1066 and
-// 2152; 4096 rows of 4, 1024 x 2048, SiLU: 42 and 78 against 41 and 68, as dW_down waits for
-// the activation there and joins the second launch.
+// f = 4096, SwiGLU: forward 1034 us and backward 2165, with h and act in 16 bits 1078 and
+// 2195; 4096 rows of 4, 1024 x 2048, SiLU: 41 and 74 against 41 and 68, as dW_down waits for
+// the activation there and joins the second launch.  The backward's first launch is bound by
+// what it reads and writes beside its operands (its tensor pipe is active 0.60 of the time,
+// 0.75 without its stores, and no more without its arithmetic).
 enum Sched { SCHED_ROWS = 0, SCHED_KSEG = 1 };
 
 // One GEMM problem of a launch.  A launch runs up to MAX_PROBLEMS independent
@@ -535,9 +537,9 @@ __global__ void __launch_bounds__(NTHREADS, 1) tc_grouped_gemm_kernel(const __gr
             }
             ++nst;
         };
-        // KEEP8: 32 columns of this lane's row, straight from its registers.  A box through
-        // shared memory waits for the TMA unit, whose queue holds the producer's loads: with
-        // three boxes a chunk the backward's first launch (32768 x 4096 x 2048) took 411 us.
+        // KEEP8: 32 columns of this lane's row, straight from its registers, as whole sectors.
+        // Through boxes, of which the backward has three a chunk, a small batch's backward
+        // took 77.4 us where this takes 74.1; the large one's is 1 % the other way.
         auto keep16 = [&](__nv_bfloat16* p, const float* v) {
             uint32_t w[16];
 #pragma unroll
