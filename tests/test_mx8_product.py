@@ -306,3 +306,27 @@ def test_activations_far_from_zero(act, out, rows):
     # the quick form (bf16) has e^-z off by up to |z| 2^-24 of it, where |z| stays below 128 (0 beyond)
     tol = torch.finfo(dt).eps / 2 * (1 + 2.0 ** -6) * want.abs() + terms + (128 * 2.0 ** -24 * want.abs() if out == "bf16" else 0)
     assert ((got - want).abs() <= tol).all(), ((got - want).abs() / tol.clamp(min=1e-300)).max()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("out,N", [("fp32", 72), ("bf16", 48), ("bf16", 40), ("mx8", 96)])
+@pytest.mark.parametrize("rows", [70, 700])
+def test_product_into_memory_of_16_byte_alignment(out, N, rows):
+    """An output that is no whole, aligned pieces of 32 bytes is stored in pieces of 16."""
+    K, E = 96, 2
+    g = torch.Generator().manual_seed(rows)
+    x = moe.mx8_quantize(torch.randn(rows, K, generator=g).cuda())
+    w = moe.mx8_quantize_weight(torch.randn(E, K, N, generator=g).cuda())
+    o = torch.tensor([0, 33, rows], dtype=torch.int32).cuda()
+    code, _ = OUTS[out]
+    m = moe.MX8Product(moe.MX8ProductConfig(rows=rows, K=K, N=N, E=E, out_dtype=code))
+    want = m.forward(x, o, w)
+    want = want.codes if out == "mx8" else want
+    es = want.element_size()
+    raw = torch.full((rows * N + 32 // es,), 7, dtype=want.dtype, device="cuda")
+    at = 16 // es                                          # 16 bytes on
+    got = raw[at:at + rows * N].view(rows, N)
+    assert got.data_ptr() % 32 == 16
+    moe.moe_mx8_grouped_product(m.cfg, x.codes, x.scales, o, w.codes, w.scales, None, None, got,
+                                m.out.scales if out == "mx8" else None)
+    assert torch.equal(got, want) and (raw[:at] == 7).all() and (raw[at + rows * N:] == 7).all()

@@ -12,15 +12,20 @@
 //                128 rows of x and its 128 rows of W (for SwiGLU the even CTA's are
 //                the gate's, the odd CTA's the up matrix's).
 //   warp 1       the even CTA's issues the block-scaled MMAs, 32 elements each.
-//   warps 2-9    epilogue: activation, rounding, 32-row boxes by TMA.
+//   warps 2-9    epilogue: activation, rounding, a lane's row in pieces of 32 bytes
+//                (fp32: 32-row boxes by TMA).
 //   warps 10-13  scales: rows' bytes to shared memory by cp.async, then to tensor memory.
 // A stage's four MMAs last 512 cycles, as the 4-bit kernel's do on twice the elements.
 //
 // Segments are not padded.  A tile starts at its segment's first row wherever that is (a
 // TMA box may start at any row); the rows past the segment's end that it then holds are
 // the next expert's, each row of a product depends on no other, and they are not stored:
-// a box that lies within the segment leaves by TMA, a box that the segment ends in by
-// plain stores of its rows.  For the same reason the scales of x are kept by rows and not
+// a lane of the epilogue holds columns of one row, and stores them or not, as whole sectors.
+// (Boxes through shared memory take a stage's room.  Without them, and with a sixth stage:
+// 1024 rows of 8 experts, 4096 -> 14336 SwiGLU in 8 bits, 156 us and 150; 2 rows of 2 of
+// them 43.9 and 42.8; 8192 rows, 14336 -> 4096, 332 and 325; the largest bf16 product 2518
+// and 2563.  fp32, four times the bytes, leaves by boxes: 32768 rows, 2048 -> 4096, silu,
+// 234 us, by lanes 260.)  For the same reason the scales of x are kept by rows and not
 // in the tensor cores' 128-row tiles, which would begin at other rows than a segment: the
 // scale warps form the tile (row r's four bytes as word r / 32 of lane r % 32) from 16
 // bytes a row, four stages' worth, in registers.
@@ -63,7 +68,6 @@ constexpr int A_BYTES = BM * BK;
 constexpr int NUM_EPI_WARPS = 8;
 constexpr int NUM_SF_WARPS = 4;            // one per lane quarter of tensor memory
 constexpr int NTHREADS = 64 + 32 * (NUM_EPI_WARPS + NUM_SF_WARPS);
-constexpr int STAGING_BYTES = NUM_EPI_WARPS * 4096;
 constexpr int CTRL_BYTES = 1024;
 constexpr int TMEM_COLS = 512;
 constexpr int ACC1 = 128;                  // second accumulator's first column (a pair's overlap in 128-255)
@@ -72,22 +76,23 @@ constexpr int SF_QUAD = BM * 16;           // scale bytes of a quad: of 128 rows
 constexpr int SF_AHEAD = 2, SF_SLOTS = SF_AHEAD + 1;     // in quads
 constexpr int RASTER_ROWS = 4096;          // rows of x that pass over an expert's weights together
 
-template <int CG> struct Ring {            // CG CTAs a tile: stages and their bytes per CTA
-    static constexpr int BN = 128 * CG;    // accumulator columns (SwiGLU: half gate, half up)
-    static constexpr int BYTES = A_BYTES + 128 * BK;
-    static constexpr int STAGES = 5;
-    static constexpr int SF_BUFS = STAGES;               // see the scale warps
-    static constexpr int SF_SLOT = 3 * SF_QUAD;          // x, and one or two row blocks of W
-    static constexpr int SMEM = 1024 + STAGES * BYTES + STAGING_BYTES + SF_SLOTS * SF_SLOT + CTRL_BYTES;
-};
-static_assert(Ring<1>::BYTES % 1024 == 0 && Ring<2>::BYTES % 1024 == 0, "128B swizzle atoms");
-static_assert(Ring<1>::SMEM <= 232448 && Ring<2>::SMEM <= 232448, "227 KB of dynamic shared memory");
-static_assert(SF_COL + Ring<2>::SF_BUFS * SF_COLS <= TMEM_COLS, "tensor memory");
-
 enum Out { OUT_F32, OUT_BF16, OUT_MX8 };
 
+template <int CG, int OT> struct Ring {    // CG CTAs a tile: stages and their bytes per CTA
+    static constexpr int BN = 128 * CG;    // accumulator columns (SwiGLU: half gate, half up)
+    static constexpr int BYTES = A_BYTES + 128 * BK;
+    static constexpr int STAGES = OT == OUT_F32 ? 5 : 6;
+    static constexpr int STAGING = OT == OUT_F32 ? NUM_EPI_WARPS * 4096 : 0;   // fp32: a box a warp
+    static constexpr int SF_BUFS = STAGES;               // see the scale warps
+    static constexpr int SF_SLOT = 3 * SF_QUAD;          // x, and one or two row blocks of W
+    static constexpr int SMEM = 1024 + STAGES * BYTES + STAGING + SF_SLOTS * SF_SLOT + CTRL_BYTES;
+    static_assert(BYTES % 1024 == 0, "128B swizzle atoms");
+    static_assert(SMEM <= 232448, "227 KB of dynamic shared memory");
+    static_assert(STAGES <= 8 && SF_COL + SF_BUFS * SF_COLS <= TMEM_COLS, "barriers and tensor memory");
+};
+
 struct Mx8Params {
-    CUtensorMap tmA, tmB0, tmB1, tmO;
+    CUtensorMap tmA, tmB0, tmB1, tmO;      // (tmO: fp32)
     const uint8_t *sa, *sb0, *sb1;         // scales of x (rows), and of the accumulator's two halves' W (tiles)
     uint8_t* out;
     uint8_t* out_scales;                   // OUT_MX8
@@ -95,6 +100,7 @@ struct Mx8Params {
     int* status;
     int64_t rows;
     int E, K, N, n_blocks, act;
+    int wide;                              // rows of out are whole, aligned pieces of 32 bytes (else of 16)
     int w_blocks;                          // W's row blocks an expert
     int a_rows;                            // rows of x that a stage loads (one CTA: fewer where there are no more)
     int pitch, out_pitch;                  // bytes of a row of scales: of x, of out
@@ -168,13 +174,13 @@ __device__ __forceinline__ int w_block(const Mx8Params& P, int nb, int h) {
 
 template <int CG, int OT, bool DUAL>
 __global__ void __launch_bounds__(NTHREADS, 1) mx8_grouped_kernel(const __grid_constant__ Mx8Params P) {
-    using R = Ring<CG>;
+    using R = Ring<CG, OT>;
     constexpr int S = R::STAGES, SB = R::SF_BUFS, BN = R::BN;
     constexpr int OUT = DUAL ? BN / 2 : BN;              // output columns of a tile
     constexpr bool F32 = OT == OUT_F32;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t* sf_smem = base + S * R::BYTES + STAGING_BYTES;
+    uint8_t* sf_smem = base + S * R::BYTES + R::STAGING;
     uint8_t* ctrl = sf_smem + SF_SLOTS * R::SF_SLOT;
     uint64_t* full = reinterpret_cast<uint64_t*>(ctrl);
     uint64_t* empty = full + 8;
@@ -202,9 +208,10 @@ __global__ void __launch_bounds__(NTHREADS, 1) mx8_grouped_kernel(const __grid_c
         mbar_init(smem_u32(drain), 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        const CUtensorMap* maps[4] = {&P.tmA, &P.tmB0, &P.tmO, &P.tmB1};
-        for (int i = 0; i < (DUAL ? 4 : 3); ++i)
-            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(maps[i])) : "memory");
+        const CUtensorMap* maps[4] = {&P.tmA, &P.tmB0, &P.tmB1, &P.tmO};
+        for (int i = 0; i < 4; ++i)
+            if (i < 2 || (DUAL && i == 2) || (F32 && i == 3))
+                asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(maps[i])) : "memory");
     }
     if (warp == 1) {
         if constexpr (CG == 1) {
@@ -477,20 +484,32 @@ __global__ void __launch_bounds__(NTHREADS, 1) mx8_grouped_kernel(const __grid_c
         // ------------------------------------------------ epilogue (each CTA, its 128 rows)
         const int qd = warp & 3, half = (warp - 2) / 4;
         const uint32_t bar_te = CG == 1 ? smem_u32(tempty) : mapa_shared(smem_u32(tempty), 0);
-        uint8_t* box = base + S * R::BYTES + (warp - 2) * 4096;      // this warp's staging box
-        constexpr int ROWB = OT == OUT_MX8 ? 64 : 128;               // bytes of its 32 rows
-        // 16-byte piece j of row r: 128-byte swizzle (64-byte for 64-byte rows)
-        auto piece = [&](int r, int j) {
-            return reinterpret_cast<uint4*>(box + r * ROWB + ((OT == OUT_MX8 ? j ^ ((r >> 1) & 3) : j ^ (r & 7)) << 4));
+        constexpr int ES = OT == OUT_F32 ? 4 : OT == OUT_BF16 ? 2 : 1;
+        // 32 columns of this lane's row, from column col on: as many as lie before column N (N
+        // is whole pieces)
+        auto pieces = [&](uint8_t* dst, int col, const uint32_t (&w)[8 * ES]) {
+#pragma unroll
+            for (int i = 0; i < ES; ++i) {
+                if (P.wide) {
+                    if (col + i * (32 / ES) < P.N) store32(dst + i * 32, w + 8 * i);
+                } else {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        if (col + i * (32 / ES) + h * (16 / ES) < P.N)
+                            *reinterpret_cast<uint4*>(dst + i * 32 + h * 16) =
+                                make_uint4(w[8 * i + 4 * h], w[8 * i + 4 * h + 1], w[8 * i + 4 * h + 2], w[8 * i + 4 * h + 3]);
+                }
+            }
         };
-        auto box_free = [&]() {                          // the last box has been read
-            if (lane == 0) bulk_wait_read<0>();
+        // fp32: 32 columns of the warp's rows as a box of 128-byte rows, 128-byte swizzle; all of
+        // it by TMA, which leaves out columns past N, or the nv < 32 rows that are the segment's
+        auto send_box = [&](const float (&o)[32], int col, int row, int nv) {
+            uint8_t* box = base + S * R::BYTES + (warp - 2) * 4096;
+            auto piece = [&](int r, int j) { return reinterpret_cast<float4*>(box + r * 128 + ((j ^ (r & 7)) << 4)); };
+            if (lane == 0) bulk_wait_read<0>();          // the last box has been read
             __syncwarp();
-        };
-        // The box to out: all rows by TMA, or the nv < 32 that are the segment's by 16 bytes
-        // a lane (N is whole 16-byte pieces; TMA leaves out columns past it by itself).
-        constexpr int ES = OT == OUT_F32 ? 4 : OT == OUT_BF16 ? 2 : 1, RP = ROWB / 16;
-        auto send = [&](int col, int row, int nv) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) *piece(lane, j) = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
             if (nv >= 32) {
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -501,10 +520,10 @@ __global__ void __launch_bounds__(NTHREADS, 1) mx8_grouped_kernel(const __grid_c
                 return;
             }
             __syncwarp();
-            const int j = lane % RP;
-            if (col + j * (16 / ES) < P.N)
-                for (int r = lane / RP; r < nv; r += 32 / RP)
-                    *reinterpret_cast<uint4*>(P.out + ((int64_t)(row + r) * P.N + col) * ES + j * 16) = *piece(r, j);
+            const int j = lane & 7;
+            if (col + 4 * j < P.N)
+                for (int r = lane >> 3; r < nv; r += 4)
+                    *reinterpret_cast<float4*>(P.out + ((int64_t)(row + r) * P.N + col) * 4 + j * 16) = *piece(r, j);
             __syncwarp();
         };
         const bool silu = P.act == MOE_MX8_ACT_SILU;
@@ -512,49 +531,37 @@ __global__ void __launch_bounds__(NTHREADS, 1) mx8_grouped_kernel(const __grid_c
         // 64 neighbouring columns of this lane's row, in two halves of 32; nv: rows of the
         // warp's 32 that are the segment's
         auto store = [&](const float (&o)[2][32], int col, int row, int nv) {
-            if (nv <= 0 || col >= P.N) return;
-            if constexpr (OT == OUT_F32) {
+            if constexpr (F32) {
+                if (nv <= 0) return;
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    if (col + 32 * i < P.N) send_box(o[i], col + 32 * i, row, nv);
+                return;
+            }
+            if (lane < nv && col < P.N) {
+                const int64_t r = row + lane;
+                uint8_t* dst = P.out + (r * P.N + col) * ES;
+                uint32_t s[2] = {0, 0};
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    if (col + 32 * i >= P.N) break;
-                    box_free();
+                    uint32_t w[8 * ES];
+                    if constexpr (OT == OUT_BF16) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        *piece(lane, j) = make_uint4(__float_as_uint(o[i][4 * j]), __float_as_uint(o[i][4 * j + 1]),
-                                                     __float_as_uint(o[i][4 * j + 2]), __float_as_uint(o[i][4 * j + 3]));
-                    send(col + 32 * i, row, nv);
-                }
-            } else if constexpr (OT == OUT_BF16) {
-                box_free();
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    uint32_t p[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float* x = o[j >> 2] + 8 * (j & 3) + 2 * k;
-                        __nv_bfloat162 b2 = __floats2bfloat162_rn(x[0], x[1]);
-                        p[k] = *reinterpret_cast<uint32_t*>(&b2);
+                        for (int j = 0; j < 16; ++j) {
+                            __nv_bfloat162 b2 = __floats2bfloat162_rn(o[i][2 * j], o[i][2 * j + 1]);
+                            w[j] = *reinterpret_cast<uint32_t*>(&b2);
+                        }
+                    } else {                                 // a block
+                        s[i] = mx8_scale_byte(amax_bits<32>(o[i]));
+                        mx8_codes<32>(o[i], s[i], w);
                     }
-                    *piece(lane, j) = make_uint4(p[0], p[1], p[2], p[3]);
-                }
-                send(col, row, nv);
-            } else {                                     // two blocks
-                box_free();
-                uint32_t s[2];
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    s[i] = mx8_scale_byte(amax_bits<32>(o[i]));
-                    uint32_t w[8];
-                    mx8_codes<32>(o[i], s[i], w);
-                    *piece(lane, 2 * i) = make_uint4(w[0], w[1], w[2], w[3]);
-                    *piece(lane, 2 * i + 1) = make_uint4(w[4], w[5], w[6], w[7]);
+                    pieces(dst + i * 32 * ES, col + 32 * i, w);
                 }
                 // (both bytes lie in the row's pitch; past the last block they stand for nothing)
-                if (lane < nv)
-                    *reinterpret_cast<uint16_t*>(P.out_scales + (int64_t)(row + lane) * P.out_pitch + col / 32) =
-                        (uint16_t)(s[0] | s[1] << 8);
-                send(col, row, nv);
+                if constexpr (OT == OUT_MX8)
+                    *reinterpret_cast<uint16_t*>(P.out_scales + r * P.out_pitch + col / 32) = (uint16_t)(s[0] | s[1] << 8);
             }
+            __syncwarp();                                // (together again for tensor memory)
         };
         // a cluster's sums: 64 columns of a lane quarter's rows, by lane, in pieces of 16 bytes
         const uint32_t sums = smem0 + (uint32_t)(qd * 2) * 8192 + lane * 16;
@@ -682,7 +689,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) mx8_grouped_kernel(const __grid_c
             }
         }
         if (split && share == 0 && !joined) cluster_sync_all();   // (no tile, or given up)
-        if (lane == 0) bulk_wait_all();
+        if (F32 && lane == 0) bulk_wait_all();
     }
     // a cluster that shares a tile meets twice, every warp of it: when the sums are
     // there (the epilogue's warps did so above), and when they have been read
@@ -720,14 +727,14 @@ int codes_map(CUtensorMap* m, const void* p, int64_t rows, int bytes, int box_ro
 template <int CG, int OT, bool DUAL>
 int launch_mx8_t(const moe_mx8_product_config& c, const Mx8Params& P, cudaStream_t st) {
     static bool attr_done[64] = {};
-    if (const int r = smem_attr_once(mx8_grouped_kernel<CG, OT, DUAL>, Ring<CG>::SMEM, attr_done)) return r;
+    if (const int r = smem_attr_once(mx8_grouped_kernel<CG, OT, DUAL>, (Ring<CG, OT>::SMEM), attr_done)) return r;
     const int64_t mt = c.rows / (CG * BM) + c.E;         // a segment may round up
     const int64_t units = std::max<int64_t>(1, std::min<int64_t>(mt * P.n_blocks, num_sms() / CG));
     const int cluster = CG == 2 ? 2 : P.ways;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(P.ways > 1 ? P.ways * P.max_tiles : CG * units));
     cfg.blockDim = dim3(NTHREADS);
-    cfg.dynamicSmemBytes = Ring<CG>::SMEM;
+    cfg.dynamicSmemBytes = (Ring<CG, OT>::SMEM);
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -790,12 +797,14 @@ int launch_mx8_product(const moe_mx8_product_config& c, const void* xq, const vo
     P.sb0 = static_cast<const uint8_t*>(dual ? gs : ws);
     P.sb1 = static_cast<const uint8_t*>(ws);
     const bool f32 = c.out_dtype == MOE_DTYPE_F32, mx8 = c.out_dtype == MOE_DTYPE_MX8;
-    const uint64_t es = f32 ? 4 : mx8 ? 1 : 2;
-    const uint64_t dims[3] = {(uint64_t)c.N, (uint64_t)c.rows, 1};
-    const uint64_t strides[2] = {c.N * es, c.N * es * c.rows};
-    const uint32_t box[3] = {mx8 ? 64u : (uint32_t)(128 / es), 32, 1};
-    MX8_TRY(encode_map(&P.tmO, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : mx8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                       out, dims, strides, box, mx8 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B));
+    const int64_t row_bytes = (int64_t)c.N * (f32 ? 4 : mx8 ? 1 : 2);
+    if (f32) {
+        const uint64_t dims[3] = {(uint64_t)c.N, (uint64_t)c.rows, 1};
+        const uint64_t strides[2] = {(uint64_t)row_bytes, (uint64_t)row_bytes * c.rows};
+        const uint32_t box[3] = {32, 32, 1};
+        MX8_TRY(encode_map(&P.tmO, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, out, dims, strides, box));
+    }
+    P.wide = (reinterpret_cast<uintptr_t>(out) | (uintptr_t)row_bytes) % 32 == 0;
     P.out = static_cast<uint8_t*>(out);
     P.out_scales = static_cast<uint8_t*>(out_scales);
     P.offsets = offsets;

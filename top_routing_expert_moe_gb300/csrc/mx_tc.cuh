@@ -155,17 +155,15 @@ inline EncodeTiledFn encode_fn() {
     });
     return fn;
 }
-// 3-D map with 128-byte swizzle unless stated: dims[0] contiguous, strides[i] the byte
-// stride of dims[i + 1]
+// 3-D map with 128-byte swizzle: dims[0] contiguous, strides[i] the byte stride of dims[i + 1]
 inline int encode_map(CUtensorMap* m, CUtensorMapDataType type, const void* ptr, const uint64_t (&dims)[3],
-                      const uint64_t (&strides)[2], const uint32_t (&box)[3],
-                      CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
+                      const uint64_t (&strides)[2], const uint32_t (&box)[3]) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return MOE_ERR_CUDA;
     const cuuint64_t d[3] = {dims[0], dims[1], dims[2]}, st[2] = {strides[0], strides[1]};
     const cuuint32_t b[3] = {box[0], box[1], box[2]}, es[3] = {1, 1, 1};
     return fn(m, type, 3, const_cast<void*>(ptr), d, st, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
                ? MOE_OK
                : MOE_ERR_CUDA;
