@@ -115,6 +115,10 @@ def test_refusals():
         layer.forward(x, x, x, x, x, checkpoint=other)
     with pytest.raises(ValueError, match="another layer"):
         layer.backward(x, checkpoint=other)
+    with pytest.raises(ValueError, match="no shared experts"):
+        layer.forward(x, x, x, x, x, shared=(x, x), checkpoint=moe.MoECheckpoint(cfg, "cpu"))
+    with pytest.raises(ValueError, match="must live on the GPU"):
+        layer.forward(x, x, x, x, x, checkpoint=moe.MoECheckpoint(cfg, "cpu"))
     with pytest.raises(RuntimeError, match="needs a forward"):
         layer.backward(x, checkpoint=moe.MoECheckpoint(cfg, "cpu"))
 

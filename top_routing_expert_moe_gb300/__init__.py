@@ -418,6 +418,8 @@ class MoELayer:
         x and the weights are to stay as they are until that backward."""
         c = self.cfg
         if checkpoint is not None:
+            if shared is not None:
+                raise ValueError("a checkpointed forward has no shared experts")
             return self._forward_kept(checkpoint, x, W_r, W_up, W_down, W_gate, bias, noise, token_mask, stream)
         if (c.f_shared > 0) != (shared is not None):
             raise ValueError("shared-expert weights are required iff cfg.f_shared > 0")
@@ -439,6 +441,7 @@ class MoELayer:
     def _forward_kept(self, k, x, W_r, W_up, W_down, W_gate, bias, noise, token_mask, stream):
         c = self.cfg
         k.check(c)
+        k.h.ptrs                                  # raises: not on the current device
         self._inputs = k.inputs = None
         moe_route(c, x, W_r, bias, noise, token_mask, k.logits, k.topk_idx, k.gate, k.counts, k.stats, self.ws,
                   stream)
@@ -453,6 +456,7 @@ class MoELayer:
 
     def _backward_kept(self, k, dout, stream, dlogits_aux, g):
         c = self.cfg
+        k.h.ptrs                                  # raises: not on the current device
         x, W_r, W_up, W_gate, W_down, bias = k.inputs
         # the same rows as in the forward: the permutation goes by the kept choices alone
         moe_permute(c, x, k.topk_idx, self.x_perm, k.perm_token, k.slot_of, k.kept, k.offsets, None, self.ws,

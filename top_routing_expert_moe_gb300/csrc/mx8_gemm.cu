@@ -33,23 +33,23 @@
 // W is kept in blocks of 128 rows x 128 elements, 16 KB each, a row block's one after the
 // other along K, and its scales in the tensor cores' tiles of 512 bytes in the same order:
 // a stage's scales of W are whole sectors, where 16 bytes a row for four stages left
-// half of each unused (16384 rows, K = 4096, N = 14336, SwiGLU: 2460 us, by rows 2560).
+// half of each unused (32768 rows, K = 4096, N = 14336, SwiGLU: 2460 us, by rows 2560).
 //
 // Few rows (decoding) are bound by W's bytes, and what they must not do is read x's few
-// lines from every CTA more often than they have to: 128 requests of every CTA for the
-// scales of one row, where only the segment's rows are asked for now, took 145 us
-// where the rest takes 69 (2 rows of each of 2 experts, K = 4096, N = 14336, SwiGLU).
+// lines from every CTA more often than they have to: with 128 requests of every CTA for
+// the scales of one row, and boxes of 128 rows for the four that there are, 2 rows of each
+// of 2 experts (K = 4096, N = 14336, SwiGLU) took 145 us where they take 43.
 //
 // Tensor memory: two accumulators of 256 columns that overlap in 128, and buffers of 16
 // columns of scales.
 //
 // What bounds it.  Large products: the power cap.  32768 rows of 8 experts, K = 4096,
-// N = 14336, SwiGLU: 2480 us, 3.1 PFLOP/s at 1440 MHz and 1.37 kW, where the tensor pipe is
-// active 0.82 of the time; with operands of zeros, which draw less, the same launch holds
-// 2070 MHz and 4.0 PFLOP/s (1925 us).  There the MMAs alone take 1646 us, the loads add
-// 4 %, the stores 4 %, the hand-over of the accumulator 2 %, the scales nothing.  Few rows:
-// HBM, 6.8 TB/s of W (64 rows of 8 experts, the same product: 143 us).  In between the 256
-// rows of a tile that a segment does not fill (2048 rows: 232 us).
+// N = 14336, SwiGLU: about 2500 us, 3.1 PFLOP/s at 1440 MHz and 1.37 kW, where the tensor pipe
+// is active 0.82 of the time; with operands of zeros, which draw less, the same launch held
+// 2070 MHz and 4.0 PFLOP/s (1925 us).  There the MMAs alone took 1646 us, the loads added
+// 5 %, the stores 4 %, the hand-over of the accumulator 2 %, the scales nothing.  Few rows:
+// HBM, 6.9 TB/s of W (64 rows of 8 experts, the same product: 140 us).  In between the rows
+// of a 256-row tile that a segment does not fill (2048 rows: 223 us).
 #include <algorithm>
 #include <cstring>
 
