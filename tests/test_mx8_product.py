@@ -177,6 +177,23 @@ def test_product_of_few_rows_over_long_depths(K, N, counts, act, out):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("counts", [[1], [3, 1], [0, 5, 0]])
+@pytest.mark.parametrize("K,N", [(8192, 136), (8224, 40), (9056, 520)])
+@pytest.mark.parametrize("act,out", [("none", "fp32"), ("swiglu", "bf16")])
+def test_product_of_few_rows_over_the_longest_depths(K, N, counts, act, out):
+    """Four CTAs a tile, whose shares differ in length."""
+    product_case(counts, K, N, act, out, seed=K + N, slack=0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("counts", [[1, 1, 1, 1], [4, 0, 0, 0], [2, 0, 1, 1]])
+def test_product_that_shares_a_depth_or_not_by_what_rows_name(counts):
+    """The launch is sized for four experts of 20 tiles: 80 do not fit the GPU in pairs of CTAs,
+    which take them in turn then, fewer do."""
+    product_case(counts, 3200, 2560, "none", "bf16", seed=sum(counts) + counts[0], slack=0)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("K", [1024, 4096])
 @pytest.mark.parametrize("act", ACTS)
 def test_product_of_few_rows_in_8_bits(K, act):

@@ -783,7 +783,11 @@ int launch_mx8_product(const moe_mx8_product_config& c, const void* xq, const vo
     //   4096 -> 14336 SwiGLU  148  153       200  154       211  156
     //   2048 -> 4096 silu      19  24         25  23         25  22
     //   14336 -> 4096          82  93        110  89        109  91
-    const bool pair = c.rows >= (int64_t)96 * c.E;
+    // Nor does it where the single CTAs' tiles fit the GPU at once (666 rows of 5 experts,
+    // 1056 -> 1000: 8.0 and 9.1; 1024 of one, 4096 -> 1024 fp32: 12.8 and 15.3).  In two
+    // turns they lose (600 of one, 4096 -> 2048 SwiGLU: 26.2 and 16.2).
+    const int64_t single = (c.rows / BM + c.E) * ((c.N + (dual ? 63 : 127)) / (dual ? 64 : 128));
+    const bool pair = c.rows >= (int64_t)96 * c.E && single > num_sms();
     const int w_rows = dual && !pair ? 64 : 128;
     // (rows of x behind the last: what is left in shared memory serves as well)
     P.a_rows = pair ? BM : (int)std::min<int64_t>(BM, (c.rows + 7) / 8 * 8);
@@ -815,12 +819,18 @@ int launch_mx8_product(const moe_mx8_product_config& c, const void* xq, const vo
     P.out_pitch = (int)mx8_pitch(c.N);
     const int cols = (pair ? 256 : 128) / (dual ? 2 : 1);       // output columns of a tile
     P.n_blocks = (c.N + cols - 1) / cols;
-    // Few tiles (a token or two in decoding): two or four CTAs share a tile's K, if each
-    // then has four stages or more.
+    // Few tiles (a token or two in decoding): the CTAs of a cluster share a tile's K where a
+    // share is long enough, us with 1, 2 and 4 of them (one row of one expert):
+    //   1024 -> 1024   6.0  7.2       2048 -> 1024   8.2  8.3  9.0
+    //   4096 -> 1024  12.6 10.6 10.1  14336 -> 4096 36.5 22.9 19.3
+    // The host knows how many experts rows can name, not how many they do: two share where
+    // the tiles might fit the GPU so, and the kernel looks whether they do (2 tokens of
+    // 8 experts, top-2, 14336 -> 4096: 25 where rows name two of them, 37 without; in
+    // turns they lose: four experts 49 for 40).
     const int64_t tiles = (c.rows / BM + std::min<int64_t>(c.E, c.rows)) * P.n_blocks;
-    const int nk = (c.K + BK - 1) / BK;
-    P.ways = pair ? 1 : nk >= 16 && tiles * 4 <= num_sms() ? 4 : nk >= 8 && tiles * 2 <= num_sms() ? 2 : 1;
-    P.max_tiles = (int)std::min<int64_t>(tiles, num_sms());
+    const int nk = (c.K + BK - 1) / BK, sms = num_sms();
+    P.ways = pair ? 1 : nk >= 64 && tiles * 4 <= sms ? 4 : nk >= 24 && tiles <= sms ? 2 : 1;
+    P.max_tiles = (int)std::min<int64_t>(tiles, sms / P.ways);
     return pair ? launch_mx8_out<2>(c, P, st) : launch_mx8_out<1>(c, P, st);
 }
 
