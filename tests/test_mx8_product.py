@@ -347,3 +347,30 @@ def test_product_into_memory_of_16_byte_alignment(out, N, rows):
     moe.moe_mx8_grouped_product(m.cfg, x.codes, x.scales, o, w.codes, w.scales, None, None, got,
                                 m.out.scales if out == "mx8" else None)
     assert torch.equal(got, want) and (raw[:at] == 7).all() and (raw[at + rows * N:] == 7).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("act", ["silu", "swiglu"])
+@pytest.mark.parametrize("out", ["fp32", "bf16", "mx8"])
+@pytest.mark.parametrize("rows,N", [(64, 64), (1000, 2560)])
+def test_activations_at_infinity(act, out, rows, N):
+    """Sums past fp32's range on either side, and far inside it: silu(inf) is inf,
+    silu(-inf) by z / (1 + e^-z) no number, silu(+-2^30) 2^30 and 0, all exactly."""
+    K, n = 64, 2.0 ** 70
+    a = torch.tensor([n, -n, n ** -1 * 2.0 ** 24, -n ** -1 * 2.0 ** 24]).repeat(rows // 4)
+    x = moe.mx8_quantize(a[:, None].expand(rows, K).contiguous().cuda())
+    o = torch.tensor([0, rows], dtype=torch.int32).cuda()
+    big = moe.mx8_quantize_weight(torch.full((1, K, N), n).cuda())
+    up = moe.mx8_quantize_weight(torch.full((1, K, N), 2.0 ** 20).cuda())
+    run = lambda act, code, *w: moe.MX8Product(moe.MX8ProductConfig(  # noqa: E731
+        rows=rows, K=K, N=N, E=1, act=act, out_dtype=code)).forward(x, o, *w)
+    z = run(moe.MX8_ACT_NONE, moe.F32, big).cpu().double()
+    assert (z[0::4] == float("inf")).all() and (z[1::4] == -float("inf")).all()
+    assert (z[2::4] == 2.0 ** 30).all() and (z[3::4] == -2.0 ** 30).all()
+    want = z / (1 + torch.exp(-z))
+    if act == "swiglu":
+        want = want * (a.double() * K * 2.0 ** 20)[:, None]
+    got = run(ACTS.index(act), OUTS[out][0], *((up, big) if act == "swiglu" else (big,)))
+    if out == "mx8":                                        # (no block is infinite)
+        got, want = got.dequantize(torch.float32), torch.where(want.isinf(), float("nan"), want)
+    assert torch.equal(got.cpu().double().nan_to_num(nan=-7.0), want.nan_to_num(nan=-7.0))

@@ -137,12 +137,15 @@ __device__ __forceinline__ void tmem_st4(uint32_t taddr, uint32_t a, uint32_t b,
 // silu for fp32 outputs, within a few units of fp32: e^-z = 2^h (1 + l ln 2), where h + l is
 // -z log2(e) in two parts, so that the product's rounding does not grow with z.  (The
 // quick form's error does, which 16 and 8 bits hide; by expf and a division the registers
-// spilled: 32768 rows, K = 2048, N = 4096, silu 439 us, so 208.)
+// spilled: 32768 rows, K = 2048, N = 4096, silu 439 us, so 211.)  Past 88 on either side e^-z
+// is that of 88: 1 + e^-z is 1, or above 2^126, by which the division gives 0, and h and l
+// are finite where z is not.
 __device__ __forceinline__ float silu_fine(float z) {
     constexpr float L = 1.44269504f, L_LO = 1.92596303e-8f, LN2 = 0.693147181f;   // log2(e) in two parts
-    const float h = -z * L, l = fmaf(-z, L_LO, fmaf(-z, L, -h));
+    const float c = fmaxf(fminf(z, 88.f), -88.f);
+    const float h = -c * L, l = fmaf(-c, L_LO, fmaf(-c, L, -h));
     float e;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(fminf(h, 126.f)));             // (no infinity times l)
+    asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(h));
     return __fdividef(z, 1.f + fmaf(e, l * LN2, e));
 }
 
