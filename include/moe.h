@@ -224,7 +224,7 @@ MOE_API int moe_route_noalloc(const moe_config* cfg, const void* x, const void* 
  * then zero rows up to a multiple of pad_m) and gather x rows into x_perm.
  *   in : x[T,d], topk_idx[T,k]
  *        (a token that names an expert twice takes one of its rows, and both slots
- *        point there)
+ *        point there; the backward calls need a token's experts to differ)
  *   out: x_perm[rows_cap,d] (rows >= offsets[E] untouched), perm_token[rows_cap]
  *        (token of each row, -1 on padding rows), slot_of[T,k] (row of (t,j),
  *        -1 if dropped), kept[E], offsets[E+1]; stats (may be NULL) gets
