@@ -25,7 +25,7 @@
 // 1024 rows of 8 experts, 4096 -> 14336 SwiGLU in 8 bits, 156 us and 150; 2 rows of 2 of
 // them 43.9 and 42.8; 8192 rows, 14336 -> 4096, 332 and 325; the largest bf16 product 2518
 // and 2563.  fp32, four times the bytes, leaves by boxes: 32768 rows, 2048 -> 4096, silu,
-// 234 us, by lanes 260.)  For the same reason the scales of x are kept by rows and not
+// 211 to 236 us from one GPU to another, by lanes 262.)  For the same reason the scales of x are kept by rows and not
 // in the tensor cores' 128-row tiles, which would begin at other rows than a segment: the
 // scale warps form the tile (row r's four bytes as word r / 32 of lane r % 32) from 16
 // bytes a row, four stages' worth, in registers.
