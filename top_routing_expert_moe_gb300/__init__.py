@@ -398,10 +398,23 @@ class MoELayer:
             self.h_shared = e(cfg.nh, Ts, fs)
             self.act_shared = e(Ts, fs)
             self.y_shared = e(Ts, d)
+        # where the layer's own buffers lie
+        self._storages = {t.untyped_storage().data_ptr() for t in vars(self).values() if isinstance(t, torch.Tensor)}
         self._grads = None
-        self._inputs = None
+        self._inputs = self._x = None
         self._shared_w = None
         self._mx4 = self._mx8 = None
+
+    def _apart(self, x, held, stream):
+        """x, or a copy of it in ``held`` (allocated here if None) where it lies in one of the
+        layer's own buffers, which are written before its backward has read it."""
+        if x.untyped_storage().data_ptr() not in self._storages:
+            return x, held
+        with _on(stream):
+            if held is None or held.shape != x.shape:
+                held = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            held.copy_(x)
+        return held, held
 
     def _shared_fwd(self, x):
         if self.cfg.f_shared <= 0:
@@ -415,7 +428,8 @@ class MoELayer:
         """The layer's output [T, d] (its own buffer).  With ``checkpoint`` (a MoECheckpoint) what
         the backward needs is kept there, the activations in 8 bits, and nothing of it in the
         layer: one layer then serves a model's every depth, each with a checkpoint of its own.
-        x and the weights are to stay as they are until that backward."""
+        x and the weights are to stay as they are until that backward; x may be the layer's own
+        last output (or lie in another of its buffers): it is then copied first."""
         c = self.cfg
         if checkpoint is not None:
             if shared is not None:
@@ -427,6 +441,7 @@ class MoELayer:
             Wu_s, Wd_s = shared[0], shared[1]
             Wg_s = shared[2] if len(shared) > 2 else None
             self._shared_w = (Wu_s, Wd_s, Wg_s)
+        x, self._x = self._apart(x, self._x, stream)
         sh = self._shared_fwd(x)
         moe_route(c, x, W_r, bias, noise, token_mask, self.logits, self.topk_idx, self.gate,
                   self.counts, self.stats, self.ws, stream)
@@ -443,6 +458,7 @@ class MoELayer:
         k.check(c)
         k.h.ptrs                                  # raises: not on the current device
         self._inputs = k.inputs = None
+        x, k.x = self._apart(x, k.x, stream)
         moe_route(c, x, W_r, bias, noise, token_mask, k.logits, k.topk_idx, k.gate, k.counts, k.stats, self.ws,
                   stream)
         moe_permute(c, x, k.topk_idx, self.x_perm, k.perm_token, k.slot_of, k.kept, k.offsets, k.stats, self.ws,
@@ -553,6 +569,7 @@ class MoELayer:
                     dW_gate_s=(torch.empty(c.d, fs, dtype=dt, device=dev)
                                if c.ffn == SWIGLU else None),
                     dW_down_s=torch.empty(fs, c.d, dtype=dt, device=dev))
+            self._storages |= {t.untyped_storage().data_ptr() for t in self._grads.values() if t is not None}
         return self._grads
 
     def shared_block(self, dout=None, dh=None, dx=None):
@@ -570,7 +587,9 @@ class MoELayer:
     def backward(self, dout, stream=None, dlogits_aux=None, checkpoint=None):
         """Gradients of the last forward, or of the forward that ``checkpoint`` was given to
         (its activations as their 8-bit numbers stand for them).  ``dlogits_aux`` [T, E] fp32:
-        a further gradient on the router logits (a balance loss's), added to the router's own."""
+        a further gradient on the router logits (a balance loss's), added to the router's own.
+        The gradients are the layer's own buffers: the next backward, another depth's too, writes
+        them again.  dout may be the last one's dx."""
         if checkpoint is not None:
             checkpoint.check(self.cfg)
         if (self._inputs if checkpoint is None else checkpoint.inputs) is None:

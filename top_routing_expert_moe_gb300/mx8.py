@@ -351,7 +351,7 @@ class MoECheckpoint:
         self.logits, self.gate, self.stats = e(c.T, c.E, dtype=f32), e(c.T, c.k, dtype=f32), e(9 + c.E, dtype=f32)
         self.topk_idx, self.slot_of, self.perm_token = e(c.T, c.k), e(c.T, c.k), e(R)
         self.counts, self.kept, self.offsets = e(c.E), e(c.E), e(c.E + 1)
-        self.inputs = None
+        self.inputs = self.x = None               # (x: a copy, where the forward's x was the layer's own memory)
 
     def check(self, cfg):
         if bytes(cfg) != bytes(self.cfg):
