@@ -70,6 +70,22 @@ def test_each_depth_keeps_a_copy_of_its_own(calls):
     assert not lies_in(cks[1].inputs[0], cks[2].inputs[0])
 
 
+def test_a_forward_that_raised_leaves_no_backward(calls, monkeypatch):
+    """Its first launches have written over what the backward of the one before needs."""
+    layer, w = moe.MoELayer(moe.MoEConfig(**CFG), "cpu"), cpu_weights()
+    x = torch.zeros(16, 128, dtype=torch.bfloat16)
+    layer.forward(x, **w)
+    layer.backward(x)
+
+    def ffn(*a, **kw):
+        raise moe.MoEError(moe.ERR_INVALID_ARG, "moe_grouped_ffn")
+    monkeypatch.setattr(moe, "moe_grouped_ffn", ffn)
+    with pytest.raises(moe.MoEError):
+        layer.forward(x, **w)
+    with pytest.raises(RuntimeError, match="forward"):
+        layer.backward(x)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("swiglu", [False, True])
 def test_a_chain_without_copies(swiglu):

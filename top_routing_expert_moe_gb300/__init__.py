@@ -441,6 +441,7 @@ class MoELayer:
             Wu_s, Wd_s = shared[0], shared[1]
             Wg_s = shared[2] if len(shared) > 2 else None
             self._shared_w = (Wu_s, Wd_s, Wg_s)
+        self._inputs = None               # the buffers are this forward's from here on
         x, self._x = self._apart(x, self._x, stream)
         sh = self._shared_fwd(x)
         moe_route(c, x, W_r, bias, noise, token_mask, self.logits, self.topk_idx, self.gate,
