@@ -524,8 +524,9 @@ class MoELayer:
         """The forward with both GEMMs' operands in microscaled 8-bit numbers: ``experts`` (an
         MX8Experts) holds the weights, ``x8`` (an MX8Tensor, quantised here if None) the rows,
         whose 16-bit copy x the router reads; the hidden rows leave the first product in 8
-        bits.  Segments are not padded.  bf16 layers without shared experts; there is no
-        backward of it."""
+        bits.  Segments are not padded: ``offsets``, ``slot_of`` and ``perm_token`` are then those
+        of the rows without padding.  bf16 layers without shared experts; there is no backward of
+        it."""
         c = self.cfg
         if c.dtype != BF16 or c.f_shared > 0:
             raise ValueError("forward_mx8 needs a bf16 layer without shared experts")
@@ -539,6 +540,9 @@ class MoELayer:
             with _on(stream):
                 self._mx8 = (MX8Dispatch(c, dev), MX8Product(MX8ProductConfig(rows, c.d, c.f, c.E, act, MX8), dev),
                              MX8Product(MX8ProductConfig(rows, c.f, c.d, c.E), dev), MX8Tensor((c.T, c.d), dev))
+            # the layer's places, which are then this forward's like the rest of its routing
+            p = self._mx8[0]
+            p.perm_token, p.slot_of, p.kept, p.offsets = self.perm_token[:rows], self.slot_of, self.kept, self.offsets
         dispatch, first, second, own = self._mx8
         if x8 is None:
             x8 = mx8_quantize(x, out=own, stream=stream)
