@@ -604,6 +604,8 @@ MOE_API int moe_mx8_grouped_product(const moe_mx8_product_config* cfg, const voi
  * act = silu(h^) (silu(g^) u^) again, into act, and
  *   dW_down = act^T dy, dh = dact silu'(h^) (dg, du likewise), dW_up, dW_gate, dx as
  * moe_grouped_ffn_backward does from these.
+ * Offsets that descend, leave 0..rows_cap or begin a segment at no multiple of 128 (as
+ * moe_permute_mx8's may) are recorded as MOE_ERR_DEVICE_BOUNDS, and nothing is written.
  *   h_codes [nh,rows_cap,f], h_scales [nh,rows_cap,P], P = moe_mx8_scale_pitch(f); the
  *   other arguments as there.  h_codes, act and dh (in moe_backward_mx8: ws) are 32-byte
  *   aligned.                                                                 */

@@ -127,6 +127,7 @@ struct TcParams {
     const int32_t* offsets;
     int* status;
     int nprob, E;
+    int rows;               // of the routed experts' buffers
 };
 static_assert(sizeof(TcParams) <= 32764, "kernel parameters within the 32 KB launch limit");
 
@@ -355,13 +356,23 @@ __global__ void __launch_bounds__(NTHREADS, 1) tc_grouped_gemm_kernel(const __gr
         sbase[P.nprob] = sl;
         prefix[sl] = acc;
     }
-    // a timeout recorded earlier on this device (not yet read by the host): skip the work
+    // Segments are whole 128-row blocks, ascending within the buffers' rows; others are
+    // recorded and no tile is computed.  (Boxes by TMA leave out rows past a buffer's end;
+    // what an epilogue's lanes fetch, or store themselves, has no such bound.)
+    if (const int e = tid - 64; P.offsets && e >= 0 && e <= P.E) {
+        const int at = offs[e];
+        if (at < 0 || at % BM != 0 || (e < P.E ? offs[e + 1] : P.rows) < at) {
+            *abort_flag = 1;
+            set_status(P.status, MOE_ERR_DEVICE_BOUNDS);
+        }
+    }
+    // a timeout recorded earlier on this device (not yet read by the host): no tiles either
     if (tid == 0 && timeout_pending(P.status)) *abort_flag = 1;
     __syncthreads();
     const uint32_t tmem_base = *tmem_slot;
-    const int total = prefix[sbase[P.nprob]];
     const uint32_t smem0 = smem_u32(base);
     const bool start_live = *abort_flag == 0;
+    const int total = start_live ? prefix[sbase[P.nprob]] : 0;
 
     if (warp == 0 && lane == 0) {
         // ------------------------------------------------ TMA producer (each CTA)
@@ -903,6 +914,7 @@ int launch_tc(const moe_config& c, const int32_t* offsets, const TcProblem* prob
     for (int i = 0; i < nprob; ++i) P.prob[i] = probs[i];
     P.nprob = nprob;
     P.E = c.E;
+    P.rows = (int)rows_cap_of(c);
     P.offsets = offsets;
     P.status = device_status_ptr();
     const int pairs = max_pairs();
