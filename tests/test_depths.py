@@ -86,6 +86,15 @@ def test_a_forward_that_raised_leaves_no_backward(calls, monkeypatch):
         layer.backward(x)
 
 
+def test_a_checkpoint_on_another_device_is_refused():
+    layer, ck = moe.MoELayer(moe.MoEConfig(**CFG), "cpu"), moe.MoECheckpoint(moe.MoEConfig(**CFG), "meta")
+    x = torch.zeros(16, 128, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="on meta, the layer on cpu"):
+        layer.forward(x, **cpu_weights(), checkpoint=ck)
+    with pytest.raises(ValueError, match="on meta, the layer on cpu"):
+        layer.backward(x, checkpoint=ck)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("swiglu", [False, True])
 def test_a_chain_without_copies(swiglu):

@@ -456,7 +456,7 @@ class MoELayer:
 
     def _forward_kept(self, k, x, W_r, W_up, W_down, W_gate, bias, noise, token_mask, stream):
         c = self.cfg
-        k.check(c)
+        k.check(self)
         k.h.ptrs                                  # raises: not on the current device
         self._inputs = k.inputs = None
         x, k.x = self._apart(x, k.x, stream)
@@ -596,7 +596,7 @@ class MoELayer:
         The gradients are the layer's own buffers: the next backward, another depth's too, writes
         them again.  dout may be the last one's dx."""
         if checkpoint is not None:
-            checkpoint.check(self.cfg)
+            checkpoint.check(self)
         if (self._inputs if checkpoint is None else checkpoint.inputs) is None:
             raise RuntimeError("backward() needs a forward() first")
         with _on(stream):
