@@ -26,6 +26,17 @@ def test_the_places_are_the_layers(calls):  # noqa: F811
     assert combine[2] is layer.slot_of
 
 
+def test_rows_of_another_shape_or_type_are_refused():
+    """The router reads x itself, also where its rows come in 8 bits beside it."""
+    layer = moe.MoELayer(moe.MoEConfig(T=8, d=128, f=128, E=2, k=1), "cpu")
+    ex, x8 = Experts((2, 128, 128), (2, 128, 128)), moe.MX8Tensor((8, 128), "cpu")
+    W_r = torch.zeros(128, 2, dtype=torch.bfloat16)
+    for x in (torch.zeros(8, 128), torch.zeros(7, 128, dtype=torch.bfloat16), torch.zeros(8, 64, dtype=torch.bfloat16)):
+        for rows in (None, x8):
+            with pytest.raises(ValueError, match="^x: expected"):
+                layer.forward_mx8(x, W_r, ex, x8=rows)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("T,cf", [(40, 0.0), (500, 0.0), (500, 0.7)])
 def test_places_after_other_forwards(T, cf):

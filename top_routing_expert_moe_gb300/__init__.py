@@ -534,6 +534,7 @@ class MoELayer:
             raise ValueError("a gate matrix is required iff cfg.ffn is SWIGLU")
         if experts.up.shape != (c.E, c.f, c.d) or experts.down.shape != (c.E, c.d, c.f):
             raise ValueError("the experts' shapes are not this layer's")
+        _checked(x, (c.T, c.d), torch.bfloat16, "x")
         if self._mx8 is None:
             dev, rows = self.out.device, mx8_rows_capacity(c)
             act = MX8_ACT_SWIGLU if c.ffn == SWIGLU else MX8_ACT_SILU
@@ -619,5 +620,6 @@ class MoELayer:
 
 # the operators around the layer (imported last: they use the helpers above)
 from .mx8 import *  # noqa: E402,F401,F403
+from .mx8 import _checked  # noqa: E402
 from .block import *  # noqa: E402,F401,F403
 from .block import _quantize_segments  # noqa: E402
