@@ -17,7 +17,8 @@ constexpr int ROW_THREADS = 256, ROW_UNROLL = 4;
 constexpr int ROW_VECS = ROW_THREADS * ROW_UNROLL;      // vectors of a CTA's turn
 
 // A CTA's turn: whole rows while they fit, else a part of one row.  Vector i of the
-// turn lies in row i / nvec of it (by a product: i and nvec stay below 2^11 then).
+// turn lies in row i / nvec of it (by a product: i and nvec stay below 2^11 then, and a row,
+// whole blocks, has at least two vectors, so that 2^32 / nvec fits 32 bits).
 struct Turns {
     int64_t rows, turns;                                // rows, and turns of `per` of them
     int nvec, per, parts;                               // vectors a row; rows a turn; turns a row
@@ -39,7 +40,7 @@ __device__ __forceinline__ Place place(const Turns& t, int64_t used, int64_t u, 
     const int i = threadIdx.x + j * ROW_THREADS;
     Place p;
     if (t.parts == 1) {
-        const int r = t.nvec == 1 ? i : (int)__umulhi((uint32_t)i, t.magic);
+        const int r = (int)__umulhi((uint32_t)i, t.magic);
         p.row = u * t.per + r;
         p.vec = i - r * t.nvec;
         if (r >= t.per) p.row = -1;
