@@ -26,6 +26,7 @@ MX8 = 2                                              # an output type beside F32
 MX8_ACT_NONE, MX8_ACT_SILU, MX8_ACT_SWIGLU = 0, 1, 2
 
 _p, _s, _on, _call = _moe._p, _moe._s, _moe._on, _moe._call
+_current_device = torch.cuda.current_device
 
 
 def _checked(t, shape, dtype, name):
@@ -83,13 +84,6 @@ def mx8_weight_bytes(E: int, K: int, N: int):
 
 def moe_mx8_dequantize_weight(dtype, E, K, N, codes, scales, out, stream=None):
     _call("moe_mx8_dequantize_weight", dtype, E, K, N, _p(codes), _p(scales), _p(out), _s(stream))
-
-
-def _current_device() -> int:
-    try:
-        return torch._C._cuda_getDevice()
-    except AttributeError:       # a private name, a microsecond quicker than the public call
-        return torch.cuda.current_device()
 
 
 class _Numbers:
