@@ -553,7 +553,9 @@ bool ring_pays(const moe_norm_config& c, bool backward) {
     return c.d >= 1024 || (c.d >= 128 && n >= (4 << 20));
 }
 struct RingPlan { int threads, stages, grid; size_t smem; };
-RingPlan ring_plan(const moe_norm_config& c, int nin, int regs, bool backward, int re = RE) {
+// `by_warp`: registers are counted as they are handed out, to whole warps from the quarter of
+// the file that their scheduler has.
+RingPlan ring_plan(const moe_norm_config& c, int nin, int regs, bool backward, int re = RE, bool by_warp = false) {
     RingPlan p = {0, 0, 0, 0};
     const int es = c.dtype == MOE_DTYPE_BF16 ? 2 : 4;
     p.threads = ((c.d + re - 1) / re + 31) / 32 * 32;
@@ -561,7 +563,8 @@ RingPlan ring_plan(const moe_norm_config& c, int nin, int regs, bool backward, i
     const int stage = nin * (int)row_pitch(c.d * es);
     // CTAs an SM by registers and threads, fewer where they would not have three stages
     // each (228 KB an SM, 3 KB of it a CTA's fixed part)
-    int per_sm = std::max(1, std::min(std::min(32, 65536 / (regs * p.threads)), 2048 / p.threads));
+    const int fit = by_warp ? 16384 / (32 * regs) * 4 / (p.threads / 32) : 65536 / (regs * p.threads);
+    int per_sm = std::max(1, std::min(std::min(32, fit), 2048 / p.threads));
     auto room = [&](int n) { return std::min(200 * 1024, 224 * 1024 / n - 3 * 1024); };
     while (per_sm > 1 && room(per_sm) < 3 * stage) --per_sm;
     p.stages = std::min(MAX_STAGES, room(per_sm) / stage);
@@ -599,8 +602,13 @@ int launch_fwd_ring(const RingPlan& p, const RingArgs& r, cudaStream_t st) {
 template <typename T, int VEC, bool Q8 = false>
 int launch_fwd(const moe_norm_config& c, const NormArgs& a, cudaStream_t st) {
     const bool heavy = c.post_norm || c.gate != MOE_GATE_NONE;
-    const int regs = Q8 ? (sizeof(T) == 2 ? (heavy ? 96 : 64) : heavy ? 64 : 48) : heavy ? 64 : 40;
-    const RingPlan p = ring_plan(c, fwd_inputs(c), regs, false, Q8 ? RE8<T> : RE);
+    // With 16 elements a thread the forms' registers differ (96 for both norms, 106 with the
+    // run-time flags), and a CTA counted that does not fit costs a second wave (65536 x 2048, full
+    // gate, 96 counted for all: 270 us, so 188; both norms at 1536 and 3584, where a scheduler's
+    // quarter does not divide evenly, 172 and 416, so 121 and 315).
+    constexpr bool by_warp = Q8 && sizeof(T) == 2;
+    const int regs = by_warp ? (form_of(a, false) == FORM_ANY ? 112 : heavy ? 96 : 64) : heavy ? 64 : Q8 ? 48 : 40;
+    const RingPlan p = ring_plan(c, fwd_inputs(c), regs, false, Q8 ? RE8<T> : RE, by_warp);
     if (p.stages) {
         RingArgs r = {};
         r.n = a;
