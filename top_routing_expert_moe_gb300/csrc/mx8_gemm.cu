@@ -134,19 +134,22 @@ __device__ __forceinline__ void tmem_st4(uint32_t taddr, uint32_t a, uint32_t b,
                  : "memory");
 }
 
-// silu for fp32 outputs, within a few units of fp32: e^-z = 2^h (1 + l ln 2), where h + l is
-// -z log2(e) in two parts, so that the product's rounding does not grow with z.  (The
-// quick form's error does, which 16 and 8 bits hide; by expf and a division the registers
-// spilled: 32768 rows, K = 2048, N = 4096, silu 439 us, so 211.)  Past 88 on either side e^-z
-// is that of 88: 1 + e^-z is 1, or above 2^126, by which the division gives 0, and h and l
-// are finite where z is not.
+// silu for fp32 outputs, within a few units of fp32 down to the last denormals: z or z t over
+// 1 + t with t = e^-|z| = 2^h (1 + l ln 2), where h + l is -|z| log2(e) in two parts, so that the
+// product's rounding does not grow with z.  The divisor stays within 1..2.  (The quick form's
+// error grows with z, and past -87.3 its divisor leaves the quick division's range: it gives 0
+// for what is at most 1e-36.  By expf and a division the registers spilled: 32768 rows, K = 2048,
+// N = 4096, silu 439 us, so 211 to 230 from one GPU to another.  The single CTA's SwiGLU spills a
+// few registers in any form: its 64 values and a cluster's sums are more than 128 hold, off the
+// path of W's bytes.)  Past 128 t is 0, and h and l are finite where z is not.
 __device__ __forceinline__ float silu_fine(float z) {
     constexpr float L = 1.44269504f, L_LO = 1.92596303e-8f, LN2 = 0.693147181f;   // log2(e) in two parts
-    const float c = fmaxf(fminf(z, 88.f), -88.f);
+    const float c = fminf(fabsf(z), 128.f);
     const float h = -c * L, l = fmaf(-c, L_LO, fmaf(-c, L, -h));
     float e;
     asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(h));
-    return __fdividef(z, 1.f + fmaf(e, l * LN2, e));
+    const float t = fmaf(e, l * LN2, e);
+    return __fdividef(z >= 0.f ? z : z * t, 1.f + t);
 }
 
 // A tile is CG * 128 rows x BN accumulator columns; tiles run over experts, then
@@ -530,6 +533,11 @@ __global__ void __launch_bounds__(NTHREADS, 1) mx8_grouped_kernel(const __grid_c
             __syncwarp();
         };
         const bool silu = P.act == MOE_MX8_ACT_SILU;
+        // The quick form is off by some 1e-6 of the value.  bf16 hides it; in 8 bits an element
+        // near the middle of two codes takes the other one more often than by the sums' own
+        // rounding (a prompt's outputs are 7.9e-5 from 64 bits, 4.2e-5 by the fine form; half a
+        // step is 6e-2 of an element), where the fine form costs 8 % (32768 rows, 2048 -> 4096,
+        // silu: 185 us and 201; two tokens, 4096 -> 14336 SwiGLU: 42.8 and 47.2).
         auto act = [](float z) { return F32 ? silu_fine(z) : silu_quick(z); };
         // 64 neighbouring columns of this lane's row, in two halves of 32; nv: rows of the
         // warp's 32 that are the segment's
