@@ -25,10 +25,10 @@
 // 1024 rows of 8 experts, 4096 -> 14336 SwiGLU in 8 bits, 156 us and 150; 2 rows of 2 of
 // them 43.9 and 42.8; 8192 rows, 14336 -> 4096, 332 and 325; the largest bf16 product 2518
 // and 2563.  fp32, four times the bytes, leaves by boxes: 32768 rows, 2048 -> 4096, silu,
-// 211 to 236 us from one GPU to another, by lanes 262.)  For the same reason the scales of x are kept by rows and not
-// in the tensor cores' 128-row tiles, which would begin at other rows than a segment: the
-// scale warps form the tile (row r's four bytes as word r / 32 of lane r % 32) from 16
-// bytes a row, four stages' worth, in registers.
+// 211 to 236 us from one GPU to another, by lanes 262.)  For the same reason the scales of x
+// are kept by rows and not in the tensor cores' 128-row tiles, which would begin at other rows
+// than a segment: the scale warps form the tile (row r's four bytes as word r / 32 of lane
+// r % 32) from 16 bytes a row, four stages' worth, in registers.
 //
 // W is kept in blocks of 128 rows x 128 elements, 16 KB each, a row block's one after the
 // other along K, and its scales in the tensor cores' tiles of 512 bytes in the same order:
@@ -794,9 +794,14 @@ int launch_mx8_product(const moe_mx8_product_config& c, const void* xq, const vo
     //   4096 -> 14336 SwiGLU  148  153       200  154       211  156
     //   2048 -> 4096 silu      19  24         25  23         25  22
     //   14336 -> 4096          82  93        110  89        109  91
-    // Nor does it where the single CTAs' tiles fit the GPU at once (666 rows of 5 experts,
-    // 1056 -> 1000: 8.0 and 9.1; 1024 of one, 4096 -> 1024 fp32: 12.8 and 15.3).  In two
-    // turns they lose (600 of one, 4096 -> 2048 SwiGLU: 26.2 and 16.2).
+    // 8 and 64 experts part at the same place, by rows an expert (4096 -> 4096): where all have
+    // as many rows single CTAs win by 10 % up to 128, pairs from 192 on (45 us and 33 for 8; 399
+    // and 210 for 64); spread from none to twice the mean, pairs win from 96 on (38.2 and 31.2;
+    // 252 and 208) and lose at 64 (28.6 and 30.9; 190 and 200).
+    // Nor does a pair pay where the single CTAs' tiles fit the GPU at once (666 rows of 5 experts,
+    // 1056 -> 1000: 8.0 and 9.1; 1024 of one, 4096 -> 1024 fp32: 12.8 and 15.3; two experts,
+    // 2048 -> 4096, 96 rows each: 10.1 and 11.1).  In two turns they lose (600 of one, 4096 ->
+    // 2048 SwiGLU: 26.2 and 16.2).
     const int64_t single = (c.rows / BM + c.E) * ((c.N + (dual ? 63 : 127)) / (dual ? 64 : 128));
     const bool pair = c.rows >= (int64_t)96 * c.E && single > num_sms();
     const int w_rows = dual && !pair ? 64 : 128;
