@@ -547,7 +547,7 @@ MOE_API int moe_mx8_dequantize_weight(int32_t dtype, int32_t E, int32_t K, int32
  *   in : codes [T,d], scales [T,P], topk_idx [T,k]
  *   out: codes_perm [rows_cap,d], scales_perm [rows_cap,P] (rows from offsets[E] on are
  *        left as they were), perm_token [rows_cap], slot_of [T,k], kept [E],
- *        offsets [E+1]; stats (may be NULL) as moe_permute's
+ *        offsets [E+1]; stats (may be NULL) as moe_permute's; outputs overlap no input
  *   ws:  moe_permute_mx8_workspace_size() bytes                              */
 MOE_API int moe_mx8_rows_capacity(const moe_config* cfg, int64_t* rows);   /* min(T*k, E*C) */
 MOE_API int moe_permute_mx8_workspace_size(const moe_config* cfg, size_t* bytes);
@@ -586,7 +586,7 @@ MOE_API int moe_check_mx8_product_config(const moe_mx8_product_config* cfg);
  *   x_codes/x_scales: 8-bit rows [rows,K]; w_*, wg_*: moe_mx8_quantize_weight of W, Wg
  *   [E,K,N] (wg_* NULL but for SWIGLU); out [rows,N] by out_dtype; out_scales
  *   [rows, moe_mx8_scale_pitch(N)] for MOE_DTYPE_MX8 (out then holds the codes of the
- *   fp32 values), else NULL.  Rows of no segment are not written.
+ *   fp32 values), else NULL.  Rows of no segment are not written.  Outputs overlap no input.
  * Offsets that descend or leave 0..rows are recorded as MOE_ERR_DEVICE_BOUNDS, and
  * nothing is written.                                                        */
 MOE_API int moe_mx8_grouped_product(const moe_mx8_product_config* cfg, const void* x_codes,

@@ -37,6 +37,20 @@ def test_rows_of_another_shape_or_type_are_refused():
                 layer.forward_mx8(x, W_r, ex, x8=rows)
 
 
+def test_rows_that_the_call_itself_writes_are_refused(calls):  # noqa: F811
+    """Square products one after the other: their tiles would be read and written at once."""
+    m = moe.MX8Product(moe.MX8ProductConfig(rows=16, K=64, N=64, E=2, out_dtype=moe.MX8), "cpu")
+    w, o = moe.MX8Weight((2, 64, 64), "cpu"), torch.zeros(3, dtype=torch.int32)
+    y = m.forward(moe.MX8Tensor((16, 64), "cpu"), o, w)
+    with pytest.raises(ValueError, match="writes"):
+        m.forward(y, o, w)
+    d = moe.MX8Dispatch(moe.MoEConfig(T=16, d=128, f=128, E=2, k=1), "cpu")
+    rows = d.forward(moe.MX8Tensor((16, 128), "cpu"), torch.zeros(16, 1, dtype=torch.int32))
+    with pytest.raises(ValueError, match="writes"):
+        d.forward(rows, torch.zeros(16, 1, dtype=torch.int32))
+    assert len(calls) == 2
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("T,cf", [(40, 0.0), (500, 0.0), (500, 0.7)])
 def test_places_after_other_forwards(T, cf):

@@ -230,6 +230,8 @@ class MX8Dispatch:
         for topk_idx [T, k] int32, -1 where a token takes part in nothing."""
         c = self.cfg
         _checked8(x, (c.T, c.d), "x")
+        if x is self.rows:
+            raise ValueError("x: the rows that this dispatch writes")
         _checked(topk_idx, (c.T, c.k), torch.int32, "topk_idx")
         if stats is not None:
             _checked(stats, (9 + c.E,), torch.float32, "stats")
@@ -276,9 +278,12 @@ class MX8Product:
                                    dtype=torch.bfloat16 if c.out_dtype == _moe.BF16 else torch.float32)
 
     def forward(self, x: MX8Tensor, offsets, w: MX8Weight, wg: MX8Weight | None = None, stream=None):
-        """out [rows, N] (rows of no segment are not written); x [rows, K], offsets
-        [E + 1] int32 as from MX8Dispatch, w (and the gate wg for SwiGLU) [E, N, K]."""
+        """out [rows, N] (rows of no segment are not written); x [rows, K], not this product's
+        own out, offsets [E + 1] int32 as from MX8Dispatch, w (and the gate wg for SwiGLU)
+        [E, N, K]."""
         _checked8(x, self._x, "x")
+        if x is self.out:                            # (tiles are written while others still read x)
+            raise ValueError("x: the rows that this product writes")
         _checked(offsets, self._offsets, torch.int32, "offsets")
         if (wg is not None) != self._dual:
             raise ValueError("wg is required iff act is MX8_ACT_SWIGLU")
