@@ -601,7 +601,7 @@ MOE_API int moe_mx8_grouped_product(const moe_mx8_product_config* cfg, const voi
  * layer without shared experts.  The forward computes with the unrounded h, as
  * moe_grouped_ffn does; act is scratch that need not outlive it.  The backward sees the
  * kept values alone: with h^ (g^, u^) what the codes stand for it forms
- * act = silu(h^) (silu(g^) u^) again, into act, and
+ * act = silu(h^) (silu(g^) u^) again, into act (bf16; no number where h^ is infinite), and
  *   dW_down = act^T dy, dh = dact silu'(h^) (dg, du likewise), dW_up, dW_gate, dx as
  * moe_grouped_ffn_backward does from these.
  * Offsets that descend, leave 0..rows_cap or begin a segment at no multiple of 128 (as
