@@ -68,6 +68,10 @@ __global__ void __launch_bounds__(PT_TOK) scan_assign_kernel(
     __shared__ unsigned picks[PT_TOK / 32][64];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int blk = blockIdx.x;
+    const int t = blk * PT_TOK + tid;
+    int sel[8];                                           // (asked for ahead of the histogram)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sel[j] = (j < k && t < T) ? topk[(size_t)t * k + j] : -1;
     if (tid < 64) s_base[tid] = s_total[tid] = 0;
     for (int i = tid; i < PT_TOK / 32 * 64; i += PT_TOK) (&picks[0][0])[i] = 0;
     __syncthreads();
@@ -84,6 +88,10 @@ __global__ void __launch_bounds__(PT_TOK) scan_assign_kernel(
         atomicAdd(&s_base[e0], before);                   // integers: order-free
         atomicAdd(&s_total[e0], total);
     }
+    // for the ranks within the tile: per warp and expert, the lanes whose token picks it
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        if (sel[j] >= 0 && sel[j] < E) atomicOr(&picks[warp][sel[j]], 1u << lane);
     __syncthreads();
     if (warp == 0) {                                      // two experts a lane
         int off = 0, kmax = 0;
@@ -134,15 +142,6 @@ __global__ void __launch_bounds__(PT_TOK) scan_assign_kernel(
         for (int r = s_off[e] + min(s_total[e], C) + blk * PT_TOK + tid; r < end; r += ntiles * PT_TOK)
             perm_token[r] = -1;
     }
-    // ranks within the tile: per warp and expert, the lanes whose token picks it
-    const int t = blk * PT_TOK + tid;
-    int sel[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        sel[j] = (j < k && t < T) ? topk[(size_t)t * k + j] : -1;
-        if (sel[j] >= 0 && sel[j] < E) atomicOr(&picks[warp][sel[j]], 1u << lane);
-    }
-    __syncthreads();
     if (t >= T) return;
     const unsigned lt = (1u << lane) - 1u;
     for (int j = 0; j < k; ++j) {
