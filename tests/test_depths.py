@@ -95,6 +95,12 @@ def test_a_checkpoint_on_another_device_is_refused():
         layer.backward(x, checkpoint=ck)
 
 
+def test_rows_that_are_no_tensor_are_refused_as_other_arguments_are():
+    layer = moe.MoELayer(moe.MoEConfig(**CFG), "cpu")
+    with pytest.raises(TypeError, match="expected a torch tensor"):
+        layer.forward([1.0], **cpu_weights())
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("swiglu", [False, True])
 def test_a_chain_without_copies(swiglu):

@@ -408,7 +408,7 @@ class MoELayer:
     def _apart(self, x, held, stream):
         """x, or a copy of it in ``held`` (allocated here if None) where it lies in one of the
         layer's own buffers, which are written before its backward has read it."""
-        if x.untyped_storage().data_ptr() not in self._storages:
+        if not isinstance(x, torch.Tensor) or x.untyped_storage().data_ptr() not in self._storages:
             return x, held
         with _on(stream):
             if held is None or held.shape != x.shape:
@@ -456,7 +456,7 @@ class MoELayer:
 
     def _forward_kept(self, k, x, W_r, W_up, W_down, W_gate, bias, noise, token_mask, stream):
         c = self.cfg
-        k.check(self)
+        k.check(c, self.out.device)
         k.h.ptrs                                  # raises: not on the current device
         self._inputs = k.inputs = None
         x, k.x = self._apart(x, k.x, stream)
@@ -597,7 +597,7 @@ class MoELayer:
         The gradients are the layer's own buffers: the next backward, another depth's too, writes
         them again.  dout may be the last one's dx."""
         if checkpoint is not None:
-            checkpoint.check(self)
+            checkpoint.check(self.cfg, self.out.device)
         if (self._inputs if checkpoint is None else checkpoint.inputs) is None:
             raise RuntimeError("backward() needs a forward() first")
         with _on(stream):

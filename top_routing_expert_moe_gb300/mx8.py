@@ -352,11 +352,11 @@ class MoECheckpoint:
         self.counts, self.kept, self.offsets = e(c.E), e(c.E), e(c.E + 1)
         self.inputs = self.x = None               # (x: a copy, where the forward's x was the layer's own memory)
 
-    def check(self, layer):
-        if bytes(layer.cfg) != bytes(self.cfg):
+    def check(self, cfg, device=None):
+        if bytes(cfg) != bytes(self.cfg):
             raise ValueError(f"the checkpoint is of another layer: {self.cfg!r}")
-        if layer.out.device != self.stats.device:
-            raise ValueError(f"the checkpoint is on {self.stats.device}, the layer on {layer.out.device}")
+        if device is not None and device != self.stats.device:
+            raise ValueError(f"the checkpoint is on {self.stats.device}, the layer on {device}")
 
     def keep_y(self, y_perm, stream=None):
         R, d = self.y.shape
