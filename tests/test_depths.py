@@ -145,3 +145,36 @@ def test_the_plain_layer_on_its_own_output():
     assert torch.equal(out, want_out)
     for n, t in layer.backward(dout).items():
         assert t is None or torch.equal(t, want[n]), n
+
+
+@pytest.mark.gpu
+def test_the_copy_is_made_on_the_given_stream():
+    """Queued behind work on that stream, with nothing on the current one to wait for."""
+    T, d, f, E, k = 300, 128, 256, 4, 2
+    cfg = moe.MoEConfig(T=T, d=d, f=f, E=E, k=k)
+    x, w, dout = layer_case(T, d, f, E, k, False, 3)
+
+    def chain(layer, stream, apart):
+        cks = [moe.MoECheckpoint(cfg) for _ in range(3)]
+        h = x
+        for c in cks:
+            h = apart(layer.forward(h, **w, checkpoint=c, stream=stream))
+        dy = dout
+        for c in reversed(cks):
+            g = layer.backward(dy, checkpoint=c, stream=stream)
+            dy = apart(g["dx"])
+        return h, g
+
+    want_h, want = chain(moe.MoELayer(cfg), None, lambda t: t.clone())
+    want = {n: t.clone() for n, t in want.items() if t is not None}
+    big = torch.randn(4096, 4096, device="cuda")
+    s = torch.cuda.Stream()
+    layer = moe.MoELayer(cfg)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        for _ in range(20):
+            big @ big                                  # the stream is busy while the calls are made
+    h, g = chain(layer, s, lambda t: t)
+    s.synchronize()
+    assert torch.equal(h, want_h) and all(torch.equal(g[n], t) for n, t in want.items())
+    assert moe.last_device_status() == 0
